@@ -51,8 +51,11 @@ typedef enum {
   COALESCE_ACT_NONE = 0,
   COALESCE_ACT_GELU_ERF = 1, /* 0.5 z (1 + erf(z / sqrt 2)) */
   COALESCE_ACT_SOFTPLUS = 2, /* ln(1 + e^z), evaluated as z above 20 */
-  COALESCE_ACT_RELU = 3      /* z > 0 ? z : 0 (the matmul-relu of the "Coalesce" README's MLIR pipeline) */
+  COALESCE_ACT_RELU = 3,     /* z > 0 ? z : 0 (the matmul-relu of the "Coalesce" README's MLIR pipeline) */
+  COALESCE_ACT_SILU = 4      /* z / (1 + e^-z): the feed-forward operators only, the other entry points refuse it */
 } coalesce_act;
+
+typedef enum { COALESCE_NORM_2 = 0, COALESCE_NORM_INF = 1 } coalesce_norm;
 
 /*
  * Y = act(A . B + bias) with the bias add and the activation applied to the
@@ -382,6 +385,136 @@ coalesce_status coalesce_autotune_mlp_forward(const void* x, int64_t ldx, const 
                                               int32_t L, void* out, int64_t ldo, int64_t M, coalesce_dtype dtype,
                                               coalesce_act hidden_act, int32_t iters, void* workspace,
                                               size_t workspace_bytes, coalesce_tune_report* report, void* stream);
+
+/*
+ * ---- Feed-forward operators -------------------------------------------------
+ *
+ * The two products of a language model's feed-forward block,
+ *   H = act(A Bg + bias_g) * (A Bu + bias_u)      (coalesce_gated_gemm)
+ *   Y = act(A B + bias) + R                       (coalesce_gemm_residual)
+ * each in one kernel, with their gradients, and the clipping of a whole list
+ * of gradients.  Common to the four GEMM entry points:
+ *   - in_dtype is F16 or BF16 (F32 inputs: COALESCE_ERR_UNSUPPORTED);
+ *     products accumulate in fp32, biases, activations and the residual are
+ *     applied in fp32, each result is rounded once (to nearest even);
+ *   - act is NONE, GELU_ERF, SOFTPLUS, RELU or SILU;
+ *   - matrices are row-major with 16-byte aligned rows and pitches of at most
+ *     2^23 elements; the extents are arbitrary (below 2^31 - 256, the product
+ *     of any two at most 2^41); bias vectors are 16-byte aligned;
+ *   - outputs must not overlap the inputs, each other or the workspace;
+ *   - `workspace` is device memory, 16-byte aligned, of at least the size that
+ *     the entry point's *_workspace_size gives for M, N, K on the current
+ *     device (0: none is needed and NULL is fine; also 0 for invalid extents
+ *     or a failed device query); its contents on entry are ignored.  Calls
+ *     that share a workspace must be ordered on one stream, and so must the
+ *     replays of captured graphs that share one;
+ *   - repeated calls give identical bits (no atomics); a row's result may
+ *     differ in its last bits between calls with another M, since the number
+ *     of rows decides how the contraction is split.
+ * Infinities and NaN in rows or columns a caller does not use stay there:
+ * padding between the row's end and the pitch is never part of a result.
+ */
+
+/*
+ * Y = act(A B + bias) + R.
+ *   A     device, M x K, in_dtype (lda);  B  device, K x N, in_dtype (ldb)
+ *   bias  device, N of in_dtype, or NULL
+ *   R     device, M x N of out_dtype (ldr), or NULL (nothing is added); may be
+ *         Y itself with ldr == ldy: the sum is then formed in place
+ *   Z     device, M x N of in_dtype (ldz), written with A B + bias, what the
+ *         backward needs; or NULL (inference, or act NONE)
+ *   Y     device, M x N of out_dtype (ldy): in_dtype or F32
+ * M == 0 or N == 0 is a no-op; K == 0 gives act(bias) + R.
+ */
+size_t coalesce_gemm_residual_workspace_size(int64_t M, int64_t N, int64_t K);
+coalesce_status coalesce_gemm_residual(const void* A, int64_t lda, const void* B, int64_t ldb, const void* bias,
+                                       const void* R, int64_t ldr, void* Z, int64_t ldz, void* Y, int64_t ldy,
+                                       int64_t M, int64_t N, int64_t K, coalesce_dtype in_dtype,
+                                       coalesce_dtype out_dtype, coalesce_act act, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of coalesce_gemm_residual for the upstream gradient dY:
+ *   dZ = dY act'(Z);  dA = dZ B^T;  dB = A^T dZ;  dbias[n] = sum_m dZ[m][n]
+ * and dR = dY, which is not written anywhere.  dZ is computed in fp32 and
+ * rounded once to in_dtype, the type of the matrix operands; dbias sums the
+ * unrounded values in fp32.  The derivative of relu at 0 is 0.
+ *   Z     as stored by the forward; may be NULL with act NONE
+ *   dY    device, M x N of dy_dtype (ldd): in_dtype or F32
+ *   dA    device, M x K of in_dtype (ldda), or NULL (not wanted; B may then be
+ *         NULL)
+ *   dB    device, K x N of grad_dtype (lddb): in_dtype or F32; or NULL (A may
+ *         then be NULL)
+ *   dbias device, N of grad_dtype, or NULL
+ * Wanted outputs are overwritten; M == 0 gives dB = 0 and dbias = 0, N == 0
+ * gives dA = 0.
+ */
+size_t coalesce_gemm_residual_backward_workspace_size(int64_t M, int64_t N, int64_t K);
+coalesce_status coalesce_gemm_residual_backward(const void* A, int64_t lda, const void* B, int64_t ldb, const void* Z,
+                                                int64_t ldz, const void* dY, int64_t ldd, void* dA, int64_t ldda,
+                                                void* dB, int64_t lddb, void* dbias, int64_t M, int64_t N, int64_t K,
+                                                coalesce_dtype in_dtype, coalesce_dtype dy_dtype,
+                                                coalesce_dtype grad_dtype, coalesce_act act, void* workspace,
+                                                size_t workspace_bytes, void* stream);
+
+/*
+ * Y = act(A Bg + bias_g) * (A Bu + bias_u): both projections, the activation
+ * and the product in one kernel.  Bg and Bu are K x N each (ldbg, ldbu): two
+ * matrices, or the two halves of one K x 2N matrix.  Zg, Zu (one pitch, both
+ * or neither) receive the two pre-activations in in_dtype for the backward.
+ * Other arguments as coalesce_gemm_residual.
+ */
+size_t coalesce_gated_gemm_workspace_size(int64_t M, int64_t N, int64_t K);
+coalesce_status coalesce_gated_gemm(const void* A, int64_t lda, const void* Bg, int64_t ldbg, const void* Bu,
+                                    int64_t ldbu, const void* bias_g, const void* bias_u, void* Zg, void* Zu,
+                                    int64_t ldz, void* Y, int64_t ldy, int64_t M, int64_t N, int64_t K,
+                                    coalesce_dtype in_dtype, coalesce_dtype out_dtype, coalesce_act act,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of coalesce_gated_gemm for the upstream gradient dY:
+ *   dZu = dY act(Zg);  dZg = dY Zu act'(Zg);  dA = dZg Bg^T + dZu Bu^T
+ *   dBg = A^T dZg;  dBu = A^T dZu;  dbias_x[n] = sum_m dZx[m][n]
+ * with the roundings, the optional outputs and the empty extents of
+ * coalesce_gemm_residual_backward.
+ */
+size_t coalesce_gated_gemm_backward_workspace_size(int64_t M, int64_t N, int64_t K);
+coalesce_status coalesce_gated_gemm_backward(const void* A, int64_t lda, const void* Bg, int64_t ldbg, const void* Bu,
+                                             int64_t ldbu, const void* Zg, const void* Zu, int64_t ldz, const void* dY,
+                                             int64_t ldd, void* dA, int64_t ldda, void* dBg, int64_t lddbg, void* dBu,
+                                             int64_t lddbu, void* dbias_g, void* dbias_u, int64_t M, int64_t N,
+                                             int64_t K, coalesce_dtype in_dtype, coalesce_dtype dy_dtype,
+                                             coalesce_dtype grad_dtype, coalesce_act act, void* workspace,
+                                             size_t workspace_bytes, void* stream);
+
+/*
+ * The norm of a list of gradients taken as one vector, and the list scaled to
+ * at most max_norm:
+ *   norm = sqrt(sum of all squares) (COALESCE_NORM_2) or the largest magnitude
+ *          (COALESCE_NORM_INF)
+ *   out[i] = grads[i] * c,  c = min(1, max_norm / (norm + 1e-6))
+ *   grads   HOST array of `count` device pointers, each to numel[i] elements
+ *           of dtypes[i] (a coalesce_dtype), dense, aligned to the element size
+ *   out     HOST array of device pointers of the same sizes and types; out[i]
+ *           may be grads[i] (in place: then not written when c is 1)
+ *   norm    device, one float, written
+ *   workspace  device, 16-byte aligned, at least
+ *           coalesce_grad_norm_workspace_size(numel, dtypes, count) bytes (0
+ *           for an empty list)
+ * Squares are summed in fp64 in a fixed order, so the sum neither overflows
+ * nor depends on timing; c is rounded to fp32, the product once to the
+ * tensor's type.  Non-finite gradients are not filtered: a NaN among them
+ * makes norm, and with it every output, NaN; an infinity gives norm = inf and
+ * c = 0.  An output must not overlap the norm, the workspace, another output
+ * or a gradient other than its own.  An empty list has norm 0.
+ */
+size_t coalesce_grad_norm_workspace_size(const int64_t* numel, const int32_t* dtypes, int64_t count);
+coalesce_status coalesce_grad_norm(const void* const* grads, const int64_t* numel, const int32_t* dtypes,
+                                   int64_t count, coalesce_norm norm_type, float* norm, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+coalesce_status coalesce_clip_grad_norm(const void* const* grads, void* const* out, const int64_t* numel,
+                                        const int32_t* dtypes, int64_t count, coalesce_norm norm_type, double max_norm,
+                                        float* norm, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Forget every tuned configuration (all devices). */
 coalesce_status coalesce_autotune_clear(void);

@@ -20,14 +20,16 @@ LIB_PATH = os.path.join(_HERE, "libcoalesce.so")
 
 OK, ERR_INVALID_ARGUMENT, ERR_UNSUPPORTED, ERR_DEVICE = 0, 1, 2, 3
 F32, F16, BF16 = 0, 1, 2
-ACT_NONE, ACT_GELU_ERF, ACT_SOFTPLUS, ACT_RELU = 0, 1, 2, 3
+ACT_NONE, ACT_GELU_ERF, ACT_SOFTPLUS, ACT_RELU, ACT_SILU = 0, 1, 2, 3, 4
+NORM_2, NORM_INF = 0, 1
 
 _DTYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 _ACTS = {"none": ACT_NONE, None: ACT_NONE, "gelu": ACT_GELU_ERF, "gelu_erf": ACT_GELU_ERF,
-         "softplus": ACT_SOFTPLUS, "relu": ACT_RELU}
+         "softplus": ACT_SOFTPLUS, "relu": ACT_RELU, "silu": ACT_SILU}
 
 # Every exported entry point of include/coalesce.h with its ctypes signature.
 _i64, _i32, _p, _sz = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t
+_f64 = ctypes.c_double
 SIGNATURES = {
     "coalesce_gemm_bias_act": (_i32, [_p, _i64, _p, _i64, _p, _p, _i64, _i64, _i64, _i64, _i32, _i32, _i32, _p]),
     "coalesce_mlp_forward": (_i32, [_p, _i64, _p, _p, _i32, _p, _i64, _i64, _i32, _i32, _p]),
@@ -44,6 +46,21 @@ SIGNATURES = {
                                                _i32, _p, _sz, _p, _p]),
     "coalesce_autotune_mlp_forward": (_i32, [_p, _i64, _p, _p, _i32, _p, _i64, _i64, _i32, _i32, _i32, _p, _sz, _p,
                                              _p]),
+    "coalesce_gemm_residual_workspace_size": (_sz, [_i64, _i64, _i64]),
+    "coalesce_gemm_residual": (_i32, [_p, _i64, _p, _i64, _p, _p, _i64, _p, _i64, _p, _i64, _i64, _i64, _i64, _i32,
+                                      _i32, _i32, _p, _sz, _p]),
+    "coalesce_gemm_residual_backward_workspace_size": (_sz, [_i64, _i64, _i64]),
+    "coalesce_gemm_residual_backward": (_i32, [_p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64,
+                                               _i64, _i64, _i32, _i32, _i32, _i32, _p, _sz, _p]),
+    "coalesce_gated_gemm_workspace_size": (_sz, [_i64, _i64, _i64]),
+    "coalesce_gated_gemm": (_i32, [_p, _i64, _p, _i64, _p, _i64, _p, _p, _p, _p, _i64, _p, _i64, _i64, _i64, _i64,
+                                   _i32, _i32, _i32, _p, _sz, _p]),
+    "coalesce_gated_gemm_backward_workspace_size": (_sz, [_i64, _i64, _i64]),
+    "coalesce_gated_gemm_backward": (_i32, [_p, _i64, _p, _i64, _p, _i64, _p, _p, _i64, _p, _i64, _p, _i64, _p, _i64,
+                                            _p, _i64, _p, _p, _i64, _i64, _i64, _i32, _i32, _i32, _i32, _p, _sz, _p]),
+    "coalesce_grad_norm_workspace_size": (_sz, [_p, _p, _i64]),
+    "coalesce_grad_norm": (_i32, [_p, _p, _p, _i64, _i32, _p, _p, _sz, _p]),
+    "coalesce_clip_grad_norm": (_i32, [_p, _p, _p, _p, _i64, _i32, _f64, _p, _p, _sz, _p]),
     "coalesce_autotune_clear": (_i32, []),
     "coalesce_bias_add": (_i32, [_p, _i64, _p, _p, _i64, _i64, _i64, _i32, _i32, _i32, _p]),
     "coalesce_activation": (_i32, [_p, _i64, _p, _i64, _i64, _i64, _i32, _i32, _p]),
@@ -624,3 +641,7 @@ class FusedMLPSoftplusWN(torch.nn.Module):
         if torch.is_grad_enabled() and (x.requires_grad or any(p.requires_grad for p in vs + gs)):
             return _FusedMLPWNFunction.apply(x, self.hidden_act, len(vs), *vs, *gs)
         return mlp_forward(x, weight_norm(vs, gs), hidden_act=self.hidden_act)
+
+
+from .ffn import (GatedFFN, GatedGrads, GemmGrads, clip_grad_norm, gated_gemm, gated_gemm_backward,  # noqa: E402,F401
+                  gated_gemm_train, gemm_residual, gemm_residual_backward, gemm_residual_train, grad_norm)

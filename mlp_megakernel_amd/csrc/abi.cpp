@@ -8,6 +8,7 @@
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
+#include <exception>
 #include <map>
 #include <mutex>
 #include <string>
@@ -958,6 +959,435 @@ coalesce_status coalesce_autotune_mlp_forward(const void* x, int64_t ldx, const 
                                 false, false, stream);
       },
       iters, stream, out, ldo * 2, M, dims[L] * 2, workspace, workspace_bytes, operands, key, report);
+}
+
+// ---- feed-forward operators ------------------------------------------------
+
+}  // extern "C"
+
+namespace {
+
+// Activations of the feed-forward operators: those of the GEMM and SiLU.
+bool valid_ffn_act(int a) { return valid_act((coalesce_act)a) || a == COALESCE_ACT_SILU; }
+int ffn_act_code(coalesce_act a) { return a == COALESCE_ACT_SILU ? (int)ACT_SILU : act_code(a); }
+DType dt_code(coalesce_dtype d) { return d == COALESCE_F32 ? DT_F32 : d == COALESCE_F16 ? DT_F16 : DT_BF16; }
+
+// Extents and types shared by the feed-forward entry points: 16-bit inputs,
+// `other` (an output or gradient type) that type or F32.
+coalesce_status check_ffn(int64_t M, int64_t N, int64_t K, coalesce_dtype in, coalesce_dtype other,
+                          coalesce_act act) {
+  if (M < 0 || N < 0 || K < 0)
+    return fail(COALESCE_ERR_INVALID_ARGUMENT, "negative extent (M=%lld N=%lld K=%lld)", (long long)M, (long long)N,
+                (long long)K);
+  if (!valid_dtype(in) || !valid_dtype(other)) return fail(COALESCE_ERR_INVALID_ARGUMENT, "unknown dtype");
+  if (!valid_ffn_act(act)) return fail(COALESCE_ERR_INVALID_ARGUMENT, "unknown activation %d", (int)act);
+  if (in == COALESCE_F32) return fail(COALESCE_ERR_UNSUPPORTED, "the feed-forward operators take fp16 or bf16 inputs");
+  if (other != in && other != COALESCE_F32)
+    return fail(COALESCE_ERR_UNSUPPORTED, "dtype combination %d and %d not supported", (int)in, (int)other);
+  const int64_t lim = kMaxExtent - 256;
+  if (M > lim || N > lim || K > lim) return fail(COALESCE_ERR_UNSUPPORTED, "extents must be below 2^31 - 256");
+  // the tile counts of all products are 32-bit
+  const int64_t area = int64_t(1) << 41;
+  if ((N && M > area / N) || (K && M > area / K) || (K && N > area / K))
+    return fail(COALESCE_ERR_UNSUPPORTED, "a product of two extents above 2^41");
+  return COALESCE_OK;
+}
+
+// A rows x cols matrix operand that has elements: present, pitch at least the
+// row and at most 2^23 (256 rows are addressed with 32-bit byte offsets),
+// 16-byte aligned rows.
+coalesce_status check_mat(const void* t, int64_t ld, int64_t cols, int64_t es, const char* name) {
+  if (!t) return fail(COALESCE_ERR_INVALID_ARGUMENT, "%s is NULL", name);
+  if (ld < cols) return fail(COALESCE_ERR_INVALID_ARGUMENT, "the pitch of %s is shorter than the row", name);
+  if (ld > (int64_t(1) << 23)) return fail(COALESCE_ERR_UNSUPPORTED, "the pitch of %s must be at most 2^23", name);
+  if (!aligned16(t) || (ld * es) % 16)
+    return fail(COALESCE_ERR_UNSUPPORTED, "%s must be 16-byte aligned with a 16-byte row pitch", name);
+  return COALESCE_OK;
+}
+coalesce_status check_vec(const void* t, const char* name) {
+  if (t && !aligned16(t)) return fail(COALESCE_ERR_UNSUPPORTED, "%s must be 16-byte aligned", name);
+  return COALESCE_OK;
+}
+
+// Operands of a call, to refuse outputs that overlap anything else.  Matrices
+// of one pitch may interleave (the halves of a wider matrix): their rows are
+// disjoint where the distance between the bases, modulo the pitch, leaves room
+// for both rows.
+struct Operand {
+  Range r;
+  const char* name;
+  bool out;
+  uint64_t row = 0, pitch = 0;  // bytes; pitch 0: one run of memory
+};
+bool interleaved(const Operand& a, const Operand& b) {
+  if (!a.pitch || a.pitch != b.pitch) return false;
+  const uint64_t dist = b.r.lo >= a.r.lo ? (uint64_t)(b.r.lo - a.r.lo) % a.pitch
+                                         : (a.pitch - (uint64_t)(a.r.lo - b.r.lo) % a.pitch) % a.pitch;
+  return dist >= a.row && dist + b.row <= a.pitch;
+}
+struct Operands {
+  Operand v[16];
+  int n = 0;
+  void mat(bool out, const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t es, const char* name) {
+    v[n++] = {span(p, rows, cols, ld, es), name, out, (uint64_t)(cols * es), (uint64_t)(ld * es)};
+  }
+  void run(bool out, const Range& r, const char* name) { v[n++] = {r, name, out}; }
+  coalesce_status check() const {
+    for (int i = 0; i < n; ++i)
+      for (int j = 0; j < i; ++j)
+        if ((v[i].out || v[j].out) && overlap(v[i].r, v[j].r) && !interleaved(v[i], v[j]))
+          return fail(COALESCE_ERR_INVALID_ARGUMENT, "%s overlaps %s", v[v[i].out ? i : j].name,
+                      v[v[i].out ? j : i].name);
+    return COALESCE_OK;
+  }
+};
+
+coalesce_status check_workspace(const void* ws, size_t have, size_t need) {
+  if (need == 0) return COALESCE_OK;
+  if (!ws) return fail(COALESCE_ERR_INVALID_ARGUMENT, "workspace is NULL (%zu bytes are needed)", need);
+  if (!aligned16(ws)) return fail(COALESCE_ERR_UNSUPPORTED, "workspace must be 16-byte aligned");
+  if (have < need)
+    return fail(COALESCE_ERR_INVALID_ARGUMENT, "workspace of %zu bytes is smaller than the %zu needed", have, need);
+  return COALESCE_OK;
+}
+
+// Forward of both operators: W[1] only for the gated product.
+coalesce_status ffn_forward(bool gated, const void* A, int64_t lda, const void* const (&B)[2], const int64_t (&ldb)[2],
+                            const void* const (&bias)[2], const void* R, int64_t ldr, void* const (&Z)[2], int64_t ldz,
+                            void* Y, int64_t ldy, int64_t M, int64_t N, int64_t K, coalesce_dtype in,
+                            coalesce_dtype out, coalesce_act act, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+  coalesce_status s = check_ffn(M, N, K, in, out, act);
+  if (s != COALESCE_OK) return s;
+  if (M == 0 || N == 0) return ok();
+  const int64_t is = dsize(in), os = dsize(out);
+  const int nw = gated ? 2 : 1;
+  static const char* const bn[2] = {"B (or Bg)", "Bu"};
+  static const char* const zn[2] = {"Z (or Zg)", "Zu"};
+  static const char* const vn[2] = {"bias (or bias_g)", "bias_u"};
+  Operands ops;
+  if ((s = check_mat(Y, ldy, N, os, "Y")) != COALESCE_OK) return s;
+  ops.mat(true, Y, M, N, ldy, os, "Y");
+  if (K > 0) {
+    if ((s = check_mat(A, lda, K, is, "A")) != COALESCE_OK) return s;
+    ops.mat(false, A, M, K, lda, is, "A");
+  }
+  if (gated && !Z[0] != !Z[1]) return fail(COALESCE_ERR_INVALID_ARGUMENT, "Zg and Zu go together");
+  for (int i = 0; i < nw; ++i) {
+    if (K > 0) {
+      if ((s = check_mat(B[i], ldb[i], N, is, bn[i])) != COALESCE_OK) return s;
+      ops.mat(false, B[i], K, N, ldb[i], is, bn[i]);
+    }
+    if ((s = check_vec(bias[i], vn[i])) != COALESCE_OK) return s;
+    ops.mat(false, bias[i], 1, N, N, is, vn[i]);
+    if (Z[i]) {
+      if ((s = check_mat(Z[i], ldz, N, is, zn[i])) != COALESCE_OK) return s;
+      ops.mat(true, Z[i], M, N, ldz, is, zn[i]);
+    }
+  }
+  if (R) {
+    if ((s = check_mat(R, ldr, N, os, "R")) != COALESCE_OK) return s;
+    if (R == Y && ldr != ldy) return fail(COALESCE_ERR_INVALID_ARGUMENT, "in-place residual with different pitches");
+    if (R != Y) ops.mat(false, R, M, N, ldr, os, "R");
+  }
+  if ((s = ops.check()) != COALESCE_OK) return s;
+  int cus = 0;
+  if ((s = current_cus(&cus)) != COALESCE_OK) return s;
+  const size_t need = ffn_forward_workspace(M, N, K, gated, cus);
+  if ((s = check_workspace(workspace, workspace_bytes, need)) != COALESCE_OK) return s;
+  if (need) {
+    ops.run(true, {(uintptr_t)workspace, (uintptr_t)workspace + need}, "the workspace");
+    if ((s = ops.check()) != COALESCE_OK) return s;
+  }
+  FfnParams p{};
+  p.X = A;
+  p.ldx = lda;
+  for (int i = 0; i < nw; ++i) {
+    p.W[i] = B[i];
+    p.ldw[i] = ldb[i];
+    p.bias[i] = bias[i];
+    p.Z[i] = Z[i];
+  }
+  p.R = R;
+  p.ldr = ldr;
+  p.ldz = ldz;
+  p.Y = Y;
+  p.ldy = ldy;
+  p.M = (int)M;
+  p.N = (int)N;
+  p.K = (int)K;
+  hipError_t e = launch_ffn_forward(p, gated, dt_code(in), dt_code(out), ffn_act_code(act), (hipStream_t)stream, cus,
+                                    workspace);
+  if (e != hipSuccess) return device_fail(e, gated ? "gated GEMM launch" : "residual GEMM launch");
+  return ok();
+}
+
+coalesce_status ffn_backward(bool gated, const void* A, int64_t lda, const void* const (&B)[2],
+                             const int64_t (&ldb)[2], const void* const (&Z)[2], int64_t ldz, const void* dY,
+                             int64_t ldd, void* dA, int64_t ldda, void* const (&dB)[2], const int64_t (&lddb)[2],
+                             void* const (&db)[2], int64_t M, int64_t N, int64_t K, coalesce_dtype in,
+                             coalesce_dtype dy, coalesce_dtype grad, coalesce_act act, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  coalesce_status s = check_ffn(M, N, K, in, dy, act);
+  if (s != COALESCE_OK) return s;
+  if ((s = check_ffn(M, N, K, in, grad, act)) != COALESCE_OK) return s;
+  const int64_t is = dsize(in), ds = dsize(dy), gs = dsize(grad);
+  const int nw = gated ? 2 : 1;
+  const bool want_dA = dA && M > 0 && K > 0;
+  const bool want_dB = (dB[0] || dB[1]) && N > 0 && K > 0;
+  const bool want_db = (db[0] || db[1]) && N > 0;
+  if (!want_dA && !want_dB && !want_db) return ok();
+  static const char* const bn[2] = {"B (or Bg)", "Bu"};
+  static const char* const zn[2] = {"Z (or Zg)", "Zu"};
+  static const char* const gn[2] = {"dB (or dBg)", "dBu"};
+  static const char* const vn[2] = {"dbias (or dbias_g)", "dbias_u"};
+  Operands ops;
+  if (M > 0 && N > 0) {
+    if ((s = check_mat(dY, ldd, N, ds, "dY")) != COALESCE_OK) return s;
+    ops.mat(false, dY, M, N, ldd, ds, "dY");
+  }
+  if (want_dB && M > 0) {
+    if ((s = check_mat(A, lda, K, is, "A")) != COALESCE_OK) return s;
+    ops.mat(false, A, M, K, lda, is, "A");
+  }
+  if (want_dA) {
+    if ((s = check_mat(dA, ldda, K, is, "dA")) != COALESCE_OK) return s;
+    ops.mat(true, dA, M, K, ldda, is, "dA");
+  }
+  for (int i = 0; i < nw; ++i) {
+    if (want_dA && N > 0) {
+      if ((s = check_mat(B[i], ldb[i], N, is, bn[i])) != COALESCE_OK) return s;
+      ops.mat(false, B[i], K, N, ldb[i], is, bn[i]);
+    }
+    if ((gated || act != COALESCE_ACT_NONE) && M > 0 && N > 0) {
+      if ((s = check_mat(Z[i], ldz, N, is, zn[i])) != COALESCE_OK) return s;
+      ops.mat(false, Z[i], M, N, ldz, is, zn[i]);
+    }
+    if (want_dB && dB[i]) {
+      if ((s = check_mat(dB[i], lddb[i], N, gs, gn[i])) != COALESCE_OK) return s;
+      ops.mat(true, dB[i], K, N, lddb[i], gs, gn[i]);
+    }
+    if (want_db && db[i]) {
+      if ((s = check_vec(db[i], vn[i])) != COALESCE_OK) return s;
+      ops.mat(true, db[i], 1, N, N, gs, vn[i]);
+    }
+  }
+  if ((s = ops.check()) != COALESCE_OK) return s;
+  FfnBwdParams p{};
+  p.X = A;
+  p.ldx = lda;
+  p.dY = dY;
+  p.ldd = ldd;
+  p.ldz = ldz;
+  if (want_dA) p.dX = dA;
+  p.lddx = ldda;
+  for (int i = 0; i < nw; ++i) {
+    p.W[i] = B[i];
+    p.ldw[i] = ldb[i];
+    p.Z[i] = Z[i];
+    if (want_dB) p.dW[i] = dB[i];
+    p.lddw[i] = lddb[i];
+    if (want_db) p.db[i] = db[i];
+  }
+  p.M = (int)M;
+  p.N = (int)N;
+  p.K = (int)K;
+  int cus = 0;
+  if ((s = current_cus(&cus)) != COALESCE_OK) return s;
+  const size_t need = ffn_backward_workspace(p, gated, cus);
+  if ((s = check_workspace(workspace, workspace_bytes, need)) != COALESCE_OK) return s;
+  if (need) {
+    ops.run(true, {(uintptr_t)workspace, (uintptr_t)workspace + need}, "the workspace");
+    if ((s = ops.check()) != COALESCE_OK) return s;
+  }
+  hipError_t e = launch_ffn_backward(p, gated, dt_code(in), dt_code(dy), dt_code(grad), ffn_act_code(act),
+                                     (hipStream_t)stream, cus, workspace);
+  if (e != hipSuccess) return device_fail(e, gated ? "gated GEMM backward launch" : "residual GEMM backward launch");
+  return ok();
+}
+
+size_t ffn_workspace_size(bool gated, bool backward, int64_t M, int64_t N, int64_t K) {
+  if (check_ffn(M, N, K, COALESCE_F16, COALESCE_F16, COALESCE_ACT_NONE) != COALESCE_OK) return 0;
+  int cus = 0;
+  if (current_cus(&cus) != COALESCE_OK) return 0;
+  ok();
+  if (!backward) return M == 0 || N == 0 ? 0 : ffn_forward_workspace(M, N, K, gated, cus);
+  FfnBwdParams p{};
+  p.M = (int)M;
+  p.N = (int)N;
+  p.K = (int)K;
+  return ffn_backward_workspace(p, gated, cus);
+}
+
+// The checked list of the gradient-norm entry points; dst may be NULL (norm
+// alone) or hold the sources themselves (in place).
+coalesce_status check_grad_list(const void* const* src, void* const* dst, const int64_t* numel, const int32_t* dtypes,
+                                int64_t count, coalesce_norm norm_type, const float* norm, ClipList* l) {
+  if (count < 0) return fail(COALESCE_ERR_INVALID_ARGUMENT, "negative tensor count");
+  if (norm_type != COALESCE_NORM_2 && norm_type != COALESCE_NORM_INF)
+    return fail(COALESCE_ERR_INVALID_ARGUMENT, "unknown norm %d", (int)norm_type);
+  if (!norm) return fail(COALESCE_ERR_INVALID_ARGUMENT, "norm is NULL");
+  if (reinterpret_cast<uintptr_t>(norm) & 3u) return fail(COALESCE_ERR_UNSUPPORTED, "norm must be 4-byte aligned");
+  if (count > 0 && (!src || !numel || !dtypes))
+    return fail(COALESCE_ERR_INVALID_ARGUMENT, "grads, numel or dtypes is NULL");
+  int64_t total = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    if (numel[i] < 0) return fail(COALESCE_ERR_INVALID_ARGUMENT, "numel[%lld] is negative", (long long)i);
+    if (!valid_dtype(dtypes[i])) return fail(COALESCE_ERR_INVALID_ARGUMENT, "unknown dtype of tensor %lld", (long long)i);
+    if (numel[i] == 0) continue;
+    if (!src[i] || (dst && !dst[i])) return fail(COALESCE_ERR_INVALID_ARGUMENT, "tensor %lld is NULL", (long long)i);
+    const uintptr_t m = (uintptr_t)dsize(dtypes[i]) - 1;
+    if (((uintptr_t)src[i] & m) || (dst && ((uintptr_t)dst[i] & m)))
+      return fail(COALESCE_ERR_UNSUPPORTED, "tensor %lld is not aligned to its element size", (long long)i);
+    if (numel[i] > (int64_t(1) << 48) - total) return fail(COALESCE_ERR_UNSUPPORTED, "more than 2^48 elements");
+    total += numel[i];
+  }
+  l->src = src;
+  l->dst = dst;
+  l->numel = numel;
+  l->dtype = dtypes;
+  l->count = count;
+  return COALESCE_OK;
+}
+
+// Outputs of a clip call must not overlap each other, the norm or an input
+// other than their own.  Sorted by address, any overlap shows between a range
+// and the furthest-reaching one before it.
+coalesce_status check_grad_overlap(const ClipList& l, const float* norm, const void* ws, size_t ws_bytes) {
+  struct Item {
+    Range r;
+    bool out;
+    int64_t i;
+  };
+  std::vector<Item> v;
+  v.reserve((size_t)l.count * 2 + 2);
+  for (int64_t i = 0; i < l.count; ++i) {
+    if (l.numel[i] == 0) continue;
+    const int64_t es = dsize(l.dtype[i]);
+    const bool in_place = l.dst && l.dst[i] == l.src[i];
+    if (!in_place) v.push_back({span(l.src[i], 1, l.numel[i], l.numel[i], es), false, i});
+    if (l.dst) v.push_back({span(l.dst[i], 1, l.numel[i], l.numel[i], es), true, i});
+  }
+  v.push_back({{(uintptr_t)norm, (uintptr_t)norm + 4}, true, -1});
+  if (ws_bytes) v.push_back({{(uintptr_t)ws, (uintptr_t)ws + ws_bytes}, true, -2});
+  std::sort(v.begin(), v.end(), [](const Item& a, const Item& b) { return a.r.lo < b.r.lo; });
+  uintptr_t end_any = 0, end_out = 0;
+  for (const Item& x : v) {
+    if (x.r.lo < end_out || (x.out && x.r.lo < end_any))
+      return fail(COALESCE_ERR_INVALID_ARGUMENT, "an output (tensor %lld) overlaps another operand", (long long)x.i);
+    end_any = std::max(end_any, x.r.hi);
+    if (x.out) end_out = std::max(end_out, x.r.hi);
+  }
+  return COALESCE_OK;
+}
+
+coalesce_status grad_norm_impl(const void* const* src, void* const* dst, const int64_t* numel, const int32_t* dtypes,
+                               int64_t count, coalesce_norm norm_type, double max_norm, float* norm, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  ClipList l{};
+  coalesce_status s = check_grad_list(src, dst, numel, dtypes, count, norm_type, norm, &l);
+  if (s != COALESCE_OK) return s;
+  int cus = 0;
+  if ((s = current_cus(&cus)) != COALESCE_OK) return s;
+  const size_t need = grad_norm_workspace(l, cus);
+  if ((s = check_workspace(workspace, workspace_bytes, need)) != COALESCE_OK) return s;
+  try {
+    if ((s = check_grad_overlap(l, norm, workspace, need)) != COALESCE_OK) return s;
+  } catch (const std::exception&) {
+    return fail(COALESCE_ERR_UNSUPPORTED, "out of host memory for a list of %lld tensors", (long long)count);
+  }
+  hipError_t e = launch_grad_norm(l, norm_type == COALESCE_NORM_INF, max_norm, norm, workspace, (hipStream_t)stream, cus);
+  if (e != hipSuccess) return device_fail(e, "gradient norm launch");
+  return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t coalesce_gemm_residual_workspace_size(int64_t M, int64_t N, int64_t K) {
+  return ffn_workspace_size(false, false, M, N, K);
+}
+size_t coalesce_gemm_residual_backward_workspace_size(int64_t M, int64_t N, int64_t K) {
+  return ffn_workspace_size(false, true, M, N, K);
+}
+size_t coalesce_gated_gemm_workspace_size(int64_t M, int64_t N, int64_t K) {
+  return ffn_workspace_size(true, false, M, N, K);
+}
+size_t coalesce_gated_gemm_backward_workspace_size(int64_t M, int64_t N, int64_t K) {
+  return ffn_workspace_size(true, true, M, N, K);
+}
+
+coalesce_status coalesce_gemm_residual(const void* A, int64_t lda, const void* B, int64_t ldb, const void* bias,
+                                       const void* R, int64_t ldr, void* Z, int64_t ldz, void* Y, int64_t ldy,
+                                       int64_t M, int64_t N, int64_t K, coalesce_dtype in_dtype,
+                                       coalesce_dtype out_dtype, coalesce_act act, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+  return ffn_forward(false, A, lda, {B, nullptr}, {ldb, 0}, {bias, nullptr}, R, ldr, {Z, nullptr}, ldz, Y, ldy, M, N, K,
+                     in_dtype, out_dtype, act, workspace, workspace_bytes, stream);
+}
+
+coalesce_status coalesce_gemm_residual_backward(const void* A, int64_t lda, const void* B, int64_t ldb, const void* Z,
+                                                int64_t ldz, const void* dY, int64_t ldd, void* dA, int64_t ldda,
+                                                void* dB, int64_t lddb, void* dbias, int64_t M, int64_t N, int64_t K,
+                                                coalesce_dtype in_dtype, coalesce_dtype dy_dtype,
+                                                coalesce_dtype grad_dtype, coalesce_act act, void* workspace,
+                                                size_t workspace_bytes, void* stream) {
+  return ffn_backward(false, A, lda, {B, nullptr}, {ldb, 0}, {Z, nullptr}, ldz, dY, ldd, dA, ldda, {dB, nullptr},
+                      {lddb, 0}, {dbias, nullptr}, M, N, K, in_dtype, dy_dtype, grad_dtype, act, workspace,
+                      workspace_bytes, stream);
+}
+
+coalesce_status coalesce_gated_gemm(const void* A, int64_t lda, const void* Bg, int64_t ldbg, const void* Bu,
+                                    int64_t ldbu, const void* bias_g, const void* bias_u, void* Zg, void* Zu,
+                                    int64_t ldz, void* Y, int64_t ldy, int64_t M, int64_t N, int64_t K,
+                                    coalesce_dtype in_dtype, coalesce_dtype out_dtype, coalesce_act act,
+                                    void* workspace, size_t workspace_bytes, void* stream) {
+  return ffn_forward(true, A, lda, {Bg, Bu}, {ldbg, ldbu}, {bias_g, bias_u}, nullptr, 0, {Zg, Zu}, ldz, Y, ldy, M, N, K,
+                     in_dtype, out_dtype, act, workspace, workspace_bytes, stream);
+}
+
+coalesce_status coalesce_gated_gemm_backward(const void* A, int64_t lda, const void* Bg, int64_t ldbg, const void* Bu,
+                                             int64_t ldbu, const void* Zg, const void* Zu, int64_t ldz, const void* dY,
+                                             int64_t ldd, void* dA, int64_t ldda, void* dBg, int64_t lddbg, void* dBu,
+                                             int64_t lddbu, void* dbias_g, void* dbias_u, int64_t M, int64_t N,
+                                             int64_t K, coalesce_dtype in_dtype, coalesce_dtype dy_dtype,
+                                             coalesce_dtype grad_dtype, coalesce_act act, void* workspace,
+                                             size_t workspace_bytes, void* stream) {
+  return ffn_backward(true, A, lda, {Bg, Bu}, {ldbg, ldbu}, {Zg, Zu}, ldz, dY, ldd, dA, ldda, {dBg, dBu},
+                      {lddbg, lddbu}, {dbias_g, dbias_u}, M, N, K, in_dtype, dy_dtype, grad_dtype, act, workspace,
+                      workspace_bytes, stream);
+}
+
+size_t coalesce_grad_norm_workspace_size(const int64_t* numel, const int32_t* dtypes, int64_t count) {
+  if (count <= 0 || !numel || !dtypes) return 0;
+  int64_t total = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    if (numel[i] < 0 || numel[i] > (int64_t(1) << 48) - total || !valid_dtype(dtypes[i])) return 0;
+    total += numel[i];
+  }
+  int cus = 0;
+  if (current_cus(&cus) != COALESCE_OK) return 0;
+  ok();
+  ClipList l{};
+  l.numel = numel;
+  l.dtype = dtypes;
+  l.count = count;
+  return grad_norm_workspace(l, cus);
+}
+
+coalesce_status coalesce_grad_norm(const void* const* grads, const int64_t* numel, const int32_t* dtypes,
+                                   int64_t count, coalesce_norm norm_type, float* norm, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  return grad_norm_impl(grads, nullptr, numel, dtypes, count, norm_type, 0.0, norm, workspace, workspace_bytes, stream);
+}
+
+coalesce_status coalesce_clip_grad_norm(const void* const* grads, void* const* out, const int64_t* numel,
+                                        const int32_t* dtypes, int64_t count, coalesce_norm norm_type, double max_norm,
+                                        float* norm, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!(max_norm >= 0.0)) return fail(COALESCE_ERR_INVALID_ARGUMENT, "max_norm must not be negative or NaN");
+  if (count > 0 && !out) return fail(COALESCE_ERR_INVALID_ARGUMENT, "out is NULL");
+  return grad_norm_impl(grads, out, numel, dtypes, count, norm_type, max_norm, norm, workspace, workspace_bytes, stream);
 }
 
 coalesce_status coalesce_autotune_clear(void) {

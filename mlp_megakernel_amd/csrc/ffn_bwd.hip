@@ -1,0 +1,254 @@
+// Backward of the feed-forward operators:
+//   gated product       dZu = dY act(Zg),  dZg = dY Zu act'(Zg)
+//   GEMM with residual  dZ  = dY act'(Z)   (and dR = dY, nothing to compute)
+//   dX = sum_i dZi Wi^T,  dWi = X^T dZi,  dbi[n] = sum_m dZi[m][n]
+// One elementwise pass turns the stored pre-activations and the arriving
+// gradient into the dZi, rounded once to the input type because they are the
+// matrix products' operands, and sums their columns in fp32 before that
+// rounding.  Both dZi Wi^T run as one K loop over two segments, both X^T dZi
+// as one launch whose tiles share X.
+#include <algorithm>
+
+#include "gemm16_core.hpp"
+
+namespace coalesce {
+namespace {
+
+typedef TileGeo<128, 128, 4, 2, 2, 1> Geo128;
+
+// act(z) and act'(z) in fp32.
+template <int ACT>
+__device__ __forceinline__ void act_and_grad(float z, float& f, float& d) {
+  if constexpr (ACT == ACT_SILU) {
+    const float s = sigmoid(z);
+    f = z * s;
+    d = s * __builtin_fmaf(z, 1.0f - s, 1.0f);
+  } else if constexpr (ACT == ACT_GELU) {
+    // Phi(z) + z phi(z), Phi from the same rational erf as the forward
+    f = gelu_erf(z);
+    const float phi = 0.398942280401432678f * __builtin_amdgcn_exp2f(z * z * -0.72134752044448170f);
+    d = __builtin_fmaf(z, phi, gelu_cdf(z));
+  } else if constexpr (ACT == ACT_SOFTPLUS) {
+    f = softplus_guarded(z);
+    d = sigmoid(z);
+  } else if constexpr (ACT == ACT_RELU) {
+    f = relu(z);
+    d = z > 0.0f ? 1.0f : 0.0f;
+  } else {
+    f = z;
+    d = 1.0f;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void load8f(const T* src, int valid, float (&f)[8]) {
+  const f32x4 a = load4<T>(src, valid), b = valid > 4 ? load4<T>(src + 4, valid - 4) : (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    f[r] = a[r];
+    f[4 + r] = b[r];
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store8f(T* dst, int valid, const float (&f)[8]) {
+  store4<T>(dst, (f32x4){f[0], f[1], f[2], f[3]}, valid);
+  if (valid > 4) store4<T>(dst + 4, (f32x4){f[4], f[5], f[6], f[7]}, valid - 4);
+}
+
+constexpr int DZ_COLS = 256, DZ_ROWS = 8;  // columns and row lanes of a workgroup (8 columns per thread)
+
+// Workgroup (column block, row chunk); partial column sums of dZi to
+// sums[(chunk * 2 + i) * N + n].
+template <typename T, typename TD, int ACT, bool GATED>
+__global__ __launch_bounds__(256) void dz_kernel(DzParams p) {
+  const int c = threadIdx.x & 31, rl = threadIdx.x >> 5;
+  const int n = blockIdx.x * DZ_COLS + c * 8;
+  const int64_t r0 = (int64_t)blockIdx.y * p.chunk_rows, r1 = min(r0 + p.chunk_rows, (int64_t)p.M);
+  float sg[8], su[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sg[i] = su[i] = 0.0f;
+  const int valid = min(8, p.N - n);
+  if (valid > 0)
+    for (int64_t m = r0 + rl; m < r1; m += DZ_ROWS) {
+      float dy[8], zg[8], zu[8], dg[8], du[8];
+      load8f<TD>((const TD*)p.dY + m * p.ldd + n, valid, dy);
+      if (ACT != ACT_NONE || GATED) load8f<T>((const T*)p.Z[0] + m * p.ldz + n, valid, zg);
+      if (GATED) load8f<T>((const T*)p.Z[1] + m * p.ldz + n, valid, zu);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float f = 0.0f, d = 1.0f;
+        if (ACT != ACT_NONE || GATED) act_and_grad<ACT>(zg[i], f, d);
+        dg[i] = GATED ? dy[i] * zu[i] * d : dy[i] * d;
+        du[i] = dy[i] * f;
+        sg[i] += dg[i];
+        su[i] += du[i];
+      }
+      if (p.dZ[0]) store8f<T>((T*)p.dZ[0] + m * p.ldw + n, valid, dg);
+      if (GATED && p.dZ[1]) store8f<T>((T*)p.dZ[1] + m * p.ldw + n, valid, du);
+    }
+  if (!p.sums) return;
+  // the 8 row lanes' sums, added in lane order
+  __shared__ float part[DZ_ROWS][DZ_COLS + 4];
+#pragma unroll
+  for (int i = 0; i < (GATED ? 2 : 1); ++i) {
+    if (i) __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) part[rl][c * 8 + e] = i ? su[e] : sg[e];
+    __syncthreads();
+    const int col = blockIdx.x * DZ_COLS + threadIdx.x;
+    if (col < p.N) {
+      float t = 0.0f;
+#pragma unroll
+      for (int r = 0; r < DZ_ROWS; ++r) t += part[r][threadIdx.x];
+      p.sums[((int64_t)blockIdx.y * 2 + i) * p.N + col] = t;
+    }
+  }
+}
+
+// db_i[n] = the chunks' column sums, added in order.
+template <typename TG>
+__global__ __launch_bounds__(256) void bias_grad_kernel(const float* sums, int chunks, int N, TG* db0, TG* db1) {
+  const int n = blockIdx.x * 256 + threadIdx.x, i = blockIdx.y;
+  TG* db = i ? db1 : db0;
+  if (n >= N || !db) return;
+  float t = 0.0f;
+#pragma unroll 4
+  for (int c = 0; c < chunks; ++c) t += sums[((int64_t)c * 2 + i) * N + n];
+  db[n] = (TG)t;
+}
+
+template <typename T, typename TD, bool GATED>
+hipError_t dz_act(const DzParams& p, int act, dim3 grid, hipStream_t stream) {
+  switch (act) {
+    case ACT_GELU: hipLaunchKernelGGL((dz_kernel<T, TD, ACT_GELU, GATED>), grid, dim3(256), 0, stream, p); break;
+    case ACT_SOFTPLUS: hipLaunchKernelGGL((dz_kernel<T, TD, ACT_SOFTPLUS, GATED>), grid, dim3(256), 0, stream, p); break;
+    case ACT_RELU: hipLaunchKernelGGL((dz_kernel<T, TD, ACT_RELU, GATED>), grid, dim3(256), 0, stream, p); break;
+    case ACT_SILU: hipLaunchKernelGGL((dz_kernel<T, TD, ACT_SILU, GATED>), grid, dim3(256), 0, stream, p); break;
+    default: hipLaunchKernelGGL((dz_kernel<T, TD, ACT_NONE, GATED>), grid, dim3(256), 0, stream, p); break;
+  }
+  return hipGetLastError();
+}
+
+size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// Row chunks of the dZ pass: about 2048 workgroups, at least 8 rows each, and
+// few enough for the grid's y extent.
+int dz_chunk_rows(int64_t M, int64_t N) {
+  const int64_t cols = (N + DZ_COLS - 1) / DZ_COLS;
+  const int64_t want = std::max<int64_t>(1, 2048 / std::max<int64_t>(1, cols));
+  int64_t rows = (M + want - 1) / want;
+  rows = (rows + DZ_ROWS - 1) / DZ_ROWS * DZ_ROWS;
+  return (int)std::max<int64_t>(rows, DZ_ROWS);
+}
+
+struct BwdPlan {
+  int64_t ldw;       // pitch of dZ in elements
+  int chunk_rows, chunks;
+  size_t dz_bytes;   // one dZ matrix
+  size_t sums_at, total;
+};
+BwdPlan bwd_plan(const FfnBwdParams& p, bool gated) {
+  BwdPlan b{};
+  b.ldw = (p.N + 7) / 8 * 8;
+  b.chunk_rows = dz_chunk_rows(p.M, p.N);
+  b.chunks = (p.M + b.chunk_rows - 1) / b.chunk_rows;
+  b.dz_bytes = align256((size_t)p.M * (size_t)b.ldw * 2);
+  b.sums_at = b.dz_bytes * (gated ? 2 : 1);
+  b.total = b.sums_at + align256((size_t)b.chunks * 2 * (size_t)p.N * 4);
+  return b;
+}
+
+template <typename T, typename TG>
+hipError_t backward_t(const FfnBwdParams& p, bool gated, bool dy32, int act, hipStream_t stream, int num_cus,
+                      char* ws) {
+  const BwdPlan b = bwd_plan(p, gated);
+  const int nw = gated ? 2 : 1;
+  const bool want_db = p.db[0] || p.db[1];
+  const bool products = p.dX || p.dW[0] || p.dW[1];
+  // without an activation dZ is dY itself
+  const bool as_is = !gated && act == ACT_NONE && !dy32;
+  DzParams d{};
+  d.dY = p.dY;
+  d.ldd = p.ldd;
+  d.Z[0] = p.Z[0];
+  d.Z[1] = p.Z[1];
+  d.ldz = p.ldz;
+  d.dZ[0] = products && !as_is ? ws : nullptr;
+  d.dZ[1] = products && gated ? ws + b.dz_bytes : nullptr;
+  d.ldw = b.ldw;
+  d.sums = want_db ? (float*)(ws + b.sums_at) : nullptr;
+  d.M = p.M;
+  d.N = p.N;
+  d.chunk_rows = b.chunk_rows;
+  hipError_t e = hipSuccess;
+  if (p.M > 0 && p.N > 0 && (d.dZ[0] || d.sums)) {
+    const dim3 grid((unsigned)((p.N + DZ_COLS - 1) / DZ_COLS), (unsigned)b.chunks);
+    if (gated)
+      e = dy32 ? dz_act<T, float, true>(d, act, grid, stream) : dz_act<T, T, true>(d, act, grid, stream);
+    else
+      e = dy32 ? dz_act<T, float, false>(d, act, grid, stream) : dz_act<T, T, false>(d, act, grid, stream);
+    if (e != hipSuccess) return e;
+  }
+  if (want_db && p.N > 0) {
+    hipLaunchKernelGGL((bias_grad_kernel<TG>), dim3((unsigned)((p.N + 255) / 256), nw), dim3(256), 0, stream,
+                       (const float*)(ws + b.sums_at), b.chunks, p.N, (TG*)p.db[0], (TG*)p.db[1]);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  const void* dZ[2] = {as_is ? p.dY : (const void*)ws, gated ? (const void*)(ws + b.dz_bytes) : nullptr};
+  const int64_t ldw = as_is ? p.ldd : b.ldw;
+  if (p.dX && p.M > 0 && p.K > 0) {
+    TileOp o{};
+    for (int i = 0; i < nw; ++i) {
+      o.a[i] = dZ[i];
+      o.lda[i] = ldw;
+      o.b[i] = p.W[i];
+      o.ldb[i] = p.ldw[i];
+    }
+    o.M = p.M;
+    o.N = p.K;
+    o.K = p.N;
+    o.segs = nw;
+    o.batch = o.splits = 1;
+    o.Y[0] = p.dX;
+    o.ldy[0] = p.lddx;
+    if ((e = launch_tile<T, T, LAY_K, LAY_K, EPI_STORE, Geo128>(o, stream, num_cus)) != hipSuccess) return e;
+  }
+  if ((p.dW[0] || p.dW[1]) && p.N > 0 && p.K > 0) {
+    TileOp o{};
+    o.a[0] = p.X;
+    o.lda[0] = p.ldx;
+    o.M = p.K;
+    o.N = p.N;
+    o.K = p.M;
+    o.segs = o.splits = 1;
+    o.batch = 0;
+    for (int i = 0; i < nw; ++i)
+      if (p.dW[i]) {
+        o.b[o.batch] = dZ[i];
+        o.ldb[o.batch] = ldw;
+        o.Y[o.batch] = p.dW[i];
+        o.ldy[o.batch] = p.lddw[i];
+        ++o.batch;
+      }
+    if ((e = launch_tile<T, TG, LAY_X, LAY_X, EPI_STORE, Geo128>(o, stream, num_cus)) != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+size_t ffn_backward_workspace(const FfnBwdParams& p, bool gated, int num_cus) { return bwd_plan(p, gated).total; }
+
+hipError_t launch_ffn_backward(const FfnBwdParams& p, bool gated, DType in, DType dy, DType grad, int act,
+                               hipStream_t stream, int num_cus, void* workspace) {
+  char* ws = (char*)workspace;
+  const bool dy32 = dy == DT_F32;
+  if (in == DT_BF16) {
+    if (grad == DT_F32) return backward_t<__bf16, float>(p, gated, dy32, act, stream, num_cus, ws);
+    return backward_t<__bf16, __bf16>(p, gated, dy32, act, stream, num_cus, ws);
+  }
+  if (grad == DT_F32) return backward_t<_Float16, float>(p, gated, dy32, act, stream, num_cus, ws);
+  return backward_t<_Float16, _Float16>(p, gated, dy32, act, stream, num_cus, ws);
+}
+
+}  // namespace coalesce

@@ -38,12 +38,11 @@
 #include <atomic>
 
 #include "common.hpp"
+#include "gemm16_core.hpp"
 #include "launch.hpp"
 
 namespace coalesce {
 namespace {
-
-constexpr int BK = 64;
 
 // Tile configurations (BM x BN workgroup tile, NW waves in a 2 x NW/2 grid):
 //   * 256 x 256, 8 waves: two waves per SIMD, each owning 128 (m) x 64 (n)
@@ -80,27 +79,13 @@ typedef Geo<128, 128, 4, 2> Geo128;
 typedef Geo<64, 64, 4, 4> Geo64;
 
 // LDS layouts, 16-byte chunks XOR-swizzled so that every fragment read is
-// free of bank conflicts whether the LDS serves 128 or 256 bytes per clock:
+// free of bank conflicts whether the LDS serves 128 or 256 bytes per clock
+// (swzA and swzB, gemm16_core.hpp):
 //   A tile: BM rows of 64 k (128 B = 8 chunks); chunk c of row m sits at slot
-//     c ^ swzA(m).  A 128-bit read by 16 lanes (rows m0..m0+15, one chunk)
-//     hits 16 distinct 16-byte slots of a 256-byte window, and any 8
-//     consecutive rows hit 8 distinct slots of a 128-byte window.
+//     c ^ swzA(m).
 //   B tile: 64 rows of BN n (512, 256 or 128 B = 32, 16 or 8 chunks); chunk c
 //     of row k sits at slot c ^ swzB(k) (below the row's chunk count, and
-//     below 16, so a chunk stays in its 256-byte part of a row).  A
-//     transposing read by 32 lanes (rows k0..k0+3 and k0+8..k0+11, two chunks,
-//     two 8-byte halves) hits 32 distinct 8-byte slots of a 256-byte window
-//     (which holds two rows when they are 128 bytes long).
-// Neither swizzle depends on the sub-tile index s, the slice ks or the half of
-// a transposing read, so those stay immediate offsets of the LDS reads.
-__device__ __forceinline__ int swzA(int m) { return ((m >> 1) & 7) ^ ((m & 1) << 2); }
-template <typename G>
-__device__ __forceinline__ int swzB(int k) {
-  if constexpr (G::CPRB >= 16)
-    return ((k & 3) << 1) | (((k >> 3) & 1) << 3);
-  else  // 128-byte rows: a 256-byte window holds two rows, k and k ^ 1
-    return (((k >> 1) & 1) << 1) | (((k >> 3) & 1) << 2);
-}
+//     below 16, so a chunk stays in its 256-byte part of a row).
 
 template <typename T>
 struct Stage {
@@ -138,30 +123,11 @@ __device__ __forceinline__ uint32_t dma_offset(const DmaPlan& d, int j) {
     const uint32_t ldb_b = (uint32_t)p.ldb * (uint32_t)sizeof(T);
     const int nlast = ((p.N - 1) >> 3) << 3;
     const int row = (d.w * G::CB + j - G::CA) * G::BRPC + (d.lane >> G::CPRB_LOG);
-    const int cB = (d.lane & (G::CPRB - 1)) ^ swzB<G>(row);
+    const int cB = (d.lane & (G::CPRB - 1)) ^ swzB<G::CPRB>(row);
     const int gn = min(d.n0 + cB * 8, nlast);
     return (uint32_t)row * ldb_b + (uint32_t)((gn - d.n0) * (int)sizeof(T));
   }
 }
-
-// Uniform (SGPR) 64-bit base for a direct copy.
-__device__ __forceinline__ const void* uniform_ptr(const void* p) {
-  const uint64_t v = (uint64_t)(uintptr_t)p;
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
-  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
-  return (const void*)(uintptr_t)(((uint64_t)hi << 32) | lo);
-}
-
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-// 16-byte direct copy: global (SGPR base + per-lane 32-bit offset) -> LDS
-// (wave-uniform byte address + 16 * lane).
-__device__ __forceinline__ void dma16_off(const void* base, uint32_t off, uint32_t lds) {
-  // one wait state between the M0 write and the LDS-DMA instruction that reads it
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds)
-               : "memory", "m0");
-}
-#pragma clang diagnostic pop
 
 // Copy j (0 .. CA + CB - 1) of a K step into stage st.
 template <typename T, typename G>
@@ -219,7 +185,7 @@ __device__ __forceinline__ void tail_fill(const GemmParams& p, int m0, int n0, i
 #pragma unroll
   for (int j = 0; j < G::CB; ++j) {
     const int row = (w * G::CB + j) * G::BRPC + (lane >> G::CPRB_LOG);
-    const int cB = (lane & (G::CPRB - 1)) ^ swzB<G>(row);
+    const int cB = (lane & (G::CPRB - 1)) ^ swzB<G::CPRB>(row);
     const int gn = min(n0 + cB * 8, nlast);
     i16x8 v = (i16x8){0, 0, 0, 0, 0, 0, 0, 0};
     if (k0 + row < p.K) v = *(const i16x8*)(B + (int64_t)(k0 + row) * p.ldb + gn);
@@ -254,7 +220,7 @@ __device__ __forceinline__ i16x4 read_af_half(Stage<T> st, int ks, int wn, int t
   const int q = lane & 15;
   const int n = wn * G::WN + 16 * t + 4 * (q & 3);
   const int k = 32 * ks + 8 * (lane >> 4) + 4 * half + (q >> 2);
-  return lds_read_tr16(st.b + k * G::BN + (((n >> 3) ^ swzB<G>(k)) << 3) + (n & 7));
+  return lds_read_tr16(st.b + k * G::BN + (((n >> 3) ^ swzB<G::CPRB>(k)) << 3) + (n & 7));
 }
 
 // One slice: NT groups of {2 copies of K step k + 2 when `copy` (a uniform
@@ -322,25 +288,6 @@ __device__ __forceinline__ void read_all(Frags<G>& f, Stage<T> st, int ks, int w
   for (int s = 0; s < G::MT; ++s) f.b[s] = read_bf<T, G>(st, ks, wm, s, lane);
 }
 
-template <typename TO>
-__device__ __forceinline__ void store4(TO* dst, f32x4 v, int valid) {
-  if constexpr (sizeof(TO) == 2) {
-    typedef TO to4 __attribute__((ext_vector_type(4)));
-    const to4 o = (to4){(TO)v[0], (TO)v[1], (TO)v[2], (TO)v[3]};
-    if (valid >= 4) {
-      *(to4*)dst = o;
-    } else {
-      for (int r = 0; r < valid; ++r) dst[r] = o[r];
-    }
-  } else {
-    if (valid >= 4) {
-      *(f32x4*)dst = v;
-    } else {
-      for (int r = 0; r < valid; ++r) dst[r] = v[r];
-    }
-  }
-}
-
 // Epilogue through LDS for a wave's full WM x WN block of a 16-bit Y (the
 // 256 x 256 and 128 x 128 tiles; the 64 x 64 tile stores from the
 // accumulators).  The
@@ -352,14 +299,6 @@ __device__ __forceinline__ void store4(TO* dst, f32x4 v, int valid) {
 // every store instruction then writes whole 128-byte lines of Y (8 rows of
 // 128 bytes, or 4 of 256).  Only the wave's own region is touched, so no
 // workgroup barrier is needed between the write and the read-back.
-template <int ROWB>
-__device__ __forceinline__ int stage_swz(int row) {
-  if constexpr (ROWB == 128)
-    return (row >> 1) & 7;
-  else
-    return row & 15;
-}
-
 template <typename T, typename TO, int ACT, bool HAS_BIAS, typename G>
 __device__ __forceinline__ void epilogue_staged(const GemmParams& p, const f32x4 (&acc)[G::NT][G::MT], char* region,
                                                 int wr0, int wc0, int lane) {
@@ -397,15 +336,6 @@ __device__ __forceinline__ void epilogue_staged(const GemmParams& p, const f32x4
     *(u32x4*)(Y + (int64_t)(wr0 + row) * p.ldy + wc0 + 8 * c) = v;
   }
 }
-
-// Workgroup barrier for LDS reuse: the wave's own LDS accesses are complete
-// (lgkmcnt 0) but its global stores and direct copies may still be in
-// flight (no vmcnt wait, unlike __syncthreads' fence); the "memory" clobber
-// keeps the compiler from moving memory accesses across it.
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
-#pragma clang diagnostic pop
 
 // Persistent kernel: the workgroups that fit on the CUs (one of 256 x 256,
 // whose two LDS stages take 128 KB, two of 128 x 128, or four or five of

@@ -1,0 +1,293 @@
+// The global norm of a list of gradients, and the list scaled by
+//   c = min(1, max_norm / (norm + 1e-6)).
+//
+// Two sweeps: the first sums squares (or takes the largest magnitude) of every
+// tensor of the list into one partial per workgroup, the second adds the
+// partials -- every workgroup all of them, in the same order, so no third
+// launch -- and scales.  The list travels in the kernel arguments, a table of
+// up to kClipTensors tensors per launch, so nothing is copied to the device and
+// the calls can be captured.  Work is cut into chunks of equal size over all
+// tensors of a table; workgroup b takes chunks b, b + grid, ...: which element
+// meets which partial does not depend on timing, so repeated calls give the
+// same bits.  Squares are summed in fp64: they neither overflow nor round
+// (an fp32 gradient above 2^64 would overflow an fp32 sum), and at HBM speed
+// the conversion and the fma hide behind the loads.
+#include <algorithm>
+
+#include "common.hpp"
+#include "launch.hpp"
+
+namespace coalesce {
+namespace {
+
+constexpr int THREADS = 256;
+
+// x c as fp32, then one rounding to T: kept apart so that every path through
+// the kernel rounds alike (a fused multiply and conversion to fp16 rounds once
+// where two instructions round twice).
+template <typename T>
+__device__ __forceinline__ T scaled(T x, float c) {
+  float r = (float)x * c;
+  asm("" : "+v"(r));
+  return (T)r;
+}
+
+// max that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b) { return (b > a || b != b) ? b : a; }
+
+template <typename T>
+struct Vec {
+  static constexpr int N = 16 / (int)sizeof(T);
+  typedef T type __attribute__((ext_vector_type(N)));
+};
+
+template <bool INF>
+struct Accum {
+  double s = 0.0;
+  float m = 0.0f;
+  __device__ __forceinline__ void add(float x) {
+    if constexpr (INF) {
+      m = max_nan(m, __builtin_fabsf(x));
+    } else {
+      const double d = (double)x;
+      s = __builtin_fma(d, d, s);
+    }
+  }
+};
+
+// The workgroup's total, in thread 0 (and, with the second step, everywhere).
+template <bool INF>
+__device__ __forceinline__ double block_total(double v) {
+  __shared__ double wave_part[THREADS / 64];
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) {
+    const double o = __shfl_xor(v, off);
+    v = INF ? (double)max_nan((float)v, (float)o) : v + o;
+  }
+  if ((threadIdx.x & 63) == 0) wave_part[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = wave_part[0];
+#pragma unroll
+  for (int i = 1; i < THREADS / 64; ++i) v = INF ? (double)max_nan((float)v, (float)wave_part[i]) : v + wave_part[i];
+  return v;
+}
+
+// Chunk c of the table: its tensor and element range.
+__device__ __forceinline__ int find_tensor(const ClipTable& t, int64_t c) {
+  int lo = 0, hi = t.count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (c < t.chunk_end[mid])
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  return lo;
+}
+
+template <typename T, bool INF>
+__global__ __launch_bounds__(THREADS) void norm_kernel(ClipTable t, double* partial) {
+  typedef typename Vec<T>::type V;
+  constexpr int VN = Vec<T>::N;
+  Accum<INF> a[4];
+  const int64_t chunks = t.chunk_end[t.count - 1];
+  for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+    const int i = find_tensor(t, c);
+    const int64_t e0 = (c - (i ? t.chunk_end[i - 1] : 0)) * t.chunk;
+    const int64_t n = min(t.numel[i] - e0, t.chunk);
+    const T* p = (const T*)t.src[i] + e0;
+    const int64_t head = min(n, (int64_t)(((16 - ((uintptr_t)p & 15)) & 15) / sizeof(T)));
+    const V* pv = (const V*)(p + head);
+    const int64_t nv = (n - head) / VN;
+    if ((int64_t)threadIdx.x < head) a[0].add((float)p[threadIdx.x]);
+    int64_t k = threadIdx.x;
+    for (; k + 3 * THREADS < nv; k += 4 * THREADS) {
+      V v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] = pv[k + u * THREADS];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int e = 0; e < VN; ++e) a[u].add((float)v[u][e]);
+    }
+    for (; k < nv; k += THREADS) {
+      const V v = pv[k];
+#pragma unroll
+      for (int e = 0; e < VN; ++e) a[0].add((float)v[e]);
+    }
+    const int64_t done = head + nv * VN;
+    if ((int64_t)threadIdx.x < n - done) a[1].add((float)p[done + threadIdx.x]);
+  }
+  double v;
+  if constexpr (INF)
+    v = (double)max_nan(max_nan(a[0].m, a[1].m), max_nan(a[2].m, a[3].m));
+  else
+    v = (a[0].s + a[1].s) + (a[2].s + a[3].s);
+  v = block_total<INF>(v);
+  if (threadIdx.x == 0) partial[blockIdx.x] = v;
+}
+
+// The norm from all partials, the same value in every thread of every
+// workgroup.
+template <bool INF>
+__device__ __forceinline__ double total_norm(const double* partial, int n) {
+  double v = 0.0;
+  for (int i = threadIdx.x; i < n; i += THREADS) v = INF ? (double)max_nan((float)v, (float)partial[i]) : v + partial[i];
+  v = block_total<INF>(v);
+  return INF ? v : __builtin_sqrt(v);
+}
+
+template <bool INF>
+__global__ __launch_bounds__(THREADS) void norm_only_kernel(const double* partial, int n, float* norm) {
+  const double v = total_norm<INF>(partial, n);
+  if (threadIdx.x == 0) norm[0] = (float)v;
+}
+
+template <typename T, bool INF>
+__global__ __launch_bounds__(THREADS) void scale_kernel(ClipTable t, const double* partial, int n_partial,
+                                                        double max_norm, float* norm) {
+  typedef typename Vec<T>::type V;
+  constexpr int VN = Vec<T>::N;
+  const double total = total_norm<INF>(partial, n_partial);
+  if (norm && blockIdx.x == 0 && threadIdx.x == 0) norm[0] = (float)total;
+  const double q = max_norm / (total + 1e-6);
+  const float coef = q < 1.0 || q != q ? (float)q : 1.0f;
+  const int64_t chunks = t.chunk_end[t.count - 1];
+  for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+    const int i = find_tensor(t, c);
+    if (coef == 1.0f && t.src[i] == t.dst[i]) continue;  // in place and nothing to scale
+    const int64_t e0 = (c - (i ? t.chunk_end[i - 1] : 0)) * t.chunk;
+    const int64_t n = min(t.numel[i] - e0, t.chunk);
+    const T* p = (const T*)t.src[i] + e0;
+    T* o = (T*)t.dst[i] + e0;
+    if ((((uintptr_t)p ^ (uintptr_t)o) & 15) != 0) {  // no common 16-byte grid
+      for (int64_t k = threadIdx.x; k < n; k += THREADS) o[k] = scaled<T>(p[k], coef);
+      continue;
+    }
+    const int64_t head = min(n, (int64_t)(((16 - ((uintptr_t)p & 15)) & 15) / sizeof(T)));
+    const V* pv = (const V*)(p + head);
+    V* ov = (V*)(o + head);
+    const int64_t nv = (n - head) / VN;
+    if ((int64_t)threadIdx.x < head) o[threadIdx.x] = scaled<T>(p[threadIdx.x], coef);
+    int64_t k = threadIdx.x;
+    for (; k + 3 * THREADS < nv; k += 4 * THREADS) {
+      V v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] = pv[k + u * THREADS];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+#pragma unroll
+        for (int e = 0; e < VN; ++e) v[u][e] = scaled<T>(v[u][e], coef);
+        ov[k + u * THREADS] = v[u];
+      }
+    }
+    for (; k < nv; k += THREADS) {
+      V v = pv[k];
+#pragma unroll
+      for (int e = 0; e < VN; ++e) v[e] = scaled<T>(v[e], coef);
+      ov[k] = v;
+    }
+    const int64_t done = head + nv * VN;
+    if ((int64_t)threadIdx.x < n - done) o[done + threadIdx.x] = scaled<T>(p[done + threadIdx.x], coef);
+  }
+}
+
+// Elements per chunk: 64 KB of a large list; of a small one as many as give
+// its launch about a workgroup per compute unit, at least 1024.
+int64_t chunk_elems(int64_t total, int64_t es, int num_cus) {
+  int64_t c = 65536 / es;
+  while (c > 1024 && total / c < num_cus) c /= 2;
+  return c;
+}
+
+// Calls fn(table, dtype) for the list's tables: tensors of one dtype, in list
+// order, empty ones left out.
+template <typename F>
+hipError_t for_tables(const ClipList& l, int num_cus, F fn) {
+  int64_t total = 0;
+  for (int64_t i = 0; i < l.count; ++i) total += l.numel[i];
+  for (int dt : {DT_F32, DT_F16, DT_BF16}) {
+    const int64_t chunk = chunk_elems(total, dt == DT_F32 ? 4 : 2, num_cus);
+    ClipTable t{};
+    t.chunk = chunk;
+    int64_t chunks = 0;
+    for (int64_t i = 0; i <= l.count; ++i) {
+      const bool end = i == l.count;
+      if (!end && (l.dtype[i] != dt || l.numel[i] == 0)) continue;
+      if (t.count == kClipTensors || (end && t.count > 0)) {
+        const hipError_t e = fn(t, dt);
+        if (e != hipSuccess) return e;
+        t.count = 0;
+        chunks = 0;
+      }
+      if (end) break;
+      chunks += (l.numel[i] + chunk - 1) / chunk;
+      t.src[t.count] = l.src ? l.src[i] : nullptr;
+      t.dst[t.count] = l.dst ? l.dst[i] : nullptr;
+      t.numel[t.count] = l.numel[i];
+      t.chunk_end[t.count] = chunks;
+      ++t.count;
+    }
+  }
+  return hipSuccess;
+}
+
+int grid_of(const ClipTable& t, int num_cus) {
+  return (int)std::min<int64_t>(t.chunk_end[t.count - 1], (int64_t)num_cus * 8);
+}
+
+template <bool INF>
+hipError_t grad_norm_t(const ClipList& l, double max_norm, float* norm, double* partial, hipStream_t stream,
+                       int num_cus) {
+  int n = 0;
+  hipError_t e = for_tables(l, num_cus, [&](const ClipTable& t, int dt) {
+    const int g = grid_of(t, num_cus);
+    double* out = partial + n;
+    n += g;
+    if (dt == DT_F32)
+      hipLaunchKernelGGL((norm_kernel<float, INF>), dim3(g), dim3(THREADS), 0, stream, t, out);
+    else if (dt == DT_F16)
+      hipLaunchKernelGGL((norm_kernel<_Float16, INF>), dim3(g), dim3(THREADS), 0, stream, t, out);
+    else
+      hipLaunchKernelGGL((norm_kernel<__bf16, INF>), dim3(g), dim3(THREADS), 0, stream, t, out);
+    return hipGetLastError();
+  });
+  if (e != hipSuccess) return e;
+  if (!l.dst || n == 0) {
+    hipLaunchKernelGGL((norm_only_kernel<INF>), dim3(1), dim3(THREADS), 0, stream, partial, n, norm);
+    return hipGetLastError();
+  }
+  bool first = true;
+  return for_tables(l, num_cus, [&](const ClipTable& t, int dt) {
+    const int g = grid_of(t, num_cus);
+    float* out = first ? norm : nullptr;
+    first = false;
+    if (dt == DT_F32)
+      hipLaunchKernelGGL((scale_kernel<float, INF>), dim3(g), dim3(THREADS), 0, stream, t, partial, n, max_norm, out);
+    else if (dt == DT_F16)
+      hipLaunchKernelGGL((scale_kernel<_Float16, INF>), dim3(g), dim3(THREADS), 0, stream, t, partial, n, max_norm,
+                         out);
+    else
+      hipLaunchKernelGGL((scale_kernel<__bf16, INF>), dim3(g), dim3(THREADS), 0, stream, t, partial, n, max_norm, out);
+    return hipGetLastError();
+  });
+}
+
+}  // namespace
+
+size_t grad_norm_workspace(const ClipList& l, int num_cus) {
+  size_t n = 0;
+  (void)for_tables(l, num_cus, [&](const ClipTable& t, int) {
+    n += (size_t)grid_of(t, num_cus);
+    return hipSuccess;
+  });
+  return n * sizeof(double);
+}
+
+hipError_t launch_grad_norm(const ClipList& l, bool inf, double max_norm, float* norm, void* workspace,
+                            hipStream_t stream, int num_cus) {
+  return inf ? grad_norm_t<true>(l, max_norm, norm, (double*)workspace, stream, num_cus)
+             : grad_norm_t<false>(l, max_norm, norm, (double*)workspace, stream, num_cus);
+}
+
+}  // namespace coalesce

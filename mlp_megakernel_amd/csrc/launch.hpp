@@ -6,7 +6,7 @@
 namespace coalesce {
 
 enum DType { DT_F32 = 0, DT_F16 = 1, DT_BF16 = 2 };
-enum Act { ACT_NONE = 0, ACT_GELU = 1, ACT_SOFTPLUS = 2, ACT_RELU = 3 };
+enum Act { ACT_NONE = 0, ACT_GELU = 1, ACT_SOFTPLUS = 2, ACT_RELU = 3, ACT_SILU = 4 };
 
 struct GemmParams {
   const void* A;
@@ -156,5 +156,95 @@ hipError_t launch_matrix_rate(const void* ops, int nsets, int iters, void* sink,
 // matrices (pitches in bytes; row_bytes even).
 hipError_t launch_compare(const void* a, int64_t pitch_a, const void* b, int64_t pitch_b, int64_t rows,
                           int64_t row_bytes, unsigned int* counter, hipStream_t stream, int num_cus);
+
+// One launch of the feed-forward operators' tile kernel (gemm16_core.hpp).
+// The extents are the product's own (m, n, contraction), whichever way the
+// operands lie in memory.
+struct TileOp {
+  const void* a[2];  // m side
+  const void* b[2];  // n side
+  int64_t lda[2], ldb[2];
+  int M, N, K;
+  int segs;    // 2: acc = a[0] b[0] + a[1] b[1], K steps of the second after the first's
+  int batch;   // 2: two products a[0] b[i] -> Y[i]
+  int splits;  // ranges of K steps, range i stored split_stride elements after range i - 1
+  int64_t split_stride;
+  const void* bias[2];
+  const void* R;  // residual, pitch ldr
+  int64_t ldr;
+  void* Z[2];  // stored pre-activations, pitch ldz, or nullptr
+  int64_t ldz;
+  void* Y[2];
+  int64_t ldy[2];
+  int act;
+  int tiles_m, tiles_n, group_m;  // set by the launcher
+};
+
+// Forward of the gated product and of the GEMM with residual (ffn_gemm.hip):
+// X is M x K, W[i] K x N.
+struct FfnParams {
+  const void* X;
+  const void* W[2];
+  const void* bias[2];
+  const void* R;
+  void* Z[2];
+  void* Y;
+  int64_t ldx, ldw[2], ldr, ldz, ldy;
+  int M, N, K;
+};
+// Workspace (bytes, 0: none) and launch; `workspace` holds that many bytes.
+size_t ffn_forward_workspace(int64_t M, int64_t N, int64_t K, bool gated, int num_cus);
+hipError_t launch_ffn_forward(const FfnParams& p, bool gated, DType in, DType out, int act, hipStream_t stream,
+                              int num_cus, void* workspace);
+
+// Backward of both (ffn_bwd.hip).  Outputs may be nullptr: not wanted.
+struct FfnBwdParams {
+  const void* X;      // M x K
+  const void* W[2];   // K x N
+  const void* Z[2];   // M x N stored pre-activations (ldz)
+  const void* dY;     // M x N (ldd)
+  void* dX;           // M x K (lddx)
+  void* dW[2];        // K x N (lddw)
+  void* db[2];        // N
+  int64_t ldx, ldw[2], ldz, ldd, lddx, lddw[2];
+  int M, N, K;
+};
+// The elementwise pass of that backward.
+struct DzParams {
+  const void* dY;
+  const void* Z[2];
+  void* dZ[2];   // pitch ldw, or nullptr
+  float* sums;   // column sums per row chunk, or nullptr
+  int64_t ldd, ldz, ldw;
+  int M, N, chunk_rows;
+};
+// (M, N, K and, for products that are not wanted, null outputs are what the size depends on)
+size_t ffn_backward_workspace(const FfnBwdParams& p, bool gated, int num_cus);
+hipError_t launch_ffn_backward(const FfnBwdParams& p, bool gated, DType in, DType dy, DType grad, int act,
+                               hipStream_t stream, int num_cus, void* workspace);
+
+// Gradient norm and clipping (gradnorm.hip): a list of dense tensors, and the
+// table of up to kClipTensors of them that one launch gets as its argument
+// (under the 4 KB of kernel arguments).
+struct ClipList {
+  const void* const* src;
+  void* const* dst;  // nullptr: the norm alone
+  const int64_t* numel;
+  const int32_t* dtype;  // DType
+  int64_t count;
+};
+constexpr int kClipTensors = 120;
+struct ClipTable {
+  const void* src[kClipTensors];
+  void* dst[kClipTensors];
+  int64_t numel[kClipTensors];
+  int64_t chunk_end[kClipTensors];  // chunks up to and including the tensor's
+  int64_t chunk;                    // elements per chunk
+  int count;
+};
+size_t grad_norm_workspace(const ClipList& l, int num_cus);
+// norm (device, one float) <- the norm; with l.dst also dst = src * min(1, max_norm / (norm + 1e-6)).
+hipError_t launch_grad_norm(const ClipList& l, bool inf, double max_norm, float* norm, void* workspace,
+                            hipStream_t stream, int num_cus);
 
 }  // namespace coalesce
