@@ -398,8 +398,8 @@ coalesce_status coalesce_autotune_mlp_forward(const void* x, int64_t ldx, const 
  *     products accumulate in fp32, biases, activations and the residual are
  *     applied in fp32, each result is rounded once (to nearest even);
  *   - act is NONE, GELU_ERF, SOFTPLUS, RELU or SILU;
- *   - matrices are row-major with 16-byte aligned rows and pitches of at most
- *     2^23 elements; the extents are arbitrary (below 2^31 - 256, the product
+ *   - matrices are row-major with 16-byte aligned rows and pitches below 2^23
+ *     elements; the extents are arbitrary (below 2^31 - 256, the product
  *     of any two at most 2^41); bias vectors are 16-byte aligned;
  *   - outputs must not overlap the inputs, each other or the workspace;
  *   - `workspace` is device memory, 16-byte aligned, of at least the size that
@@ -459,14 +459,14 @@ coalesce_status coalesce_gemm_residual_backward(const void* A, int64_t lda, cons
 
 /*
  * Y = act(A Bg + bias_g) * (A Bu + bias_u): both projections, the activation
- * and the product in one kernel.  Bg and Bu are K x N each (ldbg, ldbu): two
- * matrices, or the two halves of one K x 2N matrix.  Zg, Zu (one pitch, both
+ * and the product in one kernel.  Bg and Bu are K x N each, of one pitch ldb:
+ * two matrices, or the two halves of one K x 2N matrix.  Zg, Zu (one pitch, both
  * or neither) receive the two pre-activations in in_dtype for the backward.
  * Other arguments as coalesce_gemm_residual.
  */
 size_t coalesce_gated_gemm_workspace_size(int64_t M, int64_t N, int64_t K);
-coalesce_status coalesce_gated_gemm(const void* A, int64_t lda, const void* Bg, int64_t ldbg, const void* Bu,
-                                    int64_t ldbu, const void* bias_g, const void* bias_u, void* Zg, void* Zu,
+coalesce_status coalesce_gated_gemm(const void* A, int64_t lda, const void* Bg, const void* Bu, int64_t ldb,
+                                    const void* bias_g, const void* bias_u, void* Zg, void* Zu,
                                     int64_t ldz, void* Y, int64_t ldy, int64_t M, int64_t N, int64_t K,
                                     coalesce_dtype in_dtype, coalesce_dtype out_dtype, coalesce_act act,
                                     void* workspace, size_t workspace_bytes, void* stream);
@@ -476,13 +476,13 @@ coalesce_status coalesce_gated_gemm(const void* A, int64_t lda, const void* Bg, 
  *   dZu = dY act(Zg);  dZg = dY Zu act'(Zg);  dA = dZg Bg^T + dZu Bu^T
  *   dBg = A^T dZg;  dBu = A^T dZu;  dbias_x[n] = sum_m dZx[m][n]
  * with the roundings, the optional outputs and the empty extents of
- * coalesce_gemm_residual_backward.
+ * coalesce_gemm_residual_backward; dBg and dBu have one pitch lddb.
  */
 size_t coalesce_gated_gemm_backward_workspace_size(int64_t M, int64_t N, int64_t K);
-coalesce_status coalesce_gated_gemm_backward(const void* A, int64_t lda, const void* Bg, int64_t ldbg, const void* Bu,
-                                             int64_t ldbu, const void* Zg, const void* Zu, int64_t ldz, const void* dY,
-                                             int64_t ldd, void* dA, int64_t ldda, void* dBg, int64_t lddbg, void* dBu,
-                                             int64_t lddbu, void* dbias_g, void* dbias_u, int64_t M, int64_t N,
+coalesce_status coalesce_gated_gemm_backward(const void* A, int64_t lda, const void* Bg, const void* Bu, int64_t ldb,
+                                             const void* Zg, const void* Zu, int64_t ldz, const void* dY, int64_t ldd,
+                                             void* dA, int64_t ldda, void* dBg, void* dBu, int64_t lddb, void* dbias_g,
+                                             void* dbias_u, int64_t M, int64_t N,
                                              int64_t K, coalesce_dtype in_dtype, coalesce_dtype dy_dtype,
                                              coalesce_dtype grad_dtype, coalesce_act act, void* workspace,
                                              size_t workspace_bytes, void* stream);

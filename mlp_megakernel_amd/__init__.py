@@ -53,11 +53,11 @@ SIGNATURES = {
     "coalesce_gemm_residual_backward": (_i32, [_p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64,
                                                _i64, _i64, _i32, _i32, _i32, _i32, _p, _sz, _p]),
     "coalesce_gated_gemm_workspace_size": (_sz, [_i64, _i64, _i64]),
-    "coalesce_gated_gemm": (_i32, [_p, _i64, _p, _i64, _p, _i64, _p, _p, _p, _p, _i64, _p, _i64, _i64, _i64, _i64,
-                                   _i32, _i32, _i32, _p, _sz, _p]),
+    "coalesce_gated_gemm": (_i32, [_p, _i64, _p, _p, _i64, _p, _p, _p, _p, _i64, _p, _i64, _i64, _i64, _i64, _i32,
+                                   _i32, _i32, _p, _sz, _p]),
     "coalesce_gated_gemm_backward_workspace_size": (_sz, [_i64, _i64, _i64]),
-    "coalesce_gated_gemm_backward": (_i32, [_p, _i64, _p, _i64, _p, _i64, _p, _p, _i64, _p, _i64, _p, _i64, _p, _i64,
-                                            _p, _i64, _p, _p, _i64, _i64, _i64, _i32, _i32, _i32, _i32, _p, _sz, _p]),
+    "coalesce_gated_gemm_backward": (_i32, [_p, _i64, _p, _p, _i64, _p, _p, _i64, _p, _i64, _p, _i64, _p, _p, _i64, _p,
+                                            _p, _i64, _i64, _i64, _i32, _i32, _i32, _i32, _p, _sz, _p]),
     "coalesce_grad_norm_workspace_size": (_sz, [_p, _p, _i64]),
     "coalesce_grad_norm": (_i32, [_p, _p, _p, _i64, _i32, _p, _p, _sz, _p]),
     "coalesce_clip_grad_norm": (_i32, [_p, _p, _p, _p, _i64, _i32, _f64, _p, _p, _sz, _p]),

@@ -999,7 +999,7 @@ coalesce_status check_ffn(int64_t M, int64_t N, int64_t K, coalesce_dtype in, co
 coalesce_status check_mat(const void* t, int64_t ld, int64_t cols, int64_t es, const char* name) {
   if (!t) return fail(COALESCE_ERR_INVALID_ARGUMENT, "%s is NULL", name);
   if (ld < cols) return fail(COALESCE_ERR_INVALID_ARGUMENT, "the pitch of %s is shorter than the row", name);
-  if (ld > (int64_t(1) << 23)) return fail(COALESCE_ERR_UNSUPPORTED, "the pitch of %s must be at most 2^23", name);
+  if (ld >= (int64_t(1) << 23)) return fail(COALESCE_ERR_UNSUPPORTED, "the pitch of %s must be below 2^23", name);
   if (!aligned16(t) || (ld * es) % 16)
     return fail(COALESCE_ERR_UNSUPPORTED, "%s must be 16-byte aligned with a 16-byte row pitch", name);
   return COALESCE_OK;
@@ -1052,7 +1052,7 @@ coalesce_status check_workspace(const void* ws, size_t have, size_t need) {
 }
 
 // Forward of both operators: W[1] only for the gated product.
-coalesce_status ffn_forward(bool gated, const void* A, int64_t lda, const void* const (&B)[2], const int64_t (&ldb)[2],
+coalesce_status ffn_forward(bool gated, const void* A, int64_t lda, const void* const (&B)[2], int64_t ldb,
                             const void* const (&bias)[2], const void* R, int64_t ldr, void* const (&Z)[2], int64_t ldz,
                             void* Y, int64_t ldy, int64_t M, int64_t N, int64_t K, coalesce_dtype in,
                             coalesce_dtype out, coalesce_act act, void* workspace, size_t workspace_bytes,
@@ -1075,8 +1075,8 @@ coalesce_status ffn_forward(bool gated, const void* A, int64_t lda, const void* 
   if (gated && !Z[0] != !Z[1]) return fail(COALESCE_ERR_INVALID_ARGUMENT, "Zg and Zu go together");
   for (int i = 0; i < nw; ++i) {
     if (K > 0) {
-      if ((s = check_mat(B[i], ldb[i], N, is, bn[i])) != COALESCE_OK) return s;
-      ops.mat(false, B[i], K, N, ldb[i], is, bn[i]);
+      if ((s = check_mat(B[i], ldb, N, is, bn[i])) != COALESCE_OK) return s;
+      ops.mat(false, B[i], K, N, ldb, is, bn[i]);
     }
     if ((s = check_vec(bias[i], vn[i])) != COALESCE_OK) return s;
     ops.mat(false, bias[i], 1, N, N, is, vn[i]);
@@ -1102,9 +1102,9 @@ coalesce_status ffn_forward(bool gated, const void* A, int64_t lda, const void* 
   FfnParams p{};
   p.X = A;
   p.ldx = lda;
+  p.ldw = ldb;
   for (int i = 0; i < nw; ++i) {
     p.W[i] = B[i];
-    p.ldw[i] = ldb[i];
     p.bias[i] = bias[i];
     p.Z[i] = Z[i];
   }
@@ -1123,8 +1123,8 @@ coalesce_status ffn_forward(bool gated, const void* A, int64_t lda, const void* 
 }
 
 coalesce_status ffn_backward(bool gated, const void* A, int64_t lda, const void* const (&B)[2],
-                             const int64_t (&ldb)[2], const void* const (&Z)[2], int64_t ldz, const void* dY,
-                             int64_t ldd, void* dA, int64_t ldda, void* const (&dB)[2], const int64_t (&lddb)[2],
+                             int64_t ldb, const void* const (&Z)[2], int64_t ldz, const void* dY,
+                             int64_t ldd, void* dA, int64_t ldda, void* const (&dB)[2], int64_t lddb,
                              void* const (&db)[2], int64_t M, int64_t N, int64_t K, coalesce_dtype in,
                              coalesce_dtype dy, coalesce_dtype grad, coalesce_act act, void* workspace,
                              size_t workspace_bytes, void* stream) {
@@ -1156,16 +1156,16 @@ coalesce_status ffn_backward(bool gated, const void* A, int64_t lda, const void*
   }
   for (int i = 0; i < nw; ++i) {
     if (want_dA && N > 0) {
-      if ((s = check_mat(B[i], ldb[i], N, is, bn[i])) != COALESCE_OK) return s;
-      ops.mat(false, B[i], K, N, ldb[i], is, bn[i]);
+      if ((s = check_mat(B[i], ldb, N, is, bn[i])) != COALESCE_OK) return s;
+      ops.mat(false, B[i], K, N, ldb, is, bn[i]);
     }
     if ((gated || act != COALESCE_ACT_NONE) && M > 0 && N > 0) {
       if ((s = check_mat(Z[i], ldz, N, is, zn[i])) != COALESCE_OK) return s;
       ops.mat(false, Z[i], M, N, ldz, is, zn[i]);
     }
     if (want_dB && dB[i]) {
-      if ((s = check_mat(dB[i], lddb[i], N, gs, gn[i])) != COALESCE_OK) return s;
-      ops.mat(true, dB[i], K, N, lddb[i], gs, gn[i]);
+      if ((s = check_mat(dB[i], lddb, N, gs, gn[i])) != COALESCE_OK) return s;
+      ops.mat(true, dB[i], K, N, lddb, gs, gn[i]);
     }
     if (want_db && db[i]) {
       if ((s = check_vec(db[i], vn[i])) != COALESCE_OK) return s;
@@ -1181,12 +1181,12 @@ coalesce_status ffn_backward(bool gated, const void* A, int64_t lda, const void*
   p.ldz = ldz;
   if (want_dA) p.dX = dA;
   p.lddx = ldda;
+  p.ldw = ldb;
+  p.lddw = lddb;
   for (int i = 0; i < nw; ++i) {
     p.W[i] = B[i];
-    p.ldw[i] = ldb[i];
     p.Z[i] = Z[i];
     if (want_dB) p.dW[i] = dB[i];
-    p.lddw[i] = lddb[i];
     if (want_db) p.db[i] = db[i];
   }
   p.M = (int)M;
@@ -1194,7 +1194,7 @@ coalesce_status ffn_backward(bool gated, const void* A, int64_t lda, const void*
   p.K = (int)K;
   int cus = 0;
   if ((s = current_cus(&cus)) != COALESCE_OK) return s;
-  const size_t need = ffn_backward_workspace(p, gated, cus);
+  const size_t need = ffn_backward_workspace(M, N, K, gated, cus);
   if ((s = check_workspace(workspace, workspace_bytes, need)) != COALESCE_OK) return s;
   if (need) {
     ops.run(true, {(uintptr_t)workspace, (uintptr_t)workspace + need}, "the workspace");
@@ -1212,11 +1212,7 @@ size_t ffn_workspace_size(bool gated, bool backward, int64_t M, int64_t N, int64
   if (current_cus(&cus) != COALESCE_OK) return 0;
   ok();
   if (!backward) return M == 0 || N == 0 ? 0 : ffn_forward_workspace(M, N, K, gated, cus);
-  FfnBwdParams p{};
-  p.M = (int)M;
-  p.N = (int)N;
-  p.K = (int)K;
-  return ffn_backward_workspace(p, gated, cus);
+  return ffn_backward_workspace(M, N, K, gated, cus);
 }
 
 // The checked list of the gradient-norm entry points; dst may be NULL (norm
@@ -1323,7 +1319,7 @@ coalesce_status coalesce_gemm_residual(const void* A, int64_t lda, const void* B
                                        int64_t M, int64_t N, int64_t K, coalesce_dtype in_dtype,
                                        coalesce_dtype out_dtype, coalesce_act act, void* workspace,
                                        size_t workspace_bytes, void* stream) {
-  return ffn_forward(false, A, lda, {B, nullptr}, {ldb, 0}, {bias, nullptr}, R, ldr, {Z, nullptr}, ldz, Y, ldy, M, N, K,
+  return ffn_forward(false, A, lda, {B, nullptr}, ldb, {bias, nullptr}, R, ldr, {Z, nullptr}, ldz, Y, ldy, M, N, K,
                      in_dtype, out_dtype, act, workspace, workspace_bytes, stream);
 }
 
@@ -1333,29 +1329,29 @@ coalesce_status coalesce_gemm_residual_backward(const void* A, int64_t lda, cons
                                                 coalesce_dtype in_dtype, coalesce_dtype dy_dtype,
                                                 coalesce_dtype grad_dtype, coalesce_act act, void* workspace,
                                                 size_t workspace_bytes, void* stream) {
-  return ffn_backward(false, A, lda, {B, nullptr}, {ldb, 0}, {Z, nullptr}, ldz, dY, ldd, dA, ldda, {dB, nullptr},
-                      {lddb, 0}, {dbias, nullptr}, M, N, K, in_dtype, dy_dtype, grad_dtype, act, workspace,
+  return ffn_backward(false, A, lda, {B, nullptr}, ldb, {Z, nullptr}, ldz, dY, ldd, dA, ldda, {dB, nullptr},
+                      lddb, {dbias, nullptr}, M, N, K, in_dtype, dy_dtype, grad_dtype, act, workspace,
                       workspace_bytes, stream);
 }
 
-coalesce_status coalesce_gated_gemm(const void* A, int64_t lda, const void* Bg, int64_t ldbg, const void* Bu,
-                                    int64_t ldbu, const void* bias_g, const void* bias_u, void* Zg, void* Zu,
+coalesce_status coalesce_gated_gemm(const void* A, int64_t lda, const void* Bg, const void* Bu, int64_t ldb,
+                                    const void* bias_g, const void* bias_u, void* Zg, void* Zu,
                                     int64_t ldz, void* Y, int64_t ldy, int64_t M, int64_t N, int64_t K,
                                     coalesce_dtype in_dtype, coalesce_dtype out_dtype, coalesce_act act,
                                     void* workspace, size_t workspace_bytes, void* stream) {
-  return ffn_forward(true, A, lda, {Bg, Bu}, {ldbg, ldbu}, {bias_g, bias_u}, nullptr, 0, {Zg, Zu}, ldz, Y, ldy, M, N, K,
+  return ffn_forward(true, A, lda, {Bg, Bu}, ldb, {bias_g, bias_u}, nullptr, 0, {Zg, Zu}, ldz, Y, ldy, M, N, K,
                      in_dtype, out_dtype, act, workspace, workspace_bytes, stream);
 }
 
-coalesce_status coalesce_gated_gemm_backward(const void* A, int64_t lda, const void* Bg, int64_t ldbg, const void* Bu,
-                                             int64_t ldbu, const void* Zg, const void* Zu, int64_t ldz, const void* dY,
-                                             int64_t ldd, void* dA, int64_t ldda, void* dBg, int64_t lddbg, void* dBu,
-                                             int64_t lddbu, void* dbias_g, void* dbias_u, int64_t M, int64_t N,
+coalesce_status coalesce_gated_gemm_backward(const void* A, int64_t lda, const void* Bg, const void* Bu, int64_t ldb,
+                                             const void* Zg, const void* Zu, int64_t ldz, const void* dY, int64_t ldd,
+                                             void* dA, int64_t ldda, void* dBg, void* dBu, int64_t lddb, void* dbias_g,
+                                             void* dbias_u, int64_t M, int64_t N,
                                              int64_t K, coalesce_dtype in_dtype, coalesce_dtype dy_dtype,
                                              coalesce_dtype grad_dtype, coalesce_act act, void* workspace,
                                              size_t workspace_bytes, void* stream) {
-  return ffn_backward(true, A, lda, {Bg, Bu}, {ldbg, ldbu}, {Zg, Zu}, ldz, dY, ldd, dA, ldda, {dBg, dBu},
-                      {lddbg, lddbu}, {dbias_g, dbias_u}, M, N, K, in_dtype, dy_dtype, grad_dtype, act, workspace,
+  return ffn_backward(true, A, lda, {Bg, Bu}, ldb, {Zg, Zu}, ldz, dY, ldd, dA, ldda, {dBg, dBu},
+                      lddb, {dbias_g, dbias_u}, M, N, K, in_dtype, dy_dtype, grad_dtype, act, workspace,
                       workspace_bytes, stream);
 }
 

@@ -1,0 +1,107 @@
+// Choice of kernel for the feed-forward operators, and the pass that combines
+// the ranges of a split product.
+#include "ffn_plan.hpp"
+#include "gemm16_core.hpp"
+
+namespace coalesce {
+namespace {
+
+__device__ __forceinline__ float act_any(int act, float z) {
+  switch (act) {
+    case ACT_GELU: return gelu_erf(z);
+    case ACT_SOFTPLUS: return softplus_guarded(z);
+    case ACT_RELU: return relu(z);
+    case ACT_SILU: return silu(z);
+    default: return z;
+  }
+}
+
+// Four consecutive columns of one row per thread and iteration; the ranges are
+// added in order, so the result does not depend on timing.
+template <typename T, typename TO, int KIND>
+__global__ __launch_bounds__(256) void combine_kernel(CombineOp c) {
+  const int64_t quads = (c.N + 3) >> 2, total = (int64_t)c.M * quads;
+  const int i0 = KIND == COMBINE_STORE ? blockIdx.y : 0;
+  for (int64_t w = (int64_t)blockIdx.x * 256 + threadIdx.x; w < total; w += (int64_t)gridDim.x * 256) {
+    const int64_t m = w / quads;
+    const int n = (int)(w - m * quads) * 4;
+    const int valid = min(4, c.N - n);
+    f32x4 acc[2];
+#pragma unroll
+    for (int i = 0; i < (KIND == COMBINE_GATED ? 2 : 1); ++i) {
+      const float* p = c.P[i + i0] + m * c.ldp + n;
+      f32x4 s = *(const f32x4*)p;
+#pragma unroll 4
+      for (int k = 1; k < c.splits; ++k) s += *(const f32x4*)(p + (int64_t)k * c.split_stride);
+      acc[i] = s;
+    }
+    if constexpr (KIND == COMBINE_STORE) {
+      store4<TO>((TO*)c.Y[i0] + m * c.ldy + n, acc[0], valid);
+    } else {
+#pragma unroll
+      for (int i = 0; i < (KIND == COMBINE_GATED ? 2 : 1); ++i) {
+        if (c.bias[i]) acc[i] += load4<T>((const T*)c.bias[i] + n, valid);
+        if (c.Z[i]) store4<T>((T*)c.Z[i] + m * c.ldz + n, acc[i], valid);
+      }
+      f32x4 o = (f32x4){0.f, 0.f, 0.f, 0.f};
+      if (KIND == COMBINE_RESID && c.R) o = load4<TO>((const TO*)c.R + m * c.ldr + n, valid);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float f = act_any(c.act, acc[0][r]);
+        o[r] = KIND == COMBINE_GATED ? f * acc[1][r] : o[r] + f;
+      }
+      store4<TO>((TO*)c.Y[0] + m * c.ldy + n, o, valid);
+    }
+  }
+}
+
+template <typename T, typename TO>
+hipError_t combine_t(const CombineOp& c, CombineKind kind, hipStream_t stream, int num_cus) {
+  const int64_t blocks = ((int64_t)c.M * ((c.N + 3) / 4) + 255) / 256;
+  const dim3 grid((unsigned)std::min<int64_t>(blocks, (int64_t)num_cus * 8),
+                  kind == COMBINE_STORE ? (unsigned)c.products : 1u);
+  if (kind == COMBINE_STORE)
+    hipLaunchKernelGGL((combine_kernel<T, TO, COMBINE_STORE>), grid, dim3(256), 0, stream, c);
+  else if (kind == COMBINE_RESID)
+    hipLaunchKernelGGL((combine_kernel<T, TO, COMBINE_RESID>), grid, dim3(256), 0, stream, c);
+  else
+    hipLaunchKernelGGL((combine_kernel<T, TO, COMBINE_GATED>), grid, dim3(256), 0, stream, c);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_combine(const CombineOp& c, CombineKind kind, DType in, DType out, hipStream_t stream, int num_cus) {
+  if (kind == COMBINE_STORE && out == DT_F32) return combine_t<float, float>(c, kind, stream, num_cus);
+  if (in == DT_BF16)
+    return out == DT_F32 ? combine_t<__bf16, float>(c, kind, stream, num_cus)
+                         : combine_t<__bf16, __bf16>(c, kind, stream, num_cus);
+  return out == DT_F32 ? combine_t<_Float16, float>(c, kind, stream, num_cus)
+                       : combine_t<_Float16, _Float16>(c, kind, stream, num_cus);
+}
+
+size_t ffn_forward_workspace(int64_t M, int64_t N, int64_t K, bool gated, int num_cus) {
+  return partial_bytes(plan_tiles(M, N, gated, 1, (K + 63) / 64, num_cus), M, N, gated ? 2 : 1);
+}
+
+hipError_t launch_ffn_forward(const FfnParams& p, bool gated, DType in, DType out, int act, hipStream_t stream,
+                              int num_cus, void* workspace) {
+  if (in == DT_BF16) {
+    if (gated) return launch_gated_bf16(p, out, act, stream, num_cus, workspace);
+    return launch_resid_bf16(p, out, act, stream, num_cus, workspace);
+  }
+  if (gated) return launch_gated_f16(p, out, act, stream, num_cus, workspace);
+  return launch_resid_f16(p, out, act, stream, num_cus, workspace);
+}
+
+size_t ffn_backward_workspace(int64_t M, int64_t N, int64_t K, bool gated, int num_cus) {
+  return bwd_plan(M, N, K, gated, num_cus).total;
+}
+
+hipError_t launch_ffn_backward(const FfnBwdParams& p, bool gated, DType in, DType dy, DType grad, int act,
+                               hipStream_t stream, int num_cus, void* workspace) {
+  if (in == DT_BF16) return launch_backward_bf16(p, gated, dy, grad, act, stream, num_cus, workspace);
+  return launch_backward_f16(p, gated, dy, grad, act, stream, num_cus, workspace);
+}
+
+}  // namespace coalesce

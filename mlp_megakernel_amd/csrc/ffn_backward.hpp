@@ -7,14 +7,12 @@
 // matrix products' operands, and sums their columns in fp32 before that
 // rounding.  Both dZi Wi^T run as one K loop over two segments, both X^T dZi
 // as one launch whose tiles share X.
-#include <algorithm>
-
+#pragma once
+#include "ffn_plan.hpp"
 #include "gemm16_core.hpp"
 
 namespace coalesce {
 namespace {
-
-typedef TileGeo<128, 128, 4, 2, 2, 1> Geo128;
 
 // act(z) and act'(z) in fp32.
 template <int ACT>
@@ -54,8 +52,6 @@ __device__ __forceinline__ void store8f(T* dst, int valid, const float (&f)[8]) 
   store4<T>(dst, (f32x4){f[0], f[1], f[2], f[3]}, valid);
   if (valid > 4) store4<T>(dst + 4, (f32x4){f[4], f[5], f[6], f[7]}, valid - 4);
 }
-
-constexpr int DZ_COLS = 256, DZ_ROWS = 8;  // columns and row lanes of a workgroup (8 columns per thread)
 
 // Workgroup (column block, row chunk); partial column sums of dZi to
 // sums[(chunk * 2 + i) * N + n].
@@ -129,39 +125,50 @@ hipError_t dz_act(const DzParams& p, int act, dim3 grid, hipStream_t stream) {
   return hipGetLastError();
 }
 
-size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
-
-// Row chunks of the dZ pass: about 2048 workgroups, at least 8 rows each, and
-// few enough for the grid's y extent.
-int dz_chunk_rows(int64_t M, int64_t N) {
-  const int64_t cols = (N + DZ_COLS - 1) / DZ_COLS;
-  const int64_t want = std::max<int64_t>(1, 2048 / std::max<int64_t>(1, cols));
-  int64_t rows = (M + want - 1) / want;
-  rows = (rows + DZ_ROWS - 1) / DZ_ROWS * DZ_ROWS;
-  return (int)std::max<int64_t>(rows, DZ_ROWS);
+template <typename T, typename TO, Lay LA, Lay LB, int SEGS>
+hipError_t store_tiles(const TileOp& o, int variant, hipStream_t stream, int num_cus) {
+  if (variant == 1)
+    return launch_tile<T, TO, LA, LB, SEGS, EPI_STORE, ACT_NONE, TileGeo<256, 256, 8, 2, 1, 1>>(o, stream, num_cus);
+  if (variant == 2)
+    return launch_tile<T, TO, LA, LB, SEGS, EPI_STORE, ACT_NONE, TileGeo<128, 128, 4, 2, 2, 1>>(o, stream, num_cus);
+  return launch_tile<T, TO, LA, LB, SEGS, EPI_STORE, ACT_NONE, TileGeo<64, 64, 4, 2, 4, 1>>(o, stream, num_cus);
 }
 
-struct BwdPlan {
-  int64_t ldw;       // pitch of dZ in elements
-  int chunk_rows, chunks;
-  size_t dz_bytes;   // one dZ matrix
-  size_t sums_at, total;
-};
-BwdPlan bwd_plan(const FfnBwdParams& p, bool gated) {
-  BwdPlan b{};
-  b.ldw = (p.N + 7) / 8 * 8;
-  b.chunk_rows = dz_chunk_rows(p.M, p.N);
-  b.chunks = (p.M + b.chunk_rows - 1) / b.chunk_rows;
-  b.dz_bytes = align256((size_t)p.M * (size_t)b.ldw * 2);
-  b.sums_at = b.dz_bytes * (gated ? 2 : 1);
-  b.total = b.sums_at + align256((size_t)b.chunks * 2 * (size_t)p.N * 4);
-  return b;
+// One of the backward's products: stored directly, or split into fp32 partial
+// results that the combining pass sums.
+template <typename T, typename TO, Lay LA, Lay LB, int SEGS>
+hipError_t product(TileOp o, const TilePlan& plan, DType out, hipStream_t stream, int num_cus, float* ws) {
+  o.splits = plan.splits;
+  if (plan.splits <= 1) return store_tiles<T, TO, LA, LB, SEGS>(o, plan.variant, stream, num_cus);
+  CombineOp c{};
+  c.ldp = partial_pitch(o.N);
+  c.split_stride = (int64_t)o.M * c.ldp;
+  c.splits = o.splits;
+  c.products = o.batch;
+  const size_t one = align256((size_t)o.splits * (size_t)c.split_stride * 4) / 4;
+  for (int i = 0; i < o.batch; ++i) {
+    c.P[i] = ws + i * one;
+    c.Y[i] = o.Y[i];
+    o.Y[i] = (void*)c.P[i];
+  }
+  c.ldy = o.ldy;
+  c.M = o.M;
+  c.N = o.N;
+  o.ldy = c.ldp;
+  o.split_stride = c.split_stride;
+  hipError_t e =
+      plan.variant == 2
+          ? launch_tile<T, float, LA, LB, SEGS, EPI_STORE, ACT_NONE, TileGeo<128, 128, 4, 2, 2, 1>>(o, stream, num_cus)
+          : launch_tile<T, float, LA, LB, SEGS, EPI_STORE, ACT_NONE, TileGeo<64, 64, 4, 2, 4, 1>>(o, stream, num_cus);
+  if (e != hipSuccess) return e;
+  return launch_combine(c, COMBINE_STORE, out, out, stream, num_cus);
 }
 
 template <typename T, typename TG>
-hipError_t backward_t(const FfnBwdParams& p, bool gated, bool dy32, int act, hipStream_t stream, int num_cus,
-                      char* ws) {
-  const BwdPlan b = bwd_plan(p, gated);
+hipError_t backward_t(const FfnBwdParams& p, DType in, DType grad, bool gated, bool dy32, int act, hipStream_t stream,
+                      int num_cus, char* ws) {
+  const BwdPlan b = bwd_plan(p.M, p.N, p.K, gated, num_cus);
+  float* const partial = (float*)(ws + b.partial_at);
   const int nw = gated ? 2 : 1;
   const bool want_db = p.db[0] || p.db[1];
   const bool products = p.dX || p.dW[0] || p.dW[1];
@@ -200,55 +207,49 @@ hipError_t backward_t(const FfnBwdParams& p, bool gated, bool dy32, int act, hip
     TileOp o{};
     for (int i = 0; i < nw; ++i) {
       o.a[i] = dZ[i];
-      o.lda[i] = ldw;
       o.b[i] = p.W[i];
-      o.ldb[i] = p.ldw[i];
     }
+    o.lda = ldw;
+    o.ldb = p.ldw;
     o.M = p.M;
     o.N = p.K;
     o.K = p.N;
-    o.segs = nw;
-    o.batch = o.splits = 1;
+    o.batch = 1;
     o.Y[0] = p.dX;
-    o.ldy[0] = p.lddx;
-    if ((e = launch_tile<T, T, LAY_K, LAY_K, EPI_STORE, Geo128>(o, stream, num_cus)) != hipSuccess) return e;
+    o.ldy = p.lddx;
+    e = gated ? product<T, T, LAY_K, LAY_K, 2>(o, b.dx, in, stream, num_cus, partial)
+              : product<T, T, LAY_K, LAY_K, 1>(o, b.dx, in, stream, num_cus, partial);
+    if (e != hipSuccess) return e;
   }
   if ((p.dW[0] || p.dW[1]) && p.N > 0 && p.K > 0) {
     TileOp o{};
     o.a[0] = p.X;
-    o.lda[0] = p.ldx;
+    o.lda = p.ldx;
+    o.ldb = ldw;
+    o.ldy = p.lddw;
     o.M = p.K;
     o.N = p.N;
     o.K = p.M;
-    o.segs = o.splits = 1;
     o.batch = 0;
     for (int i = 0; i < nw; ++i)
       if (p.dW[i]) {
         o.b[o.batch] = dZ[i];
-        o.ldb[o.batch] = ldw;
         o.Y[o.batch] = p.dW[i];
-        o.ldy[o.batch] = p.lddw[i];
         ++o.batch;
       }
-    if ((e = launch_tile<T, TG, LAY_X, LAY_X, EPI_STORE, Geo128>(o, stream, num_cus)) != hipSuccess) return e;
+    e = product<T, TG, LAY_X, LAY_X, 1>(o, b.dw, grad, stream, num_cus, partial);
+    if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
 
-}  // namespace
-
-size_t ffn_backward_workspace(const FfnBwdParams& p, bool gated, int num_cus) { return bwd_plan(p, gated).total; }
-
-hipError_t launch_ffn_backward(const FfnBwdParams& p, bool gated, DType in, DType dy, DType grad, int act,
-                               hipStream_t stream, int num_cus, void* workspace) {
-  char* ws = (char*)workspace;
+template <typename T>
+hipError_t backward_typed(const FfnBwdParams& p, DType in, bool gated, DType dy, DType grad, int act,
+                          hipStream_t stream, int num_cus, void* workspace) {
   const bool dy32 = dy == DT_F32;
-  if (in == DT_BF16) {
-    if (grad == DT_F32) return backward_t<__bf16, float>(p, gated, dy32, act, stream, num_cus, ws);
-    return backward_t<__bf16, __bf16>(p, gated, dy32, act, stream, num_cus, ws);
-  }
-  if (grad == DT_F32) return backward_t<_Float16, float>(p, gated, dy32, act, stream, num_cus, ws);
-  return backward_t<_Float16, _Float16>(p, gated, dy32, act, stream, num_cus, ws);
+  if (grad == DT_F32) return backward_t<T, float>(p, in, grad, gated, dy32, act, stream, num_cus, (char*)workspace);
+  return backward_t<T, T>(p, in, grad, gated, dy32, act, stream, num_cus, (char*)workspace);
 }
 
+}  // namespace
 }  // namespace coalesce

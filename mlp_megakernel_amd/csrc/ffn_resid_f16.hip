@@ -1,0 +1,10 @@
+// GEMM with residual, f16 inputs (ffn_forward.hpp).
+#include "ffn_forward.hpp"
+
+namespace coalesce {
+
+hipError_t launch_resid_f16(const FfnParams& p, DType out, int act, hipStream_t stream, int num_cus, void* workspace) {
+  return forward_typed<_Float16, EPI_RESID>(p, DT_F16, out, act, stream, num_cus, workspace);
+}
+
+}  // namespace coalesce

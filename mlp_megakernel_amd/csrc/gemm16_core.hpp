@@ -66,6 +66,15 @@ __device__ __forceinline__ void dma16_off(const void* base, uint32_t off, uint32
                : "memory", "m0");
 }
 
+// The same through a buffer resource, at the lane's offset plus a uniform one:
+// bytes at or past the resource's size read as zero, so a tile that overhangs
+// its matrix needs no clamps.
+__device__ __forceinline__ void dma16_buf(u32x4 rsrc, uint32_t off, uint32_t shift, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %3 offen lds" ::"v"(off), "s"(rsrc),
+               "s"(lds), "s"(shift)
+               : "memory", "m0");
+}
+
 // Workgroup barrier for LDS reuse: the wave's own LDS accesses are complete
 // (lgkmcnt 0) but its global stores and direct copies may still be in
 // flight (no vmcnt wait, unlike __syncthreads' fence); the "memory" clobber
@@ -149,7 +158,7 @@ struct TileGeo {
   static constexpr bool OUTER_N = NT <= MT;           // groups run over the n side's fragments
   static constexpr int STAGE_A = BM * BK, STAGE_B = BN * BK;
   static constexpr int LDS_ELEMS = 2 * (STAGE_A + STAGE_B);
-  static_assert(CA * NW * 8 == BM && CBS * NW * 8 == SUBN && CA > 0 && CBS > 0, "copy plan does not cover the tile");
+  static_assert(CA * NW * 8 == BM && CBS * NW * 8 == SUBN && CA % 2 == 0 && CBS % 2 == 0, "copy plan does not cover the tile");
   static_assert((NG == 4 && (NI == 8 || NI == 4)) || (NG == 2 && (NI == 2 || NI == 4)), "no read plan for this wave tile");
 };
 
@@ -161,33 +170,11 @@ struct Side {
   int x0, X;
 };
 
-// 1 KB copy j of wave w of a BX-wide tile: (LDS element offset, per-lane byte
-// offset from the tile's base at k0).  32-bit arithmetic is exact: the host
-// checks that 256 rows fit in 32 bits.
-template <typename T, Lay L, int BX>
-__device__ __forceinline__ uint32_t copy_offset(const Side& s, int g, int lane) {
-  const uint32_t ld_b = (uint32_t)s.ld * (uint32_t)sizeof(T);
-  if constexpr (L == LAY_K) {
-    const int row = g * 8 + (lane >> 3);
-    const int c = (lane & 7) ^ swzA(row);
-    const int gx = min(s.x0 + row, s.X - 1);
-    return (uint32_t)(gx - s.x0) * ld_b + (uint32_t)(c * 8 * (int)sizeof(T));
-  } else {
-    constexpr int CPR = BX / 8, RPC = 64 / CPR;
-    const int row = g * RPC + lane / CPR;
-    const int c = (lane & (CPR - 1)) ^ swzB<CPR>(row);
-    const int gx = min(s.x0 + c * 8, ((s.X - 1) >> 3) << 3);
-    return (uint32_t)row * ld_b + (uint32_t)((gx - s.x0) * (int)sizeof(T));
-  }
-}
-
-template <typename T, Lay L>
-__device__ __forceinline__ const void* side_base(const Side& s, int k0) {
-  if constexpr (L == LAY_K)
-    return uniform_ptr((const T*)s.p + (int64_t)s.x0 * s.ld + k0);
-  else
-    return uniform_ptr((const T*)s.p + (int64_t)k0 * s.ld + s.x0);
-}
+// Rows of a tile in LDS that one 1 KB copy fills.
+template <Lay L, int BX>
+struct CopyRows {
+  static constexpr int N = L == LAY_K ? 8 : 512 / BX;
+};
 
 // Masked register loads of the same 16 bytes (elements at k >= K become 0):
 // the last, partial K step.
@@ -214,28 +201,57 @@ __device__ __forceinline__ i16x8 tail_chunk(const Side& s, int g, int lane, int 
   return v;
 }
 
-// MFMA operand fragment: free index x0 + (lane & 15), k = 32 ks + 8 (lane >> 4) + e.
-template <typename T, Lay L, int BX>
-__device__ __forceinline__ i16x8 read_frag(const T* t, int ks, int x0, int lane) {
+// MFMA operand fragment i of a wave's N: free index x0 + 16 i + (lane & 15), k =
+// 32 ks + 8 (lane >> 4) + e.  In LAY_X tiles the fragments of one row lie 32 i
+// apart before the swizzle, which flips the same bits: their LDS addresses are
+// one address with those bits flipped, formed per read where a wave holds
+// eight (eight addresses would not fit in the registers beside the
+// accumulators), and left to the compiler to keep where it holds fewer.
+template <typename T, Lay L, int BX, int N>
+__device__ __forceinline__ i16x8 read_frag(const T* t, int ks, int x0, int i, int lane) {
   if constexpr (L == LAY_K) {
-    const int x = x0 + (lane & 15);
+    const int x = x0 + 16 * i + (lane & 15);
     const int c = (4 * ks + (lane >> 4)) ^ swzA(x);
     return *(const i16x8*)(t + x * BK + c * 8);
   } else {
     constexpr int CPR = BX / 8;
     const int q = lane & 15;
-    const int x = x0 + 4 * (q & 3);
+    const int k0 = 8 * (lane >> 4) + (q >> 2);
     i16x4 h[2];
+    if constexpr (N == 8 && CPR >= 16) {
+      // x0 is a multiple of 128, so i alone sets bits 1..3 of the chunk
+      const int x = x0 + 4 * (q & 3);
+      const uint32_t a0 = lds_addr(t) + (uint32_t)((k0 * BX + (((x >> 3) ^ swzB<CPR>(k0)) << 3) + (x & 7)) * (int)sizeof(T));
+      uint32_t a;
+      asm volatile("v_xor_b32 %0, %1, %2" : "=v"(a) : "i"(32 * i), "v"(a0));
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int k = 32 * ks + 8 * (lane >> 4) + 4 * i + (q >> 2);
-      h[i] = lds_read_tr16(t + k * BX + (((x >> 3) ^ swzB<CPR>(k)) << 3) + (x & 7));
+      for (int u = 0; u < 2; ++u)
+        h[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) i16x4*)(uintptr_t)(a + (uint32_t)((32 * ks + 4 * u) * BX * (int)sizeof(T))));
+    } else {
+      const int x = x0 + 16 * i + 4 * (q & 3);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int k = 32 * ks + k0 + 4 * u;
+        h[u] = lds_read_tr16(t + k * BX + (((x >> 3) ^ swzB<CPR>(k)) << 3) + (x & 7));
+      }
     }
     return (i16x8){h[0][0], h[0][1], h[0][2], h[0][3], h[1][0], h[1][1], h[1][2], h[1][3]};
   }
 }
 
-// Everything a tile's K loop needs besides the accumulators.
+// The launch's arguments in the kernel-argument segment.  Code outside the K
+// loop reads them through fresh(): an opaque copy of the pointer, so that each
+// place loads what it needs instead of the whole struct living in scalar
+// registers (where it would spill, and the spills' reloads would sit in the
+// loop).
+typedef const __attribute__((address_space(4))) TileOp* Args;
+__device__ __forceinline__ Args fresh(Args k) {
+  asm volatile("" : "+s"(k));
+  return k;
+}
+
+// Where a tile lies and which K steps are its.
 struct TileAt {
   int m0, n0;   // first row and output column
   int pair;     // product of a batch of two
@@ -249,48 +265,157 @@ struct TileFrags {
   i16x8 m[G::MT];
 };
 
-template <typename T, typename TO, Lay LA, Lay LB, int EPI, typename G>
+// SEGS = 2: the K loop runs over two products, a[0] b[0] + a[1] b[1].
+template <typename T, typename TO, Lay LA, Lay LB, int SEGS, int EPI, int ACT, typename G>
 struct Tile {
-  // ---- K steps ---------------------------------------------------------
-  static __device__ __forceinline__ int steps_per_seg(const TileOp& p) { return (p.K + BK - 1) / BK; }
-  static __device__ __forceinline__ void step_at(const TileOp& p, int s, int& seg, int& k0) {
-    const int kt = steps_per_seg(p);
-    seg = s >= kt ? 1 : 0;
-    k0 = (s - seg * kt) * BK;
+  static constexpr int NA = SEGS, NB = SEGS * G::NSUB;  // matrices on either side
+  static constexpr int RA = CopyRows<LA, G::BM>::N, RB = CopyRows<LB, G::SUBN>::N;
+  static_assert(SEGS == 1 || G::NSUB == 1, "segments of a gated product are not implemented");
+
+  // What the K loop needs of the tile, in scalar registers: the matrices at
+  // the tile's first free index and k = 0, the bytes per k and per copy, and
+  // the size of a full K step's part of the matrix (the buffer's range: rows
+  // or columns outside the matrix lie past it or are never stored).
+  struct Hot {
+    const char* a[NA];
+    const char* b[NB];
+    int64_t ka, kb;
+    uint32_t ra, rb, na, nb;
+    int K;
+  };
+  // Lane offsets of a wave's copies, the two swizzle patterns per side.
+  struct Pats {
+    uint32_t a[2], b[2];
+  };
+  // Sources of one K step.
+  struct Step {
+    u32x4 a, b[G::NSUB];
+    int seg, k0;
+  };
+
+  static __device__ __forceinline__ Side side_a(Args p, const TileAt& at, int seg) {
+    return Side{p->a[SEGS == 2 ? seg : 0], p->lda, at.m0, p->M};
   }
-  static __device__ __forceinline__ Side side_a(const TileOp& p, const TileAt& at, int seg) {
-    return Side{seg ? p.a[1] : p.a[0], seg ? p.lda[1] : p.lda[0], at.m0, p.M};
-  }
-  static __device__ __forceinline__ Side side_b(const TileOp& p, const TileAt& at, int seg, int sub) {
-    const int i = seg | at.pair | sub;  // at most one of them is used by any launch
-    return Side{i ? p.b[1] : p.b[0], i ? p.ldb[1] : p.ldb[0], at.n0, p.N};
+  static __device__ __forceinline__ Side side_b(Args p, const TileAt& at, int seg, int sub) {
+    return Side{p->b[SEGS == 2 ? seg : G::NSUB == 2 ? sub : at.pair], p->ldb, at.n0, p->N};
   }
 
-  // Copy j (0 .. C - 1) of K step s into stage (a, b).
-  static __device__ __forceinline__ void copy(const TileOp& p, const TileAt& at, int j, int seg, int k0, T* a, T* b,
-                                              int wu, int lane) {
-    if (j < G::CA) {
-      const Side s = side_a(p, at, seg);
-      const int g = wu * G::CA + j;
-      dma16_off(side_base<T, LA>(s, k0), copy_offset<T, LA, G::BM>(s, g, lane), lds_addr(a) + (uint32_t)g * 1024u);
+  // Bytes from the first to behind the last one that a full K step reads.
+  template <Lay L, int BX>
+  static __device__ __forceinline__ uint32_t step_bytes(const Side& s) {
+    const int x = min(BX, s.X - s.x0);
+    if constexpr (L == LAY_K)
+      return (uint32_t)((x - 1) * s.ld + BK) * (uint32_t)sizeof(T);
+    else
+      return (uint32_t)((BK - 1) * s.ld + ((x + 7) & ~7)) * (uint32_t)sizeof(T);
+  }
+  static __device__ __forceinline__ Hot hot(Args k, const TileAt& at) {
+    const Args p = fresh(k);
+    Hot h;
+    h.K = p->K;
+    h.ra = (uint32_t)(RA * p->lda * (int)sizeof(T));
+    h.rb = (uint32_t)(RB * p->ldb * (int)sizeof(T));
+    h.ka = (LA == LAY_K ? 1 : p->lda) * (int64_t)sizeof(T);
+    h.kb = (LB == LAY_K ? 1 : p->ldb) * (int64_t)sizeof(T);
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+      const Side s = side_a(p, at, i);
+      h.a[i] = (const char*)((const T*)s.p + (LA == LAY_K ? s.x0 * s.ld : (int64_t)s.x0));
+      h.na = step_bytes<LA, G::BM>(s);
+    }
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const Side s = side_b(p, at, i, i);
+      h.b[i] = (const char*)((const T*)s.p + (LB == LAY_K ? s.x0 * s.ld : (int64_t)s.x0));
+      h.nb = step_bytes<LB, G::SUBN>(s);
+    }
+    return h;
+  }
+
+  // ---- K steps ---------------------------------------------------------
+  static __device__ __forceinline__ u32x4 rsrc(const char* p, uint32_t bytes) {
+    const uint64_t v = (uint64_t)(uintptr_t)p;
+    return (u32x4){(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v),
+                   (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32)) & 0xffffu,
+                   (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), 0x00020000u};
+  }
+  static __device__ __forceinline__ Step step_at(const Hot& h, int s) {
+    Step t;
+    t.seg = 0;
+    t.k0 = s * BK;
+    if constexpr (SEGS == 2) {
+      const int kt = (h.K + BK - 1) / BK;
+      t.seg = s >= kt ? 1 : 0;
+      t.k0 = (s - t.seg * kt) * BK;
+    }
+    t.a = rsrc((SEGS == 2 && t.seg ? h.a[NA - 1] : h.a[0]) + t.k0 * h.ka, h.na);
+#pragma unroll
+    for (int i = 0; i < G::NSUB; ++i)
+      t.b[i] = rsrc((SEGS == 2 && t.seg ? h.b[NB - 1] : h.b[i]) + t.k0 * h.kb, h.nb);
+    return t;
+  }
+
+  // Which of the two patterns copy j of a wave's NC follows: the swizzles take
+  // bit 3 (and, in rows of 512 bytes, bit 1) of the row.
+  template <Lay L, int BX, int NC>
+  static constexpr int pat_of(int j) {
+    return L == LAY_X && BX == 128 ? (NC >= 4 ? (j >> 1) & 1 : 0) : j & 1;
+  }
+  // Lane offset of copy j of wave wu, less the j RPC rows that copy() adds.
+  template <Lay L, int BX, int NC>
+  static __device__ __forceinline__ uint32_t pattern(int64_t ld, int i, int wu, int lane) {
+    constexpr int RPC = CopyRows<L, BX>::N;
+    const int j = pat_of<L, BX, NC>(1) == 1 ? i : 2 * i;  // a copy that follows pattern i
+    const int first = wu * NC * RPC, row = j * RPC;
+    const uint32_t ld_b = (uint32_t)ld * (uint32_t)sizeof(T);
+    if constexpr (L == LAY_K) {
+      const int r = lane >> 3;
+      return (uint32_t)(first + r) * ld_b + (uint32_t)((((lane & 7) ^ swzA(first + row + r)) * 8) * (int)sizeof(T));
     } else {
-      const int jj = j - G::CA, sub = jj / G::CBS;
-      const Side s = side_b(p, at, seg, sub);
-      const int g = wu * G::CBS + jj % G::CBS;
-      dma16_off(side_base<T, LB>(s, k0), copy_offset<T, LB, G::SUBN>(s, g, lane),
-                lds_addr(b) + (uint32_t)(sub * G::SUBN * BK * (int)sizeof(T)) + (uint32_t)g * 1024u);
+      constexpr int CPR = BX / 8;
+      const int r = lane / CPR;
+      return (uint32_t)(first + r) * ld_b +
+             (uint32_t)((((lane & (CPR - 1)) ^ swzB<CPR>(first + row + r)) * 8) * (int)sizeof(T));
+    }
+  }
+  static __device__ __forceinline__ Pats patterns(Args k, int wu, int lane) {
+    const Args p = fresh(k);
+    Pats o;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      o.a[i] = pattern<LA, G::BM, G::CA>(p->lda, i, wu, lane);
+      o.b[i] = pattern<LB, G::SUBN, G::CBS>(p->ldb, i, wu, lane);
+    }
+    return o;
+  }
+
+  // Copy j (0 .. C - 1) of a K step into stage (a, b).  The copies of a wave
+  // differ by a whole number of rows, a uniform offset, and by one of two
+  // swizzle patterns: two lane offsets per side are all that stays in
+  // registers.
+  static __device__ __forceinline__ void copy(const Hot& h, const Pats& pt, const Step& st, int j, T* a, T* b, int wu) {
+    if (j < G::CA) {
+      dma16_buf(st.a, pt.a[pat_of<LA, G::BM, G::CA>(j)], (uint32_t)j * h.ra, lds_addr(a) + (uint32_t)(wu * G::CA + j) * 1024u);
+    } else {
+      const int sub = (j - G::CA) / G::CBS, jj = (j - G::CA) % G::CBS;
+      dma16_buf(st.b[sub], pt.b[pat_of<LB, G::SUBN, G::CBS>(jj)], (uint32_t)jj * h.rb,
+                lds_addr(b) + (uint32_t)(sub * G::SUBN * BK * (int)sizeof(T)) + (uint32_t)(wu * G::CBS + jj) * 1024u);
     }
   }
 
-  static __device__ __forceinline__ void tail(const TileOp& p, const TileAt& at, int seg, int k0, T* a, T* b, int w,
-                                              int lane) {
+  static __device__ __forceinline__ void tail(Args k, const TileAt& at, const Step& st, T* a, T* b, int w, int lane) {
+    // the lane through an opaque copy: the addresses are formed here, not
+    // carried in registers through the K loop
+    asm volatile("" : "+v"(lane));
+    const Args p = fresh(k);
+    const int K = p->K;
     i16x8 ra[G::CA], rb[G::CB];
-    const Side sa = side_a(p, at, seg);
+    const Side sa = side_a(p, at, st.seg);
 #pragma unroll
-    for (int j = 0; j < G::CA; ++j) ra[j] = tail_chunk<T, LA, G::BM>(sa, w * G::CA + j, lane, k0, p.K);
+    for (int j = 0; j < G::CA; ++j) ra[j] = tail_chunk<T, LA, G::BM>(sa, w * G::CA + j, lane, st.k0, K);
 #pragma unroll
     for (int j = 0; j < G::CB; ++j)
-      rb[j] = tail_chunk<T, LB, G::SUBN>(side_b(p, at, seg, j / G::CBS), w * G::CBS + j % G::CBS, lane, k0, p.K);
+      rb[j] = tail_chunk<T, LB, G::SUBN>(side_b(p, at, st.seg, j / G::CBS), w * G::CBS + j % G::CBS, lane, st.k0, K);
 #pragma unroll
     for (int j = 0; j < G::CA; ++j) *(i16x8*)(a + (w * G::CA + j) * 512 + lane * 8) = ra[j];
 #pragma unroll
@@ -299,24 +424,24 @@ struct Tile {
   }
 
   // K step s, all copies at once (a tile's first two steps).
-  static __device__ __forceinline__ void fill(const TileOp& p, const TileAt& at, int s, T* a, T* b, int wu, int lane) {
-    int seg, k0;
-    step_at(p, s, seg, k0);
-    if (k0 + BK <= p.K) {
+  static __device__ __forceinline__ void fill(Args k, const TileAt& at, const Hot& h, const Pats& pt, int s, T* a, T* b,
+                                              int wu, int lane) {
+    const Step st = step_at(h, s);
+    if (st.k0 + BK <= h.K) {
 #pragma unroll
-      for (int j = 0; j < G::C; ++j) copy(p, at, j, seg, k0, a, b, wu, lane);
+      for (int j = 0; j < G::C; ++j) copy(h, pt, st, j, a, b, wu);
     } else {
-      tail(p, at, seg, k0, a, b, wu, lane);
+      tail(k, at, st, a, b, wu, lane);
     }
   }
 
   // ---- fragments and MFMAs ---------------------------------------------
   static __device__ __forceinline__ i16x8 frag_m(const T* a, int ks, int wm, int i, int lane) {
-    return read_frag<T, LA, G::BM>(a, ks, wm * G::WM + 16 * i, lane);
+    return read_frag<T, LA, G::BM, G::MT>(a, ks, wm * G::WM, i, lane);
   }
   static __device__ __forceinline__ i16x8 frag_n(const T* b, int ks, int wn, int i, int lane) {
     const int sub = i / G::NTO;
-    return read_frag<T, LB, G::SUBN>(b + sub * G::SUBN * BK, ks, wn * G::WNO + 16 * (i % G::NTO), lane);
+    return read_frag<T, LB, G::SUBN, G::NTO>(b + sub * G::SUBN * BK, ks, wn * G::WNO, i % G::NTO, lane);
   }
 
   // One 32-deep slice: NG groups of {a share of the copies of K step k + 2,
@@ -325,8 +450,7 @@ struct Tile {
   // "next" reads fetch stale but in-bounds LDS and are unused.
   static __device__ __forceinline__ void slice(const TileFrags<G>& cur, f32x4 (&acc)[G::NT][G::MT], TileFrags<G>& nxt,
                                                const T* ra, const T* rb, int rks, int wm, int wn, int lane, bool cp,
-                                               const TileOp& p, const TileAt& at, int seg, int k0, T* ca, T* cb,
-                                               int wu) {
+                                               const Hot& h, const Pats& pt, const Step& st, T* ca, T* cb, int wu) {
     auto read_outer = [&](int i) {
       if constexpr (G::OUTER_N)
         nxt.n[i] = frag_n(rb, rks, wn, i, lane);
@@ -343,7 +467,7 @@ struct Tile {
     for (int g = 0; g < G::NG; ++g) {
       if (cp) {
 #pragma unroll
-        for (int j = G::C * g / G::NG; j < G::C * (g + 1) / G::NG; ++j) copy(p, at, j, seg, k0, ca, cb, wu, lane);
+        for (int j = G::C * g / G::NG; j < G::C * (g + 1) / G::NG; ++j) copy(h, pt, st, j, ca, cb, wu);
       }
 #pragma unroll
       for (int i = 0; i < G::NI; ++i) {
@@ -375,14 +499,15 @@ struct Tile {
   }
 
   // ---- epilogue ----------------------------------------------------------
-  // Rows [wr0, wr0 + WM) x columns [wc0, wc0 + WNO) of one output matrix from
-  // value(t, s, m, n, valid), the 4 consecutive columns n.. of row m.  A
-  // 16-bit block that lies whole inside the matrix is staged in the wave's
+  // Rows [wr0, wr0 + WM) x columns [wc0, wc0 + WNO) of one output matrix:
+  // prep(t, n, valid) once per 16-wide sub-block gives what value(c, t, s, m,
+  // n, valid), the 4 consecutive columns n.. of row m, needs of its columns.
+  // A 16-bit block that lies whole inside the matrix is staged in the wave's
   // own LDS region and stored as full row segments; others are stored from
   // the registers.
-  template <typename TS, typename F>
-  static __device__ __forceinline__ void put(TS* Y, int64_t ldy, const TileOp& p, int wr0, int wc0, bool inside,
-                                             char* region, int lane, F value) {
+  template <typename TS, typename P, typename F>
+  static __device__ __forceinline__ void put(TS* Y, int64_t ldy, Args p, int wr0, int wc0, bool inside,
+                                             char* region, int lane, P prep, F value) {
     const int q = lane & 15, b = lane >> 4;
     if constexpr (sizeof(TS) == 2) {
       if (inside) {
@@ -391,10 +516,11 @@ struct Tile {
 #pragma unroll
         for (int t = 0; t < G::NTO; ++t) {
           const int chunk = 2 * t + (b >> 1);
+          const auto c = prep(t, wc0 + 16 * t + 4 * b, 4);
 #pragma unroll
           for (int s = 0; s < G::MT; ++s) {
             const int row = 16 * s + q;
-            const f32x4 v = value(t, s, wr0 + row, wc0 + 16 * t + 4 * b, 4);
+            const f32x4 v = value(c, t, s, wr0 + row, wc0 + 16 * t + 4 * b, 4);
             const to4 o = (to4){(TS)v[0], (TS)v[1], (TS)v[2], (TS)v[3]};
             *(to4*)(region + row * ROWB + ((chunk ^ stage_swz<ROWB>(row)) << 4) + ((b & 1) << 3)) = o;
           }
@@ -414,116 +540,114 @@ struct Tile {
 #pragma unroll
     for (int t = 0; t < G::NTO; ++t) {
       const int n = wc0 + 16 * t + 4 * b;
-      if (n >= p.N) continue;
-      const int valid = min(4, p.N - n);
+      if (n >= p->N) continue;
+      const int valid = min(4, p->N - n);
+      const auto c = prep(t, n, valid);
 #pragma unroll
       for (int s = 0; s < G::MT; ++s) {
         const int m = wr0 + 16 * s + q;
-        if (m < p.M) store4<TS>(Y + (int64_t)m * ldy + n, value(t, s, m, n, valid), valid);
+        if (m < p->M) store4<TS>(Y + (int64_t)m * ldy + n, value(c, t, s, m, n, valid), valid);
       }
     }
   }
 
-  template <int ACT>
-  static __device__ __forceinline__ void finish(const TileOp& p, const TileAt& at, f32x4 (&acc)[G::NT][G::MT], int wr0,
-                                                int wc0, bool inside, char* region, int lane) {
-    constexpr bool O16 = sizeof(TO) == 2;
-    // + bias, in place
-#pragma unroll
-    for (int t = 0; t < G::NT; ++t) {
-      const T* bias = (const T*)(t / G::NTO ? p.bias[1] : p.bias[0]);
-      if (bias) {
-        const int n = wc0 + 16 * (t % G::NTO) + 4 * (lane >> 4);
-        const f32x4 bv = load4<T>(bias + (n < p.N ? n : 0), min(4, p.N - n));
-#pragma unroll
-        for (int s = 0; s < G::MT; ++s) acc[t][s] += bv;
-      }
-    }
-    // the stored pre-activations of a training forward, one rounding each
-    if (p.Z[0]) {
-      put<T>((T*)p.Z[0], p.ldz, p, wr0, wc0, inside, region, lane,
-             [&](int t, int s, int, int, int) { return acc[t][s]; });
-      if constexpr (EPI == EPI_GATED)
-        put<T>((T*)p.Z[1], p.ldz, p, wr0, wc0, inside, region, lane,
-               [&](int t, int s, int, int, int) { return acc[t + G::NTO][s]; });
-    }
-    if constexpr (EPI == EPI_GATED) {
-      put<TO>((TO*)p.Y[0], p.ldy[0], p, wr0, wc0, inside, region, lane, [&](int t, int s, int, int, int) {
-        f32x4 o;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) o[r] = apply_act<ACT, O16>(acc[t][s][r]) * acc[t + G::NTO][s][r];
-        return o;
-      });
-    } else {
-      const TO* R = (const TO*)p.R;
-      put<TO>((TO*)p.Y[0], p.ldy[0], p, wr0, wc0, inside, region, lane, [&](int t, int s, int m, int n, int valid) {
-        f32x4 o = (f32x4){0.f, 0.f, 0.f, 0.f};
-        if (R) o = load4<TO>(R + (int64_t)m * p.ldr + n, valid);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) o[r] += apply_act<ACT, O16>(acc[t][s][r]);
-        return o;
-      });
-    }
+  static __device__ __forceinline__ f32x4 bias4(const void* bias, int n, int valid) {
+    return bias ? load4<T>((const T*)bias + n, valid) : (f32x4){0.f, 0.f, 0.f, 0.f};
   }
 
-  static __device__ __forceinline__ void epilogue(const TileOp& p, const TileAt& at, f32x4 (&acc)[G::NT][G::MT], int wm,
+  static __device__ __forceinline__ void epilogue(Args k, const TileAt& at, f32x4 (&acc)[G::NT][G::MT], int wm,
                                                   int wn, int wu, int lane, char* lds) {
+    const Args p = fresh(k);
     const int wr0 = at.m0 + wm * G::WM, wc0 = at.n0 + wn * G::WNO;
-    const bool inside = wr0 + G::WM <= p.M && wc0 + G::WNO <= p.N;
+    const bool inside = wr0 + G::WM <= p->M && wc0 + G::WNO <= p->N;
     char* region = lds + wu * (G::WM * G::WNO * 2);
     static_assert(G::NW * G::WM * G::WNO * 2 <= G::LDS_ELEMS * 2, "staging regions exceed the stages");
+    constexpr bool O16 = sizeof(TO) == 2;
+    auto none = [](int, int, int) { return 0; };
     if constexpr (EPI == EPI_STORE) {
 #pragma unroll
       for (int sub = 0; sub < G::NSUB; ++sub) {
         const int i = at.pair | sub;
-        TO* Y = (TO*)(i ? p.Y[1] : p.Y[0]) + (int64_t)at.split * p.split_stride;
-        put<TO>(Y, i ? p.ldy[1] : p.ldy[0], p, wr0, wc0, inside, region, lane,
-                [&](int t, int s, int, int, int) { return acc[t + sub * G::NTO][s]; });
+        TO* Y = (TO*)(i ? p->Y[1] : p->Y[0]) + (int64_t)at.split * p->split_stride;
+        put<TO>(Y, p->ldy, p, wr0, wc0, inside, region, lane, none,
+                [&](int, int t, int s, int, int, int) { return acc[t + sub * G::NTO][s]; });
       }
     } else {
-      switch (p.act) {
-        case ACT_GELU: finish<ACT_GELU>(p, at, acc, wr0, wc0, inside, region, lane); break;
-        case ACT_SOFTPLUS: finish<ACT_SOFTPLUS>(p, at, acc, wr0, wc0, inside, region, lane); break;
-        case ACT_RELU: finish<ACT_RELU>(p, at, acc, wr0, wc0, inside, region, lane); break;
-        case ACT_SILU: finish<ACT_SILU>(p, at, acc, wr0, wc0, inside, region, lane); break;
-        default: finish<ACT_NONE>(p, at, acc, wr0, wc0, inside, region, lane); break;
+      auto bias_g = [&](int, int n, int valid) { return bias4(p->bias[0], n, valid); };
+      auto bias_u = [&](int, int n, int valid) { return bias4(p->bias[1], n, valid); };
+      // the stored pre-activations of a training forward, one rounding each
+      if (p->Z[0]) {
+        put<T>((T*)p->Z[0], p->ldz, p, wr0, wc0, inside, region, lane, bias_g,
+               [&](f32x4 c, int t, int s, int, int, int) { return acc[t][s] + c; });
+        if constexpr (EPI == EPI_GATED)
+          put<T>((T*)p->Z[1], p->ldz, p, wr0, wc0, inside, region, lane, bias_u,
+                 [&](f32x4 c, int t, int s, int, int, int) { return acc[t + G::NTO][s] + c; });
+      }
+      if constexpr (EPI == EPI_GATED) {
+        struct Pair {
+          f32x4 g, u;
+        };
+        put<TO>((TO*)p->Y[0], p->ldy, p, wr0, wc0, inside, region, lane,
+                [&](int t, int n, int valid) { return Pair{bias_g(t, n, valid), bias_u(t, n, valid)}; },
+                [&](Pair c, int t, int s, int, int, int) {
+                  const f32x4 g = acc[t][s] + c.g, u = acc[t + G::NTO][s] + c.u;
+                  f32x4 o;
+#pragma unroll
+                  for (int r = 0; r < 4; ++r) o[r] = apply_act<ACT, O16>(g[r]) * u[r];
+                  return o;
+                });
+      } else {
+        const TO* R = (const TO*)p->R;
+        put<TO>((TO*)p->Y[0], p->ldy, p, wr0, wc0, inside, region, lane, bias_g,
+                [&](f32x4 c, int t, int s, int m, int n, int valid) {
+                  const f32x4 z = acc[t][s] + c;
+                  f32x4 o = (f32x4){0.f, 0.f, 0.f, 0.f};
+                  if (R) o = load4<TO>(R + (int64_t)m * p->ldr + n, valid);
+#pragma unroll
+                  for (int r = 0; r < 4; ++r) o[r] += apply_act<ACT, O16>(z[r]);
+                  return o;
+                });
       }
     }
   }
 
   // Unit of work v: one tile of one range of K steps.  The two products of a
   // batch lie side by side in the tile order, so they share the m side.
-  static __device__ __forceinline__ TileAt locate(const TileOp& p, int64_t v) {
+  static __device__ __forceinline__ TileAt locate(Args k, int64_t v) {
+    const Args p = fresh(k);
     TileAt at;
-    const int tn_all = p.tiles_n * p.batch;
-    const int64_t tiles = (int64_t)p.tiles_m * tn_all;
+    const int tn_all = p->tiles_n * p->batch;
+    const int64_t tiles = (int64_t)p->tiles_m * tn_all;
     at.split = (int)(v / tiles);
     int tm, tn;
-    tile_coords((int)(v - at.split * tiles), p.tiles_m, tn_all, p.group_m, tm, tn);
-    at.pair = tn >= p.tiles_n ? 1 : 0;
+    tile_coords((int)(v - at.split * tiles), p->tiles_m, tn_all, p->group_m, tm, tn);
+    at.pair = tn >= p->tiles_n ? 1 : 0;
     at.m0 = tm * G::BM;
-    at.n0 = (tn - at.pair * p.tiles_n) * G::ON;
-    const int64_t total = (int64_t)steps_per_seg(p) * p.segs;
-    at.s0 = (int)(total * at.split / p.splits);
-    at.ns = (int)(total * (at.split + 1) / p.splits) - at.s0;
+    at.n0 = (tn - at.pair * p->tiles_n) * G::ON;
+    const int64_t total = (int64_t)((p->K + BK - 1) / BK) * SEGS;
+    at.s0 = (int)(total * at.split / p->splits);
+    at.ns = (int)(total * (at.split + 1) / p->splits) - at.s0;
     return at;
   }
 
-  static __device__ __forceinline__ void run(const TileOp& p, T* lds) {
+  static __device__ __forceinline__ void run(Args k, T* lds) {
+    const Args p = fresh(k);
     T* const a0 = lds;
     T* const a1 = lds + G::STAGE_A;
     T* const b0 = lds + 2 * G::STAGE_A;
     T* const b1 = b0 + G::STAGE_B;
-    const int64_t total = (int64_t)p.tiles_m * p.tiles_n * p.batch * p.splits;
+    const int64_t total = (int64_t)p->tiles_m * p->tiles_n * p->batch * p->splits;
     int64_t v = blockIdx.x;
     if (v >= total) return;
     const int lane0 = threadIdx.x & 63;
     const int wu = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wu % G::WGM, wn = wu / G::WGM;
 
-    TileAt at = locate(p, v);
-    if (at.ns > 0) fill(p, at, at.s0, a0, b0, wu, lane0);
-    if (at.ns > 1) fill(p, at, at.s0 + 1, a1, b1, wu, lane0);
+    TileAt at = locate(k, v);
+    Hot h = hot(k, at);
+    const Pats pt = patterns(k, wu, lane0);
+    if (at.ns > 0) fill(k, at, h, pt, at.s0, a0, b0, wu, lane0);
+    if (at.ns > 1) fill(k, at, h, pt, at.s0 + 1, a1, b1, wu, lane0);
     while (true) {
       // the lane index through an opaque copy: everything derived from it is
       // recomputed per tile instead of being held across the K loop
@@ -550,50 +674,51 @@ struct Tile {
       for (int kt = 0; kt < at.ns; kt += 2) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const int k = kt + half;
-          if (k < at.ns) {
+          const int i = kt + half;
+          if (i < at.ns) {
             T* const ca = half ? a1 : a0;
             T* const cb = half ? b1 : b0;
             T* const na = half ? a0 : a1;
             T* const nb = half ? b0 : b1;
-            slice(f0, acc, f1, ca, cb, 1, wm, wn, lane, false, p, at, 0, 0, ca, cb, wu);
-            if (k + 1 < at.ns) {
+            Step st{};
+            slice(f0, acc, f1, ca, cb, 1, wm, wn, lane, false, h, pt, st, ca, cb, wu);
+            if (i + 1 < at.ns) {
               wait_vmcnt0();
               __syncthreads();
             }
-            int seg = 0, k0 = 0;
             bool cp = false;
-            if (k + 2 < at.ns) {
-              step_at(p, at.s0 + k + 2, seg, k0);
-              cp = k0 + BK <= p.K;
-              if (!cp) tail(p, at, seg, k0, ca, cb, wu, lane);
+            if (i + 2 < at.ns) {
+              st = step_at(h, at.s0 + i + 2);
+              cp = st.k0 + BK <= h.K;
+              if (!cp) tail(k, at, st, ca, cb, wu, lane);
             }
-            slice(f1, acc, f0, na, nb, 0, wm, wn, lane, cp, p, at, seg, k0, ca, cb, wu);
+            slice(f1, acc, f0, na, nb, 0, wm, wn, lane, cp, h, pt, st, ca, cb, wu);
           }
         }
       }
       __syncthreads();  // every wave is past its last fragment read
-      epilogue(p, at, acc, wm, wn, wu, lane, (char*)lds);
+      epilogue(k, at, acc, wm, wn, wu, lane, (char*)lds);
       lds_barrier();  // the LDS is free; the stores may still be in flight
       v += gridDim.x;
       if (v >= total) break;
-      at = locate(p, v);
-      if (at.ns > 0) fill(p, at, at.s0, a0, b0, wu, lane);
-      if (at.ns > 1) fill(p, at, at.s0 + 1, a1, b1, wu, lane);
+      at = locate(k, v);
+      h = hot(k, at);
+      if (at.ns > 0) fill(k, at, h, pt, at.s0, a0, b0, wu, lane);
+      if (at.ns > 1) fill(k, at, h, pt, at.s0 + 1, a1, b1, wu, lane);
     }
   }
 };
 
-template <typename T, typename TO, Lay LA, Lay LB, int EPI, typename G>
-__global__ __launch_bounds__(G::THREADS, G::MINW) void tile_kernel(TileOp p) {
+template <typename T, typename TO, Lay LA, Lay LB, int SEGS, int EPI, int ACT, typename G>
+__global__ __launch_bounds__(G::THREADS, G::MINW) void tile_kernel(TileOp) {  // read through the argument segment
   __shared__ __attribute__((aligned(1024))) T lds[G::LDS_ELEMS];
-  Tile<T, TO, LA, LB, EPI, G>::run(p, lds);
+  Tile<T, TO, LA, LB, SEGS, EPI, ACT, G>::run((Args)__builtin_amdgcn_kernarg_segment_ptr(), lds);
 }
 
 // Grid: min(#units of work, #CUs x workgroups per CU), the per-CU count from
 // the runtime for the compiled kernel, cached per instantiation (atomic:
 // concurrent first calls store the same value).
-template <typename T, typename TO, Lay LA, Lay LB, int EPI, typename G>
+template <typename T, typename TO, Lay LA, Lay LB, int SEGS, int EPI, int ACT, typename G>
 hipError_t launch_tile(TileOp p, hipStream_t stream, int num_cus) {
   p.tiles_m = (p.M + G::BM - 1) / G::BM;
   p.tiles_n = (p.N + G::ON - 1) / G::ON;
@@ -602,14 +727,15 @@ hipError_t launch_tile(TileOp p, hipStream_t stream, int num_cus) {
   int per_cu = per_cu_cache.load(std::memory_order_relaxed);
   if (per_cu == 0) {
     int n = 0;
-    hipError_t e = hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, tile_kernel<T, TO, LA, LB, EPI, G>, G::THREADS, 0);
+    hipError_t e = hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, tile_kernel<T, TO, LA, LB, SEGS, EPI, ACT, G>,
+                                                                G::THREADS, 0);
     if (e != hipSuccess) return e;
     per_cu = n > 0 ? n : 1;
     per_cu_cache.store(per_cu, std::memory_order_relaxed);
   }
   const int64_t total = (int64_t)p.tiles_m * p.tiles_n * p.batch * p.splits;
   const int64_t cap = (int64_t)num_cus * per_cu;
-  hipLaunchKernelGGL((tile_kernel<T, TO, LA, LB, EPI, G>), dim3((unsigned)(total < cap ? total : cap)),
+  hipLaunchKernelGGL((tile_kernel<T, TO, LA, LB, SEGS, EPI, ACT, G>), dim3((unsigned)(total < cap ? total : cap)),
                      dim3(G::THREADS), 0, stream, p);
   return hipGetLastError();
 }

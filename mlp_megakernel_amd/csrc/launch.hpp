@@ -159,13 +159,14 @@ hipError_t launch_compare(const void* a, int64_t pitch_a, const void* b, int64_t
 
 // One launch of the feed-forward operators' tile kernel (gemm16_core.hpp).
 // The extents are the product's own (m, n, contraction), whichever way the
-// operands lie in memory.
+// operands lie in memory.  The second operands: the other half of a gated
+// product, the second segment of a sum of two products, or the second product
+// of a batch.
 struct TileOp {
-  const void* a[2];  // m side
-  const void* b[2];  // n side
-  int64_t lda[2], ldb[2];
+  const void* a[2];  // m side, pitch lda
+  const void* b[2];  // n side, pitch ldb
+  int64_t lda, ldb;
   int M, N, K;
-  int segs;    // 2: acc = a[0] b[0] + a[1] b[1], K steps of the second after the first's
   int batch;   // 2: two products a[0] b[i] -> Y[i]
   int splits;  // ranges of K steps, range i stored split_stride elements after range i - 1
   int64_t split_stride;
@@ -175,12 +176,11 @@ struct TileOp {
   void* Z[2];  // stored pre-activations, pitch ldz, or nullptr
   int64_t ldz;
   void* Y[2];
-  int64_t ldy[2];
-  int act;
+  int64_t ldy;
   int tiles_m, tiles_n, group_m;  // set by the launcher
 };
 
-// Forward of the gated product and of the GEMM with residual (ffn_gemm.hip):
+// Forward of the gated product and of the GEMM with residual (ffn_forward.hpp):
 // X is M x K, W[i] K x N.
 struct FfnParams {
   const void* X;
@@ -189,15 +189,37 @@ struct FfnParams {
   const void* R;
   void* Z[2];
   void* Y;
-  int64_t ldx, ldw[2], ldr, ldz, ldy;
+  int64_t ldx, ldw, ldr, ldz, ldy;
   int M, N, K;
 };
+// Sums the ranges of a split product in order and finishes its results: an
+// elementwise kernel (ffn.hip) over partial results P[i] (fp32, pitch ldp,
+// `splits` of them split_stride elements apart).
+struct CombineOp {
+  const float* P[2];
+  int64_t ldp, split_stride;
+  int splits, products;  // products: 2 for a gated product (-> one result) or a batch (-> Y[0], Y[1])
+  const void* bias[2];
+  const void* R;
+  int64_t ldr;
+  void* Z[2];
+  int64_t ldz;
+  void* Y[2];
+  int64_t ldy;
+  int M, N, act;
+};
+enum CombineKind { COMBINE_STORE = 0, COMBINE_RESID = 1, COMBINE_GATED = 2 };
+hipError_t launch_combine(const CombineOp& c, CombineKind kind, DType in, DType out, hipStream_t stream, int num_cus);
+hipError_t launch_gated_bf16(const FfnParams& p, DType out, int act, hipStream_t stream, int num_cus, void* workspace);
+hipError_t launch_gated_f16(const FfnParams& p, DType out, int act, hipStream_t stream, int num_cus, void* workspace);
+hipError_t launch_resid_bf16(const FfnParams& p, DType out, int act, hipStream_t stream, int num_cus, void* workspace);
+hipError_t launch_resid_f16(const FfnParams& p, DType out, int act, hipStream_t stream, int num_cus, void* workspace);
 // Workspace (bytes, 0: none) and launch; `workspace` holds that many bytes.
 size_t ffn_forward_workspace(int64_t M, int64_t N, int64_t K, bool gated, int num_cus);
 hipError_t launch_ffn_forward(const FfnParams& p, bool gated, DType in, DType out, int act, hipStream_t stream,
                               int num_cus, void* workspace);
 
-// Backward of both (ffn_bwd.hip).  Outputs may be nullptr: not wanted.
+// Backward of both (ffn_backward.hpp).  Outputs may be nullptr: not wanted.
 struct FfnBwdParams {
   const void* X;      // M x K
   const void* W[2];   // K x N
@@ -206,7 +228,7 @@ struct FfnBwdParams {
   void* dX;           // M x K (lddx)
   void* dW[2];        // K x N (lddw)
   void* db[2];        // N
-  int64_t ldx, ldw[2], ldz, ldd, lddx, lddw[2];
+  int64_t ldx, ldw, ldz, ldd, lddx, lddw;
   int M, N, K;
 };
 // The elementwise pass of that backward.
@@ -218,8 +240,11 @@ struct DzParams {
   int64_t ldd, ldz, ldw;
   int M, N, chunk_rows;
 };
-// (M, N, K and, for products that are not wanted, null outputs are what the size depends on)
-size_t ffn_backward_workspace(const FfnBwdParams& p, bool gated, int num_cus);
+hipError_t launch_backward_bf16(const FfnBwdParams& p, bool gated, DType dy, DType grad, int act, hipStream_t stream,
+                                int num_cus, void* workspace);
+hipError_t launch_backward_f16(const FfnBwdParams& p, bool gated, DType dy, DType grad, int act, hipStream_t stream,
+                               int num_cus, void* workspace);
+size_t ffn_backward_workspace(int64_t M, int64_t N, int64_t K, bool gated, int num_cus);
 hipError_t launch_ffn_backward(const FfnBwdParams& p, bool gated, DType in, DType dy, DType grad, int act,
                                hipStream_t stream, int num_cus, void* workspace);
 

@@ -100,7 +100,15 @@ def _extents(A: torch.Tensor, Bs, names):
     if A.dtype not in _DTYPES:
         raise ValueError("A must be float16 or bfloat16")
     N = Bs[0].shape[1] if Bs[0].dim() == 2 else -1
-    return M, N, K, lda, [_mat(B, n, A, (K, N), A.dtype) for B, n in zip(Bs, names)]
+    return M, N, K, lda, _one_pitch(Bs, names, A, (K, N), A.dtype)
+
+
+def _one_pitch(ts, names, like, shape, dtype):
+    """The pitch that tensors of one shape and type share."""
+    ld = [_mat(t, n, like, shape, dtype) for t, n in zip(ts, names)]
+    if any(x != ld[0] for x in ld):
+        raise ValueError("%s must have one row pitch" % " and ".join(names))
+    return ld[0]
 
 
 # Workspace sizes by (function, extents, device): a user's shapes repeat.
@@ -166,7 +174,7 @@ def _out_dtype(A, residual, out_dtype, out):
 
 def _gemm_residual(A, B, residual, bias, act, out_dtype, out, preact, workspace, stream):
     lib = load_library()
-    M, N, K, lda, (ldb,) = _extents(A, (B,), ("B",))
+    M, N, K, lda, ldb = _extents(A, (B,), ("B",))
     _vec(bias, "bias", A, N, A.dtype)
     odt = _out_dtype(A, residual, out_dtype, out)
     if out is None:
@@ -206,15 +214,14 @@ def gated_gemm_train(A: torch.Tensor, Bg: torch.Tensor, Bu: torch.Tensor, bias_g
 
 
 def _preact_pitch(preact, A, M, N):
-    ldz = [_mat(z, "preact[%d]" % i, A, (M, N), A.dtype) for i, z in enumerate(preact)]
-    if len(ldz) != 2 or ldz[0] != ldz[1]:
-        raise ValueError("preact must be two tensors of one row pitch")
-    return ldz[0]
+    if len(preact) != 2:
+        raise ValueError("preact must be the two stored pre-activations")
+    return _one_pitch(preact, ("preact[0]", "preact[1]"), A, (M, N), A.dtype)
 
 
 def _gated_gemm(A, Bg, Bu, bias_g, bias_u, act, out_dtype, out, preact, workspace, stream):
     lib = load_library()
-    M, N, K, lda, (ldbg, ldbu) = _extents(A, (Bg, Bu), ("Bg", "Bu"))
+    M, N, K, lda, ldb = _extents(A, (Bg, Bu), ("Bg", "Bu"))
     _vec(bias_g, "bias_g", A, N, A.dtype)
     _vec(bias_u, "bias_u", A, N, A.dtype)
     odt = _out_dtype(A, None, out_dtype, out)
@@ -224,7 +231,7 @@ def _gated_gemm(A, Bg, Bu, bias_g, bias_u, act, out_dtype, out, preact, workspac
     ldz = 0 if preact[0] is None else _preact_pitch(preact, A, M, N)
     with _on(A.device):
         ws, nws, _keep = _workspace("coalesce_gated_gemm_workspace_size", A.device, M, N, K, workspace, stream)
-        _check(lib.coalesce_gated_gemm(_ptr(A), lda, _ptr(Bg), ldbg, _ptr(Bu), ldbu, _ptr(bias_g), _ptr(bias_u),
+        _check(lib.coalesce_gated_gemm(_ptr(A), lda, _ptr(Bg), _ptr(Bu), ldb, _ptr(bias_g), _ptr(bias_u),
                                        _ptr(preact[0]), _ptr(preact[1]), ldz, _ptr(out), ldy, M, N, K,
                                        _DTYPES[A.dtype], _dtype(out, "out"), _act(act), ws, nws, _stream(stream)))
     return out
@@ -248,7 +255,7 @@ def gemm_residual_backward(A: torch.Tensor, B: torch.Tensor, dout: torch.Tensor,
     A's dtype).  ``preact`` is what gemm_residual_train stored; without an
     activation it is not needed."""
     lib = load_library()
-    M, N, K, lda, (ldb,) = _extents(A, (B,), ("B",))
+    M, N, K, lda, ldb = _extents(A, (B,), ("B",))
     ldd = _mat(dout, "dout", A, (M, N))
     a = _act(act)
     if a != ACT_NONE and preact is None:
@@ -284,27 +291,28 @@ def gated_gemm_backward(A: torch.Tensor, Bg: torch.Tensor, Bu: torch.Tensor,
     float32), from the pre-activations that gated_gemm_train stored: dA in A's
     dtype, dBg, dBu and the bias gradients in ``grad_dtype``."""
     lib = load_library()
-    M, N, K, lda, (ldbg, ldbu) = _extents(A, (Bg, Bu), ("Bg", "Bu"))
+    M, N, K, lda, ldb = _extents(A, (Bg, Bu), ("Bg", "Bu"))
     ldd = _mat(dout, "dout", A, (M, N))
     ldz = _preact_pitch(preact, A, M, N)
-    ldda = 0
-    ldw = [0, 0]
+    ldda = lddb = 0
     dW, db = [None, None], [None, None]
     if want_dA:
         dA, ldda = _grad_out(dA, "dA", A, M, K, A.dtype, stream)
-    for i in range(2):
-        if want_dB:
-            dW[i], ldw[i] = _grad_out(None if dB is None else dB[i], "dB[%d]" % i, A, K, N, grad_dtype, stream)
-        if want_dbias:
-            db[i] = torch.empty(N, dtype=grad_dtype, device=A.device)
-            _used_on(stream, db[i])
+    if want_dB:
+        dW = list(dB) if dB is not None else [_new(K, N, grad_dtype, A.device, stream) for _ in range(2)]
+        if len(dW) != 2:
+            raise ValueError("dB must be two tensors")
+        lddb = _one_pitch(dW, ("dB[0]", "dB[1]"), A, (K, N), grad_dtype)
+    if want_dbias:
+        db = [torch.empty(N, dtype=grad_dtype, device=A.device) for _ in range(2)]
+        _used_on(stream, *db)
     g = GatedGrads(dA if want_dA else None, dW[0], dW[1], db[0], db[1])
     with _on(A.device):
         ws, nws, _keep = _workspace("coalesce_gated_gemm_backward_workspace_size", A.device, M, N, K, workspace,
                                     stream)
-        _check(lib.coalesce_gated_gemm_backward(_ptr(A), lda, _ptr(Bg), ldbg, _ptr(Bu), ldbu, _ptr(preact[0]),
+        _check(lib.coalesce_gated_gemm_backward(_ptr(A), lda, _ptr(Bg), _ptr(Bu), ldb, _ptr(preact[0]),
                                                 _ptr(preact[1]), ldz, _ptr(dout), ldd, _ptr(g.dA), ldda, _ptr(dW[0]),
-                                                ldw[0], _ptr(dW[1]), ldw[1], _ptr(db[0]), _ptr(db[1]), M, N, K,
+                                                _ptr(dW[1]), lddb, _ptr(db[0]), _ptr(db[1]), M, N, K,
                                                 _DTYPES[A.dtype], _dtype(dout, "dout"), _DTYPES[grad_dtype], _act(act),
                                                 ws, nws, _stream(stream)))
     return g

@@ -30,11 +30,11 @@ def residual(**kw):
 
 
 def gated(**kw):
-    a = dict(A=P, lda=K, Bg=2 * P, ldbg=N, Bu=3 * P, ldbu=N, bg=None, bu=None, Zg=None, Zu=None, ldz=N, Y=4 * P, ldy=N,
+    a = dict(A=P, lda=K, Bg=2 * P, Bu=3 * P, ldb=N, bg=None, bu=None, Zg=None, Zu=None, ldz=N, Y=4 * P, ldy=N,
              M=M, N=N, K=K, i=mk.F16, o=mk.F16, act=mk.ACT_SILU, ws=None, n=0)
     a.update(kw)
     return mk.load_library().coalesce_gated_gemm(*[a[k] for k in (
-        "A", "lda", "Bg", "ldbg", "Bu", "ldbu", "bg", "bu", "Zg", "Zu", "ldz", "Y", "ldy", "M", "N", "K", "i", "o",
+        "A", "lda", "Bg", "Bu", "ldb", "bg", "bu", "Zg", "Zu", "ldz", "Y", "ldy", "M", "N", "K", "i", "o",
         "act", "ws", "n")], None)
 
 
@@ -48,20 +48,19 @@ def residual_bwd(**kw):
 
 
 def gated_bwd(**kw):
-    a = dict(A=P, lda=K, Bg=2 * P, ldbg=N, Bu=3 * P, ldbu=N, Zg=4 * P, Zu=5 * P, ldz=N, dY=6 * P, ldd=N, dA=7 * P,
-             ldda=K, dBg=8 * P, lddbg=N, dBu=9 * P, lddbu=N, bg=None, bu=None, M=M, N=N, K=K, i=mk.BF16, d=mk.BF16,
+    a = dict(A=P, lda=K, Bg=2 * P, Bu=3 * P, ldb=N, Zg=4 * P, Zu=5 * P, ldz=N, dY=6 * P, ldd=N, dA=7 * P,
+             ldda=K, dBg=8 * P, dBu=9 * P, lddb=N, bg=None, bu=None, M=M, N=N, K=K, i=mk.BF16, d=mk.BF16,
              g=mk.F32, act=mk.ACT_SILU, ws=16 * P, n=1 << 30)
     a.update(kw)
     return mk.load_library().coalesce_gated_gemm_backward(*[a[k] for k in (
-        "A", "lda", "Bg", "ldbg", "Bu", "ldbu", "Zg", "Zu", "ldz", "dY", "ldd", "dA", "ldda", "dBg", "lddbg", "dBu",
-        "lddbu", "bg", "bu", "M", "N", "K", "i", "d", "g", "act", "ws", "n")], None)
+        "A", "lda", "Bg", "Bu", "ldb", "Zg", "Zu", "ldz", "dY", "ldd", "dA", "ldda", "dBg", "dBu", "lddb", "bg", "bu", "M", "N", "K", "i", "d", "g", "act", "ws", "n")], None)
 
 
 COMMON = [(dict(M=-1), INV), (dict(N=-1), INV), (dict(K=-5), INV), (dict(i=9), INV), (dict(act=5), INV),
           (dict(act=-1), INV), (dict(i=mk.F32), UNS), (dict(M=(1 << 31) - 200), UNS),
           (dict(M=1 << 21, N=1 << 21, ldy=1 << 21, ldz=1 << 21, ldd=1 << 21, ldb=1 << 21), UNS),
           (dict(A=None), INV), (dict(A=P + 8), UNS), (dict(lda=K - 1), INV), (dict(lda=K + 4), UNS),
-          (dict(lda=(1 << 23) + 8), UNS)]
+          (dict(lda=1 << 23), UNS)]
 FORWARD = [(dict(o=mk.F32 + 7), INV), (dict(Y=None), INV), (dict(Y=4 * P + 4), UNS), (dict(ldy=N - 8), INV),
            (dict(ldy=N + 4), UNS), (dict(Y=P + 16), INV)]
 
@@ -78,7 +77,7 @@ def test_residual_refuses(kw, status):
 
 @pytest.mark.parametrize("kw,status", COMMON + FORWARD + [
     (dict(o=mk.BF16), UNS), (dict(Bg=None), INV), (dict(Bu=None), INV), (dict(Bu=3 * P + 4), UNS),
-    (dict(ldbu=N - 8), INV), (dict(Zg=5 * P), INV), (dict(Zu=5 * P), INV), (dict(Zg=5 * P, Zu=5 * P), INV),
+    (dict(ldb=N - 8), INV), (dict(Zg=5 * P), INV), (dict(Zu=5 * P), INV), (dict(Zg=5 * P, Zu=5 * P), INV),
     (dict(Zg=5 * P, Zu=5 * P + 16), INV), (dict(Zg=5 * P, Zu=4 * P), INV), (dict(bu=5 * P + 2), UNS)])
 def test_gated_refuses(kw, status):
     assert gated(**kw) == status
@@ -96,7 +95,7 @@ def test_residual_backward_refuses(kw, status):
 @pytest.mark.parametrize("kw,status", COMMON + [
     (dict(d=mk.F16), UNS), (dict(g=mk.F16), UNS), (dict(Bu=None), INV), (dict(Zu=None), INV), (dict(dY=None), INV),
     (dict(dBu=8 * P), INV), (dict(dBu=8 * P + 16), INV), (dict(dBg=6 * P), INV), (dict(dA=4 * P), INV),
-    (dict(bg=10 * P, bu=10 * P), INV), (dict(lddbu=N - 4), INV)])
+    (dict(bg=10 * P, bu=10 * P), INV), (dict(lddb=N - 4), INV)])
 def test_gated_backward_refuses(kw, status):
     assert gated_bwd(**kw) == status
 
@@ -106,8 +105,8 @@ def test_accepted_requests_reach_the_device():
     assert residual(R=None, ldr=0) == DEV and residual(R=4 * P) == DEV           # none, in place
     assert residual(i=mk.F16, o=mk.F32) == DEV and gated(Zg=5 * P, Zu=6 * P) == DEV
     # halves of one matrix: weights, their gradients, the stored pre-activations
-    assert gated(Bu=2 * P + 2 * N, ldbg=2 * N, ldbu=2 * N, Zg=5 * P, Zu=5 * P + 2 * N, ldz=2 * N) == DEV
-    assert gated_bwd(dBu=8 * P + 4 * N, lddbg=2 * N, lddbu=2 * N) == DEV
+    assert gated(Bu=2 * P + 2 * N, ldb=2 * N, Zg=5 * P, Zu=5 * P + 2 * N, ldz=2 * N) == DEV
+    assert gated_bwd(dBu=8 * P + 4 * N, lddb=2 * N) == DEV
     # unwanted gradients need no matching inputs
     assert residual_bwd(dA=None, B=None) == DEV and residual_bwd(dB=None, A=None) == DEV
     assert residual_bwd(act=mk.ACT_NONE, Z=None) == DEV
