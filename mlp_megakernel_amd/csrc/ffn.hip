@@ -6,16 +6,6 @@
 namespace coalesce {
 namespace {
 
-__device__ __forceinline__ float act_any(int act, float z) {
-  switch (act) {
-    case ACT_GELU: return gelu_erf(z);
-    case ACT_SOFTPLUS: return softplus_guarded(z);
-    case ACT_RELU: return relu(z);
-    case ACT_SILU: return silu(z);
-    default: return z;
-  }
-}
-
 // Four consecutive columns of one row per thread and iteration; the ranges are
 // added in order, so the result does not depend on timing.
 template <typename T, typename TO, int KIND>
@@ -30,9 +20,16 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineOp c) {
 #pragma unroll
     for (int i = 0; i < (KIND == COMBINE_GATED ? 2 : 1); ++i) {
       const float* p = c.P[i + i0] + m * c.ldp + n;
-      f32x4 s = *(const f32x4*)p;
-#pragma unroll 4
-      for (int k = 1; k < c.splits; ++k) s += *(const f32x4*)(p + (int64_t)k * c.split_stride);
+      // eight loads in flight: the results come from other XCDs' writes
+      f32x4 s = (f32x4){0.f, 0.f, 0.f, 0.f};
+      for (int k = 0; k < c.splits; k += 8) {
+        f32x4 v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          v[u] = k + u < c.splits ? *(const f32x4*)(p + (int64_t)(k + u) * c.split_stride) : (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int u = 0; u < 8; ++u) s += v[u];
+      }
       acc[i] = s;
     }
     if constexpr (KIND == COMBINE_STORE) {
@@ -81,7 +78,7 @@ hipError_t launch_combine(const CombineOp& c, CombineKind kind, DType in, DType 
 }
 
 size_t ffn_forward_workspace(int64_t M, int64_t N, int64_t K, bool gated, int num_cus) {
-  return partial_bytes(plan_tiles(M, N, gated, 1, (K + 63) / 64, num_cus), M, N, gated ? 2 : 1);
+  return partial_bytes(plan_forward(M, N, K, gated, num_cus).tiles, M, N, gated ? 2 : 1);
 }
 
 hipError_t launch_ffn_forward(const FfnParams& p, bool gated, DType in, DType out, int act, hipStream_t stream,

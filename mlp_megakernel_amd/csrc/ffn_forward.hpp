@@ -7,6 +7,7 @@
 // (unless a training forward asks for the pre-activations).  Compiled per
 // input type and operator (ffn_gated_*.hip, ffn_resid_*.hip).
 #pragma once
+#include "ffn_few.hpp"
 #include "ffn_plan.hpp"
 #include "gemm16_core.hpp"
 
@@ -103,7 +104,11 @@ hipError_t forward_typed(const FfnParams& p, DType in, DType out, int act, hipSt
   o.ldz = p.ldz;
   o.Y[0] = p.Y;
   o.ldy = p.ldy;
-  const TilePlan plan = plan_tiles(p.M, p.N, EPI == EPI_GATED, 1, ((int64_t)p.K + BK - 1) / BK, num_cus);
+  o.act = act;
+  const ForwardPlan f = plan_forward(p.M, p.N, p.K, EPI == EPI_GATED, num_cus);
+  if (f.strip)
+    return out == DT_F32 ? launch_few<T, float, EPI>(o, f.strip, stream) : launch_few<T, T, EPI>(o, f.strip, stream);
+  const TilePlan& plan = f.tiles;
   o.splits = plan.splits;
   if (plan.splits > 1)
     return forward_split<T, EPI>(o, plan.variant, in, out, act, stream, num_cus, (float*)workspace);

@@ -17,6 +17,7 @@ size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 // steps are split.
 struct TilePlan {
   int variant, splits;
+  double ns;  // estimated time
 };
 
 // The plan with the smallest estimated time.  A launch is `units` workgroup
@@ -25,35 +26,71 @@ struct TilePlan {
 // (ns; measured over products of 512 to 16384 rows and columns, bf16).  A tile
 // has a fixed cost beside its K steps (the first copies, the epilogue), a
 // split product writes and reads its fp32 partial results once more (at about
-// 3 TB/s) in a second launch.
+// 6 TB/s, mostly caches) in a second launch; and reading the operands from memory takes its time
+// too: 4.5 TB/s with three or more tiles on each compute unit, 4.0 and 3.0 with
+// two and one, in proportion below.
 TilePlan plan_tiles(int64_t m, int64_t n, bool gated, int batch, int64_t ksteps, int num_cus) {
   static const int slots[2][3] = {{1, 2, 4}, {1, 2, 3}};
   static const double step[2][3][4] = {{{1500}, {780, 1200}, {550, 570, 720, 850}},
                                        {{1450}, {740, 1050}, {650, 700, 950}}};
   static const double fixed[3] = {6000, 4000, 3000};
-  TilePlan best{3, 1};
-  double best_t = 1e300;
+  static const int ranges[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
+  const double operand_bytes = (double)ksteps * 128.0 * ((double)m + (double)n * (gated ? 2 : batch));
+  TilePlan best{3, 1, 1e300};
   for (int v = 1; v <= 3; ++v) {
     const int bm = v == 1 ? 256 : v == 2 ? 128 : 64;
     const int bn = !gated ? bm : v == 1 ? 128 : 64;
     const int64_t tiles = ((m + bm - 1) / bm) * ((n + bn - 1) / bn) * batch;
     const int per_cu = slots[gated][v - 1];
-    for (int splits = 1; splits <= 64; ++splits) {
+    for (int splits : ranges) {
       if (splits > 1 && (v == 1 || ksteps / splits < 4)) break;
       const int64_t units = tiles * splits;
       const int64_t rounds = units / ((int64_t)num_cus * per_cu), rest = units - rounds * num_cus * per_cu;
       const int in_rest = (int)((rest + num_cus - 1) / num_cus);  // 0 .. per_cu
       double t = (double)rounds * step[gated][v - 1][per_cu - 1] + (in_rest ? step[gated][v - 1][in_rest - 1] : 0.0);
-      t = t * (double)((ksteps + splits - 1) / splits) + ((double)rounds + (in_rest > 0)) * fixed[v - 1];
-      if (splits > 1) t += 4000 + (double)splits * (double)m * (double)n * (gated ? 2 : batch) * 8.0 / 3000.0;
-      if (t < best_t) {
-        best_t = t;
-        best = {v, splits};
-      }
+      const double load = (double)units / num_cus;
+      const double gb = load >= 3 ? 4500 : load >= 2 ? 4000 : load >= 1 ? 3000 : 3000 * load;
+      t = std::max(t * (double)((ksteps + splits - 1) / splits), operand_bytes / gb) +
+          ((double)rounds + (in_rest > 0)) * fixed[v - 1];
+      if (splits > 1) t += 4000 + (double)splits * (double)m * (double)n * (gated ? 2 : batch) * 8.0 / 6000.0;
+      if (t < best.ns) best = {v, splits, t};
       if (units > 2 * (int64_t)num_cus * per_cu) break;
     }
   }
   return best;
+}
+
+// The forward's plan: the few-row kernel with strips of `strip` columns, or (0)
+// a tile plan.  The few-row kernel is bound by the reading of the weights, at
+// 4.8 TB/s of whole 128-byte lines (strips of 64 columns; narrower ones draw
+// 1.5 and 2 times the bytes), or by what one compute unit requests: about 3.5,
+// 3.0 and 2.6 ns per row of a strip, which is a line or part of one, and X's
+// rows add to that.  Measured, one token: gated 4096 x 16384 58 us against 62 of
+// split tiles, 2048 x 5464 16.4 (strips of 32) against 20.8, 1001 x 2736 6.7
+// (16) against 11.6; but 4096 x 4096, whose 64 strips leave most compute units
+// idle, 29 to 36 against 22.8.
+struct ForwardPlan {
+  int strip;
+  TilePlan tiles;
+};
+ForwardPlan plan_forward(int64_t m, int64_t n, int64_t k, bool gated, int num_cus) {
+  ForwardPlan f{0, plan_tiles(m, n, gated, 1, (k + 63) / 64, num_cus)};
+  if (m > 64) return f;
+  static const double row_ns[3] = {3.5, 3.0, 2.6}, waste[3] = {1.0, 1.5, 2.0};
+  const double nb = gated ? 2.0 : 1.0;
+  double best = f.tiles.ns;
+  for (int i = 0; i < 3; ++i) {
+    const int strip = 64 >> i;
+    const int64_t strips = (n + strip - 1) / strip, rounds = (strips + num_cus - 1) / num_cus;
+    const double t = 2700.0 + std::max((double)k * (double)n * 2.0 * nb * waste[i] / 4800.0,
+                                       (double)rounds * (double)k * (nb + (double)m / 64.0) * row_ns[i]);
+    if (t < best) {
+      best = t;
+      f.strip = strip;
+    }
+  }
+  if (f.strip) f.tiles.splits = 1;
+  return f;
 }
 
 // Partial results of a split product: fp32 matrices of pitch ldp, range after

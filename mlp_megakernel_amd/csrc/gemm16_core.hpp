@@ -118,6 +118,18 @@ __device__ __forceinline__ f32x4 load4(const T* src, int valid) {
   return v;
 }
 
+// The activation of a launch argument, where a kernel is not compiled per
+// activation.
+__device__ __forceinline__ float act_any(int act, float z) {
+  switch (act) {
+    case ACT_GELU: return gelu_erf(z);
+    case ACT_SOFTPLUS: return softplus_guarded(z);
+    case ACT_RELU: return relu(z);
+    case ACT_SILU: return silu(z);
+    default: return z;
+  }
+}
+
 // Swizzle of an epilogue staging row of ROWB bytes (64, 128 or 256), in
 // 16-byte chunks: both the 8-byte writes of 16 rows and the 16-byte
 // row-contiguous reads spread over the banks.
@@ -255,8 +267,11 @@ __device__ __forceinline__ Args fresh(Args k) {
 struct TileAt {
   int m0, n0;   // first row and output column
   int pair;     // product of a batch of two
-  int s0, ns;   // first K step (over all segments) and number of steps
   int split;
+  int s0, s1;   // range of K steps over all segments
+};
+struct Range1 {
+  int s, n;  // first K step and number of steps in one segment
 };
 
 template <typename G>
@@ -268,7 +283,6 @@ struct TileFrags {
 // SEGS = 2: the K loop runs over two products, a[0] b[0] + a[1] b[1].
 template <typename T, typename TO, Lay LA, Lay LB, int SEGS, int EPI, int ACT, typename G>
 struct Tile {
-  static constexpr int NA = SEGS, NB = SEGS * G::NSUB;  // matrices on either side
   static constexpr int RA = CopyRows<LA, G::BM>::N, RB = CopyRows<LB, G::SUBN>::N;
   static_assert(SEGS == 1 || G::NSUB == 1, "segments of a gated product are not implemented");
 
@@ -277,8 +291,8 @@ struct Tile {
   // the size of a full K step's part of the matrix (the buffer's range: rows
   // or columns outside the matrix lie past it or are never stored).
   struct Hot {
-    const char* a[NA];
-    const char* b[NB];
+    const char* a;
+    const char* b[G::NSUB];
     int64_t ka, kb;
     uint32_t ra, rb, na, nb;
     int K;
@@ -290,7 +304,7 @@ struct Tile {
   // Sources of one K step.
   struct Step {
     u32x4 a, b[G::NSUB];
-    int seg, k0;
+    int k0;
   };
 
   static __device__ __forceinline__ Side side_a(Args p, const TileAt& at, int seg) {
@@ -309,7 +323,7 @@ struct Tile {
     else
       return (uint32_t)((BK - 1) * s.ld + ((x + 7) & ~7)) * (uint32_t)sizeof(T);
   }
-  static __device__ __forceinline__ Hot hot(Args k, const TileAt& at) {
+  static __device__ __forceinline__ Hot hot(Args k, const TileAt& at, int seg) {
     const Args p = fresh(k);
     Hot h;
     h.K = p->K;
@@ -317,15 +331,12 @@ struct Tile {
     h.rb = (uint32_t)(RB * p->ldb * (int)sizeof(T));
     h.ka = (LA == LAY_K ? 1 : p->lda) * (int64_t)sizeof(T);
     h.kb = (LB == LAY_K ? 1 : p->ldb) * (int64_t)sizeof(T);
+    const Side sa = side_a(p, at, seg);
+    h.a = (const char*)((const T*)sa.p + (LA == LAY_K ? sa.x0 * sa.ld : (int64_t)sa.x0));
+    h.na = step_bytes<LA, G::BM>(sa);
 #pragma unroll
-    for (int i = 0; i < NA; ++i) {
-      const Side s = side_a(p, at, i);
-      h.a[i] = (const char*)((const T*)s.p + (LA == LAY_K ? s.x0 * s.ld : (int64_t)s.x0));
-      h.na = step_bytes<LA, G::BM>(s);
-    }
-#pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      const Side s = side_b(p, at, i, i);
+    for (int i = 0; i < G::NSUB; ++i) {
+      const Side s = side_b(p, at, seg, i);
       h.b[i] = (const char*)((const T*)s.p + (LB == LAY_K ? s.x0 * s.ld : (int64_t)s.x0));
       h.nb = step_bytes<LB, G::SUBN>(s);
     }
@@ -341,17 +352,10 @@ struct Tile {
   }
   static __device__ __forceinline__ Step step_at(const Hot& h, int s) {
     Step t;
-    t.seg = 0;
     t.k0 = s * BK;
-    if constexpr (SEGS == 2) {
-      const int kt = (h.K + BK - 1) / BK;
-      t.seg = s >= kt ? 1 : 0;
-      t.k0 = (s - t.seg * kt) * BK;
-    }
-    t.a = rsrc((SEGS == 2 && t.seg ? h.a[NA - 1] : h.a[0]) + t.k0 * h.ka, h.na);
+    t.a = rsrc(h.a + t.k0 * h.ka, h.na);
 #pragma unroll
-    for (int i = 0; i < G::NSUB; ++i)
-      t.b[i] = rsrc((SEGS == 2 && t.seg ? h.b[NB - 1] : h.b[i]) + t.k0 * h.kb, h.nb);
+    for (int i = 0; i < G::NSUB; ++i) t.b[i] = rsrc(h.b[i] + t.k0 * h.kb, h.nb);
     return t;
   }
 
@@ -403,19 +407,20 @@ struct Tile {
     }
   }
 
-  static __device__ __forceinline__ void tail(Args k, const TileAt& at, const Step& st, T* a, T* b, int w, int lane) {
+  static __device__ __forceinline__ void tail(Args k, const TileAt& at, int seg, const Step& st, T* a, T* b, int w,
+                                              int lane) {
     // the lane through an opaque copy: the addresses are formed here, not
     // carried in registers through the K loop
     asm volatile("" : "+v"(lane));
     const Args p = fresh(k);
     const int K = p->K;
     i16x8 ra[G::CA], rb[G::CB];
-    const Side sa = side_a(p, at, st.seg);
+    const Side sa = side_a(p, at, seg);
 #pragma unroll
     for (int j = 0; j < G::CA; ++j) ra[j] = tail_chunk<T, LA, G::BM>(sa, w * G::CA + j, lane, st.k0, K);
 #pragma unroll
     for (int j = 0; j < G::CB; ++j)
-      rb[j] = tail_chunk<T, LB, G::SUBN>(side_b(p, at, st.seg, j / G::CBS), w * G::CBS + j % G::CBS, lane, st.k0, K);
+      rb[j] = tail_chunk<T, LB, G::SUBN>(side_b(p, at, seg, j / G::CBS), w * G::CBS + j % G::CBS, lane, st.k0, K);
 #pragma unroll
     for (int j = 0; j < G::CA; ++j) *(i16x8*)(a + (w * G::CA + j) * 512 + lane * 8) = ra[j];
 #pragma unroll
@@ -423,15 +428,15 @@ struct Tile {
       *(i16x8*)(b + (j / G::CBS) * G::SUBN * BK + (w * G::CBS + j % G::CBS) * 512 + lane * 8) = rb[j];
   }
 
-  // K step s, all copies at once (a tile's first two steps).
-  static __device__ __forceinline__ void fill(Args k, const TileAt& at, const Hot& h, const Pats& pt, int s, T* a, T* b,
-                                              int wu, int lane) {
+  // K step s, all copies at once (a segment's first two steps).
+  static __device__ __forceinline__ void fill(Args k, const TileAt& at, int seg, const Hot& h, const Pats& pt, int s,
+                                              T* a, T* b, int wu, int lane) {
     const Step st = step_at(h, s);
     if (st.k0 + BK <= h.K) {
 #pragma unroll
       for (int j = 0; j < G::C; ++j) copy(h, pt, st, j, a, b, wu);
     } else {
-      tail(k, at, st, a, b, wu, lane);
+      tail(k, at, seg, st, a, b, wu, lane);
     }
   }
 
@@ -626,8 +631,15 @@ struct Tile {
     at.n0 = (tn - at.pair * p->tiles_n) * G::ON;
     const int64_t total = (int64_t)((p->K + BK - 1) / BK) * SEGS;
     at.s0 = (int)(total * at.split / p->splits);
-    at.ns = (int)(total * (at.split + 1) / p->splits) - at.s0;
+    at.s1 = (int)(total * (at.split + 1) / p->splits);
     return at;
+  }
+  // The part of the tile's K steps that lies in a segment.
+  static __device__ __forceinline__ Range1 part(const TileAt& at, const Hot& h, int seg) {
+    if constexpr (SEGS == 1) return Range1{at.s0, at.s1 - at.s0};
+    const int kt = (h.K + BK - 1) / BK;
+    const int lo = max(at.s0 - seg * kt, 0), hi = min(at.s1 - seg * kt, kt);
+    return Range1{lo, max(hi - lo, 0)};
   }
 
   static __device__ __forceinline__ void run(Args k, T* lds) {
@@ -644,10 +656,11 @@ struct Tile {
     const int wm = wu % G::WGM, wn = wu / G::WGM;
 
     TileAt at = locate(k, v);
-    Hot h = hot(k, at);
+    Hot h = hot(k, at, 0);
+    Range1 r = part(at, h, 0);
     const Pats pt = patterns(k, wu, lane0);
-    if (at.ns > 0) fill(k, at, h, pt, at.s0, a0, b0, wu, lane0);
-    if (at.ns > 1) fill(k, at, h, pt, at.s0 + 1, a1, b1, wu, lane0);
+    if (r.n > 0) fill(k, at, 0, h, pt, r.s, a0, b0, wu, lane0);
+    if (r.n > 1) fill(k, at, 0, h, pt, r.s + 1, a1, b1, wu, lane0);
     while (true) {
       // the lane index through an opaque copy: everything derived from it is
       // recomputed per tile instead of being held across the K loop
@@ -658,41 +671,53 @@ struct Tile {
       for (int t = 0; t < G::NT; ++t)
 #pragma unroll
         for (int s = 0; s < G::MT; ++s) acc[t][s] = (f32x4){0.f, 0.f, 0.f, 0.f};
-      TileFrags<G> f0, f1;
-      if (at.ns > 0) {
-        wait_vmcnt0();
-        __syncthreads();
+      // One pass of the pipeline per segment (a second one refills the stages:
+      // one exposed latency per tile, against pointers of both segments in the
+      // loop, which cost it 15 % through spilled registers).
+      for (int seg = 0; seg < SEGS; ++seg) {
+        if (seg > 0) {
+          h = hot(k, at, seg);
+          r = part(at, h, seg);
+          __syncthreads();  // every wave is past its last fragment read
+          if (r.n > 0) fill(k, at, seg, h, pt, r.s, a0, b0, wu, lane);
+          if (r.n > 1) fill(k, at, seg, h, pt, r.s + 1, a1, b1, wu, lane);
+        }
+        TileFrags<G> f0, f1;
+        if (r.n > 0) {
+          wait_vmcnt0();
+          __syncthreads();
 #pragma unroll
-        for (int i = 0; i < G::NT; ++i) f0.n[i] = frag_n(b0, 0, wn, i, lane);
+          for (int i = 0; i < G::NT; ++i) f0.n[i] = frag_n(b0, 0, wn, i, lane);
 #pragma unroll
-        for (int i = 0; i < G::MT; ++i) f0.m[i] = frag_m(a0, 0, wm, i, lane);
-      }
-      // Per K step k (stage cur; the other stage holds step k + 1 or is
-      // filling): slice 0 on f0 while f1 is read; barrier (cur is free, step
-      // k + 1 has landed); slice 1 on f1 while step k + 2 is copied into cur
-      // and f0 of step k + 1 is read.
-      for (int kt = 0; kt < at.ns; kt += 2) {
+          for (int i = 0; i < G::MT; ++i) f0.m[i] = frag_m(a0, 0, wm, i, lane);
+        }
+        // Per K step k (stage cur; the other stage holds step k + 1 or is
+        // filling): slice 0 on f0 while f1 is read; barrier (cur is free, step
+        // k + 1 has landed); slice 1 on f1 while step k + 2 is copied into cur
+        // and f0 of step k + 1 is read.
+        for (int kt = 0; kt < r.n; kt += 2) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int i = kt + half;
-          if (i < at.ns) {
-            T* const ca = half ? a1 : a0;
-            T* const cb = half ? b1 : b0;
-            T* const na = half ? a0 : a1;
-            T* const nb = half ? b0 : b1;
-            Step st{};
-            slice(f0, acc, f1, ca, cb, 1, wm, wn, lane, false, h, pt, st, ca, cb, wu);
-            if (i + 1 < at.ns) {
-              wait_vmcnt0();
-              __syncthreads();
+          for (int half = 0; half < 2; ++half) {
+            const int i = kt + half;
+            if (i < r.n) {
+              T* const ca = half ? a1 : a0;
+              T* const cb = half ? b1 : b0;
+              T* const na = half ? a0 : a1;
+              T* const nb = half ? b0 : b1;
+              Step st{};
+              slice(f0, acc, f1, ca, cb, 1, wm, wn, lane, false, h, pt, st, ca, cb, wu);
+              if (i + 1 < r.n) {
+                wait_vmcnt0();
+                __syncthreads();
+              }
+              bool cp = false;
+              if (i + 2 < r.n) {
+                st = step_at(h, r.s + i + 2);
+                cp = st.k0 + BK <= h.K;
+                if (!cp) tail(k, at, seg, st, ca, cb, wu, lane);
+              }
+              slice(f1, acc, f0, na, nb, 0, wm, wn, lane, cp, h, pt, st, ca, cb, wu);
             }
-            bool cp = false;
-            if (i + 2 < at.ns) {
-              st = step_at(h, at.s0 + i + 2);
-              cp = st.k0 + BK <= h.K;
-              if (!cp) tail(k, at, st, ca, cb, wu, lane);
-            }
-            slice(f1, acc, f0, na, nb, 0, wm, wn, lane, cp, h, pt, st, ca, cb, wu);
           }
         }
       }
@@ -702,9 +727,10 @@ struct Tile {
       v += gridDim.x;
       if (v >= total) break;
       at = locate(k, v);
-      h = hot(k, at);
-      if (at.ns > 0) fill(k, at, h, pt, at.s0, a0, b0, wu, lane);
-      if (at.ns > 1) fill(k, at, h, pt, at.s0 + 1, a1, b1, wu, lane);
+      h = hot(k, at, 0);
+      r = part(at, h, 0);
+      if (r.n > 0) fill(k, at, 0, h, pt, r.s, a0, b0, wu, lane);
+      if (r.n > 1) fill(k, at, 0, h, pt, r.s + 1, a1, b1, wu, lane);
     }
   }
 };

@@ -153,7 +153,9 @@ __global__ __launch_bounds__(THREADS) void scale_kernel(ClipTable t, const doubl
   const double q = max_norm / (total + 1e-6);
   const float coef = q < 1.0 || q != q ? (float)q : 1.0f;
   const int64_t chunks = t.chunk_end[t.count - 1];
-  for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+  // from the list's end to its start: what the first sweep read last may still
+  // be in the 256 MB cache
+  for (int64_t c = chunks - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
     const int i = find_tensor(t, c);
     if (coef == 1.0f && t.src[i] == t.dst[i]) continue;  // in place and nothing to scale
     const int64_t e0 = (c - (i ? t.chunk_end[i - 1] : 0)) * t.chunk;

@@ -177,6 +177,7 @@ struct TileOp {
   int64_t ldz;
   void* Y[2];
   int64_t ldy;
+  int act;                        // for kernels that are not compiled per activation
   int tiles_m, tiles_n, group_m;  // set by the launcher
 };
 

@@ -6,17 +6,14 @@ run there, on ``stream`` or that device's current stream.
 """
 from __future__ import annotations
 
-import contextlib
-import ctypes
+import array
 import math
 from typing import NamedTuple, Optional, Sequence, Tuple
 
 import torch
 
-from . import (ACT_NONE, NORM_2, NORM_INF, _ACTS, _DTYPES, _c_array, _check, _matrix, _ptr, _stream, aligned_copy,
-               aligned_empty, load_library)
-
-_i64, _i32, _vp = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p
+from . import (ACT_NONE, NORM_2, NORM_INF, _ACTS, _DTYPES, _check, _matrix, _ptr, _raw_current_stream, _stream,
+               aligned_copy, load_library)
 
 
 class GemmGrads(NamedTuple):
@@ -35,12 +32,15 @@ class GatedGrads(NamedTuple):
     dbias_u: Optional[torch.Tensor]
 
 
-_NO_GUARD = contextlib.nullcontext()
+def _current_device() -> int:
+    return torch._C._cuda_getDevice() if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device()
 
 
-def _on(device: torch.device):
-    """Context in which `device` is the current one."""
-    return _NO_GUARD if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+def _raw_stream(stream, dev: int):
+    """The raw handle of `stream`, or of device dev's current stream."""
+    if stream is None and _raw_current_stream is not None:
+        return _raw_current_stream(dev)
+    return _stream(stream)
 
 
 def _used_on(stream, *tensors):
@@ -60,87 +60,89 @@ def _act(act):
     return _ACTS[act]
 
 
-def _dtype(t: torch.Tensor, name: str):
-    if t.dtype not in _DTYPES:
-        raise ValueError("%s must be float32, float16 or bfloat16" % name)
-    return _DTYPES[t.dtype]
+def _first(A: torch.Tensor):
+    """(rows, cols, pitch, device) of the operand that the others go by."""
+    rows, cols, ld = _matrix(A, "A")
+    if A.dtype not in _DTYPES:
+        raise ValueError("A must be float16 or bfloat16")
+    return rows, cols, ld if rows > 1 else _row_pitch(cols, A.dtype), A.get_device()
 
 
-def _pitched(t: torch.Tensor, name: str):
-    """(rows, cols, ld) as _matrix gives them; a single row has no pitch, so
-    one of any length gets the next multiple of 16 bytes."""
-    rows, cols, ld = _matrix(t, name)
-    if rows <= 1:
-        per = 16 // t.element_size()
-        ld = max(per, (cols + per - 1) // per * per)
-    return rows, cols, ld
+def _row_pitch(cols: int, dtype: torch.dtype) -> int:
+    """A single row has no pitch: it gets the next multiple of 16 bytes."""
+    return max(4, (cols + 3) & -4) if dtype is torch.float32 else max(8, (cols + 7) & -8)
 
 
-def _mat(t: torch.Tensor, name: str, like: torch.Tensor, shape=None, dtype=None):
-    """The pitch of a 2-D operand on like's device, of the given shape and type."""
-    rows, cols, ld = _pitched(t, name)
-    if t.device != like.device:
-        raise ValueError("%s is on %s, not on %s" % (name, t.device, like.device))
-    if shape is not None and (rows, cols) != shape:
-        raise ValueError("%s must be %d x %d" % ((name,) + shape))
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError("%s must be %s" % (name, dtype))
+def _mat(t: torch.Tensor, name: str, rows: int, cols: int, dtype: torch.dtype, dev: int) -> int:
+    """The pitch of a rows x cols operand of `dtype` on device dev (checks only
+    what a call needs, in the order that costs least)."""
+    if t.shape != (rows, cols) or t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError("%s must be a %d x %d tensor of %s on GPU %d, not %s of %s on %s" % (
+            name, rows, cols, dtype, dev, tuple(t.shape), t.dtype, t.device))
+    st = t.stride()
+    if cols > 1 and st[1] != 1:
+        raise ValueError("%s must have unit inner stride (row-major)" % name)
+    return st[0] if rows > 1 else _row_pitch(cols, dtype)
+
+
+def _vec(t: Optional[torch.Tensor], name: str, n: int, dtype: torch.dtype, dev: int):
+    if t is not None and (t.shape != (n,) or t.dtype is not dtype or not t.is_contiguous() or t.get_device() != dev):
+        raise ValueError("%s must be a contiguous length-%d vector of %s on GPU %d" % (name, n, dtype, dev))
+
+
+def _one_pitch(ts, names, rows: int, cols: int, dtype: torch.dtype, dev: int) -> int:
+    """The pitch that two tensors of one shape and type share."""
+    if len(ts) != 2:
+        raise ValueError("%s must be two tensors" % " and ".join(names))
+    ld = _mat(ts[0], names[0], rows, cols, dtype, dev)
+    if _mat(ts[1], names[1], rows, cols, dtype, dev) != ld:
+        raise ValueError("%s must have one row pitch" % " and ".join(names))
     return ld
 
 
-def _vec(t: Optional[torch.Tensor], name: str, like: torch.Tensor, n: int, dtype):
-    if t is None:
-        return
-    if t.dim() != 1 or t.shape[0] != n or t.dtype != dtype or not t.is_contiguous() or t.device != like.device:
-        raise ValueError("%s must be a contiguous length-%d vector of %s on %s" % (name, n, dtype, like.device))
-
-
-def _extents(A: torch.Tensor, Bs, names):
-    M, K, lda = _pitched(A, "A")
-    if A.dtype not in _DTYPES:
-        raise ValueError("A must be float16 or bfloat16")
-    N = Bs[0].shape[1] if Bs[0].dim() == 2 else -1
-    return M, N, K, lda, _one_pitch(Bs, names, A, (K, N), A.dtype)
-
-
-def _one_pitch(ts, names, like, shape, dtype):
-    """The pitch that tensors of one shape and type share."""
-    ld = [_mat(t, n, like, shape, dtype) for t, n in zip(ts, names)]
-    if any(x != ld[0] for x in ld):
-        raise ValueError("%s must have one row pitch" % " and ".join(names))
-    return ld[0]
+def _cols(B: torch.Tensor, name: str) -> int:
+    if B.dim() != 2:
+        raise ValueError("%s must be 2-D" % name)
+    return B.shape[1]
 
 
 # Workspace sizes by (function, extents, device): a user's shapes repeat.
 _ws_sizes = {}
 
 
-def _workspace(name: str, device: torch.device, M: int, N: int, K: int, workspace, stream):
-    key = (name, M, N, K, device.index)
+def _workspace(name: str, dev: int, M: int, N: int, K: int, workspace, stream):
+    key = (name, M, N, K, dev)
     need = _ws_sizes.get(key)
     if need is None:
         if len(_ws_sizes) >= 4096:
             _ws_sizes.clear()
         need = _ws_sizes[key] = int(getattr(load_library(), name)(M, N, K))
-    return _take(workspace, need, device, stream)
+    return _take(workspace, need, dev, stream)
 
 
-def _take(workspace, need: int, device: torch.device, stream):
+def _take(workspace, need: int, dev: int, stream):
     """(pointer, bytes, tensor to keep alive) of the workspace given, or of one made here."""
     if workspace is None:
         if need == 0:
             return None, 0, None
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        workspace = torch.empty(need, dtype=torch.uint8, device="cuda")  # the current device is dev here
         _used_on(stream, workspace)
-    elif workspace.device != device or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on %s" % device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on GPU %d" % dev)
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 def _new(rows: int, cols: int, dtype, device, stream):
-    t = aligned_empty(rows, cols, dtype, device)
+    ld = _row_pitch(cols, dtype)
+    t = torch.empty((rows, ld), dtype=dtype, device=device)
     _used_on(stream, t)
-    return t
+    return t if ld == cols else t[:, :cols]
+
+
+def _there(dev: int, call, *args):
+    """call(*args) with device dev, not the current one, made current."""
+    with torch.cuda.device(dev):
+        return call(*args)
 
 
 def gemm_residual(A: torch.Tensor, B: torch.Tensor, residual: Optional[torch.Tensor] = None,
@@ -173,20 +175,23 @@ def _out_dtype(A, residual, out_dtype, out):
 
 
 def _gemm_residual(A, B, residual, bias, act, out_dtype, out, preact, workspace, stream):
-    lib = load_library()
-    M, N, K, lda, ldb = _extents(A, (B,), ("B",))
-    _vec(bias, "bias", A, N, A.dtype)
+    M, K, lda, dev = _first(A)
+    if _current_device() != dev:
+        return _there(dev, _gemm_residual, A, B, residual, bias, act, out_dtype, out, preact, workspace, stream)
+    N, dt = _cols(B, "B"), A.dtype
+    ldb = _mat(B, "B", K, N, dt, dev)
+    if bias is not None:
+        _vec(bias, "bias", N, dt, dev)
     odt = _out_dtype(A, residual, out_dtype, out)
     if out is None:
         out = _new(M, N, odt, A.device, stream)
-    ldy = _mat(out, "out", A, (M, N), odt)
-    ldr = 0 if residual is None else _mat(residual, "residual", A, (M, N), odt)
-    ldz = 0 if preact is None else _mat(preact, "preact", A, (M, N), A.dtype)
-    with _on(A.device):
-        ws, nws, _keep = _workspace("coalesce_gemm_residual_workspace_size", A.device, M, N, K, workspace, stream)
-        _check(lib.coalesce_gemm_residual(_ptr(A), lda, _ptr(B), ldb, _ptr(bias), _ptr(residual), ldr, _ptr(preact),
-                                          ldz, _ptr(out), ldy, M, N, K, _DTYPES[A.dtype], _dtype(out, "out"),
-                                          _act(act), ws, nws, _stream(stream)))
+    ldy = _mat(out, "out", M, N, odt, dev)
+    ldr = 0 if residual is None else _mat(residual, "residual", M, N, odt, dev)
+    ldz = 0 if preact is None else _mat(preact, "preact", M, N, dt, dev)
+    ws, nws, _keep = _workspace("coalesce_gemm_residual_workspace_size", dev, M, N, K, workspace, stream)
+    _check(load_library().coalesce_gemm_residual(
+        A.data_ptr(), lda, B.data_ptr(), ldb, _ptr(bias), _ptr(residual), ldr, _ptr(preact), ldz, out.data_ptr(), ldy, M,
+        N, K, _DTYPES[dt], _DTYPES[odt], _act(act), ws, nws, _raw_stream(stream, dev)))
     return out
 
 
@@ -197,7 +202,7 @@ def gated_gemm(A: torch.Tensor, Bg: torch.Tensor, Bu: torch.Tensor, bias_g: Opti
 
     Bg and Bu may be the two halves ``W[:, :N]`` and ``W[:, N:]`` of one matrix.
     """
-    return _gated_gemm(A, Bg, Bu, bias_g, bias_u, act, out_dtype, out, (None, None), workspace, stream)
+    return _gated_gemm(A, Bg, Bu, bias_g, bias_u, act, out_dtype, out, None, workspace, stream)
 
 
 def gated_gemm_train(A: torch.Tensor, Bg: torch.Tensor, Bu: torch.Tensor, bias_g: Optional[torch.Tensor] = None,
@@ -213,35 +218,43 @@ def gated_gemm_train(A: torch.Tensor, Bg: torch.Tensor, Bu: torch.Tensor, bias_g
     return H, tuple(preact)
 
 
-def _preact_pitch(preact, A, M, N):
-    if len(preact) != 2:
-        raise ValueError("preact must be the two stored pre-activations")
-    return _one_pitch(preact, ("preact[0]", "preact[1]"), A, (M, N), A.dtype)
+_PREACT = ("preact[0]", "preact[1]")
 
 
 def _gated_gemm(A, Bg, Bu, bias_g, bias_u, act, out_dtype, out, preact, workspace, stream):
-    lib = load_library()
-    M, N, K, lda, ldb = _extents(A, (Bg, Bu), ("Bg", "Bu"))
-    _vec(bias_g, "bias_g", A, N, A.dtype)
-    _vec(bias_u, "bias_u", A, N, A.dtype)
+    M, K, lda, dev = _first(A)
+    if _current_device() != dev:
+        return _there(dev, _gated_gemm, A, Bg, Bu, bias_g, bias_u, act, out_dtype, out, preact, workspace, stream)
+    N, dt = _cols(Bg, "Bg"), A.dtype
+    ldb = _one_pitch((Bg, Bu), ("Bg", "Bu"), K, N, dt, dev)
+    if bias_g is not None:
+        _vec(bias_g, "bias_g", N, dt, dev)
+    if bias_u is not None:
+        _vec(bias_u, "bias_u", N, dt, dev)
     odt = _out_dtype(A, None, out_dtype, out)
     if out is None:
         out = _new(M, N, odt, A.device, stream)
-    ldy = _mat(out, "out", A, (M, N), odt)
-    ldz = 0 if preact[0] is None else _preact_pitch(preact, A, M, N)
-    with _on(A.device):
-        ws, nws, _keep = _workspace("coalesce_gated_gemm_workspace_size", A.device, M, N, K, workspace, stream)
-        _check(lib.coalesce_gated_gemm(_ptr(A), lda, _ptr(Bg), _ptr(Bu), ldb, _ptr(bias_g), _ptr(bias_u),
-                                       _ptr(preact[0]), _ptr(preact[1]), ldz, _ptr(out), ldy, M, N, K,
-                                       _DTYPES[A.dtype], _dtype(out, "out"), _act(act), ws, nws, _stream(stream)))
+    ldy = _mat(out, "out", M, N, odt, dev)
+    zg = zu = None
+    ldz = 0
+    if preact is not None:
+        ldz = _one_pitch(preact, _PREACT, M, N, dt, dev)
+        zg, zu = preact[0].data_ptr(), preact[1].data_ptr()
+    ws, nws, _keep = _workspace("coalesce_gated_gemm_workspace_size", dev, M, N, K, workspace, stream)
+    _check(load_library().coalesce_gated_gemm(
+        A.data_ptr(), lda, Bg.data_ptr(), Bu.data_ptr(), ldb, _ptr(bias_g), _ptr(bias_u), zg, zu, ldz, out.data_ptr(),
+        ldy, M, N, K, _DTYPES[dt], _DTYPES[odt], _act(act), ws, nws, _raw_stream(stream, dev)))
     return out
 
 
-def _grad_out(t, name, A, rows, cols, dtype, stream):
-    """(tensor, pitch) of a wanted matrix gradient, made here if none is given."""
-    if t is None:
-        t = _new(rows, cols, dtype, A.device, stream)
-    return t, _mat(t, name, A, (rows, cols), dtype)
+def _dout(dout: torch.Tensor, A: torch.Tensor, M: int, N: int, dev: int) -> int:
+    return _mat(dout, "dout", M, N, dout.dtype if dout.dtype is torch.float32 else A.dtype, dev)
+
+
+def _grad_dtype(grad_dtype, A):
+    if grad_dtype is not torch.float32 and grad_dtype is not A.dtype:
+        raise ValueError("grad_dtype must be float32 or A's dtype")
+    return _DTYPES[grad_dtype]
 
 
 def gemm_residual_backward(A: torch.Tensor, B: torch.Tensor, dout: torch.Tensor,
@@ -254,30 +267,35 @@ def gemm_residual_backward(A: torch.Tensor, B: torch.Tensor, dout: torch.Tensor,
     or float32): dA in A's dtype, dB and dbias in ``grad_dtype`` (float32 or
     A's dtype).  ``preact`` is what gemm_residual_train stored; without an
     activation it is not needed."""
-    lib = load_library()
-    M, N, K, lda, ldb = _extents(A, (B,), ("B",))
-    ldd = _mat(dout, "dout", A, (M, N))
-    a = _act(act)
+    M, K, lda, dev = _first(A)
+    if _current_device() != dev:
+        return _there(dev, gemm_residual_backward, A, B, dout, preact, act, want_dA, want_dB, want_dbias, grad_dtype,
+                      dA, dB, workspace, stream)
+    N, dt = _cols(B, "B"), A.dtype
+    ldb = _mat(B, "B", K, N, dt, dev)
+    ldd = _dout(dout, A, M, N, dev)
+    a, gd = _act(act), _grad_dtype(grad_dtype, A)
     if a != ACT_NONE and preact is None:
         raise ValueError("the backward of an activation needs the stored pre-activation")
-    ldz = 0 if preact is None else _mat(preact, "preact", A, (M, N), A.dtype)
+    ldz = 0 if preact is None else _mat(preact, "preact", M, N, dt, dev)
     ldda = lddb = 0
     dbias = None
     if want_dA:
-        dA, ldda = _grad_out(dA, "dA", A, M, K, A.dtype, stream)
+        if dA is None:
+            dA = _new(M, K, dt, A.device, stream)
+        ldda = _mat(dA, "dA", M, K, dt, dev)
     if want_dB:
-        dB, lddb = _grad_out(dB, "dB", A, K, N, grad_dtype, stream)
+        if dB is None:
+            dB = _new(K, N, grad_dtype, A.device, stream)
+        lddb = _mat(dB, "dB", K, N, grad_dtype, dev)
     if want_dbias:
         dbias = torch.empty(N, dtype=grad_dtype, device=A.device)
         _used_on(stream, dbias)
     g = GemmGrads(dA if want_dA else None, dB if want_dB else None, dbias)
-    with _on(A.device):
-        ws, nws, _keep = _workspace("coalesce_gemm_residual_backward_workspace_size", A.device, M, N, K, workspace,
-                                    stream)
-        _check(lib.coalesce_gemm_residual_backward(_ptr(A), lda, _ptr(B), ldb, _ptr(preact), ldz, _ptr(dout), ldd,
-                                                   _ptr(g.dA), ldda, _ptr(g.dB), lddb, _ptr(dbias), M, N, K,
-                                                   _DTYPES[A.dtype], _dtype(dout, "dout"), _DTYPES[grad_dtype], a, ws,
-                                                   nws, _stream(stream)))
+    ws, nws, _keep = _workspace("coalesce_gemm_residual_backward_workspace_size", dev, M, N, K, workspace, stream)
+    _check(load_library().coalesce_gemm_residual_backward(
+        A.data_ptr(), lda, B.data_ptr(), ldb, _ptr(preact), ldz, dout.data_ptr(), ldd, _ptr(g.dA), ldda, _ptr(g.dB),
+        lddb, _ptr(dbias), M, N, K, _DTYPES[dt], _DTYPES[dout.dtype], gd, a, ws, nws, _raw_stream(stream, dev)))
     return g
 
 
@@ -290,31 +308,33 @@ def gated_gemm_backward(A: torch.Tensor, Bg: torch.Tensor, Bu: torch.Tensor,
     """Gradients of gated_gemm for the upstream gradient ``dout`` (A's dtype or
     float32), from the pre-activations that gated_gemm_train stored: dA in A's
     dtype, dBg, dBu and the bias gradients in ``grad_dtype``."""
-    lib = load_library()
-    M, N, K, lda, ldb = _extents(A, (Bg, Bu), ("Bg", "Bu"))
-    ldd = _mat(dout, "dout", A, (M, N))
-    ldz = _preact_pitch(preact, A, M, N)
+    M, K, lda, dev = _first(A)
+    if _current_device() != dev:
+        return _there(dev, gated_gemm_backward, A, Bg, Bu, preact, dout, act, want_dA, want_dB, want_dbias, grad_dtype,
+                      dA, dB, workspace, stream)
+    N, dt = _cols(Bg, "Bg"), A.dtype
+    ldb = _one_pitch((Bg, Bu), ("Bg", "Bu"), K, N, dt, dev)
+    ldd = _dout(dout, A, M, N, dev)
+    ldz = _one_pitch(preact, _PREACT, M, N, dt, dev)
+    a, gd = _act(act), _grad_dtype(grad_dtype, A)
     ldda = lddb = 0
-    dW, db = [None, None], [None, None]
+    dW, db = (None, None), (None, None)
     if want_dA:
-        dA, ldda = _grad_out(dA, "dA", A, M, K, A.dtype, stream)
+        if dA is None:
+            dA = _new(M, K, dt, A.device, stream)
+        ldda = _mat(dA, "dA", M, K, dt, dev)
     if want_dB:
-        dW = list(dB) if dB is not None else [_new(K, N, grad_dtype, A.device, stream) for _ in range(2)]
-        if len(dW) != 2:
-            raise ValueError("dB must be two tensors")
-        lddb = _one_pitch(dW, ("dB[0]", "dB[1]"), A, (K, N), grad_dtype)
+        dW = dB if dB is not None else (_new(K, N, grad_dtype, A.device, stream), _new(K, N, grad_dtype, A.device, stream))
+        lddb = _one_pitch(dW, ("dB[0]", "dB[1]"), K, N, grad_dtype, dev)
     if want_dbias:
-        db = [torch.empty(N, dtype=grad_dtype, device=A.device) for _ in range(2)]
+        db = (torch.empty(N, dtype=grad_dtype, device=A.device), torch.empty(N, dtype=grad_dtype, device=A.device))
         _used_on(stream, *db)
     g = GatedGrads(dA if want_dA else None, dW[0], dW[1], db[0], db[1])
-    with _on(A.device):
-        ws, nws, _keep = _workspace("coalesce_gated_gemm_backward_workspace_size", A.device, M, N, K, workspace,
-                                    stream)
-        _check(lib.coalesce_gated_gemm_backward(_ptr(A), lda, _ptr(Bg), _ptr(Bu), ldb, _ptr(preact[0]),
-                                                _ptr(preact[1]), ldz, _ptr(dout), ldd, _ptr(g.dA), ldda, _ptr(dW[0]),
-                                                _ptr(dW[1]), lddb, _ptr(db[0]), _ptr(db[1]), M, N, K,
-                                                _DTYPES[A.dtype], _dtype(dout, "dout"), _DTYPES[grad_dtype], _act(act),
-                                                ws, nws, _stream(stream)))
+    ws, nws, _keep = _workspace("coalesce_gated_gemm_backward_workspace_size", dev, M, N, K, workspace, stream)
+    _check(load_library().coalesce_gated_gemm_backward(
+        A.data_ptr(), lda, Bg.data_ptr(), Bu.data_ptr(), ldb, preact[0].data_ptr(), preact[1].data_ptr(), ldz,
+        dout.data_ptr(), ldd, _ptr(g.dA), ldda, _ptr(dW[0]), _ptr(dW[1]), lddb, _ptr(db[0]), _ptr(db[1]), M, N, K,
+        _DTYPES[dt], _DTYPES[dout.dtype], gd, a, ws, nws, _raw_stream(stream, dev)))
     return g
 
 
@@ -324,8 +344,6 @@ def gated_gemm_backward(A: torch.Tensor, Bg: torch.Tensor, Bu: torch.Tensor,
 
 def _dense(t: torch.Tensor) -> bool:
     """Whether the tensor's elements fill one run of memory, in any order."""
-    if t.is_contiguous():
-        return True
     n = 1
     for size, st in sorted(((s, st) for s, st in zip(t.shape, t.stride()) if s != 1), key=lambda x: x[1]):
         if st != n:
@@ -334,27 +352,35 @@ def _dense(t: torch.Tensor) -> bool:
     return True
 
 
+def _address(a: array.array) -> int:
+    return a.buffer_info()[0]
+
+
 def _grad_list(tensors, out):
+    """(count, device, sources, destinations, sizes, types): the host arrays of
+    the C call, to be kept alive until it returns."""
     tensors = list(tensors)
-    dev = tensors[0].device if tensors else torch.device("cuda", torch.cuda.current_device())
+    devs = {t.get_device() for t in tensors}
+    dev = devs.pop() if devs else _current_device()
+    if devs or dev < 0:
+        raise ValueError("the tensors must lie on one GPU")
+    try:
+        dts = array.array("i", [_DTYPES[t.dtype] for t in tensors])
+    except KeyError:
+        raise ValueError("every tensor must be float32, float16 or bfloat16") from None
+    numel = array.array("q", [t.numel() for t in tensors])
     for i, t in enumerate(tensors):
-        if t.device != dev or not t.is_cuda:
-            raise ValueError("tensor %d is on %s, not on %s" % (i, t.device, dev))
-        if t.dtype not in _DTYPES:
-            raise ValueError("tensor %d must be float32, float16 or bfloat16" % i)
-        if not _dense(t):
+        if not t.is_contiguous() and not _dense(t):
             raise ValueError("tensor %d must be dense (its elements one run of memory)" % i)
-    if out is not None:
-        if len(out) != len(tensors):
-            raise ValueError("out must hold one tensor per gradient")
-        for i, (t, o) in enumerate(zip(tensors, out)):
-            if o.shape != t.shape or o.dtype != t.dtype or o.device != dev or o.stride() != t.stride():
-                raise ValueError("out[%d] must have its gradient's shape, strides, dtype and device" % i)
-    src = _c_array(_vp, tuple([t.data_ptr() for t in tensors]))
-    numel = _c_array(_i64, tuple([t.numel() for t in tensors]))
-    dts = _c_array(_i32, tuple([_DTYPES[t.dtype] for t in tensors]))
-    dst = src if out is None else _c_array(_vp, tuple([t.data_ptr() for t in out]))
-    return len(tensors), dev, src, dst, numel, dts
+    src = array.array("Q", [t.data_ptr() for t in tensors])
+    if out is None:
+        return len(tensors), dev, src, src, numel, dts
+    if len(out) != len(tensors):
+        raise ValueError("out must hold one tensor per gradient")
+    for i, (t, o) in enumerate(zip(tensors, out)):
+        if o.shape != t.shape or o.dtype is not t.dtype or o.get_device() != dev or o.stride() != t.stride():
+            raise ValueError("out[%d] must have its gradient's shape, strides, dtype and device" % i)
+    return len(tensors), dev, src, array.array("Q", [t.data_ptr() for t in out]), numel, dts
 
 
 def _norm_code(norm_type) -> int:
@@ -367,10 +393,10 @@ def _norm_code(norm_type) -> int:
 
 def _norm_out(norm, dev, stream):
     if norm is None:
-        norm = torch.empty((), dtype=torch.float32, device=dev)
+        norm = torch.empty((), dtype=torch.float32, device="cuda")  # the current device is dev here
         _used_on(stream, norm)
-    elif norm.numel() != 1 or norm.dtype != torch.float32 or norm.device != dev:
-        raise ValueError("norm must be one float32 on %s" % dev)
+    elif norm.numel() != 1 or norm.dtype is not torch.float32 or norm.get_device() != dev:
+        raise ValueError("norm must be one float32 on GPU %d" % dev)
     return norm
 
 
@@ -378,14 +404,7 @@ def grad_norm(tensors: Sequence[torch.Tensor], norm_type=2.0, norm: Optional[tor
               workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The 2-norm or largest magnitude (``norm_type`` inf) of all the tensors
     taken as one vector, as a float32 scalar on their device (coalesce_grad_norm)."""
-    lib = load_library()
-    n, dev, src, _, numel, dts = _grad_list(tensors, None)
-    code = _norm_code(norm_type)
-    norm = _norm_out(norm, dev, stream)
-    with _on(dev):
-        ws, nws, _keep = _take(workspace, int(lib.coalesce_grad_norm_workspace_size(numel, dts, n)), dev, stream)
-        _check(lib.coalesce_grad_norm(src, numel, dts, n, code, _ptr(norm), ws, nws, _stream(stream)))
-    return norm
+    return _norm_call(_grad_list(tensors, None), None, norm_type, norm, workspace, stream)
 
 
 def clip_grad_norm(tensors: Sequence[torch.Tensor], max_norm: float, norm_type=2.0,
@@ -396,14 +415,23 @@ def clip_grad_norm(tensors: Sequence[torch.Tensor], max_norm: float, norm_type=2
     their device.  In place, or into ``out`` (one tensor per gradient, of its
     shape, strides and dtype).  Nothing synchronises with the host; tensors of
     several dtypes may be mixed."""
-    lib = load_library()
-    n, dev, src, dst, numel, dts = _grad_list(tensors, out)
-    code = _norm_code(norm_type)
+    return _norm_call(_grad_list(tensors, out), float(max_norm), norm_type, norm, workspace, stream)
+
+
+def _norm_call(lists, max_norm, norm_type, norm, workspace, stream):
+    n, dev, src, dst, numel, dts = lists
+    if _current_device() != dev:
+        return _there(dev, _norm_call, lists, max_norm, norm_type, norm, workspace, stream)
+    lib, code = load_library(), _norm_code(norm_type)
     norm = _norm_out(norm, dev, stream)
-    with _on(dev):
-        ws, nws, _keep = _take(workspace, int(lib.coalesce_grad_norm_workspace_size(numel, dts, n)), dev, stream)
-        _check(lib.coalesce_clip_grad_norm(src, dst, numel, dts, n, code, float(max_norm), _ptr(norm), ws, nws,
-                                           _stream(stream)))
+    pn, pd = _address(numel), _address(dts)
+    ws, nws, _keep = _take(workspace, int(lib.coalesce_grad_norm_workspace_size(pn, pd, n)), dev, stream)
+    if max_norm is None:
+        _check(lib.coalesce_grad_norm(_address(src), pn, pd, n, code, norm.data_ptr(), ws, nws,
+                                      _raw_stream(stream, dev)))
+    else:
+        _check(lib.coalesce_clip_grad_norm(_address(src), _address(dst), pn, pd, n, code, max_norm, norm.data_ptr(), ws,
+                                           nws, _raw_stream(stream, dev)))
     return norm
 
 
