@@ -42,11 +42,8 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineOp c) {
       }
       f32x4 o = (f32x4){0.f, 0.f, 0.f, 0.f};
       if (KIND == COMBINE_RESID && c.R) o = load4<TO>((const TO*)c.R + m * c.ldr + n, valid);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float f = act_any(c.act, acc[0][r]);
-        o[r] = KIND == COMBINE_GATED ? f * acc[1][r] : o[r] + f;
-      }
+      const f32x4 f = act_any(c.act, acc[0]);
+      o = KIND == COMBINE_GATED ? f * acc[1] : o + f;
       store4<TO>((TO*)c.Y[0] + m * c.ldy + n, o, valid);
     }
   }

@@ -156,11 +156,21 @@ hipError_t dz_act(const DzParams& p, int act, dim3 grid, hipStream_t stream) {
 
 template <typename T, typename TO, Lay LA, Lay LB, int SEGS>
 hipError_t store_tiles(const TileOp& o, int variant, hipStream_t stream, int num_cus) {
-  if (variant == 1)
-    return launch_tile<T, TO, LA, LB, SEGS, EPI_STORE, ACT_NONE, TileGeo<256, 256, 8, 2, 1, 1>>(o, stream, num_cus);
-  if (variant == 2)
-    return launch_tile<T, TO, LA, LB, SEGS, EPI_STORE, ACT_NONE, TileGeo<128, 128, 4, 2, 2, 1>>(o, stream, num_cus);
-  return launch_tile<T, TO, LA, LB, SEGS, EPI_STORE, ACT_NONE, TileGeo<64, 64, 4, 2, 4, 1>>(o, stream, num_cus);
+#define COALESCE_TILE(...) launch_tile<T, TO, LA, LB, SEGS, EPI_STORE, TileGeo<__VA_ARGS__>>(o, stream, num_cus)
+  if constexpr (LA == LAY_K) {
+    switch (variant) {
+      case kShape224: return COALESCE_TILE(224, 256, 8, 2, 1, 1);
+      case kShape192: return COALESCE_TILE(192, 256, 8, 2, 1, 1);
+      case kShape160: return COALESCE_TILE(160, 256, 8, 2, 1, 1, 3);
+    }
+  }
+  switch (variant) {
+    case kShape256: return COALESCE_TILE(256, 256, 8, 2, 1, 1);
+    case kShape128: return COALESCE_TILE(128, 128, 4, 2, 2, 1);
+    case kShape64Deep: return COALESCE_TILE(64, 64, 4, 2, 3, 1, 3);
+    default: return COALESCE_TILE(64, 64, 4, 2, 4, 1);
+  }
+#undef COALESCE_TILE
 }
 
 // One of the backward's products: stored directly, or split into fp32 partial
@@ -185,10 +195,10 @@ hipError_t product(TileOp o, const TilePlan& plan, DType out, hipStream_t stream
   c.N = o.N;
   o.ldy = c.ldp;
   o.split_stride = c.split_stride;
-  hipError_t e =
-      plan.variant == 2
-          ? launch_tile<T, float, LA, LB, SEGS, EPI_STORE, ACT_NONE, TileGeo<128, 128, 4, 2, 2, 1>>(o, stream, num_cus)
-          : launch_tile<T, float, LA, LB, SEGS, EPI_STORE, ACT_NONE, TileGeo<64, 64, 4, 2, 4, 1>>(o, stream, num_cus);
+#define COALESCE_TILE(...) launch_tile<T, float, LA, LB, SEGS, EPI_STORE, TileGeo<__VA_ARGS__>>(o, stream, num_cus)
+  const hipError_t e =
+      plan.variant == kShape128 ? COALESCE_TILE(128, 128, 4, 2, 2, 1) : COALESCE_TILE(64, 64, 4, 2, 4, 1);
+#undef COALESCE_TILE
   if (e != hipSuccess) return e;
   return launch_combine(c, COMBINE_STORE, out, out, stream, num_cus);
 }

@@ -200,11 +200,8 @@ __global__ __launch_bounds__(G::NW * 64) void few_kernel(TileOp p) {
       }
       f32x4 o = (f32x4){0.f, 0.f, 0.f, 0.f};
       if (EPI == EPI_RESID && p.R) o = load4<TO>((const TO*)p.R + (int64_t)row * p.ldr + n, valid);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float f = act_any(p.act, z[0][r]);
-        o[r] = EPI == EPI_GATED ? f * z[NB - 1][r] : o[r] + f;
-      }
+      const f32x4 f = act_any(p.act, z[0]);
+      o = EPI == EPI_GATED ? f * z[NB - 1] : o + f;
       store4<TO>((TO*)p.Y[0] + (int64_t)row * p.ldy + n, o, valid);
     }
   }

@@ -14,34 +14,33 @@
 namespace coalesce {
 namespace {
 
-template <typename T, typename TO, int EPI, int ACT>
-hipError_t forward_tiles(const TileOp& o, int variant, hipStream_t stream, int num_cus) {
-  if constexpr (EPI == EPI_GATED) {
-    // 256 rows x 128 columns of both products, waves of 64 x (64 + 64); 128 x
-    // 64, waves of 64 x (32 + 32); 64 x 64, waves of 32 x (32 + 32)
-    if (variant == 1)
-      return launch_tile<T, TO, LAY_K, LAY_X, 1, EPI, ACT, TileGeo<256, 256, 8, 4, 1, 2>>(o, stream, num_cus);
-    if (variant == 2)
-      return launch_tile<T, TO, LAY_K, LAY_X, 1, EPI, ACT, TileGeo<128, 128, 4, 2, 2, 2>>(o, stream, num_cus);
-    return launch_tile<T, TO, LAY_K, LAY_X, 1, EPI, ACT, TileGeo<64, 128, 4, 2, 2, 2>>(o, stream, num_cus);
-  } else {
-    if (variant == 1)
-      return launch_tile<T, TO, LAY_K, LAY_X, 1, EPI, ACT, TileGeo<256, 256, 8, 2, 1, 1>>(o, stream, num_cus);
-    if (variant == 2)
-      return launch_tile<T, TO, LAY_K, LAY_X, 1, EPI, ACT, TileGeo<128, 128, 4, 2, 2, 1>>(o, stream, num_cus);
-    return launch_tile<T, TO, LAY_K, LAY_X, 1, EPI, ACT, TileGeo<64, 64, 4, 2, 4, 1>>(o, stream, num_cus);
-  }
-}
-
 template <typename T, typename TO, int EPI>
-hipError_t forward_act(const TileOp& o, int act, int variant, hipStream_t stream, int num_cus) {
-  switch (act) {
-    case ACT_GELU: return forward_tiles<T, TO, EPI, ACT_GELU>(o, variant, stream, num_cus);
-    case ACT_SOFTPLUS: return forward_tiles<T, TO, EPI, ACT_SOFTPLUS>(o, variant, stream, num_cus);
-    case ACT_RELU: return forward_tiles<T, TO, EPI, ACT_RELU>(o, variant, stream, num_cus);
-    case ACT_SILU: return forward_tiles<T, TO, EPI, ACT_SILU>(o, variant, stream, num_cus);
-    default: return forward_tiles<T, TO, EPI, ACT_NONE>(o, variant, stream, num_cus);
+hipError_t forward_tiles(const TileOp& o, int variant, hipStream_t stream, int num_cus) {
+#define COALESCE_TILE(...) launch_tile<T, TO, LAY_K, LAY_X, 1, EPI, TileGeo<__VA_ARGS__>>(o, stream, num_cus)
+  if constexpr (EPI == EPI_GATED) {
+    // 256 rows x 128 columns of both products: waves of 64 x (64 + 64); 224,
+    // 192 and 160 rows: waves of half of them x (32 + 32); 128 x 64: waves of
+    // 64 x (32 + 32); 64 x 64: waves of 32 x (32 + 32)
+    switch (variant) {
+      case kShape256: return COALESCE_TILE(256, 256, 8, 4, 1, 2);
+      case kShape224: return COALESCE_TILE(224, 256, 8, 2, 1, 2);
+      case kShape192: return COALESCE_TILE(192, 256, 8, 2, 1, 2);
+      case kShape160: return COALESCE_TILE(160, 256, 8, 2, 1, 2, 3);
+      case kShape128: return COALESCE_TILE(128, 128, 4, 2, 2, 2);
+      default: return COALESCE_TILE(64, 128, 4, 2, 2, 2);
+    }
+  } else {
+    switch (variant) {
+      case kShape256: return COALESCE_TILE(256, 256, 8, 2, 1, 1);
+      case kShape224: return COALESCE_TILE(224, 256, 8, 2, 1, 1);
+      case kShape192: return COALESCE_TILE(192, 256, 8, 2, 1, 1);
+      case kShape160: return COALESCE_TILE(160, 256, 8, 2, 1, 1, 3);
+      case kShape128: return COALESCE_TILE(128, 128, 4, 2, 2, 1);
+      case kShape64Deep: return COALESCE_TILE(64, 64, 4, 2, 3, 1, 3);
+      default: return COALESCE_TILE(64, 64, 4, 2, 4, 1);
+    }
   }
+#undef COALESCE_TILE
 }
 
 // A split product: fp32 partial results of each range of K steps (128 x 128 or
@@ -72,13 +71,13 @@ hipError_t forward_split(TileOp o, int variant, DType in, DType out, int act, hi
   for (int i = 0; i < products; ++i) o.Y[i] = (void*)c.P[i];
   o.ldy = c.ldp;
   o.split_stride = c.split_stride;
+#define COALESCE_TILE(...) launch_tile<T, float, LAY_K, LAY_X, 1, EPI_STORE, TileGeo<__VA_ARGS__>>(o, stream, num_cus)
   hipError_t e;
   if constexpr (EPI == EPI_GATED)
-    e = variant == 2 ? launch_tile<T, float, LAY_K, LAY_X, 1, EPI_STORE, ACT_NONE, TileGeo<128, 128, 4, 2, 2, 2>>(o, stream, num_cus)
-                     : launch_tile<T, float, LAY_K, LAY_X, 1, EPI_STORE, ACT_NONE, TileGeo<64, 128, 4, 2, 2, 2>>(o, stream, num_cus);
+    e = variant == kShape128 ? COALESCE_TILE(128, 128, 4, 2, 2, 2) : COALESCE_TILE(64, 128, 4, 2, 2, 2);
   else
-    e = variant == 2 ? launch_tile<T, float, LAY_K, LAY_X, 1, EPI_STORE, ACT_NONE, TileGeo<128, 128, 4, 2, 2, 1>>(o, stream, num_cus)
-                     : launch_tile<T, float, LAY_K, LAY_X, 1, EPI_STORE, ACT_NONE, TileGeo<64, 64, 4, 2, 4, 1>>(o, stream, num_cus);
+    e = variant == kShape128 ? COALESCE_TILE(128, 128, 4, 2, 2, 1) : COALESCE_TILE(64, 64, 4, 2, 4, 1);
+#undef COALESCE_TILE
   if (e != hipSuccess) return e;
   return launch_combine(c, EPI == EPI_GATED ? COMBINE_GATED : COMBINE_RESID, in, out, stream, num_cus);
 }
@@ -112,8 +111,8 @@ hipError_t forward_typed(const FfnParams& p, DType in, DType out, int act, hipSt
   o.splits = plan.splits;
   if (plan.splits > 1)
     return forward_split<T, EPI>(o, plan.variant, in, out, act, stream, num_cus, (float*)workspace);
-  if (out == DT_F32) return forward_act<T, float, EPI>(o, act, plan.variant, stream, num_cus);
-  return forward_act<T, T, EPI>(o, act, plan.variant, stream, num_cus);
+  if (out == DT_F32) return forward_tiles<T, float, EPI>(o, plan.variant, stream, num_cus);
+  return forward_tiles<T, T, EPI>(o, plan.variant, stream, num_cus);
 }
 
 }  // namespace

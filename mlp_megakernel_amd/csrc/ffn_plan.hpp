@@ -12,49 +12,67 @@ constexpr int DZ_COLS = 256, DZ_ROWS = 8;  // columns and row lanes of a workgro
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// How a product runs: tile shape (1 = 256 x 256, 2 = 128 x 128, 3 = 64 x 64; of
-// a gated product 128, 64 and 64 output columns) and in how many ranges its K
-// steps are split.
+// How a product runs: tile shape and in how many ranges its K steps are split.
 struct TilePlan {
   int variant, splits;
   double ns;  // estimated time
 };
 
+// The compiled tile shapes (gemm16_core.hpp): rows, columns (of each matrix of
+// a gated product), how many a compute unit holds, the time of one K step with
+// 1, 2, ... of them on every compute unit, and the time a launch and a round of
+// tiles take beside their K steps.  Measured in ns over products of 256 to 8192
+// rows, bf16.  A step is bound by the matrix cores at 256 rows and more and more
+// by the caches below (a 160-row tile draws 0.77 of the bytes per step for 0.63
+// of the products), so the lower ones pay only where they fit the rows or fill
+// the compute units better: gated 777 x 5461 x 2048 57.8 us in 256 rows, 48.5 in
+// 160; 3000 x 4096 x 4096 180 in 256, 163 in 192.  Those lower than 256 exist
+// where the m side lies along the contraction; 160 rows and one of the 64 x 64
+// shapes have three stages (residual 512 x 4096 x 4096: 37.5 us with two, 30.2).
+struct TileShape {
+  int bm, bn, slots;
+  double step[4], launch, round;
+};
+constexpr int kShapes = 7, kShape256 = 1, kShape128 = 2, kShape64 = 3, kShape224 = 4, kShape192 = 5, kShape160 = 6,
+              kShape64Deep = 7;
+static const TileShape kPlain[kShapes] = {
+    {256, 256, 1, {1450}, 4000, 5000},          {128, 128, 2, {780, 1200}, 3000, 2000},
+    {64, 64, 4, {430, 520, 700, 850}, 3000, 1500}, {224, 256, 1, {1290}, 4000, 5000},
+    {192, 256, 1, {1180}, 4000, 5000},          {160, 256, 1, {1010}, 4000, 5000},
+    {64, 64, 3, {380, 440, 700}, 3000, 1500}};
+static const TileShape kGated[kShapes] = {
+    {256, 128, 1, {1450}, 4000, 5000}, {128, 64, 2, {740, 1050}, 3000, 2000}, {64, 64, 3, {600, 680, 950}, 3000, 1500},
+    {224, 128, 1, {1290}, 4000, 5000}, {192, 128, 1, {1180}, 4000, 5000},     {160, 128, 1, {1010}, 4000, 5000},
+    {64, 64, 0, {0}, 0, 0}};
+
 // The plan with the smallest estimated time.  A launch is `units` workgroup
-// tiles (tiles x splits); a compute unit runs up to 1, 2 or 4 (gated: 3) of
-// them at once, and one K step of all of them then takes step[units per CU]
-// (ns; measured over products of 512 to 16384 rows and columns, bf16).  A tile
-// has a fixed cost beside its K steps (the first copies, the epilogue), a
-// split product writes and reads its fp32 partial results once more (at about
-// 6 TB/s, mostly caches) in a second launch; and reading the operands from memory takes its time
-// too: 4.5 TB/s with three or more tiles on each compute unit, 4.0 and 3.0 with
-// two and one, in proportion below.
-TilePlan plan_tiles(int64_t m, int64_t n, bool gated, int batch, int64_t ksteps, int num_cus) {
-  static const int slots[2][3] = {{1, 2, 4}, {1, 2, 3}};
-  static const double step[2][3][4] = {{{1500}, {780, 1200}, {550, 570, 720, 850}},
-                                       {{1450}, {740, 1050}, {650, 700, 950}}};
-  static const double fixed[3] = {6000, 4000, 3000};
+// tiles (tiles x splits), run in rounds of what the compute units hold.  A split
+// product (128 x 128 or 64 x 64 tiles) writes and reads its fp32 partial results
+// once more, at about 6 TB/s, mostly caches, in a second launch; and reading the
+// operands from memory takes its time too: 4.5 TB/s with three or more tiles on
+// each compute unit, 4.0 and 3.0 with two and one, in proportion below.  `rows`:
+// the m side lies along the contraction, every shape may be used.
+TilePlan plan_tiles(int64_t m, int64_t n, bool gated, int batch, int64_t ksteps, bool rows, int num_cus) {
   static const int ranges[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
   const double operand_bytes = (double)ksteps * 128.0 * ((double)m + (double)n * (gated ? 2 : batch));
-  TilePlan best{3, 1, 1e300};
-  for (int v = 1; v <= 3; ++v) {
-    const int bm = v == 1 ? 256 : v == 2 ? 128 : 64;
-    const int bn = !gated ? bm : v == 1 ? 128 : 64;
-    const int64_t tiles = ((m + bm - 1) / bm) * ((n + bn - 1) / bn) * batch;
-    const int per_cu = slots[gated][v - 1];
+  TilePlan best{kShape64, 1, 1e300};
+  for (int v = 1; v <= kShapes; ++v) {
+    const TileShape& s = gated ? kGated[v - 1] : kPlain[v - 1];
+    if (s.slots == 0 || (!rows && (v == kShape224 || v == kShape192 || v == kShape160))) continue;
+    const int64_t tiles = ((m + s.bm - 1) / s.bm) * ((n + s.bn - 1) / s.bn) * batch;
     for (int splits : ranges) {
-      if (splits > 1 && (v == 1 || ksteps / splits < 4)) break;
-      const int64_t units = tiles * splits;
-      const int64_t rounds = units / ((int64_t)num_cus * per_cu), rest = units - rounds * num_cus * per_cu;
-      const int in_rest = (int)((rest + num_cus - 1) / num_cus);  // 0 .. per_cu
-      double t = (double)rounds * step[gated][v - 1][per_cu - 1] + (in_rest ? step[gated][v - 1][in_rest - 1] : 0.0);
+      if (splits > 1 && ((v != kShape128 && v != kShape64) || ksteps / splits < 4)) break;
+      const int64_t units = tiles * splits, full = (int64_t)num_cus * s.slots;
+      const int64_t rounds = units / full, rest = units - rounds * full;
+      const int in_rest = (int)((rest + num_cus - 1) / num_cus);  // 0 .. slots
+      double t = (double)rounds * s.step[s.slots - 1] + (in_rest ? s.step[in_rest - 1] : 0.0);
       const double load = (double)units / num_cus;
       const double gb = load >= 3 ? 4500 : load >= 2 ? 4000 : load >= 1 ? 3000 : 3000 * load;
-      t = std::max(t * (double)((ksteps + splits - 1) / splits), operand_bytes / gb) +
-          ((double)rounds + (in_rest > 0)) * fixed[v - 1];
-      if (splits > 1) t += 4000 + (double)splits * (double)m * (double)n * (gated ? 2 : batch) * 8.0 / 6000.0;
+      t = std::max(t * (double)((ksteps + splits - 1) / splits), operand_bytes / gb) + s.launch +
+          ((double)rounds + (in_rest > 0)) * s.round;
+      if (splits > 1) t += 4500 + (double)splits * (double)m * (double)n * (gated ? 2 : batch) * 8.0 / 6000.0;
       if (t < best.ns) best = {v, splits, t};
-      if (units > 2 * (int64_t)num_cus * per_cu) break;
+      if (units > 2 * full) break;
     }
   }
   return best;
@@ -74,7 +92,7 @@ struct ForwardPlan {
   TilePlan tiles;
 };
 ForwardPlan plan_forward(int64_t m, int64_t n, int64_t k, bool gated, int num_cus) {
-  ForwardPlan f{0, plan_tiles(m, n, gated, 1, (k + 63) / 64, num_cus)};
+  ForwardPlan f{0, plan_tiles(m, n, gated, 1, (k + 63) / 64, true, num_cus)};
   if (m > 64) return f;
   static const double row_ns[3] = {3.5, 3.0, 2.6}, waste[3] = {1.0, 1.5, 2.0};
   const double nb = gated ? 2.0 : 1.0;
@@ -134,8 +152,8 @@ BwdPlan bwd_plan(int64_t M, int64_t N, int64_t K, bool gated, int num_cus) {
   b.sums_at = b.dz_bytes * (gated ? 2 : 1);
   b.partial_at = b.sums_at + align256((size_t)b.chunks * 2 * (size_t)N * 4);
   const int products = gated ? 2 : 1;
-  b.dx = plan_tiles(M, K, false, 1, products * ((N + 63) / 64), num_cus);
-  b.dw = plan_tiles(K, N, false, products, (M + 63) / 64, num_cus);
+  b.dx = plan_tiles(M, K, false, 1, products * ((N + 63) / 64), true, num_cus);
+  b.dw = plan_tiles(K, N, false, products, (M + 63) / 64, false, num_cus);
   // the two products run one after the other and share the space
   b.total = b.partial_at + std::max(partial_bytes(b.dx, M, K, 1), partial_bytes(b.dw, K, N, products));
   return b;

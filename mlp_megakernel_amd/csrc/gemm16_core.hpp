@@ -118,16 +118,32 @@ __device__ __forceinline__ f32x4 load4(const T* src, int valid) {
   return v;
 }
 
-// The activation of a launch argument, where a kernel is not compiled per
-// activation.
-__device__ __forceinline__ float act_any(int act, float z) {
+// The activation a launch names: a uniform branch per four values, nothing
+// beside a tile's K loop (and a fifth of the kernels that one per activation
+// would take).
+template <bool OUT16 = false>
+__device__ __forceinline__ f32x4 act_any(int act, f32x4 z) {
+  f32x4 f = z;
   switch (act) {
-    case ACT_GELU: return gelu_erf(z);
-    case ACT_SOFTPLUS: return softplus_guarded(z);
-    case ACT_RELU: return relu(z);
-    case ACT_SILU: return silu(z);
-    default: return z;
+    case ACT_GELU:
+#pragma unroll
+      for (int r = 0; r < 4; ++r) f[r] = apply_act<ACT_GELU, OUT16>(z[r]);
+      break;
+    case ACT_SOFTPLUS:
+#pragma unroll
+      for (int r = 0; r < 4; ++r) f[r] = softplus_guarded(z[r]);
+      break;
+    case ACT_RELU:
+#pragma unroll
+      for (int r = 0; r < 4; ++r) f[r] = relu(z[r]);
+      break;
+    case ACT_SILU:
+#pragma unroll
+      for (int r = 0; r < 4; ++r) f[r] = silu(z[r]);
+      break;
+    default: break;
   }
+  return f;
 }
 
 // Swizzle of an epilogue staging row of ROWB bytes (64, 128 or 256), in
@@ -148,13 +164,15 @@ enum Lay { LAY_K = 0, LAY_X = 1 };
 enum Epi { EPI_STORE = 0, EPI_RESID = 1, EPI_GATED = 2 };
 
 // Tile geometry: BM x BN accumulators per workgroup, NW waves in a WGM x
-// NW / WGM grid.  NSUB = 2: the n side's tile is two sub-tiles of BN / 2
+// NW / WGM grid, NS stages in LDS.  With two stages a copy has one K step's time
+// to arrive, which a 256 x 256 tile covers; narrower tiles whose step is shorter
+// than a trip to memory take three.  NSUB = 2: the n side's tile is two sub-tiles of BN / 2
 // columns, the same columns of two matrices (the gated product: a wave holds
 // both products of its WN / 2 columns, so act(g) * u needs no exchange).
 // MINW is the launch-bounds floor of waves per SIMD.
-template <int BM_, int BN_, int NW_, int WGM_, int MINW_, int NSUB_>
+template <int BM_, int BN_, int NW_, int WGM_, int MINW_, int NSUB_, int NS_ = 2>
 struct TileGeo {
-  static constexpr int BM = BM_, BN = BN_, NW = NW_, WGM = WGM_, MINW = MINW_, NSUB = NSUB_;
+  static constexpr int BM = BM_, BN = BN_, NW = NW_, WGM = WGM_, MINW = MINW_, NSUB = NSUB_, NS = NS_;
   static constexpr int THREADS = NW * 64;
   static constexpr int WGN = NW / WGM;
   static constexpr int WM = BM / WGM, WN = BN / WGN;  // wave tile (WN over all sub-tiles)
@@ -162,16 +180,19 @@ struct TileGeo {
   static constexpr int SUBN = BN / NSUB;              // columns of one n-side sub-tile
   static constexpr int ON = SUBN;                     // output columns per workgroup tile
   static constexpr int WNO = WN / NSUB, NTO = NT / NSUB;
-  static constexpr int CA = BM / 8 / NW;              // 1 KB copies per wave and K step
+  static constexpr int NCA = BM / 8;                  // 1 KB copies of the m side per K step,
+  static constexpr int CA = (NCA + NW - 1) / NW;      // at most so many per wave
   static constexpr int CBS = SUBN / 8 / NW;
   static constexpr int CB = CBS * NSUB, C = CA + CB;
   static constexpr int NG = MT < NT ? MT : NT;        // MFMA groups per slice
   static constexpr int NI = MT < NT ? NT : MT;        // MFMAs per group
   static constexpr bool OUTER_N = NT <= MT;           // groups run over the n side's fragments
   static constexpr int STAGE_A = BM * BK, STAGE_B = BN * BK;
-  static constexpr int LDS_ELEMS = 2 * (STAGE_A + STAGE_B);
-  static_assert(CA * NW * 8 == BM && CBS * NW * 8 == SUBN && CA % 2 == 0 && CBS % 2 == 0, "copy plan does not cover the tile");
-  static_assert((NG == 4 && (NI == 8 || NI == 4)) || (NG == 2 && (NI == 2 || NI == 4)), "no read plan for this wave tile");
+  static constexpr int LDS_ELEMS = NS * (STAGE_A + STAGE_B);
+  static_assert(NCA * 8 == BM && CBS * NW * 8 == SUBN, "copy plan does not cover the tile");
+  static_assert(NS == 2 || NS == 3, "wait_steps keeps one later step in flight");
+  static_assert(LDS_ELEMS * 2 <= 160 * 1024, "the stages exceed the LDS");
+  static_assert(NG >= 2 && NI <= 8 && WM * WGM == BM && MT * 16 == WM && NT * 16 == WN, "no read plan for this wave tile");
 };
 
 // One side of the product as the copies see it: `p` is the matrix, x0 the
@@ -281,7 +302,7 @@ struct TileFrags {
 };
 
 // SEGS = 2: the K loop runs over two products, a[0] b[0] + a[1] b[1].
-template <typename T, typename TO, Lay LA, Lay LB, int SEGS, int EPI, int ACT, typename G>
+template <typename T, typename TO, Lay LA, Lay LB, int SEGS, int EPI, typename G>
 struct Tile {
   static constexpr int RA = CopyRows<LA, G::BM>::N, RB = CopyRows<LB, G::SUBN>::N;
   static_assert(SEGS == 1 || G::NSUB == 1, "segments of a gated product are not implemented");
@@ -297,9 +318,9 @@ struct Tile {
     uint32_t ra, rb, na, nb;
     int K;
   };
-  // Lane offsets of a wave's copies, the two swizzle patterns per side.
+  // Lane offset of a wave's copies, per side.
   struct Pats {
-    uint32_t a[2], b[2];
+    uint32_t a, b;
   };
   // Sources of one K step.
   struct Step {
@@ -327,8 +348,8 @@ struct Tile {
     const Args p = fresh(k);
     Hot h;
     h.K = p->K;
-    h.ra = (uint32_t)(RA * p->lda * (int)sizeof(T));
-    h.rb = (uint32_t)(RB * p->ldb * (int)sizeof(T));
+    h.ra = (uint32_t)(G::NW * RA * p->lda * (int)sizeof(T));
+    h.rb = (uint32_t)(G::NW * RB * p->ldb * (int)sizeof(T));
     h.ka = (LA == LAY_K ? 1 : p->lda) * (int64_t)sizeof(T);
     h.kb = (LB == LAY_K ? 1 : p->ldb) * (int64_t)sizeof(T);
     const Side sa = side_a(p, at, seg);
@@ -359,51 +380,50 @@ struct Tile {
     return t;
   }
 
-  // Which of the two patterns copy j of a wave's NC follows: the swizzles take
-  // bit 3 (and, in rows of 512 bytes, bit 1) of the row.
-  template <Lay L, int BX, int NC>
-  static constexpr int pat_of(int j) {
-    return L == LAY_X && BX == 128 ? (NC >= 4 ? (j >> 1) & 1 : 0) : j & 1;
-  }
-  // Lane offset of copy j of wave wu, less the j RPC rows that copy() adds.
-  template <Lay L, int BX, int NC>
-  static __device__ __forceinline__ uint32_t pattern(int64_t ld, int i, int wu, int lane) {
+  // Copy j of wave wu fills rows from (j NW + wu) RPC on: the copies of a wave
+  // differ by a whole number of NW RPC rows, a multiple of the swizzles'
+  // period, so one lane offset per side serves them all and the rows are a
+  // uniform offset.
+  template <Lay L, int BX>
+  static __device__ __forceinline__ uint32_t pattern(int64_t ld, int wu, int lane) {
     constexpr int RPC = CopyRows<L, BX>::N;
-    const int j = pat_of<L, BX, NC>(1) == 1 ? i : 2 * i;  // a copy that follows pattern i
-    const int first = wu * NC * RPC, row = j * RPC;
+    static_assert(G::NW * RPC % 16 == 0, "the swizzles repeat every 16 rows");
     const uint32_t ld_b = (uint32_t)ld * (uint32_t)sizeof(T);
     if constexpr (L == LAY_K) {
-      const int r = lane >> 3;
-      return (uint32_t)(first + r) * ld_b + (uint32_t)((((lane & 7) ^ swzA(first + row + r)) * 8) * (int)sizeof(T));
+      const int row = wu * RPC + (lane >> 3);
+      return (uint32_t)row * ld_b + (uint32_t)((((lane & 7) ^ swzA(row)) * 8) * (int)sizeof(T));
     } else {
       constexpr int CPR = BX / 8;
-      const int r = lane / CPR;
-      return (uint32_t)(first + r) * ld_b +
-             (uint32_t)((((lane & (CPR - 1)) ^ swzB<CPR>(first + row + r)) * 8) * (int)sizeof(T));
+      const int row = wu * RPC + lane / CPR;
+      return (uint32_t)row * ld_b + (uint32_t)((((lane & (CPR - 1)) ^ swzB<CPR>(row)) * 8) * (int)sizeof(T));
     }
   }
   static __device__ __forceinline__ Pats patterns(Args k, int wu, int lane) {
     const Args p = fresh(k);
-    Pats o;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      o.a[i] = pattern<LA, G::BM, G::CA>(p->lda, i, wu, lane);
-      o.b[i] = pattern<LB, G::SUBN, G::CBS>(p->ldb, i, wu, lane);
-    }
-    return o;
+    return Pats{pattern<LA, G::BM>(p->lda, wu, lane), pattern<LB, G::SUBN>(p->ldb, wu, lane)};
   }
 
-  // Copy j (0 .. C - 1) of a K step into stage (a, b).  The copies of a wave
-  // differ by a whole number of rows, a uniform offset, and by one of two
-  // swizzle patterns: two lane offsets per side are all that stays in
-  // registers.
+  // Copy j (0 .. C - 1) of a K step into stage (a, b).
   static __device__ __forceinline__ void copy(const Hot& h, const Pats& pt, const Step& st, int j, T* a, T* b, int wu) {
     if (j < G::CA) {
-      dma16_buf(st.a, pt.a[pat_of<LA, G::BM, G::CA>(j)], (uint32_t)j * h.ra, lds_addr(a) + (uint32_t)(wu * G::CA + j) * 1024u);
+      if ((j + 1) * G::NW > G::NCA && j * G::NW + wu >= G::NCA) return;
+      dma16_buf(st.a, pt.a, (uint32_t)j * h.ra, lds_addr(a) + (uint32_t)(j * G::NW + wu) * 1024u);
     } else {
       const int sub = (j - G::CA) / G::CBS, jj = (j - G::CA) % G::CBS;
-      dma16_buf(st.b[sub], pt.b[pat_of<LB, G::SUBN, G::CBS>(jj)], (uint32_t)jj * h.rb,
-                lds_addr(b) + (uint32_t)(sub * G::SUBN * BK * (int)sizeof(T)) + (uint32_t)(wu * G::CBS + jj) * 1024u);
+      dma16_buf(st.b[sub], pt.b, (uint32_t)jj * h.rb,
+                lds_addr(b) + (uint32_t)(sub * G::SUBN * BK * (int)sizeof(T)) + (uint32_t)(jj * G::NW + wu) * 1024u);
+    }
+  }
+  // Waits until at most LATER later K steps' copies of this wave are in flight.
+  template <int LATER>
+  static __device__ __forceinline__ void wait_steps(int wu) {
+    if constexpr (LATER == 0 || G::NCA % G::NW == 0) {
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LATER * G::C) : "memory");
+    } else {  // the last round of m-side copies is only some waves'
+      if (wu < G::NCA % G::NW)
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LATER * G::C) : "memory");
+      else
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LATER * (G::C - 1)) : "memory");
     }
   }
 
@@ -417,18 +437,20 @@ struct Tile {
     i16x8 ra[G::CA], rb[G::CB];
     const Side sa = side_a(p, at, seg);
 #pragma unroll
-    for (int j = 0; j < G::CA; ++j) ra[j] = tail_chunk<T, LA, G::BM>(sa, w * G::CA + j, lane, st.k0, K);
+    for (int j = 0; j < G::CA; ++j)
+      if (j * G::NW + w < G::NCA) ra[j] = tail_chunk<T, LA, G::BM>(sa, j * G::NW + w, lane, st.k0, K);
 #pragma unroll
     for (int j = 0; j < G::CB; ++j)
-      rb[j] = tail_chunk<T, LB, G::SUBN>(side_b(p, at, seg, j / G::CBS), w * G::CBS + j % G::CBS, lane, st.k0, K);
+      rb[j] = tail_chunk<T, LB, G::SUBN>(side_b(p, at, seg, j / G::CBS), j % G::CBS * G::NW + w, lane, st.k0, K);
 #pragma unroll
-    for (int j = 0; j < G::CA; ++j) *(i16x8*)(a + (w * G::CA + j) * 512 + lane * 8) = ra[j];
+    for (int j = 0; j < G::CA; ++j)
+      if (j * G::NW + w < G::NCA) *(i16x8*)(a + (j * G::NW + w) * 512 + lane * 8) = ra[j];
 #pragma unroll
     for (int j = 0; j < G::CB; ++j)
-      *(i16x8*)(b + (j / G::CBS) * G::SUBN * BK + (w * G::CBS + j % G::CBS) * 512 + lane * 8) = rb[j];
+      *(i16x8*)(b + (j / G::CBS) * G::SUBN * BK + (j % G::CBS * G::NW + w) * 512 + lane * 8) = rb[j];
   }
 
-  // K step s, all copies at once (a segment's first two steps).
+  // K step s, all copies at once (a segment's first NS steps).
   static __device__ __forceinline__ void fill(Args k, const TileAt& at, int seg, const Hot& h, const Pats& pt, int s,
                                               T* a, T* b, int wu, int lane) {
     const Step st = step_at(h, s);
@@ -486,15 +508,19 @@ struct Tile {
         read_outer(0);
 #pragma unroll
         for (int i = 0; i < (G::NI < 4 ? G::NI : 4); ++i) read_inner(i);
-      } else if (G::NI == 8) {
+      } else if (G::NI > 4) {
+        // the rest of the inner side in group 1, the outer fragments spread
+        // over the groups behind it
         if (g == 1) {
 #pragma unroll
-          for (int i = 4; i < 8; ++i) read_inner(i);
-        } else if (g == 2) {
-          read_outer(1);
-          read_outer(2);
+          for (int i = 4; i < G::NI; ++i) read_inner(i);
+          if (G::NG == 2) read_outer(1);
         } else {
-          read_outer(3);
+          constexpr int REST = G::NG - 1, LEFT = G::NG - 2;  // fragments, groups
+#pragma unroll
+          for (int i = 1 + ((g - 2) * REST + LEFT - 1) / (LEFT > 0 ? LEFT : 1);
+               i < 1 + ((g - 1) * REST + LEFT - 1) / (LEFT > 0 ? LEFT : 1); ++i)
+            read_outer(i);
         }
       } else {
         read_outer(g);
@@ -578,6 +604,7 @@ struct Tile {
                 [&](int, int t, int s, int, int, int) { return acc[t + sub * G::NTO][s]; });
       }
     } else {
+      const int act = p->act;
       auto bias_g = [&](int, int n, int valid) { return bias4(p->bias[0], n, valid); };
       auto bias_u = [&](int, int n, int valid) { return bias4(p->bias[1], n, valid); };
       // the stored pre-activations of a training forward, one rounding each
@@ -596,10 +623,7 @@ struct Tile {
                 [&](int t, int n, int valid) { return Pair{bias_g(t, n, valid), bias_u(t, n, valid)}; },
                 [&](Pair c, int t, int s, int, int, int) {
                   const f32x4 g = acc[t][s] + c.g, u = acc[t + G::NTO][s] + c.u;
-                  f32x4 o;
-#pragma unroll
-                  for (int r = 0; r < 4; ++r) o[r] = apply_act<ACT, O16>(g[r]) * u[r];
-                  return o;
+                  return act_any<O16>(act, g) * u;
                 });
       } else {
         const TO* R = (const TO*)p->R;
@@ -608,9 +632,7 @@ struct Tile {
                   const f32x4 z = acc[t][s] + c;
                   f32x4 o = (f32x4){0.f, 0.f, 0.f, 0.f};
                   if (R) o = load4<TO>(R + (int64_t)m * p->ldr + n, valid);
-#pragma unroll
-                  for (int r = 0; r < 4; ++r) o[r] += apply_act<ACT, O16>(z[r]);
-                  return o;
+                  return o + act_any<O16>(act, z);
                 });
       }
     }
@@ -644,10 +666,13 @@ struct Tile {
 
   static __device__ __forceinline__ void run(Args k, T* lds) {
     const Args p = fresh(k);
-    T* const a0 = lds;
-    T* const a1 = lds + G::STAGE_A;
-    T* const b0 = lds + 2 * G::STAGE_A;
-    T* const b1 = b0 + G::STAGE_B;
+    auto sa = [&](int i) { return lds + i * G::STAGE_A; };
+    auto sb = [&](int i) { return lds + G::NS * G::STAGE_A + i * G::STAGE_B; };
+    auto fill_first = [&](const TileAt& at, int seg, const Hot& h, const Range1& r, const Pats& pt, int wu, int lane) {
+#pragma unroll
+      for (int i = 0; i < G::NS; ++i)
+        if (i < r.n) fill(k, at, seg, h, pt, r.s + i, sa(i), sb(i), wu, lane);
+    };
     const int64_t total = (int64_t)p->tiles_m * p->tiles_n * p->batch * p->splits;
     int64_t v = blockIdx.x;
     if (v >= total) return;
@@ -659,8 +684,7 @@ struct Tile {
     Hot h = hot(k, at, 0);
     Range1 r = part(at, h, 0);
     const Pats pt = patterns(k, wu, lane0);
-    if (r.n > 0) fill(k, at, 0, h, pt, r.s, a0, b0, wu, lane0);
-    if (r.n > 1) fill(k, at, 0, h, pt, r.s + 1, a1, b1, wu, lane0);
+    fill_first(at, 0, h, r, pt, wu, lane0);
     while (true) {
       // the lane index through an opaque copy: everything derived from it is
       // recomputed per tile instead of being held across the K loop
@@ -679,44 +703,45 @@ struct Tile {
           h = hot(k, at, seg);
           r = part(at, h, seg);
           __syncthreads();  // every wave is past its last fragment read
-          if (r.n > 0) fill(k, at, seg, h, pt, r.s, a0, b0, wu, lane);
-          if (r.n > 1) fill(k, at, seg, h, pt, r.s + 1, a1, b1, wu, lane);
+          fill_first(at, seg, h, r, pt, wu, lane);
         }
         TileFrags<G> f0, f1;
         if (r.n > 0) {
           wait_vmcnt0();
           __syncthreads();
 #pragma unroll
-          for (int i = 0; i < G::NT; ++i) f0.n[i] = frag_n(b0, 0, wn, i, lane);
+          for (int i = 0; i < G::NT; ++i) f0.n[i] = frag_n(sb(0), 0, wn, i, lane);
 #pragma unroll
-          for (int i = 0; i < G::MT; ++i) f0.m[i] = frag_m(a0, 0, wm, i, lane);
+          for (int i = 0; i < G::MT; ++i) f0.m[i] = frag_m(sa(0), 0, wm, i, lane);
         }
-        // Per K step k (stage cur; the other stage holds step k + 1 or is
-        // filling): slice 0 on f0 while f1 is read; barrier (cur is free, step
-        // k + 1 has landed); slice 1 on f1 while step k + 2 is copied into cur
-        // and f0 of step k + 1 is read.
-        for (int kt = 0; kt < r.n; kt += 2) {
+        // Per K step i (stage c; the other stages hold the next steps or are
+        // filling): slice 0 on f0 while f1 is read; barrier (stage c is free,
+        // step i + 1 has landed); slice 1 on f1 while step i + NS is copied into
+        // stage c and f0 of step i + 1 is read.
+        for (int kt = 0; kt < r.n; kt += G::NS) {
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int i = kt + half;
+          for (int c = 0; c < G::NS; ++c) {
+            const int i = kt + c;
             if (i < r.n) {
-              T* const ca = half ? a1 : a0;
-              T* const cb = half ? b1 : b0;
-              T* const na = half ? a0 : a1;
-              T* const nb = half ? b0 : b1;
+              const int nx = (c + 1) % G::NS;
               Step st{};
-              slice(f0, acc, f1, ca, cb, 1, wm, wn, lane, false, h, pt, st, ca, cb, wu);
+              slice(f0, acc, f1, sa(c), sb(c), 1, wm, wn, lane, false, h, pt, st, sa(c), sb(c), wu);
               if (i + 1 < r.n) {
-                wait_vmcnt0();
-                __syncthreads();
+                // the copies of step i + 2 may stay in flight, if that step has
+                // any
+                if (G::NS > 2 && i + 2 < r.n && (r.s + i + 2) * BK + BK <= h.K)
+                  wait_steps<G::NS - 2>(wu);
+                else
+                  wait_vmcnt0();
+                lds_barrier();
               }
               bool cp = false;
-              if (i + 2 < r.n) {
-                st = step_at(h, r.s + i + 2);
+              if (i + G::NS < r.n) {
+                st = step_at(h, r.s + i + G::NS);
                 cp = st.k0 + BK <= h.K;
-                if (!cp) tail(k, at, seg, st, ca, cb, wu, lane);
+                if (!cp) tail(k, at, seg, st, sa(c), sb(c), wu, lane);
               }
-              slice(f1, acc, f0, na, nb, 0, wm, wn, lane, cp, h, pt, st, ca, cb, wu);
+              slice(f1, acc, f0, sa(nx), sb(nx), 0, wm, wn, lane, cp, h, pt, st, sa(c), sb(c), wu);
             }
           }
         }
@@ -729,22 +754,21 @@ struct Tile {
       at = locate(k, v);
       h = hot(k, at, 0);
       r = part(at, h, 0);
-      if (r.n > 0) fill(k, at, 0, h, pt, r.s, a0, b0, wu, lane);
-      if (r.n > 1) fill(k, at, 0, h, pt, r.s + 1, a1, b1, wu, lane);
+      fill_first(at, 0, h, r, pt, wu, lane);
     }
   }
 };
 
-template <typename T, typename TO, Lay LA, Lay LB, int SEGS, int EPI, int ACT, typename G>
+template <typename T, typename TO, Lay LA, Lay LB, int SEGS, int EPI, typename G>
 __global__ __launch_bounds__(G::THREADS, G::MINW) void tile_kernel(TileOp) {  // read through the argument segment
   __shared__ __attribute__((aligned(1024))) T lds[G::LDS_ELEMS];
-  Tile<T, TO, LA, LB, SEGS, EPI, ACT, G>::run((Args)__builtin_amdgcn_kernarg_segment_ptr(), lds);
+  Tile<T, TO, LA, LB, SEGS, EPI, G>::run((Args)__builtin_amdgcn_kernarg_segment_ptr(), lds);
 }
 
 // Grid: min(#units of work, #CUs x workgroups per CU), the per-CU count from
 // the runtime for the compiled kernel, cached per instantiation (atomic:
 // concurrent first calls store the same value).
-template <typename T, typename TO, Lay LA, Lay LB, int SEGS, int EPI, int ACT, typename G>
+template <typename T, typename TO, Lay LA, Lay LB, int SEGS, int EPI, typename G>
 hipError_t launch_tile(TileOp p, hipStream_t stream, int num_cus) {
   p.tiles_m = (p.M + G::BM - 1) / G::BM;
   p.tiles_n = (p.N + G::ON - 1) / G::ON;
@@ -753,7 +777,7 @@ hipError_t launch_tile(TileOp p, hipStream_t stream, int num_cus) {
   int per_cu = per_cu_cache.load(std::memory_order_relaxed);
   if (per_cu == 0) {
     int n = 0;
-    hipError_t e = hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, tile_kernel<T, TO, LA, LB, SEGS, EPI, ACT, G>,
+    hipError_t e = hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, tile_kernel<T, TO, LA, LB, SEGS, EPI, G>,
                                                                 G::THREADS, 0);
     if (e != hipSuccess) return e;
     per_cu = n > 0 ? n : 1;
@@ -761,7 +785,7 @@ hipError_t launch_tile(TileOp p, hipStream_t stream, int num_cus) {
   }
   const int64_t total = (int64_t)p.tiles_m * p.tiles_n * p.batch * p.splits;
   const int64_t cap = (int64_t)num_cus * per_cu;
-  hipLaunchKernelGGL((tile_kernel<T, TO, LA, LB, SEGS, EPI, ACT, G>), dim3((unsigned)(total < cap ? total : cap)),
+  hipLaunchKernelGGL((tile_kernel<T, TO, LA, LB, SEGS, EPI, G>), dim3((unsigned)(total < cap ? total : cap)),
                      dim3(G::THREADS), 0, stream, p);
   return hipGetLastError();
 }

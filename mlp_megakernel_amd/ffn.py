@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import array
 import math
+import operator
 from typing import NamedTuple, Optional, Sequence, Tuple
 
 import torch
@@ -356,31 +357,42 @@ def _address(a: array.array) -> int:
     return a.buffer_info()[0]
 
 
+_tensor = torch.Tensor
+_dtype_of = operator.attrgetter("dtype")
+
+
 def _grad_list(tensors, out):
     """(count, device, sources, destinations, sizes, types): the host arrays of
     the C call, to be kept alive until it returns."""
     tensors = list(tensors)
-    devs = {t.get_device() for t in tensors}
+    devs = set(map(_tensor.get_device, tensors))
     dev = devs.pop() if devs else _current_device()
     if devs or dev < 0:
         raise ValueError("the tensors must lie on one GPU")
     try:
-        dts = array.array("i", [_DTYPES[t.dtype] for t in tensors])
+        dts = array.array("i", map(_DTYPES.__getitem__, map(_dtype_of, tensors)))
     except KeyError:
         raise ValueError("every tensor must be float32, float16 or bfloat16") from None
-    numel = array.array("q", [t.numel() for t in tensors])
-    for i, t in enumerate(tensors):
-        if not t.is_contiguous() and not _dense(t):
-            raise ValueError("tensor %d must be dense (its elements one run of memory)" % i)
-    src = array.array("Q", [t.data_ptr() for t in tensors])
+    numel = array.array("q", map(_tensor.numel, tensors))
+    src = array.array("Q", map(_tensor.data_ptr, tensors))
+    plain = all(map(_tensor.is_contiguous, tensors))
+    if not plain:
+        for i, t in enumerate(tensors):
+            if not _dense(t):
+                raise ValueError("tensor %d must be dense (its elements one run of memory)" % i)
     if out is None:
         return len(tensors), dev, src, src, numel, dts
-    if len(out) != len(tensors):
-        raise ValueError("out must hold one tensor per gradient")
-    for i, (t, o) in enumerate(zip(tensors, out)):
-        if o.shape != t.shape or o.dtype is not t.dtype or o.get_device() != dev or o.stride() != t.stride():
-            raise ValueError("out[%d] must have its gradient's shape, strides, dtype and device" % i)
-    return len(tensors), dev, src, array.array("Q", [t.data_ptr() for t in out]), numel, dts
+    out = list(out)
+    # contiguous tensors go by their sizes, others by shape and strides
+    same = len(out) == len(tensors) and set(map(_tensor.get_device, out)) <= {dev} and \
+        list(map(_dtype_of, out)) == list(map(_dtype_of, tensors))
+    if same and plain:
+        same = array.array("q", map(_tensor.numel, out)) == numel and all(map(_tensor.is_contiguous, out))
+    elif same:
+        same = all(o.shape == t.shape and o.stride() == t.stride() for t, o in zip(tensors, out))
+    if not same:
+        raise ValueError("out must hold one tensor per gradient, of its size, memory order, dtype and device")
+    return len(tensors), dev, src, array.array("Q", map(_tensor.data_ptr, out)), numel, dts
 
 
 def _norm_code(norm_type) -> int:
@@ -413,7 +425,7 @@ def clip_grad_norm(tensors: Sequence[torch.Tensor], max_norm: float, norm_type=2
     """Scale gradients so that their global norm is at most ``max_norm``
     (coalesce_clip_grad_norm) and return the norm they had, a float32 scalar on
     their device.  In place, or into ``out`` (one tensor per gradient, of its
-    shape, strides and dtype).  Nothing synchronises with the host; tensors of
+    size, memory order and dtype).  Nothing synchronises with the host; tensors of
     several dtypes may be mixed."""
     return _norm_call(_grad_list(tensors, out), float(max_norm), norm_type, norm, workspace, stream)
 
