@@ -64,12 +64,18 @@ TilePlan plan_tiles(int64_t m, int64_t n, bool gated, int batch, int64_t ksteps,
       if (splits > 1 && ((v != kShape128 && v != kShape64) || ksteps / splits < 4)) break;
       const int64_t units = tiles * splits, full = (int64_t)num_cus * s.slots;
       const int64_t rounds = units / full, rest = units - rounds * full;
-      const int in_rest = (int)((rest + num_cus - 1) / num_cus);  // 0 .. slots
-      double t = (double)rounds * s.step[s.slots - 1] + (in_rest ? s.step[in_rest - 1] : 0.0);
+      // the last round's step: between the times of the tile counts around its
+      // load (the compute units share the caches, so the ones with a tile more
+      // are not the slower for it)
+      const double x = (double)rest / num_cus;
+      const int i = std::min(std::max((int)x, 1), s.slots);
+      const double last = rest == 0 ? 0.0 : i < s.slots && x > i ? s.step[i - 1] + (x - i) * (s.step[i] - s.step[i - 1])
+                                                                 : s.step[i - 1];
+      double t = (double)rounds * s.step[s.slots - 1] + last;
       const double load = (double)units / num_cus;
       const double gb = load >= 3 ? 4500 : load >= 2 ? 4000 : load >= 1 ? 3000 : 3000 * load;
       t = std::max(t * (double)((ksteps + splits - 1) / splits), operand_bytes / gb) + s.launch +
-          ((double)rounds + (in_rest > 0)) * s.round;
+          ((double)rounds + (rest > 0)) * s.round;
       if (splits > 1) t += 4500 + (double)splits * (double)m * (double)n * (gated ? 2 : batch) * 8.0 / 6000.0;
       if (t < best.ns) best = {v, splits, t};
       if (units > 2 * full) break;

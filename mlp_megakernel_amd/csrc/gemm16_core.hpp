@@ -187,11 +187,15 @@ struct TileGeo {
   static constexpr int NG = MT < NT ? MT : NT;        // MFMA groups per slice
   static constexpr int NI = MT < NT ? NT : MT;        // MFMAs per group
   static constexpr bool OUTER_N = NT <= MT;           // groups run over the n side's fragments
-  static constexpr int STAGE_A = BM * BK, STAGE_B = BN * BK;
+  // The last round of m-side copies may have more waves than rows are left:
+  // their copies (out of the range, zeros) get room behind the tile's rows, or,
+  // where three stages leave none, one place behind the stages.
+  static constexpr bool ROOM = NS * (CA * NW * 8 + BN) * BK * 2 <= 160 * 1024;
+  static constexpr int STAGE_A = (ROOM ? CA * NW * 8 : BM) * BK, STAGE_B = BN * BK;
   static constexpr int LDS_ELEMS = NS * (STAGE_A + STAGE_B);
   static_assert(NCA * 8 == BM && CBS * NW * 8 == SUBN, "copy plan does not cover the tile");
   static_assert(NS == 2 || NS == 3, "wait_steps keeps one later step in flight");
-  static_assert(LDS_ELEMS * 2 <= 160 * 1024, "the stages exceed the LDS");
+  static_assert(LDS_ELEMS * 2 + (ROOM ? 0 : 1024) <= 160 * 1024, "the stages exceed the LDS");
   static_assert(NG >= 2 && NI <= 8 && WM * WGM == BM && MT * 16 == WM && NT * 16 == WN, "no read plan for this wave tile");
 };
 
@@ -404,10 +408,20 @@ struct Tile {
   }
 
   // Copy j (0 .. C - 1) of a K step into stage (a, b).
-  static __device__ __forceinline__ void copy(const Hot& h, const Pats& pt, const Step& st, int j, T* a, T* b, int wu) {
+  // The m side's stages lie first in the LDS, lds_stage is a's number.
+  static __device__ __forceinline__ void copy(const Hot& h, const Pats& pt, const Step& st, int j, uint32_t lds_stage,
+                                              T* a, T* b, int wu) {
     if (j < G::CA) {
-      if ((j + 1) * G::NW > G::NCA && j * G::NW + wu >= G::NCA) return;
-      dma16_buf(st.a, pt.a, (uint32_t)j * h.ra, lds_addr(a) + (uint32_t)(j * G::NW + wu) * 1024u);
+      u32x4 r = st.a;
+      uint32_t at = (uint32_t)(j * G::NW + wu) * 1024u;
+      if (!G::ROOM && (j + 1) * G::NW > G::NCA) {
+        // waves without a copy left copy zeros from an empty range, so that all
+        // waves count the same number
+        const bool mine = j * G::NW + wu < G::NCA;
+        r[2] = mine ? r[2] : 0u;
+        at = mine ? at : (uint32_t)(G::LDS_ELEMS * (int)sizeof(T)) - lds_stage * (uint32_t)(G::STAGE_A * (int)sizeof(T));
+      }
+      dma16_buf(r, pt.a, (uint32_t)j * h.ra, lds_addr(a) + at);
     } else {
       const int sub = (j - G::CA) / G::CBS, jj = (j - G::CA) % G::CBS;
       dma16_buf(st.b[sub], pt.b, (uint32_t)jj * h.rb,
@@ -416,35 +430,35 @@ struct Tile {
   }
   // Waits until at most LATER later K steps' copies of this wave are in flight.
   template <int LATER>
-  static __device__ __forceinline__ void wait_steps(int wu) {
-    if constexpr (LATER == 0 || G::NCA % G::NW == 0) {
-      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LATER * G::C) : "memory");
-    } else {  // the last round of m-side copies is only some waves'
-      if (wu < G::NCA % G::NW)
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LATER * G::C) : "memory");
-      else
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LATER * (G::C - 1)) : "memory");
-    }
+  static __device__ __forceinline__ void wait_steps() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LATER * G::C) : "memory");
   }
 
+  // The m side's copy j of wave w; past the last one it again (the same bytes
+  // to the same place).  w comes in a vector register: a comparison with the
+  // uniform wave number here makes the compiler keep the whole tile's addresses
+  // in vector registers, read back to scalars at each copy.
+  static __device__ __forceinline__ int m_chunk(int j, int w) {
+    return G::ROOM || (j + 1) * G::NW <= G::NCA ? j * G::NW + w : min(j * G::NW + w, G::NCA - 1);
+  }
   static __device__ __forceinline__ void tail(Args k, const TileAt& at, int seg, const Step& st, T* a, T* b, int w,
                                               int lane) {
     // the lane through an opaque copy: the addresses are formed here, not
     // carried in registers through the K loop
     asm volatile("" : "+v"(lane));
+    int wv = w;
+    asm volatile("" : "+v"(wv));
     const Args p = fresh(k);
     const int K = p->K;
     i16x8 ra[G::CA], rb[G::CB];
     const Side sa = side_a(p, at, seg);
 #pragma unroll
-    for (int j = 0; j < G::CA; ++j)
-      if (j * G::NW + w < G::NCA) ra[j] = tail_chunk<T, LA, G::BM>(sa, j * G::NW + w, lane, st.k0, K);
+    for (int j = 0; j < G::CA; ++j) ra[j] = tail_chunk<T, LA, G::BM>(sa, m_chunk(j, wv), lane, st.k0, K);
 #pragma unroll
     for (int j = 0; j < G::CB; ++j)
       rb[j] = tail_chunk<T, LB, G::SUBN>(side_b(p, at, seg, j / G::CBS), j % G::CBS * G::NW + w, lane, st.k0, K);
 #pragma unroll
-    for (int j = 0; j < G::CA; ++j)
-      if (j * G::NW + w < G::NCA) *(i16x8*)(a + (j * G::NW + w) * 512 + lane * 8) = ra[j];
+    for (int j = 0; j < G::CA; ++j) *(i16x8*)(a + m_chunk(j, wv) * 512 + lane * 8) = ra[j];
 #pragma unroll
     for (int j = 0; j < G::CB; ++j)
       *(i16x8*)(b + (j / G::CBS) * G::SUBN * BK + (j % G::CBS * G::NW + w) * 512 + lane * 8) = rb[j];
@@ -452,11 +466,11 @@ struct Tile {
 
   // K step s, all copies at once (a segment's first NS steps).
   static __device__ __forceinline__ void fill(Args k, const TileAt& at, int seg, const Hot& h, const Pats& pt, int s,
-                                              T* a, T* b, int wu, int lane) {
+                                              uint32_t stage, T* a, T* b, int wu, int lane) {
     const Step st = step_at(h, s);
     if (st.k0 + BK <= h.K) {
 #pragma unroll
-      for (int j = 0; j < G::C; ++j) copy(h, pt, st, j, a, b, wu);
+      for (int j = 0; j < G::C; ++j) copy(h, pt, st, j, stage, a, b, wu);
     } else {
       tail(k, at, seg, st, a, b, wu, lane);
     }
@@ -477,7 +491,8 @@ struct Tile {
   // "next" reads fetch stale but in-bounds LDS and are unused.
   static __device__ __forceinline__ void slice(const TileFrags<G>& cur, f32x4 (&acc)[G::NT][G::MT], TileFrags<G>& nxt,
                                                const T* ra, const T* rb, int rks, int wm, int wn, int lane, bool cp,
-                                               const Hot& h, const Pats& pt, const Step& st, T* ca, T* cb, int wu) {
+                                               const Hot& h, const Pats& pt, const Step& st, uint32_t stage, T* ca, T* cb,
+                                               int wu) {
     auto read_outer = [&](int i) {
       if constexpr (G::OUTER_N)
         nxt.n[i] = frag_n(rb, rks, wn, i, lane);
@@ -494,7 +509,7 @@ struct Tile {
     for (int g = 0; g < G::NG; ++g) {
       if (cp) {
 #pragma unroll
-        for (int j = G::C * g / G::NG; j < G::C * (g + 1) / G::NG; ++j) copy(h, pt, st, j, ca, cb, wu);
+        for (int j = G::C * g / G::NG; j < G::C * (g + 1) / G::NG; ++j) copy(h, pt, st, j, stage, ca, cb, wu);
       }
 #pragma unroll
       for (int i = 0; i < G::NI; ++i) {
@@ -671,7 +686,7 @@ struct Tile {
     auto fill_first = [&](const TileAt& at, int seg, const Hot& h, const Range1& r, const Pats& pt, int wu, int lane) {
 #pragma unroll
       for (int i = 0; i < G::NS; ++i)
-        if (i < r.n) fill(k, at, seg, h, pt, r.s + i, sa(i), sb(i), wu, lane);
+        if (i < r.n) fill(k, at, seg, h, pt, r.s + i, (uint32_t)i, sa(i), sb(i), wu, lane);
     };
     const int64_t total = (int64_t)p->tiles_m * p->tiles_n * p->batch * p->splits;
     int64_t v = blockIdx.x;
@@ -725,12 +740,12 @@ struct Tile {
             if (i < r.n) {
               const int nx = (c + 1) % G::NS;
               Step st{};
-              slice(f0, acc, f1, sa(c), sb(c), 1, wm, wn, lane, false, h, pt, st, sa(c), sb(c), wu);
+              slice(f0, acc, f1, sa(c), sb(c), 1, wm, wn, lane, false, h, pt, st, c, sa(c), sb(c), wu);
               if (i + 1 < r.n) {
                 // the copies of step i + 2 may stay in flight, if that step has
                 // any
                 if (G::NS > 2 && i + 2 < r.n && (r.s + i + 2) * BK + BK <= h.K)
-                  wait_steps<G::NS - 2>(wu);
+                  wait_steps<G::NS - 2>();
                 else
                   wait_vmcnt0();
                 lds_barrier();
@@ -741,7 +756,7 @@ struct Tile {
                 cp = st.k0 + BK <= h.K;
                 if (!cp) tail(k, at, seg, st, sa(c), sb(c), wu, lane);
               }
-              slice(f1, acc, f0, sa(nx), sb(nx), 0, wm, wn, lane, cp, h, pt, st, sa(c), sb(c), wu);
+              slice(f1, acc, f0, sa(nx), sb(nx), 0, wm, wn, lane, cp, h, pt, st, c, sa(c), sb(c), wu);
             }
           }
         }
@@ -761,7 +776,7 @@ struct Tile {
 
 template <typename T, typename TO, Lay LA, Lay LB, int SEGS, int EPI, typename G>
 __global__ __launch_bounds__(G::THREADS, G::MINW) void tile_kernel(TileOp) {  // read through the argument segment
-  __shared__ __attribute__((aligned(1024))) T lds[G::LDS_ELEMS];
+  __shared__ __attribute__((aligned(1024))) T lds[G::LDS_ELEMS + (G::ROOM ? 0 : 512)];
   Tile<T, TO, LA, LB, SEGS, EPI, G>::run((Args)__builtin_amdgcn_kernarg_segment_ptr(), lds);
 }
 
