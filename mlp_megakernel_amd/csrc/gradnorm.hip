@@ -12,6 +12,14 @@
 // same bits.  Squares are summed in fp64: they neither overflow nor round
 // (an fp32 gradient above 2^64 would overflow an fp32 sum), and at HBM speed
 // the conversion and the fma hide behind the loads.
+//
+// Both sweeps are bound by memory.  The second one goes from the list's end to
+// its start, so that it finds the last kKeepBytes, which the first one reads
+// through the caches, in the 256 MB one; what lies before them is read past the
+// caches (non-temporal), and so are the results of a list above kPastBytes
+// written.  1.2 GB of bf16: 705 us with every access through the caches, 647
+// past them, 625 with 160 MB kept (the norm alone 214 -> 188 us, 6.4 TB/s); a
+// list of 64 MB 38 us past them and 35 through them, of 128 MB 71 and 80.
 #include <algorithm>
 
 #include "common.hpp"
@@ -21,6 +29,22 @@ namespace coalesce {
 namespace {
 
 constexpr int THREADS = 256;
+constexpr int64_t kKeepBytes = int64_t(160) << 20, kPastBytes = int64_t(80) << 20;
+
+template <bool PAST, typename V>
+__device__ __forceinline__ V load_past(const V* p) {
+  if constexpr (PAST)
+    return __builtin_nontemporal_load(p);
+  else
+    return *p;
+}
+template <bool PAST, typename V>
+__device__ __forceinline__ void store_past(V* p, V v) {
+  if constexpr (PAST)
+    __builtin_nontemporal_store(v, p);
+  else
+    *p = v;
+}
 
 // x c as fp32, then one rounding to T: kept apart so that every path through
 // the kernel rounds alike (a fused multiply and conversion to fp16 rounds once
@@ -85,10 +109,36 @@ __device__ __forceinline__ int find_tensor(const ClipTable& t, int64_t c) {
   return lo;
 }
 
-template <typename T, bool INF>
-__global__ __launch_bounds__(THREADS) void norm_kernel(ClipTable t, double* partial) {
+// One chunk of n elements at p, added to the thread's four accumulators.
+template <typename T, bool INF, bool PAST>
+__device__ __forceinline__ void add_chunk(const T* p, int64_t n, Accum<INF> (&a)[4]) {
   typedef typename Vec<T>::type V;
   constexpr int VN = Vec<T>::N;
+  const int64_t head = min(n, (int64_t)(((16 - ((uintptr_t)p & 15)) & 15) / sizeof(T)));
+  const V* pv = (const V*)(p + head);
+  const int64_t nv = (n - head) / VN;
+  if ((int64_t)threadIdx.x < head) a[0].add((float)p[threadIdx.x]);
+  int64_t k = threadIdx.x;
+  for (; k + 3 * THREADS < nv; k += 4 * THREADS) {
+    V v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = load_past<PAST>(pv + k + u * THREADS);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int e = 0; e < VN; ++e) a[u].add((float)v[u][e]);
+  }
+  for (; k < nv; k += THREADS) {
+    const V v = load_past<PAST>(pv + k);
+#pragma unroll
+    for (int e = 0; e < VN; ++e) a[0].add((float)v[e]);
+  }
+  const int64_t done = head + nv * VN;
+  if ((int64_t)threadIdx.x < n - done) a[1].add((float)p[done + threadIdx.x]);
+}
+
+template <typename T, bool INF>
+__global__ __launch_bounds__(THREADS) void norm_kernel(ClipTable t, double* partial) {
   Accum<INF> a[4];
   const int64_t chunks = t.chunk_end[t.count - 1];
   for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
@@ -96,27 +146,10 @@ __global__ __launch_bounds__(THREADS) void norm_kernel(ClipTable t, double* part
     const int64_t e0 = (c - (i ? t.chunk_end[i - 1] : 0)) * t.chunk;
     const int64_t n = min(t.numel[i] - e0, t.chunk);
     const T* p = (const T*)t.src[i] + e0;
-    const int64_t head = min(n, (int64_t)(((16 - ((uintptr_t)p & 15)) & 15) / sizeof(T)));
-    const V* pv = (const V*)(p + head);
-    const int64_t nv = (n - head) / VN;
-    if ((int64_t)threadIdx.x < head) a[0].add((float)p[threadIdx.x]);
-    int64_t k = threadIdx.x;
-    for (; k + 3 * THREADS < nv; k += 4 * THREADS) {
-      V v[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) v[u] = pv[k + u * THREADS];
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int e = 0; e < VN; ++e) a[u].add((float)v[u][e]);
-    }
-    for (; k < nv; k += THREADS) {
-      const V v = pv[k];
-#pragma unroll
-      for (int e = 0; e < VN; ++e) a[0].add((float)v[e]);
-    }
-    const int64_t done = head + nv * VN;
-    if ((int64_t)threadIdx.x < n - done) a[1].add((float)p[done + threadIdx.x]);
+    if (c < t.keep)
+      add_chunk<T, INF, true>(p, n, a);
+    else
+      add_chunk<T, INF, false>(p, n, a);
   }
   double v;
   if constexpr (INF)
@@ -143,54 +176,60 @@ __global__ __launch_bounds__(THREADS) void norm_only_kernel(const double* partia
   if (threadIdx.x == 0) norm[0] = (float)v;
 }
 
-template <typename T, bool INF>
-__global__ __launch_bounds__(THREADS) void scale_kernel(ClipTable t, const double* partial, int n_partial,
-                                                        double max_norm, float* norm) {
+// o = p c over n elements.
+template <typename T, bool PAST>
+__device__ __forceinline__ void scale_chunk(const T* p, T* o, int64_t n, float coef) {
   typedef typename Vec<T>::type V;
   constexpr int VN = Vec<T>::N;
+  if ((((uintptr_t)p ^ (uintptr_t)o) & 15) != 0) {  // no common 16-byte grid
+    for (int64_t k = threadIdx.x; k < n; k += THREADS) o[k] = scaled<T>(p[k], coef);
+    return;
+  }
+  const int64_t head = min(n, (int64_t)(((16 - ((uintptr_t)p & 15)) & 15) / sizeof(T)));
+  const V* pv = (const V*)(p + head);
+  V* ov = (V*)(o + head);
+  const int64_t nv = (n - head) / VN;
+  if ((int64_t)threadIdx.x < head) o[threadIdx.x] = scaled<T>(p[threadIdx.x], coef);
+  int64_t k = threadIdx.x;
+  for (; k + 3 * THREADS < nv; k += 4 * THREADS) {
+    V v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = load_past<PAST>(pv + k + u * THREADS);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+#pragma unroll
+      for (int e = 0; e < VN; ++e) v[u][e] = scaled<T>(v[u][e], coef);
+      store_past<PAST>(ov + k + u * THREADS, v[u]);
+    }
+  }
+  for (; k < nv; k += THREADS) {
+    V v = load_past<PAST>(pv + k);
+#pragma unroll
+    for (int e = 0; e < VN; ++e) v[e] = scaled<T>(v[e], coef);
+    store_past<PAST>(ov + k, v);
+  }
+  const int64_t done = head + nv * VN;
+  if ((int64_t)threadIdx.x < n - done) o[done + threadIdx.x] = scaled<T>(p[done + threadIdx.x], coef);
+}
+
+template <typename T, bool INF>
+__global__ __launch_bounds__(THREADS) void scale_kernel(ClipTable t, const double* partial, int n_partial,
+                                                        double max_norm, bool past, float* norm) {
   const double total = total_norm<INF>(partial, n_partial);
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) norm[0] = (float)total;
   const double q = max_norm / (total + 1e-6);
   const float coef = q < 1.0 || q != q ? (float)q : 1.0f;
-  const int64_t chunks = t.chunk_end[t.count - 1];
-  // from the list's end to its start: what the first sweep read last may still
-  // be in the 256 MB cache
-  for (int64_t c = chunks - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
+  for (int64_t c = t.chunk_end[t.count - 1] - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
     const int i = find_tensor(t, c);
     if (coef == 1.0f && t.src[i] == t.dst[i]) continue;  // in place and nothing to scale
     const int64_t e0 = (c - (i ? t.chunk_end[i - 1] : 0)) * t.chunk;
     const int64_t n = min(t.numel[i] - e0, t.chunk);
     const T* p = (const T*)t.src[i] + e0;
     T* o = (T*)t.dst[i] + e0;
-    if ((((uintptr_t)p ^ (uintptr_t)o) & 15) != 0) {  // no common 16-byte grid
-      for (int64_t k = threadIdx.x; k < n; k += THREADS) o[k] = scaled<T>(p[k], coef);
-      continue;
-    }
-    const int64_t head = min(n, (int64_t)(((16 - ((uintptr_t)p & 15)) & 15) / sizeof(T)));
-    const V* pv = (const V*)(p + head);
-    V* ov = (V*)(o + head);
-    const int64_t nv = (n - head) / VN;
-    if ((int64_t)threadIdx.x < head) o[threadIdx.x] = scaled<T>(p[threadIdx.x], coef);
-    int64_t k = threadIdx.x;
-    for (; k + 3 * THREADS < nv; k += 4 * THREADS) {
-      V v[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) v[u] = pv[k + u * THREADS];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-#pragma unroll
-        for (int e = 0; e < VN; ++e) v[u][e] = scaled<T>(v[u][e], coef);
-        ov[k + u * THREADS] = v[u];
-      }
-    }
-    for (; k < nv; k += THREADS) {
-      V v = pv[k];
-#pragma unroll
-      for (int e = 0; e < VN; ++e) v[e] = scaled<T>(v[e], coef);
-      ov[k] = v;
-    }
-    const int64_t done = head + nv * VN;
-    if ((int64_t)threadIdx.x < n - done) o[done + threadIdx.x] = scaled<T>(p[done + threadIdx.x], coef);
+    if (past)
+      scale_chunk<T, true>(p, o, n, coef);
+    else
+      scale_chunk<T, false>(p, o, n, coef);
   }
 }
 
@@ -202,32 +241,52 @@ int64_t chunk_elems(int64_t total, int64_t es, int num_cus) {
   return c;
 }
 
-// Calls fn(table, dtype) for the list's tables: tensors of one dtype, in list
-// order, empty ones left out.
+int64_t dtype_bytes(int dt) { return dt == DT_F32 ? 4 : 2; }
+
+// Calls fn(table, dtype) for the list's tables: tensors of one dtype, empty ones
+// left out, in list order or (`backwards`) the tables from the list's end, each
+// in list order within itself.
 template <typename F>
-hipError_t for_tables(const ClipList& l, int num_cus, F fn) {
-  int64_t total = 0;
-  for (int64_t i = 0; i < l.count; ++i) total += l.numel[i];
-  for (int dt : {DT_F32, DT_F16, DT_BF16}) {
-    const int64_t chunk = chunk_elems(total, dt == DT_F32 ? 4 : 2, num_cus);
+hipError_t for_tables(const ClipList& l, int num_cus, bool backwards, F fn) {
+  int64_t total = 0, bytes = 0;
+  for (int64_t i = 0; i < l.count; ++i) {
+    total += l.numel[i];
+    bytes += l.numel[i] * dtype_bytes(l.dtype[i]);
+  }
+  int64_t before = 0;  // bytes of the tables so far
+  static const int order[2][3] = {{DT_F32, DT_F16, DT_BF16}, {DT_BF16, DT_F16, DT_F32}};
+  for (int dt : order[backwards]) {
+    const int64_t es = dtype_bytes(dt), chunk = chunk_elems(total, es, num_cus);
     ClipTable t{};
     t.chunk = chunk;
-    int64_t chunks = 0;
-    for (int64_t i = 0; i <= l.count; ++i) {
-      const bool end = i == l.count;
+    for (int64_t k = 0; k <= l.count; ++k) {
+      const bool end = k == l.count;
+      const int64_t i = backwards ? l.count - 1 - k : k;
       if (!end && (l.dtype[i] != dt || l.numel[i] == 0)) continue;
       if (t.count == kClipTensors || (end && t.count > 0)) {
+        if (backwards) {
+          std::reverse(t.src, t.src + t.count);
+          std::reverse(t.dst, t.dst + t.count);
+          std::reverse(t.numel, t.numel + t.count);
+        }
+        int64_t chunks = 0, elems = 0;
+        for (int j = 0; j < t.count; ++j) {
+          chunks += (t.numel[j] + chunk - 1) / chunk;
+          elems += t.numel[j];
+          t.chunk_end[j] = chunks;
+        }
+        // the list's last kKeepBytes, to a chunk
+        const int64_t cut = bytes - kKeepBytes - before;
+        t.keep = cut <= 0 ? 0 : std::min(chunks, cut / (chunk * es));
+        before += elems * es;
         const hipError_t e = fn(t, dt);
         if (e != hipSuccess) return e;
         t.count = 0;
-        chunks = 0;
       }
       if (end) break;
-      chunks += (l.numel[i] + chunk - 1) / chunk;
       t.src[t.count] = l.src ? l.src[i] : nullptr;
       t.dst[t.count] = l.dst ? l.dst[i] : nullptr;
       t.numel[t.count] = l.numel[i];
-      t.chunk_end[t.count] = chunks;
       ++t.count;
     }
   }
@@ -242,7 +301,7 @@ template <bool INF>
 hipError_t grad_norm_t(const ClipList& l, double max_norm, float* norm, double* partial, hipStream_t stream,
                        int num_cus) {
   int n = 0;
-  hipError_t e = for_tables(l, num_cus, [&](const ClipTable& t, int dt) {
+  hipError_t e = for_tables(l, num_cus, false, [&](const ClipTable& t, int dt) {
     const int g = grid_of(t, num_cus);
     double* out = partial + n;
     n += g;
@@ -259,18 +318,23 @@ hipError_t grad_norm_t(const ClipList& l, double max_norm, float* norm, double* 
     hipLaunchKernelGGL((norm_only_kernel<INF>), dim3(1), dim3(THREADS), 0, stream, partial, n, norm);
     return hipGetLastError();
   }
+  int64_t bytes = 0;
+  for (int64_t i = 0; i < l.count; ++i) bytes += l.numel[i] * dtype_bytes(l.dtype[i]);
+  const bool past = bytes > kPastBytes;
   bool first = true;
-  return for_tables(l, num_cus, [&](const ClipTable& t, int dt) {
+  return for_tables(l, num_cus, true, [&](const ClipTable& t, int dt) {
     const int g = grid_of(t, num_cus);
     float* out = first ? norm : nullptr;
     first = false;
     if (dt == DT_F32)
-      hipLaunchKernelGGL((scale_kernel<float, INF>), dim3(g), dim3(THREADS), 0, stream, t, partial, n, max_norm, out);
+      hipLaunchKernelGGL((scale_kernel<float, INF>), dim3(g), dim3(THREADS), 0, stream, t, partial, n, max_norm, past,
+                         out);
     else if (dt == DT_F16)
       hipLaunchKernelGGL((scale_kernel<_Float16, INF>), dim3(g), dim3(THREADS), 0, stream, t, partial, n, max_norm,
-                         out);
+                         past, out);
     else
-      hipLaunchKernelGGL((scale_kernel<__bf16, INF>), dim3(g), dim3(THREADS), 0, stream, t, partial, n, max_norm, out);
+      hipLaunchKernelGGL((scale_kernel<__bf16, INF>), dim3(g), dim3(THREADS), 0, stream, t, partial, n, max_norm, past,
+                         out);
     return hipGetLastError();
   });
 }
@@ -279,7 +343,7 @@ hipError_t grad_norm_t(const ClipList& l, double max_norm, float* norm, double* 
 
 size_t grad_norm_workspace(const ClipList& l, int num_cus) {
   size_t n = 0;
-  (void)for_tables(l, num_cus, [&](const ClipTable& t, int) {
+  (void)for_tables(l, num_cus, false, [&](const ClipTable& t, int) {
     n += (size_t)grid_of(t, num_cus);
     return hipSuccess;
   });

@@ -266,6 +266,7 @@ struct ClipTable {
   int64_t numel[kClipTensors];
   int64_t chunk_end[kClipTensors];  // chunks up to and including the tensor's
   int64_t chunk;                    // elements per chunk
+  int64_t keep;                     // chunks from this on are read through the caches, those before it past them
   int count;
 };
 size_t grad_norm_workspace(const ClipList& l, int num_cus);
