@@ -90,7 +90,7 @@ __device__ __forceinline__ void dz8(const float (&dy)[8], const float (&zg)[8], 
 // ragged column blocks are apart, so that no test of `valid` stands between a
 // load and the next: with the tests in one loop, 8192 x 16384 of a gated bf16
 // product took 314 us; now 236 us for 0.8 GB read and 0.5 GB written (5.6 TB/s,
-// above a large copy's 5.1), and 777 x 2730 in fp16 15.6 us instead of 20.
+// above a large copy's 5.1), and 1537 x 2731 in fp16 15.6 us instead of 20.
 template <typename T, typename TD, int ACT, bool GATED>
 __global__ __launch_bounds__(256) void dz_kernel(DzParams p) {
   constexpr bool NEEDS_Z = ACT != ACT_NONE || GATED;

@@ -1,6 +1,6 @@
 // The 16-bit MFMA tile machinery of the feed-forward operators: one workgroup
 // tile kernel over operands in either orientation, with the epilogue as a
-// template argument (ffn_gemm.hip, ffn_bwd.hip), and the building blocks it
+// template argument (ffn_forward.hpp, ffn_backward.hpp), and the building blocks it
 // shares with the plain fused GEMM (gemm16.hip).
 //
 //   acc[m][n] = sum_k Am[m][k] Bn[k][n]
@@ -14,8 +14,8 @@
 //          read.
 // So all three products of a layer (X W, dZ W^T, X^T dZ) run from the caller's
 // row-major matrices without a transposed copy.  The schedule is the one of the
-// plain fused GEMM: two LDS stages of a 64-deep K step, filled by direct
-// 16-byte copies two steps ahead; each 32-deep slice issued as groups of
+// plain fused GEMM: two (or three) LDS stages of a 64-deep K step, filled by direct
+// 16-byte copies that many steps ahead; each 32-deep slice issued as groups of
 // {copies, MFMAs, a share of the next slice's fragment reads}; persistent
 // workgroups whose next tile's copies start while the last stores drain.
 #pragma once
@@ -485,7 +485,7 @@ struct Tile {
     return read_frag<T, LB, G::SUBN, G::NTO>(b + sub * G::SUBN * BK, ks, wn * G::WNO, i % G::NTO, lane);
   }
 
-  // One 32-deep slice: NG groups of {a share of the copies of K step k + 2,
+  // One 32-deep slice: NG groups of {a share of the copies of K step k + NS,
   // NI MFMAs, a share of the next slice's fragment reads, those its first
   // group needs first}, a scheduling fence after each.  On the last step the
   // "next" reads fetch stale but in-bounds LDS and are unused.

@@ -9,9 +9,11 @@ from __future__ import annotations
 import array
 import math
 import operator
+import weakref
 from typing import NamedTuple, Optional, Sequence, Tuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (ACT_NONE, NORM_2, NORM_INF, _ACTS, _DTYPES, _check, _matrix, _ptr, _raw_current_stream, _stream,
                aligned_copy, load_library)
@@ -460,21 +462,42 @@ def _rows16(t: torch.Tensor) -> torch.Tensor:
     return aligned_copy(t, t.device)
 
 
+class _EagerGraph:
+    """Held by an autograd node made outside a capture, on the default stream:
+    the tensors that its graph's leaves are."""
+    alive = weakref.WeakSet()
+
+    def __init__(self, tensors):
+        self.leaves = [weakref.ref(t) for t in tensors if t is not None and t.requires_grad and t.is_leaf]
+        self.alive.add(self)
+
+    @classmethod
+    def refuse_capture(cls, tensors):
+        """While such a graph lives, autograd adds to its leaves' gradients on the
+        default stream.  A captured backward would make that stream, which
+        cannot be captured, wait for the capturing one: the process ends."""
+        for g in list(cls.alive):
+            if any(r() is t for r in g.leaves for t in tensors):
+                raise RuntimeError("an autograd graph of the same leaves, made on the default stream, is still alive: "
+                                   "drop its outputs before the capture, or warm up on the stream of the capture")
+
+
 class _GatedFFNFunction(torch.autograd.Function):
     """x + (act(x Wg + bg) * (x Wu + bu)) Wd + bd as one autograd node."""
 
     @staticmethod
-    def forward(ctx, x, act, residual, Wg, Wu, Wd, bg, bu, bd):
+    def forward(ctx, graph, x, act, residual, Wg, Wu, Wd, bg, bu, bd):
         H, (Zg, Zu) = gated_gemm_train(x, Wg, Wu, bg, bu, act=act)
         y = gemm_residual(H, Wd, x if residual else None, bd)
-        ctx.act, ctx.residual = act, residual
+        ctx.act, ctx.residual, ctx.graph = act, residual, graph
         ctx.save_for_backward(x, Wg, Wu, Wd, Zg, Zu, H)
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, Wg, Wu, Wd, Zg, Zu, H = ctx.saved_tensors
-        need = ctx.needs_input_grad
+        need = ctx.needs_input_grad[1:]
         dy = _rows16(dy.to(x.dtype))
         down = gemm_residual_backward(H, Wd, dy, want_dB=need[5], want_dbias=need[8], grad_dtype=Wd.dtype)
         up = gated_gemm_backward(x, Wg, Wu, (Zg, Zu), down.dA, act=ctx.act, want_dA=need[0],
@@ -482,7 +505,7 @@ class _GatedFFNFunction(torch.autograd.Function):
         dx = up.dA
         if need[0] and ctx.residual:
             dx = dx + dy
-        return dx, None, None, up.dBg, up.dBu, down.dB, up.dbias_g, up.dbias_u, down.dbias
+        return None, dx, None, None, up.dBg, up.dBu, down.dB, up.dbias_g, up.dbias_u, down.dbias
 
 
 class GatedFFN(torch.nn.Module):
@@ -490,6 +513,10 @@ class GatedFFN(torch.nn.Module):
 
     Weights in the x @ W orientation.  ``residual=False`` leaves out the
     ``x +``, ``bias=False`` (the default) the biases.  x is ``[..., D]``.
+
+    The forward and backward can be captured in a graph after a warm-up on a
+    side stream; a capture while an autograd graph of the same leaves, made on
+    the default stream, is alive raises an error.
     """
 
     def __init__(self, D: int, H: int, act="silu", bias: bool = False, residual: bool = True, device="cuda",
@@ -513,7 +540,13 @@ class GatedFFN(torch.nn.Module):
         x2 = _rows16(x.reshape(-1, self.D))
         Wg, Wu, Wd = _rows16(self.Wg), _rows16(self.Wu), _rows16(self.Wd)
         if torch.is_grad_enabled() and (x.requires_grad or any(p.requires_grad for p in self.parameters())):
-            y = _GatedFFNFunction.apply(x2, self.act, self.residual, Wg, Wu, Wd, self.bg, self.bu, self.bd)
+            leaves = (x, *self.parameters())
+            graph = None
+            if torch.cuda.is_current_stream_capturing():
+                _EagerGraph.refuse_capture(leaves)
+            elif torch.cuda.current_stream(x.device) == torch.cuda.default_stream(x.device):
+                graph = _EagerGraph(leaves)
+            y = _GatedFFNFunction.apply(graph, x2, self.act, self.residual, Wg, Wu, Wd, self.bg, self.bu, self.bd)
         else:
             h = gated_gemm(x2, Wg, Wu, self.bg, self.bu, act=self.act)
             y = gemm_residual(h, Wd, x2 if self.residual else None, self.bd)
