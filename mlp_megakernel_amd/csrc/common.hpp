@@ -63,8 +63,9 @@ __device__ __forceinline__ float erf_sqrt2(float z) {
   return zc * (P * __builtin_amdgcn_rcpf(Q));  // erf(z / sqrt 2)
 }
 __device__ __forceinline__ float gelu_erf(float z) {
+  const float e = erf_sqrt2(z);
   const float h = 0.5f * z;
-  return __builtin_fmaf(h, erf_sqrt2(z), h);
+  return __builtin_fmaf(h, e, h);
 }
 // The normal distribution function Phi(z) = (1 + erf(z / sqrt 2)) / 2 from the
 // same rational (GELU = z Phi(z); its derivative is Phi(z) + z phi(z)).
