@@ -545,9 +545,27 @@ struct Tile {
   }
 
   // ---- epilogue ----------------------------------------------------------
+  // A wave's WM x WNO block of a 16-bit matrix into its staging region, whole
+  // row segments at a time, in the places put() gives its own values.  (The
+  // residual, read where it is added, came as 32-byte pieces of 16 rows per
+  // load: 4096 x 4096 with K = 64 26.6 us, and 13 without a residual.)
+  template <typename TS>
+  static __device__ __forceinline__ void stage_rows(const TS* src, int64_t ld, char* region, int lane) {
+    constexpr int ROWB = G::WNO * 2, CPR = ROWB / 16, RPI = 64 / CPR;
+    const uint32_t ld_b = (uint32_t)ld * 2u;
+    const u32x4 r = rsrc((const char*)src, (uint32_t)(G::WM - 1) * ld_b + (uint32_t)ROWB);
+    const int rsub = lane / CPR, c = lane % CPR;
+#pragma unroll
+    for (int i = 0; i < G::WM / RPI; ++i)
+      dma16_buf(r, (uint32_t)rsub * ld_b + (uint32_t)((c ^ stage_swz<ROWB>(RPI * i + rsub)) << 4),
+                (uint32_t)(RPI * i) * ld_b, lds_addr(region) + (uint32_t)i * 1024u);
+    wait_vmcnt0();
+  }
+
   // Rows [wr0, wr0 + WM) x columns [wc0, wc0 + WNO) of one output matrix:
   // prep(t, n, valid) once per 16-wide sub-block gives what value(c, t, s, m,
-  // n, valid), the 4 consecutive columns n.. of row m, needs of its columns.
+  // n, valid, cell), the 4 consecutive columns n.. of row m, needs of its
+  // columns; cell is their place in the staging region, if they go through it.
   // A 16-bit block that lies whole inside the matrix is staged in the wave's
   // own LDS region and stored as full row segments; others are stored from
   // the registers.
@@ -566,9 +584,10 @@ struct Tile {
 #pragma unroll
           for (int s = 0; s < G::MT; ++s) {
             const int row = 16 * s + q;
-            const f32x4 v = value(c, t, s, wr0 + row, wc0 + 16 * t + 4 * b, 4);
+            char* cell = region + row * ROWB + ((chunk ^ stage_swz<ROWB>(row)) << 4) + ((b & 1) << 3);
+            const f32x4 v = value(c, t, s, wr0 + row, wc0 + 16 * t + 4 * b, 4, cell);
             const to4 o = (to4){(TS)v[0], (TS)v[1], (TS)v[2], (TS)v[3]};
-            *(to4*)(region + row * ROWB + ((chunk ^ stage_swz<ROWB>(row)) << 4) + ((b & 1) << 3)) = o;
+            *(to4*)cell = o;
           }
         }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -592,7 +611,7 @@ struct Tile {
 #pragma unroll
       for (int s = 0; s < G::MT; ++s) {
         const int m = wr0 + 16 * s + q;
-        if (m < p->M) store4<TS>(Y + (int64_t)m * ldy + n, value(c, t, s, m, n, valid), valid);
+        if (m < p->M) store4<TS>(Y + (int64_t)m * ldy + n, value(c, t, s, m, n, valid, (const char*)nullptr), valid);
       }
     }
   }
@@ -616,7 +635,7 @@ struct Tile {
         const int i = at.pair | sub;
         TO* Y = (TO*)(i ? p->Y[1] : p->Y[0]) + (int64_t)at.split * p->split_stride;
         put<TO>(Y, p->ldy, p, wr0, wc0, inside, region, lane, none,
-                [&](int, int t, int s, int, int, int) { return acc[t + sub * G::NTO][s]; });
+                [&](int, int t, int s, int, int, int, const char*) { return acc[t + sub * G::NTO][s]; });
       }
     } else {
       const int act = p->act;
@@ -625,10 +644,10 @@ struct Tile {
       // the stored pre-activations of a training forward, one rounding each
       if (p->Z[0]) {
         put<T>((T*)p->Z[0], p->ldz, p, wr0, wc0, inside, region, lane, bias_g,
-               [&](f32x4 c, int t, int s, int, int, int) { return acc[t][s] + c; });
+               [&](f32x4 c, int t, int s, int, int, int, const char*) { return acc[t][s] + c; });
         if constexpr (EPI == EPI_GATED)
           put<T>((T*)p->Z[1], p->ldz, p, wr0, wc0, inside, region, lane, bias_u,
-                 [&](f32x4 c, int t, int s, int, int, int) { return acc[t + G::NTO][s] + c; });
+                 [&](f32x4 c, int t, int s, int, int, int, const char*) { return acc[t + G::NTO][s] + c; });
       }
       if constexpr (EPI == EPI_GATED) {
         struct Pair {
@@ -636,17 +655,18 @@ struct Tile {
         };
         put<TO>((TO*)p->Y[0], p->ldy, p, wr0, wc0, inside, region, lane,
                 [&](int t, int n, int valid) { return Pair{bias_g(t, n, valid), bias_u(t, n, valid)}; },
-                [&](Pair c, int t, int s, int, int, int) {
+                [&](Pair c, int t, int s, int, int, int, const char*) {
                   const f32x4 g = acc[t][s] + c.g, u = acc[t + G::NTO][s] + c.u;
                   return act_any<O16>(act, g) * u;
                 });
       } else {
         const TO* R = (const TO*)p->R;
+        if (O16 && R && inside) stage_rows<TO>(R + (int64_t)wr0 * p->ldr + wc0, p->ldr, region, lane);
         put<TO>((TO*)p->Y[0], p->ldy, p, wr0, wc0, inside, region, lane, bias_g,
-                [&](f32x4 c, int t, int s, int m, int n, int valid) {
+                [&](f32x4 c, int t, int s, int m, int n, int valid, const char* cell) {
                   const f32x4 z = acc[t][s] + c;
                   f32x4 o = (f32x4){0.f, 0.f, 0.f, 0.f};
-                  if (R) o = load4<TO>(R + (int64_t)m * p->ldr + n, valid);
+                  if (R) o = load4<TO>(cell ? (const TO*)cell : R + (int64_t)m * p->ldr + n, valid);
                   return o + act_any<O16>(act, z);
                 });
       }
