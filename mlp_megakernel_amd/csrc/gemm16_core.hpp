@@ -737,13 +737,13 @@ struct Tile {
         if (seg > 0) {
           h = hot(k, at, seg);
           r = part(at, h, seg);
-          __syncthreads();  // every wave is past its last fragment read
+          lds_barrier();  // every wave is past its last fragment read
           fill_first(at, seg, h, r, pt, wu, lane);
         }
         TileFrags<G> f0, f1;
         if (r.n > 0) {
           wait_vmcnt0();
-          __syncthreads();
+          lds_barrier();
 #pragma unroll
           for (int i = 0; i < G::NT; ++i) f0.n[i] = frag_n(sb(0), 0, wn, i, lane);
 #pragma unroll
@@ -766,7 +766,7 @@ struct Tile {
                 // any
                 if (G::NS > 2 && i + 2 < r.n && (r.s + i + 2) * BK + BK <= h.K)
                   wait_steps<G::NS - 2>();
-                else
+                else if (EPI != EPI_STORE || G::NS > 2 || i > 0)  // both of two stages have landed before step 0
                   wait_vmcnt0();
                 lds_barrier();
               }
@@ -781,7 +781,7 @@ struct Tile {
           }
         }
       }
-      __syncthreads();  // every wave is past its last fragment read
+      lds_barrier();  // every wave is past its last fragment read
       epilogue(k, at, acc, wm, wn, wu, lane, (char*)lds);
       lds_barrier();  // the LDS is free; the stores may still be in flight
       v += gridDim.x;
