@@ -217,6 +217,7 @@ hipError_t store_tiles(const TileOp& o, int variant, hipStream_t stream, int num
   switch (variant) {
     case kShape256: return COALESCE_TILE(256, 256, 8, 2, 1, 1);
     case kShape128: return COALESCE_TILE(128, 128, 4, 2, 2, 1);
+    case kShape128Deep: return COALESCE_TILE(128, 128, 4, 2, 1, 1, 3);
     case kShape64Deep: return COALESCE_TILE(64, 64, 4, 2, 3, 1, 3);
     default: return COALESCE_TILE(64, 64, 4, 2, 4, 1);
   }
@@ -246,8 +247,9 @@ hipError_t product(TileOp o, const TilePlan& plan, DType out, hipStream_t stream
   o.ldy = c.ldp;
   o.split_stride = c.split_stride;
 #define COALESCE_TILE(...) launch_tile<T, float, LA, LB, SEGS, EPI_STORE, TileGeo<__VA_ARGS__>>(o, stream, num_cus)
-  const hipError_t e =
-      plan.variant == kShape128 ? COALESCE_TILE(128, 128, 4, 2, 2, 1) : COALESCE_TILE(64, 64, 4, 2, 4, 1);
+  const hipError_t e = plan.variant == kShape128       ? COALESCE_TILE(128, 128, 4, 2, 2, 1)
+                       : plan.variant == kShape128Deep ? COALESCE_TILE(128, 128, 4, 2, 1, 1, 3)
+                                                       : COALESCE_TILE(64, 64, 4, 2, 4, 1);
 #undef COALESCE_TILE
   if (e != hipSuccess) return e;
   return launch_combine(c, COMBINE_STORE, out, out, stream, num_cus);

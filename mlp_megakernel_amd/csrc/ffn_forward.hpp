@@ -36,6 +36,7 @@ hipError_t forward_tiles(const TileOp& o, int variant, hipStream_t stream, int n
       case kShape192: return COALESCE_TILE(192, 256, 8, 2, 1, 1);
       case kShape160: return COALESCE_TILE(160, 256, 8, 2, 1, 1, 3);
       case kShape128: return COALESCE_TILE(128, 128, 4, 2, 2, 1);
+      case kShape128Deep: return COALESCE_TILE(128, 128, 4, 2, 1, 1, 3);
       case kShape64Deep: return COALESCE_TILE(64, 64, 4, 2, 3, 1, 3);
       default: return COALESCE_TILE(64, 64, 4, 2, 4, 1);
     }
@@ -76,7 +77,9 @@ hipError_t forward_split(TileOp o, int variant, DType in, DType out, int act, hi
   if constexpr (EPI == EPI_GATED)
     e = variant == kShape128 ? COALESCE_TILE(128, 128, 4, 2, 2, 2) : COALESCE_TILE(64, 128, 4, 2, 2, 2);
   else
-    e = variant == kShape128 ? COALESCE_TILE(128, 128, 4, 2, 2, 1) : COALESCE_TILE(64, 64, 4, 2, 4, 1);
+    e = variant == kShape128       ? COALESCE_TILE(128, 128, 4, 2, 2, 1)
+        : variant == kShape128Deep ? COALESCE_TILE(128, 128, 4, 2, 1, 1, 3)
+                                   : COALESCE_TILE(64, 64, 4, 2, 4, 1);
 #undef COALESCE_TILE
   if (e != hipSuccess) return e;
   return launch_combine(c, EPI == EPI_GATED ? COMBINE_GATED : COMBINE_RESID, in, out, stream, num_cus);

@@ -27,23 +27,26 @@ struct TilePlan {
 // of the products), so the lower ones pay only where they fit the rows or fill
 // the compute units better: gated 777 x 5461 x 2048 57.8 us in 256 rows, 48.5 in
 // 160; 3000 x 4096 x 4096 180 in 256, 163 in 192.  Those lower than 256 exist
-// where the m side lies along the contraction; 160 rows and one of the 64 x 64
-// shapes have three stages (residual 512 x 4096 x 4096: 37.5 us with two, 30.2).
+// where the m side lies along the contraction; 160 rows and the shapes called deep
+// have three stages, which pays where a compute unit holds few tiles (64 x 64:
+// residual 512 x 4096 x 4096 37.5 us with two, 30.2; 128 x 128: residual 2048 x
+// 2048 x 4096 53.7 with two, 45.0).  The gated product has no deep ones.
 struct TileShape {
   int bm, bn, slots;
   double step[4], launch, round;
 };
-constexpr int kShapes = 7, kShape256 = 1, kShape128 = 2, kShape64 = 3, kShape224 = 4, kShape192 = 5, kShape160 = 6,
-              kShape64Deep = 7;
+constexpr int kShapes = 8, kShape256 = 1, kShape128 = 2, kShape64 = 3, kShape224 = 4, kShape192 = 5, kShape160 = 6,
+              kShape64Deep = 7, kShape128Deep = 8;
 static const TileShape kPlain[kShapes] = {
     {256, 256, 1, {1450}, 4000, 5000},          {128, 128, 2, {780, 1200}, 3000, 2000},
     {64, 64, 4, {430, 520, 700, 850}, 3000, 1500}, {224, 256, 1, {1290}, 4000, 5000},
     {192, 256, 1, {1180}, 4000, 5000},          {160, 256, 1, {1010}, 4000, 5000},
-    {64, 64, 3, {380, 440, 700}, 3000, 1500}};
+    {64, 64, 3, {380, 440, 700}, 3000, 1500},
+    {128, 128, 1, {600}, 4000, 5000}};
 static const TileShape kGated[kShapes] = {
     {256, 128, 1, {1450}, 4000, 5000}, {128, 64, 2, {740, 1050}, 3000, 2000}, {64, 64, 3, {600, 680, 950}, 3000, 1500},
     {224, 128, 1, {1290}, 4000, 5000}, {192, 128, 1, {1180}, 4000, 5000},     {160, 128, 1, {1010}, 4000, 5000},
-    {64, 64, 0, {0}, 0, 0}};
+    {64, 64, 0, {0}, 0, 0},            {128, 64, 0, {0}, 0, 0}};
 
 // The plan with the smallest estimated time.  A launch is `units` workgroup
 // tiles (tiles x splits), run in rounds of what the compute units hold.  A split
@@ -61,7 +64,7 @@ TilePlan plan_tiles(int64_t m, int64_t n, bool gated, int batch, int64_t ksteps,
     if (s.slots == 0 || (!rows && (v == kShape224 || v == kShape192 || v == kShape160))) continue;
     const int64_t tiles = ((m + s.bm - 1) / s.bm) * ((n + s.bn - 1) / s.bn) * batch;
     for (int splits : ranges) {
-      if (splits > 1 && ((v != kShape128 && v != kShape64) || ksteps / splits < 4)) break;
+      if (splits > 1 && ((v != kShape128 && v != kShape64 && v != kShape128Deep) || ksteps / splits < 4)) break;
       const int64_t units = tiles * splits, full = (int64_t)num_cus * s.slots;
       const int64_t rounds = units / full, rest = units - rounds * full;
       // the last round's step: between the times of the tile counts around its
