@@ -17,11 +17,13 @@ FORWARD = [(1, 40, 64), (17, 40, 64), (40, 40, 64), (1, 4100, 64), (17, 4100, 64
            (17, 8200, 64), (63, 8200, 70), (1, 40, 2050), (65, 40, 64), (65, 40, 1001), (65, 200, 64), (3000, 1030, 64),
            (1025, 1030, 4100), (500, 1030, 4100), (1537, 2731, 64), (4100, 5461, 130), (8200, 4100, 130),
            (1537, 4100, 130), (3000, 4100, 130), (500, 8200, 520), (500, 16400, 130), (1537, 2731, 520),
-           (2050, 4100, 130), (2050, 520, 4100), (3000, 200, 4100), (1537, 4100, 200), (8192, 4096, 64)]
+           (2050, 4100, 130), (2050, 520, 4100), (3000, 200, 4100), (1537, 4100, 200), (8192, 4096, 64), (777, 4100, 2050),
+           (900, 900, 8200), (900, 1000, 8200)]
 BACKWARD = [(1, 40, 64), (777, 40, 64), (40, 200, 64), (1, 40, 130), (65, 40, 130), (500, 4100, 520), (4100, 1030, 200),
             (257, 4100, 1001), (1, 8200, 200), (4100, 40, 1001), (2050, 200, 4100), (3000, 40, 4100), (500, 40, 8200),
             (8200, 40, 4100), (1300, 8200, 200), (4100, 1540, 200), (4100, 2731, 200), (3000, 200, 4100),
-            (8192, 72, 4096)]
+            (8192, 72, 4096), (2050, 2731, 520), (3000, 2731, 520), (3000, 2731, 1030), (900, 8200, 1000),
+            (8200, 900, 1000), (8200, 500, 1000)]
 
 
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
