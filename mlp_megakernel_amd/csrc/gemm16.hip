@@ -38,7 +38,7 @@
 #include <atomic>
 
 #include "common.hpp"
-#include "gemm16_core.hpp"
+#include "gemm16_common.hpp"
 #include "launch.hpp"
 
 namespace coalesce {
@@ -80,7 +80,7 @@ typedef Geo<64, 64, 4, 4> Geo64;
 
 // LDS layouts, 16-byte chunks XOR-swizzled so that every fragment read is
 // free of bank conflicts whether the LDS serves 128 or 256 bytes per clock
-// (swzA and swzB, gemm16_core.hpp):
+// (swzA and swzB, gemm16_common.hpp):
 //   A tile: BM rows of 64 k (128 B = 8 chunks); chunk c of row m sits at slot
 //     c ^ swzA(m).
 //   B tile: 64 rows of BN n (512, 256 or 128 B = 32, 16 or 8 chunks); chunk c
@@ -128,6 +128,25 @@ __device__ __forceinline__ uint32_t dma_offset(const DmaPlan& d, int j) {
     return (uint32_t)row * ldb_b + (uint32_t)((gn - d.n0) * (int)sizeof(T));
   }
 }
+
+// Uniform (SGPR) 64-bit base for a direct copy.
+__device__ __forceinline__ const void* uniform_ptr(const void* p) {
+  const uint64_t v = (uint64_t)(uintptr_t)p;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return (const void*)(uintptr_t)(((uint64_t)hi << 32) | lo);
+}
+
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+// 16-byte direct copy: global (SGPR base + per-lane 32-bit offset) -> LDS
+// (wave-uniform byte address + 16 * lane).
+__device__ __forceinline__ void dma16_off(const void* base, uint32_t off, uint32_t lds) {
+  // one wait state between the M0 write and the LDS-DMA instruction that reads it
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds)
+               : "memory", "m0");
+}
+#pragma clang diagnostic pop
 
 // Copy j (0 .. CA + CB - 1) of a K step into stage st.
 template <typename T, typename G>

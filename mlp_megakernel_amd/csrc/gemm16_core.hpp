@@ -1,7 +1,6 @@
 // The 16-bit MFMA tile machinery of the feed-forward operators: one workgroup
 // tile kernel over operands in either orientation, with the epilogue as a
-// template argument (ffn_forward.hpp, ffn_backward.hpp), and the building blocks it
-// shares with the plain fused GEMM (gemm16.hip).
+// template argument (ffn_forward.hpp, ffn_backward.hpp).
 //
 //   acc[m][n] = sum_k Am[m][k] Bn[k][n]
 //
@@ -21,85 +20,24 @@
 #pragma once
 #include <atomic>
 
-#include "common.hpp"
+#include "gemm16_common.hpp"
 #include "launch.hpp"
 
 namespace coalesce {
 namespace {
 
-constexpr int BK = 64;
-
-// LDS swizzles, in 16-byte chunks.  LAY_K rows (64 k, 128 B = 8 chunks): chunk
-// c of row m sits at slot c ^ swzA(m): a 128-bit read by 16 lanes (rows
-// m0..m0+15, one chunk) hits 16 distinct 16-byte slots of a 256-byte window,
-// and any 8 consecutive rows hit 8 distinct slots of a 128-byte window.
-// LAY_X rows (CPR chunks of the free index): chunk c of row k sits at slot c ^
-// swzB<CPR>(k): a transposing read by 32 lanes (rows k0..k0+3 and
-// k0+8..k0+11, two chunks, two 8-byte halves) hits 32 distinct 8-byte slots of
-// a 256-byte window (which holds two rows when they are 128 bytes long).
-// Neither depends on the sub-tile index, the slice or the half of a
-// transposing read, so those stay immediate offsets of the LDS reads.
-__device__ __forceinline__ int swzA(int m) { return ((m >> 1) & 7) ^ ((m & 1) << 2); }
-template <int CPR>
-__device__ __forceinline__ int swzB(int k) {
-  if constexpr (CPR >= 16)
-    return ((k & 3) << 1) | (((k >> 3) & 1) << 3);
-  else  // 128-byte rows: a 256-byte window holds two rows, k and k ^ 1
-    return (((k >> 1) & 1) << 1) | (((k >> 3) & 1) << 2);
-}
-
-// Uniform (SGPR) 64-bit base for a direct copy.
-__device__ __forceinline__ const void* uniform_ptr(const void* p) {
-  const uint64_t v = (uint64_t)(uintptr_t)p;
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
-  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
-  return (const void*)(uintptr_t)(((uint64_t)hi << 32) | lo);
-}
-
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
-// 16-byte direct copy: global (SGPR base + per-lane 32-bit offset) -> LDS
-// (wave-uniform byte address + 16 * lane).
-__device__ __forceinline__ void dma16_off(const void* base, uint32_t off, uint32_t lds) {
-  // one wait state between the M0 write and the LDS-DMA instruction that reads it
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds)
-               : "memory", "m0");
-}
-
-// The same through a buffer resource, at the lane's offset plus a uniform one:
-// bytes at or past the resource's size read as zero, so a tile that overhangs
-// its matrix needs no clamps.
+// 16-byte direct copy through a buffer resource, at the lane's offset plus a
+// uniform one, to LDS (wave-uniform byte address + 16 * lane): bytes at or past
+// the resource's size read as zero, so a tile that overhangs its matrix needs no
+// clamps.
 __device__ __forceinline__ void dma16_buf(u32x4 rsrc, uint32_t off, uint32_t shift, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %3 offen lds" ::"v"(off), "s"(rsrc),
                "s"(lds), "s"(shift)
                : "memory", "m0");
 }
-
-// Workgroup barrier for LDS reuse: the wave's own LDS accesses are complete
-// (lgkmcnt 0) but its global stores and direct copies may still be in
-// flight (no vmcnt wait, unlike __syncthreads' fence); the "memory" clobber
-// keeps the compiler from moving memory accesses across it.
-__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 #pragma clang diagnostic pop
-
-template <typename TO>
-__device__ __forceinline__ void store4(TO* dst, f32x4 v, int valid) {
-  if constexpr (sizeof(TO) == 2) {
-    typedef TO to4 __attribute__((ext_vector_type(4)));
-    const to4 o = (to4){(TO)v[0], (TO)v[1], (TO)v[2], (TO)v[3]};
-    if (valid >= 4) {
-      *(to4*)dst = o;
-    } else {
-      for (int r = 0; r < valid; ++r) dst[r] = o[r];
-    }
-  } else {
-    if (valid >= 4) {
-      *(f32x4*)dst = v;
-    } else {
-      for (int r = 0; r < valid; ++r) dst[r] = v[r];
-    }
-  }
-}
 
 // 4 consecutive elements as fp32 (0 past `valid`); src is 4-element aligned.
 template <typename T>
@@ -145,20 +83,6 @@ __device__ __forceinline__ f32x4 act_any(int act, f32x4 z) {
   }
   return f;
 }
-
-// Swizzle of an epilogue staging row of ROWB bytes (64, 128 or 256), in
-// 16-byte chunks: both the 8-byte writes of 16 rows and the 16-byte
-// row-contiguous reads spread over the banks.
-template <int ROWB>
-__device__ __forceinline__ int stage_swz(int row) {
-  if constexpr (ROWB == 64)
-    return (row >> 2) & 3;
-  else if constexpr (ROWB == 128)
-    return (row >> 1) & 7;
-  else
-    return row & 15;
-}
-
 
 enum Lay { LAY_K = 0, LAY_X = 1 };
 enum Epi { EPI_STORE = 0, EPI_RESID = 1, EPI_GATED = 2 };
