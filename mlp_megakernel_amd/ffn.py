@@ -6,9 +6,7 @@ run there, on ``stream`` or that device's current stream.
 """
 from __future__ import annotations
 
-import array
 import math
-import operator
 import weakref
 from typing import NamedTuple, Optional, Sequence, Tuple
 
@@ -345,56 +343,15 @@ def gated_gemm_backward(A: torch.Tensor, Bg: torch.Tensor, Bu: torch.Tensor,
 # Gradient norm and clipping
 # ---------------------------------------------------------------------------
 
-def _dense(t: torch.Tensor) -> bool:
-    """Whether the tensor's elements fill one run of memory, in any order."""
-    n = 1
-    for size, st in sorted(((s, st) for s, st in zip(t.shape, t.stride()) if s != 1), key=lambda x: x[1]):
-        if st != n:
-            return False
-        n *= size
-    return True
-
-
-def _address(a: array.array) -> int:
-    return a.buffer_info()[0]
-
-
-_tensor = torch.Tensor
-_dtype_of = operator.attrgetter("dtype")
-
-
 def _grad_list(tensors, out):
     """(count, device, sources, destinations, sizes, types): the host arrays of
-    the C call, to be kept alive until it returns."""
-    tensors = list(tensors)
-    devs = set(map(_tensor.get_device, tensors))
-    dev = devs.pop() if devs else _current_device()
-    if devs or dev < 0:
-        raise ValueError("the tensors must lie on one GPU")
+    the C call (bytes objects, to be kept alive until it returns)."""
     try:
-        dts = array.array("i", map(_DTYPES.__getitem__, map(_dtype_of, tensors)))
-    except KeyError:
-        raise ValueError("every tensor must be float32, float16 or bfloat16") from None
-    numel = array.array("q", map(_tensor.numel, tensors))
-    src = array.array("Q", map(_tensor.data_ptr, tensors))
-    plain = all(map(_tensor.is_contiguous, tensors))
-    if not plain:
-        for i, t in enumerate(tensors):
-            if not _dense(t):
-                raise ValueError("tensor %d must be dense (its elements one run of memory)" % i)
-    if out is None:
-        return len(tensors), dev, src, src, numel, dts
-    out = list(out)
-    # contiguous tensors go by their sizes, others by shape and strides
-    same = len(out) == len(tensors) and set(map(_tensor.get_device, out)) <= {dev} and \
-        list(map(_dtype_of, out)) == list(map(_dtype_of, tensors))
-    if same and plain:
-        same = array.array("q", map(_tensor.numel, out)) == numel and all(map(_tensor.is_contiguous, out))
-    elif same:
-        same = all(o.shape == t.shape and o.stride() == t.stride() for t, o in zip(tensors, out))
-    if not same:
-        raise ValueError("out must hold one tensor per gradient, of its size, memory order, dtype and device")
-    return len(tensors), dev, src, array.array("Q", map(_tensor.data_ptr, out)), numel, dts
+        from ._marshal import grad_list
+    except ImportError as e:
+        raise RuntimeError("%s is not built (python -m mlp_megakernel_amd.build)" % e.name) from None
+    n, dev, *arrays = grad_list(tensors, out)
+    return (n, _current_device() if n == 0 else dev, *arrays)
 
 
 def _norm_code(norm_type) -> int:
@@ -438,14 +395,13 @@ def _norm_call(lists, max_norm, norm_type, norm, workspace, stream):
         return _there(dev, _norm_call, lists, max_norm, norm_type, norm, workspace, stream)
     lib, code = load_library(), _norm_code(norm_type)
     norm = _norm_out(norm, dev, stream)
-    pn, pd = _address(numel), _address(dts)
-    ws, nws, _keep = _take(workspace, int(lib.coalesce_grad_norm_workspace_size(pn, pd, n)), dev, stream)
+    ws, nws, _keep = _take(workspace, int(lib.coalesce_grad_norm_workspace_size(numel, dts, n)), dev, stream)
     if max_norm is None:
-        _check(lib.coalesce_grad_norm(_address(src), pn, pd, n, code, norm.data_ptr(), ws, nws,
+        _check(lib.coalesce_grad_norm(src, numel, dts, n, code, norm.data_ptr(), ws, nws,
                                       _raw_stream(stream, dev)))
     else:
-        _check(lib.coalesce_clip_grad_norm(_address(src), _address(dst), pn, pd, n, code, max_norm, norm.data_ptr(), ws,
-                                           nws, _raw_stream(stream, dev)))
+        _check(lib.coalesce_clip_grad_norm(src, dst, numel, dts, n, code, max_norm, norm.data_ptr(), ws, nws,
+                                           _raw_stream(stream, dev)))
     return norm
 
 
