@@ -92,7 +92,7 @@ TilePlan plan_tiles(int64_t m, int64_t n, bool gated, int batch, int64_t ksteps,
 // 4.8 TB/s of whole 128-byte lines (strips of 64 columns; narrower ones draw
 // 1.5 and 2 times the bytes), or by what one compute unit requests: about 3.5,
 // 3.0 and 2.6 ns per row of a strip, which is a line or part of one, and X's
-// rows add to that.  Measured, one token: gated 4096 x 16384 58 us against 62 of
+// rows add to that.  Measured, one token: gated 4096 x 16384 55 us against 60 of
 // split tiles, 2048 x 5464 16.4 (strips of 32) against 20.8, 1001 x 2736 6.7
 // (16) against 11.6; but 4096 x 4096, whose 64 strips leave most compute units
 // idle, 29 to 36 against 22.8.

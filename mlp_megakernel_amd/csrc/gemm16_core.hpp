@@ -472,7 +472,7 @@ struct Tile {
   // A wave's WM x WNO block of a 16-bit matrix into its staging region, whole
   // row segments at a time, in the places put() gives its own values.  (The
   // residual, read where it is added, came as 32-byte pieces of 16 rows per
-  // load: 4096 x 4096 with K = 64 26.6 us, and 13 without a residual.)
+  // load: 4096 x 4096 with K = 64 26.8 us, so 20.6, and 13 without a residual.)
   template <typename TS>
   static __device__ __forceinline__ void stage_rows(const TS* src, int64_t ld, char* region, int lane) {
     constexpr int ROWB = G::WNO * 2, CPR = ROWB / 16, RPI = 64 / CPR;

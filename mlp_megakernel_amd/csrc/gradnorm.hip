@@ -18,7 +18,7 @@
 // through the caches, in the 256 MB one; what lies before them is read past the
 // caches (non-temporal), and so are the results of a list above kPastBytes
 // written.  1.2 GB of bf16: 705 us with every access through the caches, 647
-// past them, 625 with 160 MB kept (the norm alone 214 -> 188 us, 6.4 TB/s); a
+// past them, 607 with 160 MB kept (the norm alone 214 -> 184 us, 6.5 TB/s); a
 // list of 64 MB 38 us past them and 35 through them, of 128 MB 71 and 80.
 #include <algorithm>
 
