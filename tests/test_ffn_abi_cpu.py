@@ -162,7 +162,10 @@ def test_binding_refuses():
                  lambda: mk.gemm_residual_backward(a, a, a), lambda: mk.gated_gemm_backward(a, a, a, (a, a), a)):
         with pytest.raises(ValueError):
             call()
-    with pytest.raises(ValueError):
-        mk.clip_grad_norm([a], 1.0)
+    for grads, out in (([a], None), ([None], None), ([1.0], None), ([], [a]), ([a], [a]), ([a, a], [a])):
+        with pytest.raises(ValueError):
+            mk.clip_grad_norm(grads, 1.0, out=out)
+    with pytest.raises(TypeError):
+        mk.clip_grad_norm(3, 1.0)
     with pytest.raises(ValueError):
         mk.GatedFFN(8, 8, act="swish?", device="cpu")

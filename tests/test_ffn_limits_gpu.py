@@ -97,6 +97,28 @@ def test_clip_above_2_31_elements():
     assert abs(float(t[-1]) * want / 2 - 1) <= 2.0 ** -8 and abs(float(small[5]) * want / -3 - 1) <= 2.0 ** -22
 
 
+@pytest.mark.parametrize("norm_type", [2, math.inf])
+def test_clip_of_many_large_tensors(norm_type):
+    # several tables of every type, more than the cache holds: each part of the
+    # list read and written its own way
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    ts = [randn(gen, 1500000 + 7 * i, dt=(torch.bfloat16, torch.float32, torch.float16)[i % 3 if i % 10 else 0])
+          for i in range(150)]
+    assert sum(t.numel() * t.element_size() for t in ts) > 500 << 20
+    want = torch.stack([t.double().norm(norm_type) for t in ts]).norm(norm_type)
+    outs = [torch.empty_like(t) for t in ts]
+    norm = mk.clip_grad_norm(ts, 0.5, norm_type=norm_type, out=outs)
+    # one rounding of the norm to fp32
+    assert abs(float(norm) - float(want)) <= 2.0 ** -24 * 1.001 * float(want)
+    c = 0.5 / (want + 1e-6)
+    for t, o in zip(ts, outs):
+        v = t.double() * c
+        # c and the product rounded to fp32, the product to the type
+        assert bool(((o.double() - v).abs() <= 2 * 2.0 ** -24 * v.abs() + ref.half_step(v, t.dtype)).all())
+    again = mk.clip_grad_norm(ts, 0.5, norm_type=norm_type)
+    assert torch.equal(norm, again) and all(torch.equal(a, b) for a, b in zip(ts, outs))
+
+
 def test_two_calls_at_once():
     gen = torch.Generator(device="cuda").manual_seed(4)
     jobs = []
