@@ -26,7 +26,8 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineOp c) {
         f32x4 v[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u)
-          v[u] = k + u < c.splits ? *(const f32x4*)(p + (int64_t)(k + u) * c.split_stride) : (f32x4){0.f, 0.f, 0.f, 0.f};
+          v[u] = k + u < c.splits ? *(const f32x4*)(p + (int64_t)(k + u) * c.split_stride)
+                                  : (f32x4){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int u = 0; u < 8; ++u) s += v[u];
       }

@@ -179,7 +179,8 @@ __global__ __launch_bounds__(256) void bias_grad_kernel(const float* sums, int c
     for (int k = g; k < chunks; k += 8 * GROUPS) {
       float v[8];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) v[u] = k + u * GROUPS < chunks ? sums[((int64_t)(k + u * GROUPS) * 2 + i) * N + n] : 0.0f;
+      for (int u = 0; u < 8; ++u)
+        v[u] = k + u * GROUPS < chunks ? sums[((int64_t)(k + u * GROUPS) * 2 + i) * N + n] : 0.0f;
 #pragma unroll
       for (int u = 0; u < 8; ++u) t += v[u];
     }

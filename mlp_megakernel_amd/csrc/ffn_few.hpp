@@ -209,8 +209,8 @@ __global__ __launch_bounds__(G::NW * 64) void few_kernel(TileOp p) {
 
 template <typename T, typename TO, int EPI, typename G>
 hipError_t few_launch(const TileOp& o, hipStream_t stream) {
-  hipLaunchKernelGGL((few_kernel<T, TO, EPI, G>), dim3((unsigned)(((o.N + G::SN - 1) / G::SN + 7) / 8 * 8)), dim3(G::NW * 64),
-                     0, stream, o);
+  const unsigned strips = (unsigned)(((o.N + G::SN - 1) / G::SN + 7) / 8 * 8);  // whole rounds of the 8 XCDs
+  hipLaunchKernelGGL((few_kernel<T, TO, EPI, G>), dim3(strips), dim3(G::NW * 64), 0, stream, o);
   return hipGetLastError();
 }
 

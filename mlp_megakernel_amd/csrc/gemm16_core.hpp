@@ -120,7 +120,8 @@ struct TileGeo {
   static_assert(NCA * 8 == BM && CBS * NW * 8 == SUBN, "copy plan does not cover the tile");
   static_assert(NS == 2 || NS == 3, "wait_steps keeps one later step in flight");
   static_assert(LDS_ELEMS * 2 + (ROOM ? 0 : 1024) <= 160 * 1024, "the stages exceed the LDS");
-  static_assert(NG >= 2 && NI <= 8 && WM * WGM == BM && MT * 16 == WM && NT * 16 == WN, "no read plan for this wave tile");
+  static_assert(NG >= 2 && NI <= 8 && WM * WGM == BM && MT * 16 == WM && NT * 16 == WN,
+                "no read plan for this wave tile");
 };
 
 // One side of the product as the copies see it: `p` is the matrix, x0 the
@@ -182,7 +183,8 @@ __device__ __forceinline__ i16x8 read_frag(const T* t, int ks, int x0, int i, in
     if constexpr (N == 8 && CPR >= 16) {
       // x0 is a multiple of 128, so i alone sets bits 1..3 of the chunk
       const int x = x0 + 4 * (q & 3);
-      const uint32_t a0 = lds_addr(t) + (uint32_t)((k0 * BX + (((x >> 3) ^ swzB<CPR>(k0)) << 3) + (x & 7)) * (int)sizeof(T));
+      const uint32_t a0 =
+          lds_addr(t) + (uint32_t)((k0 * BX + (((x >> 3) ^ swzB<CPR>(k0)) << 3) + (x & 7)) * (int)sizeof(T));
       uint32_t a;
       asm volatile("v_xor_b32 %0, %1, %2" : "=v"(a) : "i"(32 * i), "v"(a0));
 #pragma unroll

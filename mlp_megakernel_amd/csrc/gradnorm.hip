@@ -165,7 +165,8 @@ __global__ __launch_bounds__(THREADS) void norm_kernel(ClipTable t, double* part
 template <bool INF>
 __device__ __forceinline__ double total_norm(const double* partial, int n) {
   double v = 0.0;
-  for (int i = threadIdx.x; i < n; i += THREADS) v = INF ? (double)max_nan((float)v, (float)partial[i]) : v + partial[i];
+  for (int i = threadIdx.x; i < n; i += THREADS)
+    v = INF ? (double)max_nan((float)v, (float)partial[i]) : v + partial[i];
   v = block_total<INF>(v);
   return INF ? v : __builtin_sqrt(v);
 }

@@ -191,8 +191,8 @@ def _gemm_residual(A, B, residual, bias, act, out_dtype, out, preact, workspace,
     ldz = 0 if preact is None else _mat(preact, "preact", M, N, dt, dev)
     ws, nws, _keep = _workspace("coalesce_gemm_residual_workspace_size", dev, M, N, K, workspace, stream)
     _check(load_library().coalesce_gemm_residual(
-        A.data_ptr(), lda, B.data_ptr(), ldb, _ptr(bias), _ptr(residual), ldr, _ptr(preact), ldz, out.data_ptr(), ldy, M,
-        N, K, _DTYPES[dt], _DTYPES[odt], _act(act), ws, nws, _raw_stream(stream, dev)))
+        A.data_ptr(), lda, B.data_ptr(), ldb, _ptr(bias), _ptr(residual), ldr, _ptr(preact), ldz, out.data_ptr(), ldy,
+        M, N, K, _DTYPES[dt], _DTYPES[odt], _act(act), ws, nws, _raw_stream(stream, dev)))
     return out
 
 
@@ -325,7 +325,7 @@ def gated_gemm_backward(A: torch.Tensor, Bg: torch.Tensor, Bu: torch.Tensor,
             dA = _new(M, K, dt, A.device, stream)
         ldda = _mat(dA, "dA", M, K, dt, dev)
     if want_dB:
-        dW = dB if dB is not None else (_new(K, N, grad_dtype, A.device, stream), _new(K, N, grad_dtype, A.device, stream))
+        dW = dB if dB is not None else tuple(_new(K, N, grad_dtype, A.device, stream) for _ in range(2))
         lddb = _one_pitch(dW, ("dB[0]", "dB[1]"), K, N, grad_dtype, dev)
     if want_dbias:
         db = (torch.empty(N, dtype=grad_dtype, device=A.device), torch.empty(N, dtype=grad_dtype, device=A.device))
