@@ -125,6 +125,35 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+def _stream_object(stream, device) -> torch.cuda.Stream:
+    """The torch.cuda.Stream of a stream argument: one itself, or a raw handle (0: the default stream)."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    raw = int(stream)
+    return torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
+
+
+def _empty(shape, dtype: torch.dtype, device, stream=None, result: bool = True) -> torch.Tensor:
+    """torch.empty for a call that runs on ``stream`` (None: the current one).
+
+    The memory comes from the pool of that stream: a block freed on the current
+    stream may still be in use by work queued there, which ``stream`` does not
+    wait for.  A ``result`` goes back to the caller, whose current stream may
+    use it until it is freed.
+    """
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    device = torch.device(device)
+    stream, here = _stream_object(stream, device), torch.cuda.current_stream(device)
+    if stream.device != here.device:
+        raise ValueError("the stream is one of %s, the tensors are on %s" % (stream.device, here.device))
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if result and stream != here and t.numel():
+        t.record_stream(here)
+    return t
+
+
 def _matrix(t: torch.Tensor, name: str):
     """(rows, cols, ld) of a 2-D device tensor with unit inner stride."""
     shape = t.shape

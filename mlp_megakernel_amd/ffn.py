@@ -2,7 +2,9 @@
 
 As the rest of the binding: argument checks and marshalling only, all
 arithmetic in ``libcoalesce.so``.  Tensors must live on one device; the calls
-run there, on ``stream`` or that device's current stream.
+run there, on ``stream`` or that device's current stream.  What a call makes
+(results, workspace) is allocated for that stream; that ``stream`` has waited
+for the inputs is the caller's part.
 """
 from __future__ import annotations
 
@@ -13,8 +15,8 @@ from typing import NamedTuple, Optional, Sequence, Tuple
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (ACT_NONE, NORM_2, NORM_INF, _ACTS, _DTYPES, _check, _matrix, _ptr, _raw_current_stream, _stream,
-               aligned_copy, load_library)
+from . import (ACT_NONE, NORM_2, NORM_INF, _ACTS, _DTYPES, _check, _empty, _matrix, _ptr, _raw_current_stream,
+               _stream, aligned_copy, load_library)
 
 
 class GemmGrads(NamedTuple):
@@ -42,17 +44,6 @@ def _raw_stream(stream, dev: int):
     if stream is None and _raw_current_stream is not None:
         return _raw_current_stream(dev)
     return _stream(stream)
-
-
-def _used_on(stream, *tensors):
-    """Tell the allocator that tensors it made here are used on another stream."""
-    if stream is None:
-        return
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream))
-    for t in tensors:
-        if t is not None and t.numel():
-            t.record_stream(stream)
 
 
 def _act(act):
@@ -126,8 +117,7 @@ def _take(workspace, need: int, dev: int, stream):
     if workspace is None:
         if need == 0:
             return None, 0, None
-        workspace = torch.empty(need, dtype=torch.uint8, device="cuda")  # the current device is dev here
-        _used_on(stream, workspace)
+        workspace = _empty(need, torch.uint8, "cuda", stream, result=False)  # the current device is dev here
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on GPU %d" % dev)
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
@@ -135,8 +125,7 @@ def _take(workspace, need: int, dev: int, stream):
 
 def _new(rows: int, cols: int, dtype, device, stream):
     ld = _row_pitch(cols, dtype)
-    t = torch.empty((rows, ld), dtype=dtype, device=device)
-    _used_on(stream, t)
+    t = _empty((rows, ld), dtype, device, stream)
     return t if ld == cols else t[:, :cols]
 
 
@@ -290,8 +279,7 @@ def gemm_residual_backward(A: torch.Tensor, B: torch.Tensor, dout: torch.Tensor,
             dB = _new(K, N, grad_dtype, A.device, stream)
         lddb = _mat(dB, "dB", K, N, grad_dtype, dev)
     if want_dbias:
-        dbias = torch.empty(N, dtype=grad_dtype, device=A.device)
-        _used_on(stream, dbias)
+        dbias = _empty(N, grad_dtype, A.device, stream)
     g = GemmGrads(dA if want_dA else None, dB if want_dB else None, dbias)
     ws, nws, _keep = _workspace("coalesce_gemm_residual_backward_workspace_size", dev, M, N, K, workspace, stream)
     _check(load_library().coalesce_gemm_residual_backward(
@@ -328,8 +316,7 @@ def gated_gemm_backward(A: torch.Tensor, Bg: torch.Tensor, Bu: torch.Tensor,
         dW = dB if dB is not None else tuple(_new(K, N, grad_dtype, A.device, stream) for _ in range(2))
         lddb = _one_pitch(dW, ("dB[0]", "dB[1]"), K, N, grad_dtype, dev)
     if want_dbias:
-        db = (torch.empty(N, dtype=grad_dtype, device=A.device), torch.empty(N, dtype=grad_dtype, device=A.device))
-        _used_on(stream, *db)
+        db = _empty(N, grad_dtype, A.device, stream), _empty(N, grad_dtype, A.device, stream)
     g = GatedGrads(dA if want_dA else None, dW[0], dW[1], db[0], db[1])
     ws, nws, _keep = _workspace("coalesce_gated_gemm_backward_workspace_size", dev, M, N, K, workspace, stream)
     _check(load_library().coalesce_gated_gemm_backward(
@@ -364,8 +351,7 @@ def _norm_code(norm_type) -> int:
 
 def _norm_out(norm, dev, stream):
     if norm is None:
-        norm = torch.empty((), dtype=torch.float32, device="cuda")  # the current device is dev here
-        _used_on(stream, norm)
+        norm = _empty((), torch.float32, "cuda", stream)  # the current device is dev here
     elif norm.numel() != 1 or norm.dtype is not torch.float32 or norm.get_device() != dev:
         raise ValueError("norm must be one float32 on GPU %d" % dev)
     return norm
