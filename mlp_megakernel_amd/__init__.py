@@ -169,12 +169,13 @@ def _matrix(t: torch.Tensor, name: str):
     return rows, cols, ld
 
 
-def aligned_empty(rows: int, cols: int, dtype: torch.dtype, device="cuda") -> torch.Tensor:
-    """rows x cols tensor whose leading dimension is padded to a multiple of 16 bytes."""
+def aligned_empty(rows: int, cols: int, dtype: torch.dtype, device="cuda", stream=None) -> torch.Tensor:
+    """rows x cols tensor whose leading dimension is padded to a multiple of 16 bytes,
+    for work on ``stream`` (None: the current one)."""
     es = torch.tensor([], dtype=dtype).element_size()
     per = 16 // es
     ld = max(per, (cols + per - 1) // per * per)
-    return torch.empty((rows, ld), dtype=dtype, device=device)[:, :cols]
+    return _empty((rows, ld), dtype, device, stream)[:, :cols]
 
 
 def aligned_copy(t: torch.Tensor, device="cuda") -> torch.Tensor:
@@ -187,13 +188,13 @@ def gemm_bias_act(A: torch.Tensor, B: torch.Tensor, bias: Optional[torch.Tensor]
                   out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None, stream=None):
     """Y = act(A @ B + bias) in one fused kernel (coalesce_gemm_bias_act)."""
     lib = load_library()
-    M, N, K, lda, ldb, ldy, out, odt = _gemm_args(A, B, bias, out_dtype, out)
+    M, N, K, lda, ldb, ldy, out, odt = _gemm_args(A, B, bias, out_dtype, out, stream)
     _check(lib.coalesce_gemm_bias_act(_ptr(A), lda, _ptr(B), ldb, _ptr(bias), _ptr(out), ldy, M, N, K,
                                       _DTYPES[A.dtype], _DTYPES[odt], _ACTS[act], _stream(stream)))
     return out
 
 
-def _gemm_args(A, B, bias, out_dtype, out):
+def _gemm_args(A, B, bias, out_dtype, out, stream):
     M, K, lda = _matrix(A, "A")
     K2, N, ldb = _matrix(B, "B")
     if K2 != K:
@@ -205,7 +206,7 @@ def _gemm_args(A, B, bias, out_dtype, out):
             raise ValueError("bias must be a contiguous length-N vector of the input dtype")
     odt = out_dtype or (out.dtype if out is not None else A.dtype)
     if out is None:
-        out = aligned_empty(M, N, odt, A.device)
+        out = aligned_empty(M, N, odt, A.device, stream)
     Mo, No, ldy = _matrix(out, "out")
     if (Mo, No) != (M, N) or out.dtype != odt:
         raise ValueError("out must be M x N of out_dtype")
@@ -259,7 +260,7 @@ def mlp_forward(x: torch.Tensor, weights: Sequence[torch.Tensor], hidden_act="so
     M, ldx, dims = _chain_dims(x, weights)
     L = len(weights)
     if out is None:
-        out = aligned_empty(M, dims[-1], x.dtype, x.device)
+        out = aligned_empty(M, dims[-1], x.dtype, x.device, stream)
     Mo, Do, ldo = _matrix(out, "out")
     if (Mo, Do) != (M, dims[-1]):
         raise ValueError("out must be M x dims[L]")
@@ -290,13 +291,13 @@ def mlp_forward_train(x: torch.Tensor, weights: Sequence[torch.Tensor], hidden_a
     M, ldx, dims = _chain_dims(x, weights)
     L = len(weights)
     if out is None:
-        out = aligned_empty(M, dims[-1], x.dtype, x.device)
+        out = aligned_empty(M, dims[-1], x.dtype, x.device, stream)
     Mo, Do, ldo = _matrix(out, "out")
     if (Mo, Do) != (M, dims[-1]):
         raise ValueError("out must be M x dims[L]")
     if acts is None:
         pitch = max(4, (max(dims[1:-1], default=4) + 3) // 4 * 4)
-        acts = [torch.empty((M, pitch), dtype=torch.float32, device=x.device)[:, :dims[l]] for l in range(1, L)]
+        acts = [_empty((M, pitch), torch.float32, x.device, stream)[:, :dims[l]] for l in range(1, L)]
     if len(acts) != L - 1:
         raise ValueError("need L - 1 activation buffers")
     lda = _acts_pitch(acts, M, dims)
@@ -335,14 +336,14 @@ def mlp_backward(x: torch.Tensor, weights: Sequence[torch.Tensor], acts: Sequenc
         raise ValueError("need the L - 1 stored activations")
     lda = _acts_pitch(acts, M, dims)
     if dW is None:
-        dW = [torch.empty((dims[l], dims[l + 1]), dtype=torch.float32, device=x.device) for l in range(L)]
+        dW = [_empty((dims[l], dims[l + 1]), torch.float32, x.device, stream) for l in range(L)]
     for l, g in enumerate(dW):
         if g.shape != (dims[l], dims[l + 1]) or g.dtype != torch.float32 or not g.is_contiguous():
             raise ValueError("dW[%d] must be a contiguous dims[l] x dims[l+1] float32 tensor" % l)
     ldq = 0
     if want_dx:
         if dx is None:
-            dx = aligned_empty(M, dims[0], x.dtype, x.device)
+            dx = aligned_empty(M, dims[0], x.dtype, x.device, stream)
         Mq, Dq, ldq = _matrix(dx, "dx")
         if (Mq, Dq) != (M, dims[0]) or dx.dtype != x.dtype:
             raise ValueError("dx must be M x dims[0] of x's dtype")
@@ -350,7 +351,7 @@ def mlp_backward(x: torch.Tensor, weights: Sequence[torch.Tensor], acts: Sequenc
         dx = None
     need = mlp_backward_workspace_size(dims, M)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _empty(need, torch.uint8, x.device, stream, result=False)
     _check(lib.coalesce_mlp_backward(_ptr(x), ldx, _ptr_array(weights), _dims_array(dims), L,
                                      _ptr_array(acts) if L > 1 else None, lda, _ptr(dout), ldd, _ptr_array(dW),
                                      _ptr(dx), ldq, M, _DTYPES[x.dtype], _ACTS[hidden_act], _ptr(workspace),
@@ -410,7 +411,7 @@ def weight_norm(vs: Sequence[torch.Tensor], gs: Sequence[torch.Tensor], Ws: Opti
     lib = load_library()
     dims = _wn_dims(vs, gs)
     if Ws is None:
-        Ws = [torch.empty_like(v) for v in vs]
+        Ws = [_empty(v.shape, v.dtype, v.device, stream) for v in vs]
     for W, v in zip(Ws, vs):
         if W.shape != v.shape or W.dtype != v.dtype or not W.is_contiguous():
             raise ValueError("every W must be a contiguous tensor shaped like its v")
@@ -428,8 +429,8 @@ def weight_norm_backward(vs: Sequence[torch.Tensor], gs: Sequence[torch.Tensor],
     for i, (dW, v) in enumerate(zip(dWs, vs)):
         if dW.shape != v.shape or dW.dtype != torch.float32 or not dW.is_contiguous():
             raise ValueError("dW[%d] must be a contiguous float32 tensor shaped like v[%d]" % (i, i))
-    dvs = [torch.empty(v.shape, dtype=torch.float32, device=v.device) for v in vs]
-    dgs = [torch.empty(g.shape, dtype=torch.float32, device=g.device) for g in gs]
+    dvs = [_empty(v.shape, torch.float32, v.device, stream) for v in vs]
+    dgs = [_empty(g.shape, torch.float32, g.device, stream) for g in gs]
     _check(lib.coalesce_weight_norm_backward(_ptr_array(vs), _ptr_array(gs), _ptr_array(dWs), _ptr_array(dvs),
                                              _ptr_array(dgs), _dims_array(dims), len(vs), F16,
                                              _stream(stream)))
@@ -446,9 +447,9 @@ class TuneReport(ctypes.Structure):
         return {name: getattr(self, name) for name, _ in self._fields_}
 
 
-def _tune_workspace(rows, row_bytes, device):
+def _tune_workspace(rows, row_bytes, device, stream):
     n = ((rows * row_bytes + 255) // 256) * 256 + 256
-    return torch.empty(n, dtype=torch.uint8, device=device)
+    return _empty(n, torch.uint8, device, stream, result=False)
 
 
 def autotune_gemm_bias_act(A: torch.Tensor, B: torch.Tensor, bias: Optional[torch.Tensor] = None, act="gelu",
@@ -458,8 +459,8 @@ def autotune_gemm_bias_act(A: torch.Tensor, B: torch.Tensor, bias: Optional[torc
     shape (coalesce_autotune_gemm_bias_act); later gemm_bias_act calls with
     the same shape use the winner."""
     lib = load_library()
-    M, N, K, lda, ldb, ldy, out, odt = _gemm_args(A, B, bias, out_dtype, out)
-    ws = _tune_workspace(M, N * out.element_size(), A.device)
+    M, N, K, lda, ldb, ldy, out, odt = _gemm_args(A, B, bias, out_dtype, out, stream)
+    ws = _tune_workspace(M, N * out.element_size(), A.device, stream)
     rep = TuneReport()
     _check(lib.coalesce_autotune_gemm_bias_act(_ptr(A), lda, _ptr(B), ldb, _ptr(bias), _ptr(out), ldy, M, N, K,
                                                _DTYPES[A.dtype], _DTYPES[odt], _ACTS[act], int(iters), _ptr(ws),
@@ -476,11 +477,11 @@ def autotune_mlp_forward(x: torch.Tensor, weights: Sequence[torch.Tensor], hidde
     M, ldx, dims = _chain_dims(x, weights)
     L = len(weights)
     if out is None:
-        out = aligned_empty(M, dims[-1], x.dtype, x.device)
+        out = aligned_empty(M, dims[-1], x.dtype, x.device, stream)
     Mo, Do, ldo = _matrix(out, "out")
     if (Mo, Do) != (M, dims[-1]):
         raise ValueError("out must be M x dims[L]")
-    ws = _tune_workspace(M, dims[-1] * out.element_size(), x.device)
+    ws = _tune_workspace(M, dims[-1] * out.element_size(), x.device, stream)
     rep = TuneReport()
     _check(lib.coalesce_autotune_mlp_forward(_ptr(x), ldx, _ptr_array(weights), _dims_array(dims), L,
                                              _ptr(out), ldo, M, _DTYPES[x.dtype], _ACTS[hidden_act], int(iters),
@@ -498,7 +499,7 @@ def bias_add(X: torch.Tensor, bias: torch.Tensor, out: Optional[torch.Tensor] = 
     lib = load_library()
     M, N, ldx = _matrix(X, "X")
     if out is None:
-        out = aligned_empty(M, N, X.dtype, X.device)
+        out = aligned_empty(M, N, X.dtype, X.device, stream)
     _, _, ldy = _matrix(out, "out")
     dt = _DTYPES[X.dtype]
     _check(lib.coalesce_bias_add(_ptr(X), ldx, _ptr(bias), _ptr(out), ldy, M, N, dt, _DTYPES[bias.dtype],
@@ -511,7 +512,7 @@ def activation(X: torch.Tensor, act="gelu", out: Optional[torch.Tensor] = None, 
     lib = load_library()
     M, N, ldx = _matrix(X, "X")
     if out is None:
-        out = aligned_empty(M, N, X.dtype, X.device)
+        out = aligned_empty(M, N, X.dtype, X.device, stream)
     _, _, ldy = _matrix(out, "out")
     _check(lib.coalesce_activation(_ptr(X), ldx, _ptr(out), ldy, M, N, _DTYPES[X.dtype], _ACTS[act],
                                    _stream(stream)))

@@ -97,3 +97,34 @@ def test_default_stream_by_its_handle():
         H = mk.gated_gemm(A, Bg, Bu, stream=0)
     torch.cuda.synchronize()
     assert torch.equal(H, mk.gated_gemm(A, Bg, Bu))
+
+
+def _chain():
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda").half()  # noqa: E731
+    x, Ws, dy = r(3000, 128), [r(128, 128) / 16 for _ in range(3)], r(3000, 128)
+    acts = mk.mlp_forward_train(x, Ws)[1]
+    g = [r(128).abs() for _ in Ws]
+    X, b = r(700, 136), r(136)
+    f32 = [w.float() for w in Ws]
+    return {
+        "gemm_bias_act": lambda s: mk.gemm_bias_act(x, Ws[0], g[0], stream=s),
+        "mlp_forward": lambda s: mk.mlp_forward(x, Ws, stream=s),
+        "mlp_forward_train": lambda s: mk.mlp_forward_train(x, Ws, stream=s),
+        "mlp_backward": lambda s: mk.mlp_backward(x, Ws, acts, dy, stream=s),
+        "weight_norm": lambda s: mk.weight_norm(Ws, g, stream=s),
+        "weight_norm_backward": lambda s: mk.weight_norm_backward(Ws, g, f32, stream=s),
+        "bias_add": lambda s: mk.bias_add(X, b, stream=s),
+        "activation": lambda s: mk.activation(X, stream=s),
+    }
+
+
+CHAIN = ["gemm_bias_act", "mlp_forward", "mlp_forward_train", "mlp_backward", "weight_norm", "weight_norm_backward",
+         "bias_add", "activation"]
+
+
+@pytest.mark.parametrize("name", CHAIN)
+def test_other_entry_points_take_no_memory_in_use(name):
+    call = _chain()[name]
+    _beside(call, _tensors(call(None)), torch.cuda.Stream())
+    progress(name)
