@@ -45,7 +45,7 @@ typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 // GELU in fp32 (the tanh approximation is off by ~1e-3), with no branch and
 // 17 VALU operations instead of the library erff's ~30 plus divergent
 // branches.
-__device__ __forceinline__ float erf_sqrt2(float z) {
+__device__ __forceinline__ float gelu_erf(float z) {
   const float zc = __builtin_amdgcn_fmed3f(z, -5.656854249f, 5.656854249f);
   const float u = zc * zc;
   float P = 4.390178103e-08f;
@@ -60,16 +60,10 @@ __device__ __forceinline__ float erf_sqrt2(float z) {
   Q = __builtin_fmaf(Q, u, 2.883771099e-02f);
   Q = __builtin_fmaf(Q, u, 2.524295846e-01f);
   Q = __builtin_fmaf(Q, u, 1.0f);
-  return zc * (P * __builtin_amdgcn_rcpf(Q));  // erf(z / sqrt 2)
-}
-__device__ __forceinline__ float gelu_erf(float z) {
-  const float e = erf_sqrt2(z);
+  const float e = zc * (P * __builtin_amdgcn_rcpf(Q));
   const float h = 0.5f * z;
   return __builtin_fmaf(h, e, h);
 }
-// The normal distribution function Phi(z) = (1 + erf(z / sqrt 2)) / 2 from the
-// same rational (GELU = z Phi(z); its derivative is Phi(z) + z phi(z)).
-__device__ __forceinline__ float gelu_cdf(float z) { return __builtin_fmaf(0.5f, erf_sqrt2(z), 0.5f); }
 
 // The same GELU with a degree-3/4 rational (same derivation, erf_fit.py):
 // 2.1e-5 absolute error on GELU in fp32, under 0.03 of an ulp of a bf16 or
@@ -106,21 +100,12 @@ __device__ __forceinline__ float softplus_guarded(float z) {
 // comparison does).
 __device__ __forceinline__ float relu(float z) { return __builtin_fmaxf(z, 0.0f); }
 
-// silu(z) = z / (1 + e^-z), the sigmoid from the hardware base-2 exponential
-// and reciprocal (about 2 ulp; a z of minus infinity gives NaN, as z times the
-// sigmoid does).
-__device__ __forceinline__ float sigmoid(float z) {
-  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
-}
-__device__ __forceinline__ float silu(float z) { return z * sigmoid(z); }
-
 // OUT16: the result is rounded to bf16 / fp16 (the shorter GELU suffices).
 template <int ACT, bool OUT16 = false>
 __device__ __forceinline__ float apply_act(float z) {
   if constexpr (ACT == ACT_GELU) return OUT16 ? gelu_erf16(z) : gelu_erf(z);
   else if constexpr (ACT == ACT_SOFTPLUS) return softplus_guarded(z);
   else if constexpr (ACT == ACT_RELU) return relu(z);
-  else if constexpr (ACT == ACT_SILU) return silu(z);
   else return z;
 }
 

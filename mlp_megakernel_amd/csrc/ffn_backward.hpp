@@ -14,30 +14,6 @@
 namespace coalesce {
 namespace {
 
-// act(z) and act'(z) in fp32.
-template <int ACT>
-__device__ __forceinline__ void act_and_grad(float z, float& f, float& d) {
-  if constexpr (ACT == ACT_SILU) {
-    const float s = sigmoid(z);
-    f = z * s;
-    d = s * __builtin_fmaf(z, 1.0f - s, 1.0f);
-  } else if constexpr (ACT == ACT_GELU) {
-    // Phi(z) + z phi(z), Phi from the same rational erf as the forward
-    f = gelu_erf(z);
-    const float phi = 0.398942280401432678f * __builtin_amdgcn_exp2f(z * z * -0.72134752044448170f);
-    d = __builtin_fmaf(z, phi, gelu_cdf(z));
-  } else if constexpr (ACT == ACT_SOFTPLUS) {
-    f = softplus_guarded(z);
-    d = sigmoid(z);
-  } else if constexpr (ACT == ACT_RELU) {
-    f = relu(z);
-    d = z > 0.0f ? 1.0f : 0.0f;
-  } else {
-    f = z;
-    d = 1.0f;
-  }
-}
-
 // Eight consecutive elements, whole (16-byte accesses) or `valid` of them.
 template <typename T>
 __device__ __forceinline__ void load8(const T* src, float (&f)[8]) {

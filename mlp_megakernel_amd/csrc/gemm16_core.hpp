@@ -20,6 +20,7 @@
 #pragma once
 #include <atomic>
 
+#include "ffn_act.hpp"
 #include "gemm16_common.hpp"
 #include "launch.hpp"
 
@@ -54,34 +55,6 @@ __device__ __forceinline__ f32x4 load4(const T* src, int valid) {
       if (r < valid) v[r] = (float)src[r];
   }
   return v;
-}
-
-// The activation a launch names: a uniform branch per four values, nothing
-// beside a tile's K loop (and a fifth of the kernels that one per activation
-// would take).
-template <bool OUT16 = false>
-__device__ __forceinline__ f32x4 act_any(int act, f32x4 z) {
-  f32x4 f = z;
-  switch (act) {
-    case ACT_GELU:
-#pragma unroll
-      for (int r = 0; r < 4; ++r) f[r] = apply_act<ACT_GELU, OUT16>(z[r]);
-      break;
-    case ACT_SOFTPLUS:
-#pragma unroll
-      for (int r = 0; r < 4; ++r) f[r] = softplus_guarded(z[r]);
-      break;
-    case ACT_RELU:
-#pragma unroll
-      for (int r = 0; r < 4; ++r) f[r] = relu(z[r]);
-      break;
-    case ACT_SILU:
-#pragma unroll
-      for (int r = 0; r < 4; ++r) f[r] = silu(z[r]);
-      break;
-    default: break;
-  }
-  return f;
 }
 
 enum Lay { LAY_K = 0, LAY_X = 1 };
@@ -583,7 +556,7 @@ struct Tile {
                 [&](int t, int n, int valid) { return Pair{bias_g(t, n, valid), bias_u(t, n, valid)}; },
                 [&](Pair c, int t, int s, int, int, int, const char*) {
                   const f32x4 g = acc[t][s] + c.g, u = acc[t + G::NTO][s] + c.u;
-                  return act_any<O16>(act, g) * u;
+                  return act_any(act, g) * u;
                 });
       } else {
         const TO* R = (const TO*)p->R;
@@ -593,7 +566,7 @@ struct Tile {
                   const f32x4 z = acc[t][s] + c;
                   f32x4 o = (f32x4){0.f, 0.f, 0.f, 0.f};
                   if (R) o = load4<TO>(cell ? (const TO*)cell : R + (int64_t)m * p->ldr + n, valid);
-                  return o + act_any<O16>(act, z);
+                  return o + act_any(act, z);
                 });
       }
     }

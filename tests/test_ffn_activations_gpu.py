@@ -1,0 +1,99 @@
+"""The activations of the feed-forward operators where their values are small or
+not finite, on every kernel that applies them: the few-row kernel, whole and
+ragged tiles, and the pass that joins a split contraction.
+
+The pre-activations are exact: each output column n picks the contraction index
+n mod 16 with a weight of one, so z[m][n] = A[m][n mod 16] and every other
+product is zero.  What is left is the activation's own error, a product or a sum
+in fp32 (half a step, 2^-24) and the rounding of the result."""
+import pytest
+import torch
+
+import ffn_reference as ref
+import mlp_megakernel_amd as mk
+from helpers import progress
+
+pytestmark = pytest.mark.gpu
+
+# rows, columns, contraction: few rows in strips of 16, 32 and 64; whole and
+# ragged tiles of every height; split contractions
+SHAPES = [(1, 40, 64), (17, 4100, 64), (40, 8200, 72), (64, 200, 64), (65, 40, 64), (70, 300, 4100), (500, 1030, 4100),
+          (1300, 1030, 64), (3000, 1030, 64), (4100, 5461, 130), (8192, 4096, 64)]
+# Relative errors in units of 2^-24; the hardware's exponential, logarithm and
+# reciprocal are good to 1 ulp (2 units).
+#  * gelu: nine Horner steps of positive terms (1 unit each) with coefficients
+#    rounded to fp32 (1 each for numerator and denominator), reciprocal 2,
+#    exponential 2, three products 3: 18; the exponent z^2 (-log2(e) / 2) carries
+#    2.5 roundings, z^2 / 2 times 2.5 units in the exponential: 1.25 z^2.  The fit
+#    itself is good to 5.1e-9 (0.1 units).
+def gelu_rel(z):
+    return (18.5 + 1.25 * z * z) * ref.U32
+
+
+def pick(M, N, K, dt, values):
+    """A, B with A @ B = the values, in turn over rows and the first 16 indices of the contraction."""
+    n = M * 16
+    A = torch.zeros(M, (K + 7) // 8 * 8, dtype=dt, device="cuda")
+    A[:, :16] = values.to(dt).repeat((n + values.numel() - 1) // values.numel())[:n].view(M, 16)
+    B = torch.zeros(K, (N + 7) // 8 * 8, dtype=dt, device="cuda")
+    c = torch.arange(N, device="cuda")
+    B[c % 16, c] = 1.0
+    z = A[:, :16].double()[:, c.remainder(16)]
+    return A[:, :K], B[:, :N], z
+
+
+FLUSH = 2.0 ** -126     # what is below may be taken as zero
+
+
+def within(got, v, e, dtype, what):
+    ref.check(got, (v, ref.rounded(v, e, dtype) + FLUSH), what)
+
+
+def gelu64(z):
+    return z * 0.5 * torch.erfc(-z / 2.0 ** 0.5)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("out32", [False, True])
+def test_gelu_keeps_its_tail(dt, out32):
+    od = torch.float32 if out32 else dt
+    # the tail, both sides of zero, and far beyond
+    zs = torch.cat([torch.linspace(-14.0, 9.0, 1187), torch.tensor([-1000.0, -100.0, -20.0, 0.0, 1e-4, -1e-4, 20.0])])
+    for shape in SHAPES:
+        M, N, K = shape
+        A, B, z = pick(M, N, K, dt, zs.cuda())
+        up = 64.0
+        f = gelu64(z)
+        e = f.abs() * gelu_rel(z) + z.abs() * FLUSH    # the exponential flushed
+        Y = mk.gemm_residual(A, B, act="gelu", out_dtype=od)
+        within(Y, f, e, od, "act %s" % (shape,))
+        # times u = 64 z
+        H = mk.gated_gemm(A, B, mk.aligned_copy(B * up), act="gelu", out_dtype=od)
+        v = f * (up * z)
+        within(H, v, (up * z).abs() * e + ref.U32 * v.abs(), od, "gated %s" % (shape,))
+        progress("gelu %s %s %s" % (dt, od, shape))
+
+
+def grads(zs, dt, act):
+    """act(z) and act'(z) in fp32 as the backward takes them: the bias gradients of one row, dY = Zu = 1."""
+    n = zs.numel()
+    z = zs.to(dt).cuda()[None, :].contiguous()
+    one = torch.ones_like(z)
+    A, B = torch.zeros(1, 8, dtype=dt, device="cuda"), torch.zeros(8, n, dtype=dt, device="cuda")
+    g = mk.gated_gemm_backward(A, B, B, (z, one), one.float(), act=act, want_dA=False, want_dB=False, want_dbias=True)
+    r = mk.gemm_residual_backward(A, B, one, z, act=act, want_dA=False, want_dB=False, want_dbias=True)
+    assert torch.equal(r.dbias, g.dbias_g)
+    return z[0].double(), g.dbias_u, g.dbias_g
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+def test_gelu_of_the_backward(dt):
+    zs = torch.cat([torch.linspace(-14.0, 9.0, 4094), torch.tensor([-1000.0, 0.0])])
+    z, f, d = grads(zs, dt, "gelu")
+    v, u = gelu64(z), ref.U32
+    ref.check(f, (v, v.abs() * gelu_rel(z) + z.abs() * FLUSH + FLUSH), "gelu")
+    # Phi(z) + z phi(z): the two terms' errors (phi: exponential 2, constant and
+    # two products 3) and the sum's rounding
+    cdf, zphi = 0.5 * torch.erfc(-z / 2.0 ** 0.5), z * torch.exp(-z * z / 2) / (2 * torch.pi) ** 0.5
+    e = cdf * gelu_rel(z) + zphi.abs() * (5 + 1.25 * z * z) * u + (cdf + zphi).abs() * u
+    ref.check(d, (cdf + zphi, e + z.abs() * FLUSH + FLUSH), "gelu'")
