@@ -41,6 +41,19 @@ __device__ __forceinline__ float sigmoid(float z) {
 }
 __device__ __forceinline__ float silu(float z) { return z * sigmoid(z); }
 
+// softplus(z) = ln(1 + e^z): z above 20, and where t = e^z is small, by the series
+// of ln(1 + t), since 1 + t drops t's last bits (at -10 all but 9 of them, below
+// -17 all).  Its first five terms leave 2^-25 / 6 relative at t = 2^-5.
+__device__ __forceinline__ float softplus(float z) {
+  const float t = __builtin_amdgcn_exp2f(z * 1.44269504088896341f);
+  float p = __builtin_fmaf(t, -0.2f, 0.25f);
+  p = __builtin_fmaf(t, -p, 0.333333333f);
+  p = __builtin_fmaf(t, -p, 0.5f);
+  p = __builtin_fmaf(t, -p, 1.0f);
+  const float s = t < 0.03125f ? t * p : __builtin_amdgcn_logf(1.0f + t) * 0.693147180559945309f;
+  return z > 20.0f ? z : s;
+}
+
 // The activation a launch names: a uniform branch per four values, nothing
 // beside a tile's K loop (and a fifth of the kernels that one per activation
 // would take).
@@ -56,7 +69,7 @@ __device__ __forceinline__ f32x4 act_any(int act, f32x4 z) {
       break;
     case ACT_SOFTPLUS:
 #pragma unroll
-      for (int r = 0; r < 4; ++r) f[r] = softplus_guarded(z[r]);
+      for (int r = 0; r < 4; ++r) f[r] = softplus(z[r]);
       break;
     case ACT_RELU:
 #pragma unroll
@@ -85,7 +98,7 @@ __device__ __forceinline__ void act_and_grad(float z, float& f, float& d) {
     f = z * cdf;
     d = __builtin_fmaf(z, 0.398942280401432678f * e, cdf);
   } else if constexpr (ACT == ACT_SOFTPLUS) {
-    f = softplus_guarded(z);
+    f = softplus(z);
     d = sigmoid(z);
   } else if constexpr (ACT == ACT_RELU) {
     f = relu(z);

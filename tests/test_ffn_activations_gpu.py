@@ -97,3 +97,46 @@ def test_gelu_of_the_backward(dt):
     cdf, zphi = 0.5 * torch.erfc(-z / 2.0 ** 0.5), z * torch.exp(-z * z / 2) / (2 * torch.pi) ** 0.5
     e = cdf * gelu_rel(z) + zphi.abs() * (5 + 1.25 * z * z) * u + (cdf + zphi).abs() * u
     ref.check(d, (cdf + zphi, e + z.abs() * FLUSH + FLUSH), "gelu'")
+
+
+# Hardware exponential of z log2(e) (constant and product rounded: 1.5 |z| units,
+# its own ulp 2), as the sigmoid adds 1 (1 unit) and takes a reciprocal (2).
+def sigmoid_rel(z):
+    return (5 + 1.5 * z.abs()) * ref.U32
+
+
+def softplus64(z):
+    return torch.clamp(z, min=0) + torch.log1p(torch.exp(-z.abs()))
+
+
+def softplus_err(z):
+    """Below ln(2^-5) the series of ln(1 + t): t's error, two products, 0.1 for the terms left out.  Above, 1 + t is
+    rounded (1 unit of 1 + t, so of the logarithm) with t's error beside it, then the logarithm (2) and its base
+    change (1.5).  Above 20 z itself: e^-20 is below a unit."""
+    u, f, t = ref.U32, softplus64(z), torch.exp(torch.clamp(z, max=20.0))
+    et = (2 + 1.5 * z.abs()) * u
+    return torch.where(z < -3.4, f * (et + 2.1 * u), torch.zeros_like(f)) + \
+        torch.where((z > -3.5) & (z <= 20), u + et * t / (1 + t) + 3.5 * u * f, u * f.abs()) + FLUSH
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("out32", [False, True])
+def test_softplus_keeps_its_tail(dt, out32):
+    od = torch.float32 if out32 else dt
+    zs = torch.cat([torch.linspace(-40.0, 25.0, 1187), torch.tensor([-100.0, -17.5, -10.0, 0.0, 1e-4])])
+    for shape in SHAPES:
+        A, B, z = pick(*shape, dt, zs.cuda())
+        f, e = softplus64(z), softplus_err(z)
+        within(mk.gemm_residual(A, B, act="softplus", out_dtype=od), f, e, od, "act %s" % (shape,))
+        H = mk.gated_gemm(A, B, mk.aligned_copy(B * 32.0), act="softplus", out_dtype=od)
+        v = f * (32.0 * z)
+        within(H, v, (32.0 * z).abs() * e + ref.U32 * v.abs(), od, "gated %s" % (shape,))
+        progress("softplus %s %s %s" % (dt, od, shape))
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+def test_softplus_of_the_backward(dt):
+    z, f, d = grads(torch.cat([torch.linspace(-40.0, 25.0, 4093), torch.tensor([-100.0, -17.5, 0.0])]), dt, "softplus")
+    ref.check(f, (softplus64(z), softplus_err(z)), "softplus")
+    s = torch.sigmoid(z)
+    ref.check(d, (s, s * sigmoid_rel(z) + 2 * FLUSH), "softplus'")
