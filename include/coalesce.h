@@ -412,7 +412,11 @@ coalesce_status coalesce_autotune_mlp_forward(const void* x, int64_t ldx, const 
  *     differ in its last bits between calls with another M, since the number
  *     of rows decides how the contraction is split.
  * Infinities and NaN in rows or columns a caller does not use stay there:
- * padding between the row's end and the pitch is never part of a result.
+ * padding between the row's end and the pitch is never part of a result.  In
+ * the values themselves they go through as in the formulas: a NaN
+ * pre-activation gives NaN with every act (RELU too, unlike
+ * coalesce_gemm_bias_act), minus infinity gives 0 with RELU and SOFTPLUS and NaN
+ * with GELU_ERF and SILU (-inf times 0).
  */
 
 /*

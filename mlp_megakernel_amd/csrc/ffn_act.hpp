@@ -54,6 +54,10 @@ __device__ __forceinline__ float softplus(float z) {
   return z > 20.0f ? z : s;
 }
 
+// relu_nan(z) = z < 0 ? 0 : z: a NaN stays one, where max(z, 0) gives 0 and a residual
+// added to it would hide that the product was none.
+__device__ __forceinline__ float relu_nan(float z) { return z < 0.0f ? 0.0f : z; }
+
 // The activation a launch names: a uniform branch per four values, nothing
 // beside a tile's K loop (and a fifth of the kernels that one per activation
 // would take).
@@ -73,7 +77,7 @@ __device__ __forceinline__ f32x4 act_any(int act, f32x4 z) {
       break;
     case ACT_RELU:
 #pragma unroll
-      for (int r = 0; r < 4; ++r) f[r] = relu(z[r]);
+      for (int r = 0; r < 4; ++r) f[r] = relu_nan(z[r]);
       break;
     case ACT_SILU:
 #pragma unroll
@@ -101,7 +105,7 @@ __device__ __forceinline__ void act_and_grad(float z, float& f, float& d) {
     f = softplus(z);
     d = sigmoid(z);
   } else if constexpr (ACT == ACT_RELU) {
-    f = relu(z);
+    f = relu_nan(z);
     d = z > 0.0f ? 1.0f : 0.0f;
   } else {
     f = z;

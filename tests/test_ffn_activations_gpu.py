@@ -140,3 +140,39 @@ def test_softplus_of_the_backward(dt):
     ref.check(f, (softplus64(z), softplus_err(z)), "softplus")
     s = torch.sigmoid(z)
     ref.check(d, (s, s * sigmoid_rel(z) + 2 * FLUSH), "softplus'")
+
+
+# The formulas at values that are not finite, as 64-bit arithmetic evaluates
+# them: z Phi(z) and z sigma(z) at minus infinity are -inf * 0.
+NAN, INF = float("nan"), float("inf")
+NONFINITE = {"none": (NAN, INF, -INF), "relu": (NAN, INF, 0.0), "silu": (NAN, INF, NAN), "gelu": (NAN, INF, NAN),
+             "softplus": (NAN, INF, 0.0)}
+
+
+@pytest.mark.parametrize("act", sorted(NONFINITE))
+@pytest.mark.parametrize("out32", [False, True])
+def test_values_that_are_not_finite(act, out32):
+    d = torch.bfloat16
+    od = torch.float32 if out32 else d
+    want = torch.tensor(NONFINITE[act], device="cuda", dtype=torch.float64)
+    for M, N, K in SHAPES:
+        # z[m][n] = A[m][0]: rows of NaN, infinity, minus infinity and 1.5 in turn
+        A = torch.zeros(M, (K + 7) // 8 * 8, dtype=d, device="cuda")
+        A[:, 0] = torch.tensor([NAN, INF, -INF, 1.5], device="cuda").repeat((M + 3) // 4)[:M]
+        B = torch.zeros(K, (N + 7) // 8 * 8, dtype=d, device="cuda")
+        B[0] = 1.0
+        A, B = A[:, :K], B[:, :N]
+        R = torch.full((M, (N + 7) // 8 * 8), 2.0, dtype=od, device="cuda")[:, :N]
+        Y = mk.gemm_residual(A, B, R, act=act, out_dtype=od)
+        H = mk.gated_gemm(A, B, B, act=act, out_dtype=od)
+        for i in range(min(M, 3)):
+            y = torch.full_like(Y[i::4], float(want[i] + 2.0))
+            h = torch.full_like(H[i::4], float(want[i] * (NAN, INF, -INF)[i]))
+            assert torch.equal(Y[i::4].nan_to_num(nan=7.0), y.nan_to_num(nan=7.0)), (act, M, N, K, i)
+            assert torch.equal(H[i::4].nan_to_num(nan=7.0), h.nan_to_num(nan=7.0)), (act, M, N, K, i)
+        assert bool(torch.isfinite(Y[3::4]).all()) and bool(torch.isfinite(H[3::4]).all())
+
+
+def test_relu_of_the_backward_keeps_nan():
+    z, f, d = grads(torch.tensor([NAN, -1.0, 0.0, 2.0]), torch.bfloat16, "relu")
+    assert bool(torch.isnan(f[0])) and f[1:].tolist() == [0.0, 0.0, 2.0] and d.tolist() == [0.0, 0.0, 0.0, 1.0]
