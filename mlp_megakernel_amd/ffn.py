@@ -10,13 +10,13 @@ from __future__ import annotations
 
 import math
 import weakref
-from typing import NamedTuple, Optional, Sequence, Tuple
+from typing import Iterable, NamedTuple, Optional, Tuple
 
 import torch
 from torch.autograd.function import once_differentiable
 
 from . import (ACT_NONE, NORM_2, NORM_INF, _ACTS, _DTYPES, _check, _empty, _matrix, _ptr, _raw_current_stream,
-               _stream, aligned_copy, load_library)
+               _stream, _stream_object, aligned_copy, load_library)
 
 
 class GemmGrads(NamedTuple):
@@ -330,6 +330,23 @@ def gated_gemm_backward(A: torch.Tensor, Bg: torch.Tensor, Bu: torch.Tensor,
 # Gradient norm and clipping
 # ---------------------------------------------------------------------------
 
+def _held(tensors, stream):
+    """`tensors` as a list or tuple.  Those of a generator may be made as it
+    runs and live only in the list: it has to outlive the launch, and `stream`
+    has to wait for them, as no caller could tell it to."""
+    if tensors is None or isinstance(tensors, (list, tuple)):
+        return tensors
+    tensors = list(tensors)
+    if stream is not None:
+        for t in tensors:
+            if isinstance(t, torch.Tensor) and t.is_cuda:
+                on, here = _stream_object(stream, t.device), torch.cuda.current_stream(t.device)
+                if on != here:
+                    on.wait_stream(here)
+                    t.record_stream(on)
+    return tensors
+
+
 def _grad_list(tensors, out):
     """(count, device, sources, destinations, sizes, types): the host arrays of
     the C call (bytes objects, to be kept alive until it returns)."""
@@ -357,21 +374,23 @@ def _norm_out(norm, dev, stream):
     return norm
 
 
-def grad_norm(tensors: Sequence[torch.Tensor], norm_type=2.0, norm: Optional[torch.Tensor] = None,
+def grad_norm(tensors: Iterable[torch.Tensor], norm_type=2.0, norm: Optional[torch.Tensor] = None,
               workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The 2-norm or largest magnitude (``norm_type`` inf) of all the tensors
     taken as one vector, as a float32 scalar on their device (coalesce_grad_norm)."""
+    tensors = _held(tensors, stream)
     return _norm_call(_grad_list(tensors, None), None, norm_type, norm, workspace, stream)
 
 
-def clip_grad_norm(tensors: Sequence[torch.Tensor], max_norm: float, norm_type=2.0,
-                   out: Optional[Sequence[torch.Tensor]] = None, norm: Optional[torch.Tensor] = None,
+def clip_grad_norm(tensors: Iterable[torch.Tensor], max_norm: float, norm_type=2.0,
+                   out: Optional[Iterable[torch.Tensor]] = None, norm: Optional[torch.Tensor] = None,
                    workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Scale gradients so that their global norm is at most ``max_norm``
     (coalesce_clip_grad_norm) and return the norm they had, a float32 scalar on
     their device.  In place, or into ``out`` (one tensor per gradient, of its
     size, memory order and dtype).  Nothing synchronises with the host; tensors of
     several dtypes may be mixed."""
+    tensors, out = _held(tensors, stream), _held(out, stream)
     return _norm_call(_grad_list(tensors, out), float(max_norm), norm_type, norm, workspace, stream)
 
 
