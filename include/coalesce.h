@@ -520,6 +520,27 @@ coalesce_status coalesce_clip_grad_norm(const void* const* grads, void* const* o
                                         const int32_t* dtypes, int64_t count, coalesce_norm norm_type, double max_norm,
                                         float* norm, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * The same over a list in which matrices may have rows that lie apart, as the
+ * gradients of the entry points above do where a row is not a multiple of 16
+ * bytes, or the halves of a wider matrix: tensor i is numel[i] / cols[i] rows of
+ * cols[i] elements, ld[i] elements apart in grads[i] and ld_out[i] in out[i]
+ * (equal where out[i] is grads[i]).  cols[i] == 0: dense, ld[i] is not read;
+ * cols NULL: all are.  What stands between the rows is neither taken into the
+ * norm nor written.
+ */
+size_t coalesce_grad_norm_rows_workspace_size(const int64_t* numel, const int64_t* cols, const int32_t* dtypes,
+                                              int64_t count);
+coalesce_status coalesce_grad_norm_rows(const void* const* grads, const int64_t* numel, const int64_t* cols,
+                                        const int64_t* ld, const int32_t* dtypes, int64_t count,
+                                        coalesce_norm norm_type, float* norm, void* workspace, size_t workspace_bytes,
+                                        void* stream);
+coalesce_status coalesce_clip_grad_norm_rows(const void* const* grads, void* const* out, const int64_t* numel,
+                                             const int64_t* cols, const int64_t* ld, const int64_t* ld_out,
+                                             const int32_t* dtypes, int64_t count, coalesce_norm norm_type,
+                                             double max_norm, float* norm, void* workspace, size_t workspace_bytes,
+                                             void* stream);
+
 /* Forget every tuned configuration (all devices). */
 coalesce_status coalesce_autotune_clear(void);
 

@@ -61,6 +61,9 @@ SIGNATURES = {
     "coalesce_grad_norm_workspace_size": (_sz, [_p, _p, _i64]),
     "coalesce_grad_norm": (_i32, [_p, _p, _p, _i64, _i32, _p, _p, _sz, _p]),
     "coalesce_clip_grad_norm": (_i32, [_p, _p, _p, _p, _i64, _i32, _f64, _p, _p, _sz, _p]),
+    "coalesce_grad_norm_rows_workspace_size": (_sz, [_p, _p, _p, _i64]),
+    "coalesce_grad_norm_rows": (_i32, [_p, _p, _p, _p, _p, _i64, _i32, _p, _p, _sz, _p]),
+    "coalesce_clip_grad_norm_rows": (_i32, [_p, _p, _p, _p, _p, _p, _p, _i64, _i32, _f64, _p, _p, _sz, _p]),
     "coalesce_autotune_clear": (_i32, []),
     "coalesce_bias_add": (_i32, [_p, _i64, _p, _p, _i64, _i64, _i64, _i32, _i32, _i32, _p]),
     "coalesce_activation": (_i32, [_p, _i64, _p, _i64, _i64, _i64, _i32, _i32, _p]),

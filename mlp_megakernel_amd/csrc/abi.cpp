@@ -1217,8 +1217,9 @@ size_t ffn_workspace_size(bool gated, bool backward, int64_t M, int64_t N, int64
 
 // The checked list of the gradient-norm entry points; dst may be NULL (norm
 // alone) or hold the sources themselves (in place).
-coalesce_status check_grad_list(const void* const* src, void* const* dst, const int64_t* numel, const int32_t* dtypes,
-                                int64_t count, coalesce_norm norm_type, const float* norm, ClipList* l) {
+coalesce_status check_grad_list(const void* const* src, void* const* dst, const int64_t* numel, const int64_t* cols,
+                                const int64_t* ld, const int64_t* ld_out, const int32_t* dtypes, int64_t count,
+                                coalesce_norm norm_type, const float* norm, ClipList* l) {
   if (count < 0) return fail(COALESCE_ERR_INVALID_ARGUMENT, "negative tensor count");
   if (norm_type != COALESCE_NORM_2 && norm_type != COALESCE_NORM_INF)
     return fail(COALESCE_ERR_INVALID_ARGUMENT, "unknown norm %d", (int)norm_type);
@@ -1237,7 +1238,21 @@ coalesce_status check_grad_list(const void* const* src, void* const* dst, const 
       return fail(COALESCE_ERR_UNSUPPORTED, "tensor %lld is not aligned to its element size", (long long)i);
     if (numel[i] > (int64_t(1) << 48) - total) return fail(COALESCE_ERR_UNSUPPORTED, "more than 2^48 elements");
     total += numel[i];
+    if (!cols || cols[i] == 0) continue;
+    if (cols[i] < 0 || numel[i] % cols[i])
+      return fail(COALESCE_ERR_INVALID_ARGUMENT, "tensor %lld is no matrix of %lld columns", (long long)i,
+                  (long long)cols[i]);
+    if (ld[i] < cols[i] || (dst && ld_out[i] < cols[i]))
+      return fail(COALESCE_ERR_INVALID_ARGUMENT, "the pitch of tensor %lld is shorter than its row", (long long)i);
+    const int64_t rows = numel[i] / cols[i], lim = (int64_t(1) << 48) / rows;
+    if (ld[i] > lim || (dst && ld_out[i] > lim))
+      return fail(COALESCE_ERR_UNSUPPORTED, "tensor %lld spans more than 2^48 elements", (long long)i);
+    if (dst && src[i] == dst[i] && ld[i] != ld_out[i])
+      return fail(COALESCE_ERR_INVALID_ARGUMENT, "tensor %lld in place with different pitches", (long long)i);
   }
+  l->cols = cols;
+  l->ld = ld;
+  l->ld_out = ld_out;
   l->src = src;
   l->dst = dst;
   l->numel = numel;
@@ -1251,8 +1266,7 @@ coalesce_status check_grad_list(const void* const* src, void* const* dst, const 
 // and the furthest-reaching one before it.
 coalesce_status check_grad_overlap(const ClipList& l, const float* norm, const void* ws, size_t ws_bytes) {
   struct Item {
-    Range r;
-    bool out;
+    Operand o;
     int64_t i;
   };
   std::vector<Item> v;
@@ -1261,27 +1275,39 @@ coalesce_status check_grad_overlap(const ClipList& l, const float* norm, const v
     if (l.numel[i] == 0) continue;
     const int64_t es = dsize(l.dtype[i]);
     const bool in_place = l.dst && l.dst[i] == l.src[i];
-    if (!in_place) v.push_back({span(l.src[i], 1, l.numel[i], l.numel[i], es), false, i});
-    if (l.dst) v.push_back({span(l.dst[i], 1, l.numel[i], l.numel[i], es), true, i});
+    const int64_t cols = l.cols && l.cols[i] ? l.cols[i] : l.numel[i], rows = l.numel[i] / cols;
+    auto add = [&](const void* p, int64_t ld, bool out) {
+      v.push_back({{span(p, rows, cols, ld, es), "", out, (uint64_t)(cols * es), (uint64_t)(ld * es)}, i});
+    };
+    if (!in_place) add(l.src[i], rows > 1 ? l.ld[i] : cols, false);
+    if (l.dst) add(l.dst[i], rows > 1 ? l.ld_out[i] : cols, true);
   }
-  v.push_back({{(uintptr_t)norm, (uintptr_t)norm + 4}, true, -1});
-  if (ws_bytes) v.push_back({{(uintptr_t)ws, (uintptr_t)ws + ws_bytes}, true, -2});
-  std::sort(v.begin(), v.end(), [](const Item& a, const Item& b) { return a.r.lo < b.r.lo; });
+  v.push_back({{{(uintptr_t)norm, (uintptr_t)norm + 4}, "", true}, -1});
+  if (ws_bytes) v.push_back({{{(uintptr_t)ws, (uintptr_t)ws + ws_bytes}, "", true}, -2});
+  std::sort(v.begin(), v.end(), [](const Item& a, const Item& b) { return a.o.r.lo < b.o.r.lo; });
   uintptr_t end_any = 0, end_out = 0;
-  for (const Item& x : v) {
-    if (x.r.lo < end_out || (x.out && x.r.lo < end_any))
-      return fail(COALESCE_ERR_INVALID_ARGUMENT, "an output (tensor %lld) overlaps another operand", (long long)x.i);
+  for (size_t k = 0; k < v.size(); ++k) {
+    const Operand& x = v[k].o;
+    if (x.r.lo < end_out || (x.out && x.r.lo < end_any)) {
+      // matrices of one pitch may lie between each other's rows
+      for (size_t j = 0; j < k; ++j)
+        if ((x.out || v[j].o.out) && overlap(v[j].o.r, x.r) && !(l.cols && interleaved(v[j].o, x)))
+          return fail(COALESCE_ERR_INVALID_ARGUMENT, "an output (tensor %lld) overlaps another operand",
+                      (long long)v[k].i);
+    }
     end_any = std::max(end_any, x.r.hi);
     if (x.out) end_out = std::max(end_out, x.r.hi);
   }
   return COALESCE_OK;
 }
 
-coalesce_status grad_norm_impl(const void* const* src, void* const* dst, const int64_t* numel, const int32_t* dtypes,
-                               int64_t count, coalesce_norm norm_type, double max_norm, float* norm, void* workspace,
+coalesce_status grad_norm_impl(const void* const* src, void* const* dst, const int64_t* numel, const int64_t* cols,
+                               const int64_t* ld, const int64_t* ld_out, const int32_t* dtypes, int64_t count,
+                               coalesce_norm norm_type, double max_norm, float* norm, void* workspace,
                                size_t workspace_bytes, void* stream) {
   ClipList l{};
-  coalesce_status s = check_grad_list(src, dst, numel, dtypes, count, norm_type, norm, &l);
+  if (cols && (!ld || (dst && !ld_out))) return fail(COALESCE_ERR_INVALID_ARGUMENT, "cols without ld or ld_out");
+  coalesce_status s = check_grad_list(src, dst, numel, cols, ld, ld_out, dtypes, count, norm_type, norm, &l);
   if (s != COALESCE_OK) return s;
   int cus = 0;
   if ((s = current_cus(&cus)) != COALESCE_OK) return s;
@@ -1356,10 +1382,16 @@ coalesce_status coalesce_gated_gemm_backward(const void* A, int64_t lda, const v
 }
 
 size_t coalesce_grad_norm_workspace_size(const int64_t* numel, const int32_t* dtypes, int64_t count) {
+  return coalesce_grad_norm_rows_workspace_size(numel, nullptr, dtypes, count);
+}
+
+size_t coalesce_grad_norm_rows_workspace_size(const int64_t* numel, const int64_t* cols, const int32_t* dtypes,
+                                              int64_t count) {
   if (count <= 0 || !numel || !dtypes) return 0;
   int64_t total = 0;
   for (int64_t i = 0; i < count; ++i) {
     if (numel[i] < 0 || numel[i] > (int64_t(1) << 48) - total || !valid_dtype(dtypes[i])) return 0;
+    if (cols && cols[i] && (cols[i] < 0 || numel[i] % cols[i])) return 0;
     total += numel[i];
   }
   int cus = 0;
@@ -1369,21 +1401,41 @@ size_t coalesce_grad_norm_workspace_size(const int64_t* numel, const int32_t* dt
   l.numel = numel;
   l.dtype = dtypes;
   l.count = count;
+  l.cols = cols;
   return grad_norm_workspace(l, cus);
 }
 
 coalesce_status coalesce_grad_norm(const void* const* grads, const int64_t* numel, const int32_t* dtypes,
                                    int64_t count, coalesce_norm norm_type, float* norm, void* workspace,
                                    size_t workspace_bytes, void* stream) {
-  return grad_norm_impl(grads, nullptr, numel, dtypes, count, norm_type, 0.0, norm, workspace, workspace_bytes, stream);
+  return coalesce_grad_norm_rows(grads, numel, nullptr, nullptr, dtypes, count, norm_type, norm, workspace,
+                                 workspace_bytes, stream);
+}
+
+coalesce_status coalesce_grad_norm_rows(const void* const* grads, const int64_t* numel, const int64_t* cols,
+                                        const int64_t* ld, const int32_t* dtypes, int64_t count,
+                                        coalesce_norm norm_type, float* norm, void* workspace, size_t workspace_bytes,
+                                        void* stream) {
+  return grad_norm_impl(grads, nullptr, numel, cols, ld, nullptr, dtypes, count, norm_type, 0.0, norm, workspace,
+                        workspace_bytes, stream);
 }
 
 coalesce_status coalesce_clip_grad_norm(const void* const* grads, void* const* out, const int64_t* numel,
                                         const int32_t* dtypes, int64_t count, coalesce_norm norm_type, double max_norm,
                                         float* norm, void* workspace, size_t workspace_bytes, void* stream) {
+  return coalesce_clip_grad_norm_rows(grads, out, numel, nullptr, nullptr, nullptr, dtypes, count, norm_type, max_norm,
+                                      norm, workspace, workspace_bytes, stream);
+}
+
+coalesce_status coalesce_clip_grad_norm_rows(const void* const* grads, void* const* out, const int64_t* numel,
+                                             const int64_t* cols, const int64_t* ld, const int64_t* ld_out,
+                                             const int32_t* dtypes, int64_t count, coalesce_norm norm_type,
+                                             double max_norm, float* norm, void* workspace, size_t workspace_bytes,
+                                             void* stream) {
   if (!(max_norm >= 0.0)) return fail(COALESCE_ERR_INVALID_ARGUMENT, "max_norm must not be negative or NaN");
   if (count > 0 && !out) return fail(COALESCE_ERR_INVALID_ARGUMENT, "out is NULL");
-  return grad_norm_impl(grads, out, numel, dtypes, count, norm_type, max_norm, norm, workspace, workspace_bytes, stream);
+  return grad_norm_impl(grads, out, numel, cols, ld, ld_out, dtypes, count, norm_type, max_norm, norm, workspace,
+                        workspace_bytes, stream);
 }
 
 coalesce_status coalesce_autotune_clear(void) {

@@ -79,6 +79,15 @@ struct Accum {
   }
 };
 
+// A thread's four accumulators together.
+template <bool INF>
+__device__ __forceinline__ double thread_total(const Accum<INF> (&a)[4]) {
+  if constexpr (INF)
+    return (double)max_nan(max_nan(a[0].m, a[1].m), max_nan(a[2].m, a[3].m));
+  else
+    return (a[0].s + a[1].s) + (a[2].s + a[3].s);
+}
+
 // The workgroup's total, in thread 0 (and, with the second step, everywhere).
 template <bool INF>
 __device__ __forceinline__ double block_total(double v) {
@@ -96,8 +105,9 @@ __device__ __forceinline__ double block_total(double v) {
   return v;
 }
 
-// Chunk c of the table: its tensor and element range.
-__device__ __forceinline__ int find_tensor(const ClipTable& t, int64_t c) {
+// The tensor of chunk c of a table.
+template <typename Table>
+__device__ __forceinline__ int find_tensor(const Table& t, int64_t c) {
   int lo = 0, hi = t.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
@@ -109,32 +119,33 @@ __device__ __forceinline__ int find_tensor(const ClipTable& t, int64_t c) {
   return lo;
 }
 
-// One chunk of n elements at p, added to the thread's four accumulators.
-template <typename T, bool INF, bool PAST>
-__device__ __forceinline__ void add_chunk(const T* p, int64_t n, Accum<INF> (&a)[4]) {
+// One chunk of n elements at p, added to the four accumulators of thread `tid`
+// of the NT that share it.
+template <typename T, bool INF, bool PAST, int NT = THREADS>
+__device__ __forceinline__ void add_chunk(const T* p, int64_t n, Accum<INF> (&a)[4], int tid) {
   typedef typename Vec<T>::type V;
   constexpr int VN = Vec<T>::N;
   const int64_t head = min(n, (int64_t)(((16 - ((uintptr_t)p & 15)) & 15) / sizeof(T)));
   const V* pv = (const V*)(p + head);
   const int64_t nv = (n - head) / VN;
-  if ((int64_t)threadIdx.x < head) a[0].add((float)p[threadIdx.x]);
-  int64_t k = threadIdx.x;
-  for (; k + 3 * THREADS < nv; k += 4 * THREADS) {
+  if ((int64_t)tid < head) a[0].add((float)p[tid]);
+  int64_t k = tid;
+  for (; k + 3 * NT < nv; k += 4 * NT) {
     V v[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) v[u] = load_past<PAST>(pv + k + u * THREADS);
+    for (int u = 0; u < 4; ++u) v[u] = load_past<PAST>(pv + k + u * NT);
 #pragma unroll
     for (int u = 0; u < 4; ++u)
 #pragma unroll
       for (int e = 0; e < VN; ++e) a[u].add((float)v[u][e]);
   }
-  for (; k < nv; k += THREADS) {
+  for (; k < nv; k += NT) {
     const V v = load_past<PAST>(pv + k);
 #pragma unroll
     for (int e = 0; e < VN; ++e) a[0].add((float)v[e]);
   }
   const int64_t done = head + nv * VN;
-  if ((int64_t)threadIdx.x < n - done) a[1].add((float)p[done + threadIdx.x]);
+  if ((int64_t)tid < n - done) a[1].add((float)p[done + tid]);
 }
 
 template <typename T, bool INF>
@@ -147,16 +158,55 @@ __global__ __launch_bounds__(THREADS) void norm_kernel(ClipTable t, double* part
     const int64_t n = min(t.numel[i] - e0, t.chunk);
     const T* p = (const T*)t.src[i] + e0;
     if (c < t.keep)
-      add_chunk<T, INF, true>(p, n, a);
+      add_chunk<T, INF, true>(p, n, a, threadIdx.x);
     else
-      add_chunk<T, INF, false>(p, n, a);
+      add_chunk<T, INF, false>(p, n, a, threadIdx.x);
   }
-  double v;
-  if constexpr (INF)
-    v = (double)max_nan(max_nan(a[0].m, a[1].m), max_nan(a[2].m, a[3].m));
-  else
-    v = (a[0].s + a[1].s) + (a[2].s + a[3].s);
-  v = block_total<INF>(v);
+  const double v = block_total<INF>(thread_total(a));
+  if (threadIdx.x == 0) partial[blockIdx.x] = v;
+}
+
+// Where piece c of a table of matrices lies: `rows` rows from row r0 on,
+// elements [c0, c0 + n) of each.  A piece is as many whole rows as `chunk`
+// elements hold, or a part of one row that is longer.
+struct Piece {
+  int64_t r0, rows, c0, n;
+};
+__device__ __forceinline__ Piece piece_at(const ClipRows& t, int i, int64_t c) {
+  const int64_t k = c - (i ? t.chunk_end[i - 1] : 0), cols = t.cols[i], parts = (cols + t.chunk - 1) / t.chunk;
+  Piece p;
+  if (parts > 1) {
+    p.r0 = k / parts;
+    p.rows = 1;
+    p.c0 = (k - p.r0 * parts) * t.chunk;
+    p.n = min(cols - p.c0, t.chunk);
+  } else {
+    const int64_t per = t.chunk / cols;
+    p.r0 = k * per;
+    p.rows = min(t.rows[i] - p.r0, per);
+    p.c0 = 0;
+    p.n = cols;
+  }
+  return p;
+}
+
+// Matrices whose rows lie apart (what stands between the rows is not touched): a
+// wave takes a piece, one row after the other.  Bound by memory where a row is
+// some hundred bytes or more: norm and scaling of six 2731 x 1001 fp32 gradients,
+// 66 MB, 41 us against 34 of dense ones, one of 4096 x 11003 in bf16 48 against 49;
+// 100000 rows of 5, a row's latency each, 41 against 14.
+template <typename T, bool INF>
+__global__ __launch_bounds__(THREADS) void norm_rows_kernel(ClipRows t, double* partial) {
+  Accum<INF> a[4];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int64_t chunks = t.chunk_end[t.count - 1];
+  for (int64_t c = (int64_t)blockIdx.x * (THREADS / 64) + wave; c < chunks; c += (int64_t)gridDim.x * (THREADS / 64)) {
+    const int i = find_tensor(t, c);
+    const Piece q = piece_at(t, i, c);
+    const T* p = (const T*)t.src[i] + q.r0 * t.ld[i] + q.c0;
+    for (int64_t r = 0; r < q.rows; ++r) add_chunk<T, INF, false, 64>(p + r * t.ld[i], q.n, a, lane);
+  }
+  const double v = block_total<INF>(thread_total(a));
   if (threadIdx.x == 0) partial[blockIdx.x] = v;
 }
 
@@ -177,49 +227,55 @@ __global__ __launch_bounds__(THREADS) void norm_only_kernel(const double* partia
   if (threadIdx.x == 0) norm[0] = (float)v;
 }
 
-// o = p c over n elements.
-template <typename T, bool PAST>
-__device__ __forceinline__ void scale_chunk(const T* p, T* o, int64_t n, float coef) {
+// o = p c over n elements, by thread `tid` of NT.
+template <typename T, bool PAST, int NT = THREADS>
+__device__ __forceinline__ void scale_chunk(const T* p, T* o, int64_t n, float coef, int tid) {
   typedef typename Vec<T>::type V;
   constexpr int VN = Vec<T>::N;
   if ((((uintptr_t)p ^ (uintptr_t)o) & 15) != 0) {  // no common 16-byte grid
-    for (int64_t k = threadIdx.x; k < n; k += THREADS) o[k] = scaled<T>(p[k], coef);
+    for (int64_t k = tid; k < n; k += NT) o[k] = scaled<T>(p[k], coef);
     return;
   }
   const int64_t head = min(n, (int64_t)(((16 - ((uintptr_t)p & 15)) & 15) / sizeof(T)));
   const V* pv = (const V*)(p + head);
   V* ov = (V*)(o + head);
   const int64_t nv = (n - head) / VN;
-  if ((int64_t)threadIdx.x < head) o[threadIdx.x] = scaled<T>(p[threadIdx.x], coef);
-  int64_t k = threadIdx.x;
-  for (; k + 3 * THREADS < nv; k += 4 * THREADS) {
+  if ((int64_t)tid < head) o[tid] = scaled<T>(p[tid], coef);
+  int64_t k = tid;
+  for (; k + 3 * NT < nv; k += 4 * NT) {
     V v[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) v[u] = load_past<PAST>(pv + k + u * THREADS);
+    for (int u = 0; u < 4; ++u) v[u] = load_past<PAST>(pv + k + u * NT);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
 #pragma unroll
       for (int e = 0; e < VN; ++e) v[u][e] = scaled<T>(v[u][e], coef);
-      store_past<PAST>(ov + k + u * THREADS, v[u]);
+      store_past<PAST>(ov + k + u * NT, v[u]);
     }
   }
-  for (; k < nv; k += THREADS) {
+  for (; k < nv; k += NT) {
     V v = load_past<PAST>(pv + k);
 #pragma unroll
     for (int e = 0; e < VN; ++e) v[e] = scaled<T>(v[e], coef);
     store_past<PAST>(ov + k, v);
   }
   const int64_t done = head + nv * VN;
-  if ((int64_t)threadIdx.x < n - done) o[done + threadIdx.x] = scaled<T>(p[done + threadIdx.x], coef);
+  if ((int64_t)tid < n - done) o[done + tid] = scaled<T>(p[done + tid], coef);
+}
+
+// c = min(1, max_norm / (norm + 1e-6)) in every thread; a NaN stays one.
+template <bool INF>
+__device__ __forceinline__ float scale_of(const double* partial, int n_partial, double max_norm, float* norm) {
+  const double total = total_norm<INF>(partial, n_partial);
+  if (norm && blockIdx.x == 0 && threadIdx.x == 0) norm[0] = (float)total;
+  const double q = max_norm / (total + 1e-6);
+  return q < 1.0 || q != q ? (float)q : 1.0f;
 }
 
 template <typename T, bool INF>
 __global__ __launch_bounds__(THREADS) void scale_kernel(ClipTable t, const double* partial, int n_partial,
                                                         double max_norm, bool past, float* norm) {
-  const double total = total_norm<INF>(partial, n_partial);
-  if (norm && blockIdx.x == 0 && threadIdx.x == 0) norm[0] = (float)total;
-  const double q = max_norm / (total + 1e-6);
-  const float coef = q < 1.0 || q != q ? (float)q : 1.0f;
+  const float coef = scale_of<INF>(partial, n_partial, max_norm, norm);
   for (int64_t c = t.chunk_end[t.count - 1] - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
     const int i = find_tensor(t, c);
     if (coef == 1.0f && t.src[i] == t.dst[i]) continue;  // in place and nothing to scale
@@ -228,9 +284,26 @@ __global__ __launch_bounds__(THREADS) void scale_kernel(ClipTable t, const doubl
     const T* p = (const T*)t.src[i] + e0;
     T* o = (T*)t.dst[i] + e0;
     if (past)
-      scale_chunk<T, true>(p, o, n, coef);
+      scale_chunk<T, true>(p, o, n, coef, threadIdx.x);
     else
-      scale_chunk<T, false>(p, o, n, coef);
+      scale_chunk<T, false>(p, o, n, coef, threadIdx.x);
+  }
+}
+
+template <typename T, bool INF>
+__global__ __launch_bounds__(THREADS) void scale_rows_kernel(ClipRows t, const double* partial, int n_partial,
+                                                             double max_norm, float* norm) {
+  const float coef = scale_of<INF>(partial, n_partial, max_norm, norm);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int64_t step = (int64_t)gridDim.x * (THREADS / 64);
+  for (int64_t c = t.chunk_end[t.count - 1] - 1 - ((int64_t)blockIdx.x * (THREADS / 64) + wave); c >= 0; c -= step) {
+    const int i = find_tensor(t, c);
+    if (coef == 1.0f && t.src[i] == t.dst[i]) continue;
+    const Piece q = piece_at(t, i, c);
+    const T* p = (const T*)t.src[i] + q.r0 * t.ld[i] + q.c0;
+    T* o = (T*)t.dst[i] + q.r0 * t.ld_out[i] + q.c0;
+    for (int64_t r = 0; r < q.rows; ++r)
+      scale_chunk<T, false, 64>(p + r * t.ld[i], o + r * t.ld_out[i], q.n, coef, lane);
   }
 }
 
@@ -244,13 +317,16 @@ int64_t chunk_elems(int64_t total, int64_t es, int num_cus) {
 
 int64_t dtype_bytes(int dt) { return dt == DT_F32 ? 4 : 2; }
 
-// Calls fn(table, dtype) for the list's tables: tensors of one dtype, empty ones
-// left out, in list order or (`backwards`) the tables from the list's end, each
+bool lies_apart(const ClipList& l, int64_t i) { return l.cols && l.cols[i] != 0; }
+
+// Calls fn(table, dtype) for the list's tables of dense tensors: of one dtype,
+// empty ones left out, in list order or (`backwards`) the tables from the list's end, each
 // in list order within itself.
 template <typename F>
 hipError_t for_tables(const ClipList& l, int num_cus, bool backwards, F fn) {
   int64_t total = 0, bytes = 0;
   for (int64_t i = 0; i < l.count; ++i) {
+    if (lies_apart(l, i)) continue;
     total += l.numel[i];
     bytes += l.numel[i] * dtype_bytes(l.dtype[i]);
   }
@@ -263,7 +339,7 @@ hipError_t for_tables(const ClipList& l, int num_cus, bool backwards, F fn) {
     for (int64_t k = 0; k <= l.count; ++k) {
       const bool end = k == l.count;
       const int64_t i = backwards ? l.count - 1 - k : k;
-      if (!end && (l.dtype[i] != dt || l.numel[i] == 0)) continue;
+      if (!end && (l.dtype[i] != dt || l.numel[i] == 0 || lies_apart(l, i))) continue;
       if (t.count == kClipTensors || (end && t.count > 0)) {
         if (backwards) {
           std::reverse(t.src, t.src + t.count);
@@ -294,8 +370,46 @@ hipError_t for_tables(const ClipList& l, int num_cus, bool backwards, F fn) {
   return hipSuccess;
 }
 
+// The same for the tables of matrices whose rows lie apart.
+template <typename F>
+hipError_t for_row_tables(const ClipList& l, int num_cus, F fn) {
+  if (!l.cols) return hipSuccess;
+  int64_t total = 0;
+  for (int64_t i = 0; i < l.count; ++i)
+    if (lies_apart(l, i)) total += l.numel[i];
+  for (int dt : {DT_F32, DT_F16, DT_BF16}) {
+    ClipRows t{};
+    // a wave's piece: a quarter of a workgroup's chunk
+    t.chunk = chunk_elems(total, dtype_bytes(dt), num_cus) / (THREADS / 64);
+    for (int64_t i = 0; i <= l.count; ++i) {
+      const bool end = i == l.count;
+      if (!end && (l.dtype[i] != dt || l.numel[i] == 0 || !lies_apart(l, i))) continue;
+      if (t.count == kClipMatrices || (end && t.count > 0)) {
+        const hipError_t e = fn(t, dt);
+        if (e != hipSuccess) return e;
+        t.count = 0;
+      }
+      if (end) break;
+      const int k = t.count++;
+      t.src[k] = l.src ? l.src[i] : nullptr;
+      t.dst[k] = l.dst ? l.dst[i] : nullptr;
+      t.cols[k] = l.cols[i];
+      t.rows[k] = l.numel[i] / l.cols[i];
+      t.ld[k] = l.ld ? l.ld[i] : 0;
+      t.ld_out[k] = l.ld_out ? l.ld_out[i] : 0;
+      const int64_t parts = (t.cols[k] + t.chunk - 1) / t.chunk, per = t.chunk / t.cols[k];
+      t.chunk_end[k] = (k ? t.chunk_end[k - 1] : 0) + (parts > 1 ? t.rows[k] * parts : (t.rows[k] + per - 1) / per);
+    }
+  }
+  return hipSuccess;
+}
+
 int grid_of(const ClipTable& t, int num_cus) {
   return (int)std::min<int64_t>(t.chunk_end[t.count - 1], (int64_t)num_cus * 8);
+}
+int grid_of(const ClipRows& t, int num_cus) {
+  const int64_t waves = THREADS / 64;
+  return (int)std::min<int64_t>((t.chunk_end[t.count - 1] + waves - 1) / waves, (int64_t)num_cus * 8);
 }
 
 template <bool INF>
@@ -315,6 +429,19 @@ hipError_t grad_norm_t(const ClipList& l, double max_norm, float* norm, double* 
     return hipGetLastError();
   });
   if (e != hipSuccess) return e;
+  e = for_row_tables(l, num_cus, [&](const ClipRows& t, int dt) {
+    const int g = grid_of(t, num_cus);
+    double* out = partial + n;
+    n += g;
+    if (dt == DT_F32)
+      hipLaunchKernelGGL((norm_rows_kernel<float, INF>), dim3(g), dim3(THREADS), 0, stream, t, out);
+    else if (dt == DT_F16)
+      hipLaunchKernelGGL((norm_rows_kernel<_Float16, INF>), dim3(g), dim3(THREADS), 0, stream, t, out);
+    else
+      hipLaunchKernelGGL((norm_rows_kernel<__bf16, INF>), dim3(g), dim3(THREADS), 0, stream, t, out);
+    return hipGetLastError();
+  });
+  if (e != hipSuccess) return e;
   if (!l.dst || n == 0) {
     hipLaunchKernelGGL((norm_only_kernel<INF>), dim3(1), dim3(THREADS), 0, stream, partial, n, norm);
     return hipGetLastError();
@@ -323,6 +450,21 @@ hipError_t grad_norm_t(const ClipList& l, double max_norm, float* norm, double* 
   for (int64_t i = 0; i < l.count; ++i) bytes += l.numel[i] * dtype_bytes(l.dtype[i]);
   const bool past = bytes > kPastBytes;
   bool first = true;
+  e = for_row_tables(l, num_cus, [&](const ClipRows& t, int dt) {
+    const int g = grid_of(t, num_cus);
+    float* out = first ? norm : nullptr;
+    first = false;
+    if (dt == DT_F32)
+      hipLaunchKernelGGL((scale_rows_kernel<float, INF>), dim3(g), dim3(THREADS), 0, stream, t, partial, n, max_norm, out);
+    else if (dt == DT_F16)
+      hipLaunchKernelGGL((scale_rows_kernel<_Float16, INF>), dim3(g), dim3(THREADS), 0, stream, t, partial, n, max_norm,
+                         out);
+    else
+      hipLaunchKernelGGL((scale_rows_kernel<__bf16, INF>), dim3(g), dim3(THREADS), 0, stream, t, partial, n, max_norm,
+                         out);
+    return hipGetLastError();
+  });
+  if (e != hipSuccess) return e;
   return for_tables(l, num_cus, true, [&](const ClipTable& t, int dt) {
     const int g = grid_of(t, num_cus);
     float* out = first ? norm : nullptr;
@@ -345,6 +487,10 @@ hipError_t grad_norm_t(const ClipList& l, double max_norm, float* norm, double* 
 size_t grad_norm_workspace(const ClipList& l, int num_cus) {
   size_t n = 0;
   (void)for_tables(l, num_cus, false, [&](const ClipTable& t, int) {
+    n += (size_t)grid_of(t, num_cus);
+    return hipSuccess;
+  });
+  (void)for_row_tables(l, num_cus, [&](const ClipRows& t, int) {
     n += (size_t)grid_of(t, num_cus);
     return hipSuccess;
   });

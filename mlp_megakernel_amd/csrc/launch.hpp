@@ -249,15 +249,18 @@ size_t ffn_backward_workspace(int64_t M, int64_t N, int64_t K, bool gated, int n
 hipError_t launch_ffn_backward(const FfnBwdParams& p, bool gated, DType in, DType dy, DType grad, int act,
                                hipStream_t stream, int num_cus, void* workspace);
 
-// Gradient norm and clipping (gradnorm.hip): a list of dense tensors, and the
-// table of up to kClipTensors of them that one launch gets as its argument
-// (under the 4 KB of kernel arguments).
+// Gradient norm and clipping (gradnorm.hip): a list of tensors, and the tables
+// of them that one launch gets as its argument (under the 4 KB of kernel
+// arguments): up to kClipTensors dense ones, or up to kClipMatrices whose rows
+// lie apart.
 struct ClipList {
   const void* const* src;
   void* const* dst;  // nullptr: the norm alone
   const int64_t* numel;
   const int32_t* dtype;  // DType
   int64_t count;
+  const int64_t* cols;       // nullptr: all dense; else columns of a tensor whose rows lie apart, 0: dense
+  const int64_t *ld, *ld_out;  // their pitches in elements
 };
 constexpr int kClipTensors = 120;
 struct ClipTable {
@@ -267,6 +270,15 @@ struct ClipTable {
   int64_t chunk_end[kClipTensors];  // chunks up to and including the tensor's
   int64_t chunk;                    // elements per chunk
   int64_t keep;                     // chunks from this on are read through the caches, those before it past them
+  int count;
+};
+constexpr int kClipMatrices = 64;
+struct ClipRows {
+  const void* src[kClipMatrices];
+  void* dst[kClipMatrices];
+  int64_t rows[kClipMatrices], cols[kClipMatrices], ld[kClipMatrices], ld_out[kClipMatrices];
+  int64_t chunk_end[kClipMatrices];  // pieces up to and including the tensor's
+  int64_t chunk;                     // elements per piece
   int count;
 };
 size_t grad_norm_workspace(const ClipList& l, int num_cus);

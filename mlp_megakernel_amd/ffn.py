@@ -348,8 +348,10 @@ def _held(tensors, stream):
 
 
 def _grad_list(tensors, out):
-    """(count, device, sources, destinations, sizes, types): the host arrays of
-    the C call (bytes objects, to be kept alive until it returns)."""
+    """(count, device, sources, destinations, sizes, types, columns, pitches,
+    pitches of the destinations): the host arrays of the C call (bytes objects,
+    to be kept alive until it returns; the last three None for a list of dense
+    tensors)."""
     try:
         from ._marshal import grad_list
     except ImportError as e:
@@ -389,24 +391,26 @@ def clip_grad_norm(tensors: Iterable[torch.Tensor], max_norm: float, norm_type=2
     (coalesce_clip_grad_norm) and return the norm they had, a float32 scalar on
     their device.  In place, or into ``out`` (one tensor per gradient, of its
     size, memory order and dtype).  Nothing synchronises with the host; tensors of
-    several dtypes may be mixed."""
+    several dtypes may be mixed.  A tensor is dense or a matrix of unit inner
+    stride, as the gradients of :func:`gated_gemm_backward` are."""
     tensors, out = _held(tensors, stream), _held(out, stream)
     return _norm_call(_grad_list(tensors, out), float(max_norm), norm_type, norm, workspace, stream)
 
 
 def _norm_call(lists, max_norm, norm_type, norm, workspace, stream):
-    n, dev, src, dst, numel, dts = lists
+    n, dev, src, dst, numel, dts, cols, ld, ld_out = lists
     if _current_device() != dev:
         return _there(dev, _norm_call, lists, max_norm, norm_type, norm, workspace, stream)
     lib, code = load_library(), _norm_code(norm_type)
     norm = _norm_out(norm, dev, stream)
-    ws, nws, _keep = _take(workspace, int(lib.coalesce_grad_norm_workspace_size(numel, dts, n)), dev, stream)
+    need = int(lib.coalesce_grad_norm_rows_workspace_size(numel, cols, dts, n))
+    ws, nws, _keep = _take(workspace, need, dev, stream)
     if max_norm is None:
-        _check(lib.coalesce_grad_norm(src, numel, dts, n, code, norm.data_ptr(), ws, nws,
-                                      _raw_stream(stream, dev)))
-    else:
-        _check(lib.coalesce_clip_grad_norm(src, dst, numel, dts, n, code, max_norm, norm.data_ptr(), ws, nws,
+        _check(lib.coalesce_grad_norm_rows(src, numel, cols, ld, dts, n, code, norm.data_ptr(), ws, nws,
                                            _raw_stream(stream, dev)))
+    else:
+        _check(lib.coalesce_clip_grad_norm_rows(src, dst, numel, cols, ld, ld_out, dts, n, code, max_norm,
+                                                norm.data_ptr(), ws, nws, _raw_stream(stream, dev)))
     return norm
 
 
