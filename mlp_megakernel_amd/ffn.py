@@ -13,6 +13,7 @@ import weakref
 from typing import Iterable, NamedTuple, Optional, Tuple
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import (ACT_NONE, NORM_2, NORM_INF, _ACTS, _DTYPES, _check, _empty, _matrix, _ptr, _raw_current_stream,
@@ -447,6 +448,16 @@ class _EagerGraph:
                                    "drop its outputs before the capture, or warm up on the stream of the capture")
 
 
+def _refuse_recorded(tensors):
+    """The plain calls are no torch operations: what records those would miss
+    them, a tangent be lost and a trace return memory that nothing wrote."""
+    if torch.jit.is_tracing():
+        raise RuntimeError("GatedFFN without gradients cannot be traced: trace it with gradients enabled")
+    if getattr(forward_ad, "_current_level", 0) >= 0 and \
+            any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise NotImplementedError("GatedFFN has no forward-mode derivative")
+
+
 class _GatedFFNFunction(torch.autograd.Function):
     """x + (act(x Wg + bg) * (x Wu + bu)) Wd + bd as one autograd node."""
 
@@ -481,7 +492,8 @@ class GatedFFN(torch.nn.Module):
 
     The forward and backward can be captured in a graph after a warm-up on a
     side stream; a capture while an autograd graph of the same leaves, made on
-    the default stream, is alive raises an error.
+    the default stream, is alive raises an error.  So do second derivatives,
+    forward-mode ones and torch.jit.trace without gradients.
     """
 
     def __init__(self, D: int, H: int, act="silu", bias: bool = False, residual: bool = True, device="cuda",
@@ -513,6 +525,7 @@ class GatedFFN(torch.nn.Module):
                 graph = _EagerGraph(leaves)
             y = _GatedFFNFunction.apply(graph, x2, self.act, self.residual, Wg, Wu, Wd, self.bg, self.bu, self.bd)
         else:
+            _refuse_recorded((x2, Wg, Wu, Wd, self.bg, self.bu, self.bd))
             h = gated_gemm(x2, Wg, Wu, self.bg, self.bu, act=self.act)
             y = gemm_residual(h, Wd, x2 if self.residual else None, self.bd)
         return y.reshape(shape)

@@ -1,0 +1,46 @@
+"""GatedFFN called in ways that its kernels do not serve: each is refused, and
+what stands next to it still works."""
+import pytest
+import torch
+import torch.autograd.forward_ad as fw
+
+import mlp_megakernel_amd as mk
+
+pytestmark = pytest.mark.gpu
+
+
+def _module(**kw):
+    torch.manual_seed(0)
+    m = mk.GatedFFN(64, 128, **kw)
+    return m, torch.randn(8, 64, device="cuda", dtype=torch.bfloat16)
+
+
+@pytest.mark.parametrize("frozen", [False, True])
+def test_forward_mode_is_refused(frozen):
+    m, x = _module()
+    want = m(x).detach()
+    m.requires_grad_(not frozen)
+    v = torch.ones_like(x)
+    with fw.dual_level():
+        with torch.set_grad_enabled(frozen):      # frozen parameters, or no_grad: the call without autograd
+            with pytest.raises(NotImplementedError):
+                m(fw.make_dual(x, v))
+            assert torch.equal(m(x), want)
+        # a parameter that carries a tangent
+        p = {k: t.detach() for k, t in m.named_parameters()}
+        p["Wd"] = fw.make_dual(p["Wd"], torch.ones_like(p["Wd"]))
+        with pytest.raises(NotImplementedError):
+            torch.func.functional_call(m, p, (x,))
+
+
+def test_trace_without_gradients_is_refused():
+    m, x = _module()
+    with torch.no_grad(), pytest.raises(RuntimeError, match="traced"):
+        torch.jit.trace(m, (x,), check_trace=False)
+    m.requires_grad_(False)
+    with pytest.raises(RuntimeError, match="traced"):
+        torch.jit.trace(m, (x,), check_trace=False)
+    m.requires_grad_(True)
+    t = torch.jit.trace(m, (x,), check_trace=False)
+    y = torch.randn_like(x)
+    assert torch.equal(t(y), m(y))
