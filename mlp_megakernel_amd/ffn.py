@@ -514,6 +514,8 @@ class GatedFFN(torch.nn.Module):
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         shape = x.shape
+        if not shape or shape[-1] != self.D:
+            raise ValueError("x must be [..., %d], not %s" % (self.D, tuple(shape)))
         x2 = _rows16(x.reshape(-1, self.D))
         Wg, Wu, Wd = _rows16(self.Wg), _rows16(self.Wu), _rows16(self.Wd)
         if torch.is_grad_enabled() and (x.requires_grad or any(p.requires_grad for p in self.parameters())):

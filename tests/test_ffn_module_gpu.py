@@ -44,3 +44,17 @@ def test_trace_without_gradients_is_refused():
     t = torch.jit.trace(m, (x,), check_trace=False)
     y = torch.randn_like(x)
     assert torch.equal(t(y), m(y))
+
+
+@pytest.mark.parametrize("shape", [(4, 32), (2, 128), (64, 1), (32,), (2, 2, 32)])
+def test_inputs_of_another_width_are_refused(shape):
+    # 64 elements each row, or a multiple: they would fill rows of the right width
+    m, _ = _module()
+    x = torch.randn(shape, device="cuda", dtype=torch.bfloat16)
+    for grad in (False, True):
+        with torch.set_grad_enabled(grad), pytest.raises(ValueError, match="64"):
+            m(x)
+    for good in ((64,), (0, 64), (3, 1, 64), (2, 0, 64)):
+        assert m(torch.zeros(good, device="cuda", dtype=torch.bfloat16)).shape == good
+    with pytest.raises(ValueError):
+        m(torch.zeros((), device="cuda", dtype=torch.bfloat16))
