@@ -428,6 +428,13 @@ def _rows16(t: torch.Tensor) -> torch.Tensor:
     return aligned_copy(t, t.device)
 
 
+def _vec16(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    """`t` contiguous and 16-byte aligned (a copy if it is not, as a slice of a flat buffer need not be)."""
+    if t is None or (t.data_ptr() % 16 == 0 and t.is_contiguous()):
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
 class _EagerGraph:
     """Held by an autograd node made outside a capture, on the default stream:
     the tensors that its graph's leaves are."""
@@ -518,6 +525,7 @@ class GatedFFN(torch.nn.Module):
             raise ValueError("x must be [..., %d], not %s" % (self.D, tuple(shape)))
         x2 = _rows16(x.reshape(-1, self.D))
         Wg, Wu, Wd = _rows16(self.Wg), _rows16(self.Wu), _rows16(self.Wd)
+        bg, bu, bd = _vec16(self.bg), _vec16(self.bu), _vec16(self.bd)
         if torch.is_grad_enabled() and (x.requires_grad or any(p.requires_grad for p in self.parameters())):
             leaves = (x, *self.parameters())
             graph = None
@@ -525,9 +533,9 @@ class GatedFFN(torch.nn.Module):
                 _EagerGraph.refuse_capture(leaves)
             elif torch.cuda.current_stream(x.device) == torch.cuda.default_stream(x.device):
                 graph = _EagerGraph(leaves)
-            y = _GatedFFNFunction.apply(graph, x2, self.act, self.residual, Wg, Wu, Wd, self.bg, self.bu, self.bd)
+            y = _GatedFFNFunction.apply(graph, x2, self.act, self.residual, Wg, Wu, Wd, bg, bu, bd)
         else:
-            _refuse_recorded((x2, Wg, Wu, Wd, self.bg, self.bu, self.bd))
-            h = gated_gemm(x2, Wg, Wu, self.bg, self.bu, act=self.act)
-            y = gemm_residual(h, Wd, x2 if self.residual else None, self.bd)
+            _refuse_recorded((x2, Wg, Wu, Wd, bg, bu, bd))
+            h = gated_gemm(x2, Wg, Wu, bg, bu, act=self.act)
+            y = gemm_residual(h, Wd, x2 if self.residual else None, bd)
         return y.reshape(shape)

@@ -58,3 +58,28 @@ def test_inputs_of_another_width_are_refused(shape):
         assert m(torch.zeros(good, device="cuda", dtype=torch.bfloat16)).shape == good
     with pytest.raises(ValueError):
         m(torch.zeros((), device="cuda", dtype=torch.bfloat16))
+
+
+@pytest.mark.parametrize("D,H", [(72, 128), (71, 130)])
+def test_parameters_in_one_flat_buffer(D, H):
+    # as an optimizer's or a checkpoint's flat buffer holds them: only element alignment
+    torch.manual_seed(1)
+    m, plain = (mk.GatedFFN(D, H, bias=True) for _ in range(2))
+    flat = torch.zeros(sum(p.numel() for p in m.parameters()) + 3, device="cuda", dtype=torch.bfloat16)
+    at = 3
+    for p, q in zip(m.parameters(), plain.parameters()):
+        q.data.normal_(std=0.1)
+        part = flat[at:at + p.numel()].view(p.shape)
+        part.copy_(q.data)
+        p.data = part
+        at += p.numel()
+    assert any(p.data_ptr() % 16 for p in (m.bg, m.bu, m.bd))
+    x = torch.randn(20, D, device="cuda", dtype=torch.bfloat16)
+    a, b = m(x), plain(x)
+    a.backward(x)
+    b.backward(x)
+    assert torch.equal(a, b)
+    for p, q in zip(m.parameters(), plain.parameters()):
+        assert torch.equal(p.grad, q.grad)
+    with torch.no_grad():
+        assert torch.equal(m(x), a)
