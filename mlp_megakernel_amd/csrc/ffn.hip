@@ -50,29 +50,34 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineOp c) {
   }
 }
 
-template <typename T, typename TO>
-hipError_t combine_t(const CombineOp& c, CombineKind kind, hipStream_t stream, int num_cus) {
+template <typename T, typename TO, int KIND>
+hipError_t combine_t(const CombineOp& c, hipStream_t stream, int num_cus) {
   const int64_t blocks = ((int64_t)c.M * ((c.N + 3) / 4) + 255) / 256;
   const dim3 grid((unsigned)std::min<int64_t>(blocks, (int64_t)num_cus * 8),
-                  kind == COMBINE_STORE ? (unsigned)c.products : 1u);
-  if (kind == COMBINE_STORE)
-    hipLaunchKernelGGL((combine_kernel<T, TO, COMBINE_STORE>), grid, dim3(256), 0, stream, c);
-  else if (kind == COMBINE_RESID)
-    hipLaunchKernelGGL((combine_kernel<T, TO, COMBINE_RESID>), grid, dim3(256), 0, stream, c);
-  else
-    hipLaunchKernelGGL((combine_kernel<T, TO, COMBINE_GATED>), grid, dim3(256), 0, stream, c);
+                  KIND == COMBINE_STORE ? (unsigned)c.products : 1u);
+  hipLaunchKernelGGL((combine_kernel<T, TO, KIND>), grid, dim3(256), 0, stream, c);
   return hipGetLastError();
+}
+
+// An epilogue of one input type, to that type or fp32.
+template <typename T, int KIND>
+hipError_t combine_in(const CombineOp& c, DType out, hipStream_t stream, int num_cus) {
+  return out == DT_F32 ? combine_t<T, float, KIND>(c, stream, num_cus) : combine_t<T, T, KIND>(c, stream, num_cus);
 }
 
 }  // namespace
 
 hipError_t launch_combine(const CombineOp& c, CombineKind kind, DType in, DType out, hipStream_t stream, int num_cus) {
-  if (kind == COMBINE_STORE && out == DT_F32) return combine_t<float, float>(c, kind, stream, num_cus);
-  if (in == DT_BF16)
-    return out == DT_F32 ? combine_t<__bf16, float>(c, kind, stream, num_cus)
-                         : combine_t<__bf16, __bf16>(c, kind, stream, num_cus);
-  return out == DT_F32 ? combine_t<_Float16, float>(c, kind, stream, num_cus)
-                       : combine_t<_Float16, _Float16>(c, kind, stream, num_cus);
+  if (kind == COMBINE_STORE) {  // no bias, activation or residual: the inputs' type does not matter
+    if (out == DT_F32) return combine_t<float, float, COMBINE_STORE>(c, stream, num_cus);
+    return out == DT_BF16 ? combine_t<__bf16, __bf16, COMBINE_STORE>(c, stream, num_cus)
+                          : combine_t<_Float16, _Float16, COMBINE_STORE>(c, stream, num_cus);
+  }
+  if (kind == COMBINE_RESID)
+    return in == DT_BF16 ? combine_in<__bf16, COMBINE_RESID>(c, out, stream, num_cus)
+                         : combine_in<_Float16, COMBINE_RESID>(c, out, stream, num_cus);
+  return in == DT_BF16 ? combine_in<__bf16, COMBINE_GATED>(c, out, stream, num_cus)
+                       : combine_in<_Float16, COMBINE_GATED>(c, out, stream, num_cus);
 }
 
 size_t ffn_forward_workspace(int64_t M, int64_t N, int64_t K, bool gated, int num_cus) {
