@@ -154,7 +154,7 @@ def gemm_residual_train(A: torch.Tensor, B: torch.Tensor, residual: Optional[tor
     """(Y, Z): gemm_residual and the pre-activation Z = A @ B + bias that
     gemm_residual_backward needs, in A's dtype."""
     if preact is None:
-        preact = _new(A.shape[0], B.shape[1], A.dtype, A.device, stream)
+        preact = _new(_first(A)[0], _cols(B, "B"), A.dtype, A.device, stream)
     Y = _gemm_residual(A, B, residual, bias, act, out_dtype, out, preact, workspace, stream)
     return Y, preact
 
@@ -204,7 +204,8 @@ def gated_gemm_train(A: torch.Tensor, Bg: torch.Tensor, Bu: torch.Tensor, bias_g
     """(H, (Zg, Zu)): gated_gemm and the two pre-activations that
     gated_gemm_backward needs, in A's dtype and of one row pitch."""
     if preact is None:
-        preact = tuple(_new(A.shape[0], Bg.shape[1], A.dtype, A.device, stream) for _ in range(2))
+        M, N = _first(A)[0], _cols(Bg, "Bg")
+        preact = tuple(_new(M, N, A.dtype, A.device, stream) for _ in range(2))
     H = _gated_gemm(A, Bg, Bu, bias_g, bias_u, act, out_dtype, out, preact, workspace, stream)
     return H, tuple(preact)
 

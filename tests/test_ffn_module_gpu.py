@@ -83,3 +83,15 @@ def test_parameters_in_one_flat_buffer(D, H):
         assert torch.equal(p.grad, q.grad)
     with torch.no_grad():
         assert torch.equal(m(x), a)
+
+
+def test_training_forms_check_their_arguments():
+    A, B = (torch.zeros(s, device="cuda", dtype=torch.bfloat16) for s in ((8, 64), (64, 32)))
+    for bad in (B[0], B[None], B.cpu(), B.float(), B[:32]):
+        for call in (lambda: mk.gemm_residual_train(A, bad), lambda: mk.gated_gemm_train(A, bad, bad)):
+            with pytest.raises(ValueError):
+                call()
+    for bad in (A[0], A[None], A.cpu(), A.float()):
+        for call in (lambda: mk.gemm_residual_train(bad, B), lambda: mk.gated_gemm_train(bad, B, B)):
+            with pytest.raises(ValueError):
+                call()
