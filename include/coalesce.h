@@ -441,8 +441,11 @@ coalesce_status coalesce_gemm_residual(const void* A, int64_t lda, const void* B
  * Gradients of coalesce_gemm_residual for the upstream gradient dY:
  *   dZ = dY act'(Z);  dA = dZ B^T;  dB = A^T dZ;  dbias[n] = sum_m dZ[m][n]
  * and dR = dY, which is not written anywhere.  dZ is computed in fp32 and
- * rounded once to in_dtype, the type of the matrix operands; dbias sums the
- * unrounded values in fp32.  The derivative of relu at 0 is 0.
+ * rounded once to in_dtype, the type of the matrix operands: half a step of
+ * in_dtype on each, and in F16 that type's range too, so that a dZ above 65504
+ * is infinite and one below 2^-25 zero in dA and dB, whatever the products would
+ * have been (scale the loss accordingly); dbias sums the unrounded values in
+ * fp32.  The derivative of relu at 0 is 0.
  *   Z     as stored by the forward; may be NULL with act NONE
  *   dY    device, M x N of dy_dtype (ldd): in_dtype or F32
  *   dA    device, M x K of in_dtype (ldda), or NULL (not wanted; B may then be

@@ -5,7 +5,10 @@
 // One elementwise pass turns the stored pre-activations and the arriving
 // gradient into the dZi, rounded once to the input type because they are the
 // matrix products' operands, and sums their columns in fp32 before that
-// rounding.  Both dZi Wi^T run as one K loop over two segments, both X^T dZi
+// rounding.  The rounding adds its half step to that of the result (bf16: 0.0023
+// of a gradient's norm against 0.0017, fp16 0.00029 against 0.00021), and in
+// fp16 the range ends at 65504 and 2^-24; two operands per value (high and low
+// part) would avoid both at twice the matrix work.  Both dZi Wi^T run as one K loop over two segments, both X^T dZi
 // as one launch whose tiles share X.
 #pragma once
 #include "ffn_plan.hpp"

@@ -28,9 +28,9 @@ struct TilePlan {
 // the compute units better: gated 777 x 5461 x 2048 57.8 us in 256 rows, 48.5 in
 // 160; 3000 x 4096 x 4096 180 in 256, 163 in 192.  Those lower than 256 exist
 // where the m side lies along the contraction; 160 rows and the shapes called deep
-// have three stages, which pays where a compute unit holds few tiles (64 x 64:
-// residual 512 x 4096 x 4096 37.5 us with two, 30.2; 128 x 128: residual 2048 x
-// 2048 x 4096 53.7 with two, 45.0).  The gated product has no deep ones.
+// have three stages, which pays where a compute unit holds few tiles (bf16 with a
+// bf16 residual: 64 x 64, 512 x 4096 x 4096 37.2 us without them, 30.4 with; 128 x
+// 128, 2048 x 2048 x 4096 55.5 and 48.2).  The gated product has no deep ones.
 struct TileShape {
   int bm, bn, slots;
   double step[4], launch, round;

@@ -4,7 +4,9 @@
 // Two sweeps: the first sums squares (or takes the largest magnitude) of every
 // tensor of the list into one partial per workgroup, the second adds the
 // partials -- every workgroup all of them, in the same order, so no third
-// launch -- and scales.  The list travels in the kernel arguments, a table of
+// launch -- and scales.  A table has up to 2048 partials, so those reads grow with
+// the square of the number of tables: nothing at hundreds of tensors, 2048 x 8
+// bytes per workgroup and table, but what would count at tens of thousands.  The list travels in the kernel arguments, a table of
 // up to kClipTensors tensors per launch, so nothing is copied to the device and
 // the calls can be captured.  Work is cut into chunks of equal size over all
 // tensors of a table; workgroup b takes chunks b, b + grid, ...: which element

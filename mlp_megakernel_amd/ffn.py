@@ -483,6 +483,8 @@ class _GatedFFNFunction(torch.autograd.Function):
         x, Wg, Wu, Wd, Zg, Zu, H = ctx.saved_tensors
         need = ctx.needs_input_grad[1:]
         dy = _rows16(dy.to(x.dtype))
+        # dH is rounded to the type as H was: it is an operand of the next products'
+        # dZ.  The skip's dy joins dx after dx's own rounding, a second half step.
         down = gemm_residual_backward(H, Wd, dy, want_dB=need[5], want_dbias=need[8], grad_dtype=Wd.dtype)
         up = gated_gemm_backward(x, Wg, Wu, (Zg, Zu), down.dA, act=ctx.act, want_dA=need[0],
                                  want_dB=need[3] or need[4], want_dbias=need[6] or need[7], grad_dtype=Wg.dtype)
@@ -502,6 +504,9 @@ class GatedFFN(torch.nn.Module):
     side stream; a capture while an autograd graph of the same leaves, made on
     the default stream, is alive raises an error.  So do second derivatives,
     forward-mode ones and torch.jit.trace without gradients.
+
+    Widths that are no multiples of 8 work, but the kernels read rows on 16-byte
+    boundaries: the weights of such a block are copied at every call.
     """
 
     def __init__(self, D: int, H: int, act="silu", bias: bool = False, residual: bool = True, device="cuda",
