@@ -501,9 +501,10 @@ class GatedFFN(torch.nn.Module):
     ``x +``, ``bias=False`` (the default) the biases.  x is ``[..., D]``.
 
     The forward and backward can be captured in a graph after a warm-up on a
-    side stream; a capture while an autograd graph of the same leaves, made on
-    the default stream, is alive raises an error.  So do second derivatives,
-    forward-mode ones and torch.jit.trace without gradients.
+    side stream; a capture while an autograd graph that a GatedFFN made of the
+    same leaves on the default stream is alive raises an error (graphs that other
+    operations made of them there are not seen: drop those first).  So do
+    second derivatives, forward-mode ones and torch.jit.trace without gradients.
 
     Widths that are no multiples of 8 work, but the kernels read rows on 16-byte
     boundaries: the weights of such a block are copied at every call.
