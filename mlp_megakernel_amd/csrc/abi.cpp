@@ -5,7 +5,6 @@
 
 #include <algorithm>
 #include <atomic>
-#include <cstdarg>
 #include <cstdint>
 #include <cstdio>
 #include <exception>
@@ -14,81 +13,9 @@
 #include <string>
 #include <vector>
 
-#include "../../include/coalesce.h"
-#include "launch.hpp"
+#include "abi_check.hpp"
 
 using namespace coalesce;
-
-namespace {
-
-thread_local char g_last_error[512] = "";
-
-coalesce_status fail(coalesce_status s, const char* fmt, ...) {
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap);
-  va_end(ap);
-  return s;
-}
-
-coalesce_status ok() {
-  g_last_error[0] = '\0';
-  return COALESCE_OK;
-}
-
-coalesce_status device_fail(hipError_t e, const char* what) {
-  return fail(COALESCE_ERR_DEVICE, "%s: %s", what, hipGetErrorString(e));
-}
-
-constexpr int kMaxDevices = 64;
-std::mutex g_props_mutex;
-int g_cu_count[kMaxDevices] = {0};
-
-// CU count of the current device, queried once per device.
-coalesce_status current_cus(int* out) {
-  int dev = 0;
-  hipError_t e = hipGetDevice(&dev);
-  if (e != hipSuccess) return device_fail(e, "hipGetDevice");
-  if (dev < 0 || dev >= kMaxDevices) return fail(COALESCE_ERR_UNSUPPORTED, "device ordinal %d out of range", dev);
-  std::lock_guard<std::mutex> lock(g_props_mutex);
-  if (g_cu_count[dev] == 0) {
-    int cus = 0;
-    e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
-    if (e != hipSuccess) return device_fail(e, "hipDeviceGetAttribute");
-    if (cus <= 0) return fail(COALESCE_ERR_DEVICE, "device reports %d compute units", cus);
-    g_cu_count[dev] = cus;
-  }
-  *out = g_cu_count[dev];
-  return COALESCE_OK;
-}
-
-bool valid_dtype(int d) { return d == COALESCE_F32 || d == COALESCE_F16 || d == COALESCE_BF16; }
-bool valid_act(int a) {
-  return a == COALESCE_ACT_NONE || a == COALESCE_ACT_GELU_ERF || a == COALESCE_ACT_SOFTPLUS || a == COALESCE_ACT_RELU;
-}
-int64_t dsize(int d) { return d == COALESCE_F32 ? 4 : 2; }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-const int64_t kMaxExtent = (int64_t)INT32_MAX;
-
-// Byte range [lo, hi) covered by a rows x cols matrix with leading dimension ld.
-struct Range {
-  uintptr_t lo, hi;
-};
-Range span(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t es) {
-  uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  if (!p || rows <= 0 || cols <= 0) return {lo, lo};
-  return {lo, lo + (uintptr_t)(((rows - 1) * ld + cols) * es)};
-}
-bool overlap(Range a, Range b) { return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi; }
-
-int act_code(coalesce_act a) {
-  return a == COALESCE_ACT_GELU_ERF ? ACT_GELU
-         : a == COALESCE_ACT_SOFTPLUS ? ACT_SOFTPLUS
-         : a == COALESCE_ACT_RELU     ? ACT_RELU
-                                      : ACT_NONE;
-}
-
-}  // namespace
 
 namespace {
 
@@ -967,11 +894,6 @@ coalesce_status coalesce_autotune_mlp_forward(const void* x, int64_t ldx, const 
 
 namespace {
 
-// Activations of the feed-forward operators: those of the GEMM and SiLU.
-bool valid_ffn_act(int a) { return valid_act((coalesce_act)a) || a == COALESCE_ACT_SILU; }
-int ffn_act_code(coalesce_act a) { return a == COALESCE_ACT_SILU ? (int)ACT_SILU : act_code(a); }
-DType dt_code(coalesce_dtype d) { return d == COALESCE_F32 ? DT_F32 : d == COALESCE_F16 ? DT_F16 : DT_BF16; }
-
 // Extents and types shared by the feed-forward entry points: 16-bit inputs,
 // `other` (an output or gradient type) that type or F32.
 coalesce_status check_ffn(int64_t M, int64_t N, int64_t K, coalesce_dtype in, coalesce_dtype other,
@@ -990,64 +912,6 @@ coalesce_status check_ffn(int64_t M, int64_t N, int64_t K, coalesce_dtype in, co
   const int64_t area = int64_t(1) << 41;
   if ((N && M > area / N) || (K && M > area / K) || (K && N > area / K))
     return fail(COALESCE_ERR_UNSUPPORTED, "a product of two extents above 2^41");
-  return COALESCE_OK;
-}
-
-// A rows x cols matrix operand that has elements: present, pitch at least the
-// row and at most 2^23 (256 rows are addressed with 32-bit byte offsets),
-// 16-byte aligned rows.
-coalesce_status check_mat(const void* t, int64_t ld, int64_t cols, int64_t es, const char* name) {
-  if (!t) return fail(COALESCE_ERR_INVALID_ARGUMENT, "%s is NULL", name);
-  if (ld < cols) return fail(COALESCE_ERR_INVALID_ARGUMENT, "the pitch of %s is shorter than the row", name);
-  if (ld >= (int64_t(1) << 23)) return fail(COALESCE_ERR_UNSUPPORTED, "the pitch of %s must be below 2^23", name);
-  if (!aligned16(t) || (ld * es) % 16)
-    return fail(COALESCE_ERR_UNSUPPORTED, "%s must be 16-byte aligned with a 16-byte row pitch", name);
-  return COALESCE_OK;
-}
-coalesce_status check_vec(const void* t, const char* name) {
-  if (t && !aligned16(t)) return fail(COALESCE_ERR_UNSUPPORTED, "%s must be 16-byte aligned", name);
-  return COALESCE_OK;
-}
-
-// Operands of a call, to refuse outputs that overlap anything else.  Matrices
-// of one pitch may interleave (the halves of a wider matrix): their rows are
-// disjoint where the distance between the bases, modulo the pitch, leaves room
-// for both rows.
-struct Operand {
-  Range r;
-  const char* name;
-  bool out;
-  uint64_t row = 0, pitch = 0;  // bytes; pitch 0: one run of memory
-};
-bool interleaved(const Operand& a, const Operand& b) {
-  if (!a.pitch || a.pitch != b.pitch) return false;
-  const uint64_t dist = b.r.lo >= a.r.lo ? (uint64_t)(b.r.lo - a.r.lo) % a.pitch
-                                         : (a.pitch - (uint64_t)(a.r.lo - b.r.lo) % a.pitch) % a.pitch;
-  return dist >= a.row && dist + b.row <= a.pitch;
-}
-struct Operands {
-  Operand v[16];
-  int n = 0;
-  void mat(bool out, const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t es, const char* name) {
-    v[n++] = {span(p, rows, cols, ld, es), name, out, (uint64_t)(cols * es), (uint64_t)(ld * es)};
-  }
-  void run(bool out, const Range& r, const char* name) { v[n++] = {r, name, out}; }
-  coalesce_status check() const {
-    for (int i = 0; i < n; ++i)
-      for (int j = 0; j < i; ++j)
-        if ((v[i].out || v[j].out) && overlap(v[i].r, v[j].r) && !interleaved(v[i], v[j]))
-          return fail(COALESCE_ERR_INVALID_ARGUMENT, "%s overlaps %s", v[v[i].out ? i : j].name,
-                      v[v[i].out ? j : i].name);
-    return COALESCE_OK;
-  }
-};
-
-coalesce_status check_workspace(const void* ws, size_t have, size_t need) {
-  if (need == 0) return COALESCE_OK;
-  if (!ws) return fail(COALESCE_ERR_INVALID_ARGUMENT, "workspace is NULL (%zu bytes are needed)", need);
-  if (!aligned16(ws)) return fail(COALESCE_ERR_UNSUPPORTED, "workspace must be 16-byte aligned");
-  if (have < need)
-    return fail(COALESCE_ERR_INVALID_ARGUMENT, "workspace of %zu bytes is smaller than the %zu needed", have, need);
   return COALESCE_OK;
 }
 
