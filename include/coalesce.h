@@ -544,6 +544,93 @@ coalesce_status coalesce_clip_grad_norm_rows(const void* const* grads, void* con
                                              double max_norm, float* norm, void* workspace, size_t workspace_bytes,
                                              void* stream);
 
+/*
+ * ---- Operators around the feed-forward products ------------------------------
+ *
+ * What a block x + dropout(FFN(layer_norm(x))) needs next to the products: the
+ * norm and its gradients, the dropout, and (further below) the same products
+ * on 8-bit operands.  Matrices as above: row-major, 16-byte aligned rows, pitches
+ * below 2^23 elements, any extents (below 2^31 - 256, at most 2^41 elements);
+ * vectors 16-byte aligned, statistics 4-byte aligned.  Outputs must not overlap
+ * the inputs, each other or the workspace, but for the in-place forms that are
+ * named.  Repeated calls give identical bits.  Values between a row's end and the
+ * pitch are never part of a result and are left as they were.
+ *
+ * The dropout mask: element (m, n) of a matrix is dropped where word n mod 4 of
+ * Philox4x32-10 (Salmon et al., SC 2011) at the counter (n / 4, m, offset low 32
+ * bits, offset high 32 bits) under the key `seed` is below round(p 2^32), kept
+ * and multiplied by 1 / (1 - p) otherwise.  So the mask depends on the place, the
+ * seed and the offset alone, and nothing of it is stored.  A dropped element is 0
+ * even where it was infinite or NaN.  p lies in [0, 1]; 1 drops everything.
+ * device_seed, where it is not NULL, is device memory (8-byte aligned) that holds
+ * {seed, offset} and is read when the kernel runs, in place of the arguments: a
+ * captured graph whose replays are to have masks of their own writes it between
+ * them.
+ */
+
+/*
+ * Layer norm of each row of a residual stream:
+ *   s = X,  or with R  s = R + dropout(X)
+ *   Y = (s - mean) rstd weight + bias
+ *   mean = sum_n s / N;  rstd = 1 / sqrt(sum_n (s - mean)^2 / N + eps)
+ *   X      device, M x N (ldx): without R the stream, of stream_dtype; with R the
+ *          branch that is added to it, of dtype
+ *   R      device, M x N of stream_dtype (ldr), or NULL
+ *   S      device, M x N of stream_dtype (lds), written with the sum, or NULL (it
+ *          is not wanted, or there is no R); may be R itself with lds == ldr
+ *   weight, bias  device, N of weight_dtype, or NULL (1 and 0)
+ *   Y      device, M x N of dtype (ldy)
+ *   mean, rstd  device, M floats each, written for the backward, or NULL
+ * stream_dtype and weight_dtype are dtype or F32.  All of it is fp32, the mean
+ * before the squares of the deviations; Y comes from the sum before its rounding.
+ * p, seed, offset, device_seed: the mask (without R p must be 0).  M == 0 or N == 0
+ * is a no-op.  eps must be a number of at least 0.
+ */
+coalesce_status coalesce_layer_norm(const void* X, int64_t ldx, const void* R, int64_t ldr, void* S, int64_t lds,
+                                    const void* weight, const void* bias, void* Y, int64_t ldy, float* mean,
+                                    float* rstd, int64_t M, int64_t N, coalesce_dtype dtype,
+                                    coalesce_dtype stream_dtype, coalesce_dtype weight_dtype, double eps, double p,
+                                    uint64_t seed, uint64_t offset, const uint64_t* device_seed, void* stream);
+
+/*
+ * Its gradients for the upstream gradient dY, from the stream S that was normed
+ * (the sum, as written) and the statistics of the forward:
+ *   g = dY weight;  xh = (S - mean) rstd
+ *   dX = rstd (g - sum_n g / N - xh sum_n (g xh) / N) + dS
+ *   dB = dropout(dX before its rounding)
+ *   dweight[n] = sum_m dY xh;  dbias[n] = sum_m dY
+ *   dS     device, M x N of stream_dtype (ldg), the gradient that arrives along
+ *          the stream, or NULL; may be dX itself with ldg == ldx
+ *   dX     device, M x N of stream_dtype (ldx), or NULL
+ *   dB     device, M x N of dtype (ldb), the gradient of the branch, or NULL
+ *   dweight, dbias  device, N of grad_dtype (dtype or F32), or NULL; overwritten,
+ *          with 0 where M is 0
+ *   workspace  device, 16-byte aligned, at least
+ *          coalesce_layer_norm_backward_workspace_size(M, N) bytes where dweight
+ *          or dbias is wanted
+ */
+size_t coalesce_layer_norm_backward_workspace_size(int64_t M, int64_t N);
+coalesce_status coalesce_layer_norm_backward(const void* S, int64_t lds, const void* weight, const float* mean,
+                                             const float* rstd, const void* dY, int64_t ldy, const void* dS,
+                                             int64_t ldg, void* dX, int64_t ldx, void* dB, int64_t ldb, void* dweight,
+                                             void* dbias, int64_t M, int64_t N, coalesce_dtype dtype,
+                                             coalesce_dtype stream_dtype, coalesce_dtype weight_dtype,
+                                             coalesce_dtype grad_dtype, double p, uint64_t seed, uint64_t offset,
+                                             const uint64_t* device_seed, void* workspace, size_t workspace_bytes,
+                                             void* stream);
+
+/*
+ * Y = R + dropout(X), or dropout(X) where R is NULL; the gradient in X is the same
+ * call on dY without R.
+ *   X  device, M x N of dtype (ldx)
+ *   R  device, M x N of out_dtype (ldr), or NULL; may be Y with ldr == ldy
+ *   Y  device, M x N of out_dtype (dtype or F32); may be X with ldx == ldy and one
+ *      type
+ */
+coalesce_status coalesce_dropout(const void* X, int64_t ldx, const void* R, int64_t ldr, void* Y, int64_t ldy,
+                                 int64_t M, int64_t N, coalesce_dtype dtype, coalesce_dtype out_dtype, double p,
+                                 uint64_t seed, uint64_t offset, const uint64_t* device_seed, void* stream);
+
 /* Forget every tuned configuration (all devices). */
 coalesce_status coalesce_autotune_clear(void);
 

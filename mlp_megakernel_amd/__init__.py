@@ -29,7 +29,7 @@ _ACTS = {"none": ACT_NONE, None: ACT_NONE, "gelu": ACT_GELU_ERF, "gelu_erf": ACT
 
 # Every exported entry point of include/coalesce.h with its ctypes signature.
 _i64, _i32, _p, _sz = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t
-_f64 = ctypes.c_double
+_f64, _u64 = ctypes.c_double, ctypes.c_uint64
 SIGNATURES = {
     "coalesce_gemm_bias_act": (_i32, [_p, _i64, _p, _i64, _p, _p, _i64, _i64, _i64, _i64, _i32, _i32, _i32, _p]),
     "coalesce_mlp_forward": (_i32, [_p, _i64, _p, _p, _i32, _p, _i64, _i64, _i32, _i32, _p]),
@@ -64,6 +64,12 @@ SIGNATURES = {
     "coalesce_grad_norm_rows_workspace_size": (_sz, [_p, _p, _p, _i64]),
     "coalesce_grad_norm_rows": (_i32, [_p, _p, _p, _p, _p, _i64, _i32, _p, _p, _sz, _p]),
     "coalesce_clip_grad_norm_rows": (_i32, [_p, _p, _p, _p, _p, _p, _p, _i64, _i32, _f64, _p, _p, _sz, _p]),
+    "coalesce_layer_norm": (_i32, [_p, _i64, _p, _i64, _p, _i64, _p, _p, _p, _i64, _p, _p, _i64, _i64, _i32, _i32,
+                                   _i32, _f64, _f64, _u64, _u64, _p, _p]),
+    "coalesce_layer_norm_backward_workspace_size": (_sz, [_i64, _i64]),
+    "coalesce_layer_norm_backward": (_i32, [_p, _i64, _p, _p, _p, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _p, _i64,
+                                            _i64, _i32, _i32, _i32, _i32, _f64, _u64, _u64, _p, _p, _sz, _p]),
+    "coalesce_dropout": (_i32, [_p, _i64, _p, _i64, _p, _i64, _i64, _i64, _i32, _i32, _f64, _u64, _u64, _p, _p]),
     "coalesce_autotune_clear": (_i32, []),
     "coalesce_bias_add": (_i32, [_p, _i64, _p, _p, _i64, _i64, _i64, _i32, _i32, _i32, _p]),
     "coalesce_activation": (_i32, [_p, _i64, _p, _i64, _i64, _i64, _i32, _i32, _p]),
@@ -678,3 +684,5 @@ class FusedMLPSoftplusWN(torch.nn.Module):
 
 from .ffn import (GatedFFN, GatedGrads, GemmGrads, clip_grad_norm, gated_gemm, gated_gemm_backward,  # noqa: E402,F401
                   gated_gemm_train, gemm_residual, gemm_residual_backward, gemm_residual_train, grad_norm)
+from .norm import (NormGrads, add_layer_norm, add_layer_norm_train, dropout, dropout_backward,  # noqa: E402,F401
+                   layer_norm, layer_norm_backward, layer_norm_train)

@@ -1,0 +1,63 @@
+// Internal launch interface of the operators around the feed-forward products:
+// layer norm, dropout, quantisation and the 8-bit products.
+#pragma once
+#include "launch.hpp"
+
+namespace coalesce {
+
+// A dropout mask: an element is dropped where its word is at most `last`.
+struct Drop {
+  bool on;
+  uint32_t last;
+  float scale;  // 1 / (1 - p)
+  uint64_t seed, offset;
+  const uint64_t* device_seed;  // {seed, offset} in device memory, or nullptr
+};
+
+// Layer norm of M rows of N.  The stream (the norm's input) is of type TS, the
+// operand (what it gives, and the branch added in front of it) of type T.
+struct NormParams {
+  const void* X;  // without R the stream, with R the branch
+  const void* R;  // stream that the branch is added to, or nullptr
+  void* S;        // the sum, or nullptr
+  void* Y;
+  const void *weight, *bias;  // or nullptr
+  float *mean, *rstd;         // or nullptr
+  int64_t ldx, ldr, lds, ldy;
+  int M, N;
+  float eps;
+  DType wt;  // type of weight and bias
+  Drop drop;
+};
+hipError_t launch_norm(const NormParams& p, DType operand, DType stream_type, hipStream_t stream, int num_cus);
+
+struct NormBwdParams {
+  const void* S;   // the stream (TS)
+  const void* dY;  // gradient of the norm's result (T)
+  const void* dS;  // gradient that arrives along the stream (TS), or nullptr
+  void* dX;        // the stream's gradient (TS), or nullptr
+  void* dB;        // the branch's (T), or nullptr
+  const void* weight;
+  const float *mean, *rstd;
+  void *dweight, *dbias;  // of type gt, or nullptr
+  float* partial;         // the workspace
+  int64_t lds, ldy, ldg, ldx, ldb;
+  int M, N;
+  int groups, ldp;  // partial sums per column and their pitch (set by the launcher)
+  DType wt, gt;
+  Drop drop;
+};
+size_t norm_backward_workspace(int64_t M, int64_t N, int num_cus);
+hipError_t launch_norm_backward(NormBwdParams p, DType operand, DType stream_type, hipStream_t stream, int num_cus);
+
+struct DropoutParams {
+  const void* X;
+  const void* R;  // of the result's type, or nullptr
+  void* Y;
+  int64_t ldx, ldr, ldy;
+  int M, N;
+  Drop drop;
+};
+hipError_t launch_dropout(const DropoutParams& p, DType in, DType out, hipStream_t stream);
+
+}  // namespace coalesce

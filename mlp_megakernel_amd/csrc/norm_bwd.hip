@@ -1,0 +1,386 @@
+// Backward of the layer norm on gfx950, from the stream s and the statistics of
+// the forward:
+//   g = dY w;  xh = (s - mean) rstd
+//   ds = rstd (g - sum(g) / N - xh sum(g xh) / N) + dS       the stream's gradient
+//   dbranch = keep(ds) / (1 - p)                             that of the branch added in front
+//   dw = sum over rows of dY xh;  db = sum over rows of dY
+// One sweep over the rows computes all of it: workgroups take rows in turn, a
+// thread keeps the sums of its columns in registers from row to row while the next
+// row's loads are in flight, and writes them once as a partial sum.  A second small
+// launch adds the partials in order (no atomics: the same bits every time).
+// Sums and statistics are fp32.  Rows longer than the registers take one kernel per
+// row and one per block of columns instead.
+#include <algorithm>
+
+#include "philox.hpp"
+#include "rows.hpp"
+
+namespace coalesce {
+namespace {
+
+// TPR threads per row, CH times 8 columns each; rows of one wave lie four to a
+// workgroup, whose waves' sums meet in LDS at the end.
+template <typename T, typename TS, int TPR, int CH>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwdParams p) {
+  constexpr int THREADS = TPR < 256 ? 256 : TPR, ROWS = THREADS / TPR, WAVES = TPR / 64;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int sub = wave / WAVES;  // of the workgroup's rows
+  const int t = threadIdx.x % TPR;
+  __shared__ f32x2 part[2][WAVES];
+  float aw[CH][8], ab[CH][8], w[CH][8];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) aw[c][e] = ab[c][e] = 0.0f, w[c][e] = 1.0f;
+    if (p.weight) read_vec<T>(p.weight, p.wt == DT_F32, (c * TPR + t) * 8, p.N, w[c]);
+  }
+  const DropKey key = drop_key(p.drop);
+  const float inv_n = 1.0f / (float)p.N;
+
+  // A row past the last one reads nothing (resources without a range).
+  struct In {
+    Raw8<T> dy[CH];
+    Raw8<TS> s[CH], g[CH];
+    float mean, rstd;
+  };
+  auto load = [&](int64_t row, In& in) {
+    const bool there = row < p.M;
+    const int cols = there ? p.N : 0;
+    if (!there) row = 0;
+    const Row<T> dy = Row<T>::in(p.dY, p.ldy, row, cols);
+    const Row<TS> s = Row<TS>::in(p.S, p.lds, row, cols);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      in.dy[c] = dy.load((c * TPR + t) * 8);
+      in.s[c] = s.load((c * TPR + t) * 8);
+    }
+    if (p.dS) {
+      const Row<TS> g = Row<TS>::in(p.dS, p.ldg, row, cols);
+#pragma unroll
+      for (int c = 0; c < CH; ++c) in.g[c] = g.load((c * TPR + t) * 8);
+    }
+    in.mean = there ? p.mean[row] : 0.0f;
+    in.rstd = there ? p.rstd[row] : 0.0f;
+  };
+
+  const int64_t step = (int64_t)gridDim.x * ROWS;
+  int64_t row0 = (int64_t)blockIdx.x * ROWS;
+  // The next row's loads go out before this one's arithmetic, where the registers
+  // of 1024 threads leave room for both.
+  constexpr bool AHEAD = TPR < 1024;
+  In in, nx;
+  if constexpr (AHEAD) load(row0 + sub, in);
+  for (int parity = 0; row0 < p.M; row0 += step, parity ^= 1) {
+    const int64_t row = row0 + sub;
+    if constexpr (AHEAD)
+      load(row0 + step + sub, nx);
+    else
+      load(row, in);
+    float dy[CH][8], xh[CH][8], c1 = 0.0f, c2 = 0.0f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int n = (c * TPR + t) * 8;
+      Row<T>::widen(in.dy[c], n, p.N, dy[c]);
+      Row<TS>::widen(in.s[c], n, p.N, xh[c]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        // past the row's end dY is 0: nothing of it counts
+        xh[c][e] = (xh[c][e] - in.mean) * in.rstd;
+        const float g = dy[c][e] * w[c][e];
+        c1 += g;
+        c2 = __builtin_fmaf(g, xh[c][e], c2);
+        aw[c][e] = __builtin_fmaf(dy[c][e], xh[c][e], aw[c][e]);
+        ab[c][e] += dy[c][e];
+      }
+    }
+    c1 = wave_sum(c1);
+    c2 = wave_sum(c2);
+    if constexpr (WAVES > 1) {
+      // two places in turn: a wave that is a row ahead writes the other one
+      if ((threadIdx.x & 63) == 0) part[parity][wave] = (f32x2){c1, c2};
+      __syncthreads();
+      c1 = part[parity][0][0];
+      c2 = part[parity][0][1];
+#pragma unroll
+      for (int i = 1; i < WAVES; ++i) {
+        c1 += part[parity][i][0];
+        c2 += part[parity][i][1];
+      }
+    }
+    c1 *= inv_n;
+    c2 *= inv_n;
+    if (row < p.M && (p.dX || p.dB)) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int n = (c * TPR + t) * 8;
+        float g[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] = 0.0f;
+        if (p.dS) Row<TS>::widen(in.g[c], n, p.N, g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float d = __builtin_fmaf(dy[c][e], w[c][e], -c1);
+          g[e] = __builtin_fmaf(in.rstd, __builtin_fmaf(-xh[c][e], c2, d), g[e]);
+        }
+        if (p.dX) Row<TS>::out(p.dX, p.ldx, row, p.N).store(n, g, (TS*)p.dX + row * p.ldx);
+        if (p.dB) {
+          if (p.drop.on) drop8(key, (uint32_t)row, (uint32_t)n, g);
+          Row<T>::out(p.dB, p.ldb, row, p.N).store(n, g, (T*)p.dB + row * p.ldb);
+        }
+      }
+    }
+    if constexpr (AHEAD) in = nx;
+  }
+
+  if (!p.dweight && !p.dbias) return;
+  // partial[0]: dw, partial[1]: db, a row of ldp per workgroup
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    float* out = p.partial + ((int64_t)k * gridDim.x + blockIdx.x) * p.ldp;
+    if constexpr (ROWS > 1) {
+      __shared__ f32x4 meet[ROWS][2 * CH][64];
+      __syncthreads();
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float(&a)[8] = k ? ab[c] : aw[c];
+          meet[sub][2 * c + h][t] = (f32x4){a[4 * h], a[4 * h + 1], a[4 * h + 2], a[4 * h + 3]};
+        }
+      __syncthreads();
+      for (int i = threadIdx.x; i < 2 * CH * 64; i += THREADS) {
+        const int q = i >> 6, l = i & 63, n = ((q >> 1) * TPR + l) * 8 + 4 * (q & 1);
+        f32x4 s = meet[0][q][l];
+#pragma unroll
+        for (int r = 1; r < ROWS; ++r) s += meet[r][q][l];
+        if (n < p.ldp) *(f32x4*)(out + n) = s;
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int n = (c * TPR + t) * 8 + 4 * h;
+          const float(&a)[8] = k ? ab[c] : aw[c];
+          if (n < p.ldp) *(f32x4*)(out + n) = (f32x4){a[4 * h], a[4 * h + 1], a[4 * h + 2], a[4 * h + 3]};
+        }
+    }
+  }
+}
+
+// Rows longer than the registers: one workgroup per row, two passes.
+template <typename T, typename TS>
+__global__ __launch_bounds__(1024) void norm_bwd_long_kernel(NormBwdParams p) {
+  __shared__ f32x2 part[16];
+  const int64_t row = blockIdx.x;
+  const Row<T> dyr = Row<T>::in(p.dY, p.ldy, row, p.N);
+  const Row<TS> sr = Row<TS>::in(p.S, p.lds, row, p.N);
+  const float mean = p.mean[row], rstd = p.rstd[row];
+  const DropKey key = drop_key(p.drop);
+  auto read = [&](int n, float (&g)[8], float (&xh)[8]) {
+    float w[8];
+    dyr.read(n, g);
+    sr.read(n, xh);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = 1.0f;
+    if (p.weight) read_vec<T>(p.weight, p.wt == DT_F32, n, p.N, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      g[e] *= w[e];
+      xh[e] = (xh[e] - mean) * rstd;
+    }
+  };
+  float c1 = 0.0f, c2 = 0.0f;
+  for (int n = threadIdx.x * 8; n < p.N; n += 8192) {
+    float g[8], xh[8];
+    read(n, g, xh);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      c1 += g[e];
+      c2 = __builtin_fmaf(g[e], xh[e], c2);
+    }
+  }
+  c1 = wave_sum(c1);
+  c2 = wave_sum(c2);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = (f32x2){c1, c2};
+  __syncthreads();
+  c1 = c2 = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    c1 += part[i][0];
+    c2 += part[i][1];
+  }
+  const float inv_n = 1.0f / (float)p.N;
+  c1 *= inv_n;
+  c2 *= inv_n;
+  for (int n = threadIdx.x * 8; n < p.N; n += 8192) {
+    float g[8], xh[8], s[8];
+    read(n, g, xh);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] = 0.0f;
+    if (p.dS) Row<TS>::in(p.dS, p.ldg, row, p.N).read(n, s);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[e] = __builtin_fmaf(rstd, __builtin_fmaf(-xh[e], c2, g[e] - c1), s[e]);
+    if (p.dX) Row<TS>::out(p.dX, p.ldx, row, p.N).store(n, g, (TS*)p.dX + row * p.ldx);
+    if (p.dB) {
+      if (p.drop.on) drop8(key, (uint32_t)row, (uint32_t)n, g);
+      Row<T>::out(p.dB, p.ldb, row, p.N).store(n, g, (T*)p.dB + row * p.ldb);
+    }
+  }
+}
+
+// Their column sums: 256 columns per workgroup, eight row lanes, a range of rows.
+template <typename T, typename TS>
+__global__ __launch_bounds__(256) void norm_cols_kernel(NormBwdParams p) {
+  __shared__ float meet[8][256];
+  const int l = threadIdx.x & 31, lane = threadIdx.x >> 5;
+  const int n = (int)blockIdx.x * 256 + l * 8;
+  const int64_t first = (int64_t)p.M * blockIdx.y / p.groups, last = (int64_t)p.M * (blockIdx.y + 1) / p.groups;
+  float aw[8], ab[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) aw[e] = ab[e] = 0.0f;
+  for (int64_t r0 = first; r0 < last; r0 += 8) {
+    const int64_t row = r0 + lane;
+    if (row >= last) break;
+    float dy[8], s[8];
+    const T* dp = (const T*)p.dY + row * p.ldy + n;
+    const TS* sp = (const TS*)p.S + row * p.lds + n;
+    const float mean = p.mean[row], rstd = p.rstd[row];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const bool in = n + e < p.N;
+      dy[e] = in ? (float)dp[e] : 0.0f;
+      s[e] = in ? (float)sp[e] : mean;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      aw[e] = __builtin_fmaf(dy[e], (s[e] - mean) * rstd, aw[e]);
+      ab[e] += dy[e];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) meet[lane][l * 8 + e] = k ? ab[e] : aw[e];
+    __syncthreads();
+    const int col = threadIdx.x, at = (int)blockIdx.x * 256 + col;
+    float s = meet[0][col];
+#pragma unroll
+    for (int r = 1; r < 8; ++r) s += meet[r][col];
+    if (at < p.ldp) p.partial[((int64_t)k * p.groups + blockIdx.y) * p.ldp + at] = s;
+  }
+}
+
+// dw and db from the partial sums: 64 columns per workgroup, 16 of them side by
+// side per row lane of four, each lane its part of the partials; the 16 lanes are
+// added in order.
+template <typename TG>
+__global__ __launch_bounds__(256) void norm_sums_kernel(NormBwdParams p) {
+  __shared__ f32x4 meet[16][16];
+  TG* const out = (TG*)(blockIdx.y ? p.dbias : p.dweight);
+  if (!out) return;
+  const int q = threadIdx.x & 15, lane = threadIdx.x >> 4;
+  const int n = (int)blockIdx.x * 64 + q * 4;
+  const float* src = p.partial + (int64_t)blockIdx.y * p.groups * p.ldp + n;
+  f32x4 s = (f32x4){0.f, 0.f, 0.f, 0.f};
+  if (n < p.ldp) {
+    for (int g = lane; g < p.groups; g += 128) {
+      f32x4 v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        v[u] = g + 16 * u < p.groups ? *(const f32x4*)(src + (int64_t)(g + 16 * u) * p.ldp) : (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int u = 0; u < 8; ++u) s += v[u];
+    }
+  }
+  meet[lane][q] = s;
+  __syncthreads();
+  if (threadIdx.x >= 64) return;
+  const int c = threadIdx.x, at = (int)blockIdx.x * 64 + c;
+  float a = 0.0f;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) a += meet[r][c >> 2][c & 3];
+  if (at < p.N) out[at] = (TG)a;
+}
+
+constexpr int kLongRow = 16384;
+
+// Partial sums per column: of the workgroups of the sweep, or of the ranges of rows
+// of a long one.
+struct SumsPlan {
+  int groups, ldp;
+};
+SumsPlan sums_plan(int64_t M, int64_t N, int num_cus) {
+  SumsPlan s;
+  s.ldp = (int)((N + 7) / 8 * 8);
+  if (N > kLongRow) {
+    s.groups = (int)std::min<int64_t>((M + 63) / 64, 64);
+    return s;
+  }
+  const int64_t rows = N <= 1024 ? 4 : 1;
+  const int64_t per_cu = N <= 4096 ? 4 : N <= 8192 ? 2 : 1;
+  s.groups = (int)std::min<int64_t>((M + rows - 1) / rows, num_cus * per_cu);
+  return s;
+}
+
+template <typename T, typename TS>
+hipError_t bwd_typed(NormBwdParams p, hipStream_t stream, int num_cus) {
+  const SumsPlan plan = sums_plan(p.M, p.N, num_cus);
+  p.groups = plan.groups;
+  p.ldp = plan.ldp;
+  const bool sums = p.dweight || p.dbias;
+  if (p.M > 0) {
+#define COALESCE_NORM(TPR, CH) \
+  hipLaunchKernelGGL((norm_bwd_kernel<T, TS, TPR, CH>), dim3(p.groups), dim3(TPR < 256 ? 256 : TPR), 0, stream, p)
+    if (p.N <= 512)
+      COALESCE_NORM(64, 1);
+    else if (p.N <= 1024)
+      COALESCE_NORM(64, 2);
+    else if (p.N <= 2048)
+      COALESCE_NORM(256, 1);
+    else if (p.N <= 4096)
+      COALESCE_NORM(256, 2);
+    else if (p.N <= 8192)
+      COALESCE_NORM(512, 2);
+    else if (p.N <= kLongRow)
+      COALESCE_NORM(1024, 2);
+    else {
+      if (p.dX || p.dB)
+        hipLaunchKernelGGL((norm_bwd_long_kernel<T, TS>), dim3((unsigned)p.M), dim3(1024), 0, stream, p);
+      if (sums)
+        hipLaunchKernelGGL((norm_cols_kernel<T, TS>), dim3((unsigned)((p.ldp + 255) / 256), p.groups), dim3(256), 0,
+                           stream, p);
+    }
+#undef COALESCE_NORM
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !sums) return e;
+  }
+  if (!sums) return hipSuccess;
+  const dim3 grid((unsigned)((p.N + 63) / 64), 2);
+  if (p.gt == DT_F32)
+    hipLaunchKernelGGL((norm_sums_kernel<float>), grid, dim3(256), 0, stream, p);
+  else if (p.gt == DT_BF16)
+    hipLaunchKernelGGL((norm_sums_kernel<__bf16>), grid, dim3(256), 0, stream, p);
+  else
+    hipLaunchKernelGGL((norm_sums_kernel<_Float16>), grid, dim3(256), 0, stream, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t norm_backward_workspace(int64_t M, int64_t N, int num_cus) {
+  const SumsPlan plan = sums_plan(M, N, num_cus);
+  return (size_t)plan.groups * (size_t)plan.ldp * 8;
+}
+
+hipError_t launch_norm_backward(NormBwdParams p, DType operand, DType stream_type, hipStream_t stream, int num_cus) {
+  if (operand == DT_F32) return bwd_typed<float, float>(p, stream, num_cus);
+  if (operand == DT_BF16)
+    return stream_type == DT_F32 ? bwd_typed<__bf16, float>(p, stream, num_cus)
+                                 : bwd_typed<__bf16, __bf16>(p, stream, num_cus);
+  return stream_type == DT_F32 ? bwd_typed<_Float16, float>(p, stream, num_cus)
+                               : bwd_typed<_Float16, _Float16>(p, stream, num_cus);
+}
+
+}  // namespace coalesce
