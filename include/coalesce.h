@@ -631,6 +631,53 @@ coalesce_status coalesce_dropout(const void* X, int64_t ldx, const void* R, int6
                                  int64_t M, int64_t N, coalesce_dtype dtype, coalesce_dtype out_dtype, double p,
                                  uint64_t seed, uint64_t offset, const uint64_t* device_seed, void* stream);
 
+/*
+ * Quantisation to 8-bit integers with one scale per row of X (tokens of
+ * activations), or per column (output channels of weights, which are turned
+ * over: Q is then N x M, channel by channel, the layout the products below read):
+ *   scale = amax / 127;  q = x (127 / amax) rounded to the nearest, ties to even
+ * where amax is the row's (column's) largest magnitude and each operation is one of
+ * fp32.  q lies in [-127, 127].  Where amax is 0 scale and q are 0 (also without
+ * elements); a row that holds an infinity or a NaN has scale NaN and q = 0.
+ *   X      device, M x N of dtype (ldx)
+ *   Q      device, M x N (columns: N x M) bytes, pitch ldq (a multiple of 16)
+ *   scale  device, M (columns: N) floats, 16-byte aligned
+ */
+coalesce_status coalesce_quantize_rows(const void* X, int64_t ldx, int8_t* Q, int64_t ldq, float* scale, int64_t M,
+                                       int64_t N, coalesce_dtype dtype, void* stream);
+coalesce_status coalesce_quantize_columns(const void* X, int64_t ldx, int8_t* Q, int64_t ldq, float* scale, int64_t M,
+                                          int64_t N, coalesce_dtype dtype, void* stream);
+
+/*
+ * The products of the feed-forward block on 8-bit operands with a scale per token
+ * and per channel:
+ *   z[m][n] = scale_a[m] scale_b[n] sum_k A[m][k] B[n][k] + bias[n]
+ *   coalesce_gemm_int8        Y = act(z) + R
+ *   coalesce_gated_gemm_int8  Y = act(zg) zu
+ *   A      device, M x K bytes (lda);  B  device, N x K bytes (ldb): one row per
+ *          channel, as coalesce_quantize_columns gives; pitches are multiples of 16
+ *   scale_a, scale_b  device, M and N floats, 16-byte aligned
+ *   bias   device, N floats, 16-byte aligned, or NULL
+ *   R      device, M x N of out_dtype (ldr), or NULL; may be Y with ldr == ldy
+ *   Y      device, M x N of out_dtype: F32, F16 or BF16 (ldy)
+ * The sums are exact (int32; K is at most 131071, where they cannot overflow with
+ * any bytes, -128 among them); scales, bias, act and R are applied in fp32 and each
+ * result rounded once.  So a row's result does not depend on the other rows, unlike
+ * that of the 16-bit products.  Activations, extents, workspaces and overlaps as
+ * there; M == 0 or N == 0 is a no-op, K == 0 gives act(bias) + R.
+ */
+size_t coalesce_gemm_int8_workspace_size(int64_t M, int64_t N, int64_t K);
+coalesce_status coalesce_gemm_int8(const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb, const float* scale_a,
+                                   const float* scale_b, const float* bias, const void* R, int64_t ldr, void* Y,
+                                   int64_t ldy, int64_t M, int64_t N, int64_t K, coalesce_dtype out_dtype,
+                                   coalesce_act act, void* workspace, size_t workspace_bytes, void* stream);
+size_t coalesce_gated_gemm_int8_workspace_size(int64_t M, int64_t N, int64_t K);
+coalesce_status coalesce_gated_gemm_int8(const int8_t* A, int64_t lda, const int8_t* Bg, const int8_t* Bu, int64_t ldb,
+                                         const float* scale_a, const float* scale_g, const float* scale_u,
+                                         const float* bias_g, const float* bias_u, void* Y, int64_t ldy, int64_t M,
+                                         int64_t N, int64_t K, coalesce_dtype out_dtype, coalesce_act act,
+                                         void* workspace, size_t workspace_bytes, void* stream);
+
 /* Forget every tuned configuration (all devices). */
 coalesce_status coalesce_autotune_clear(void);
 

@@ -70,6 +70,14 @@ SIGNATURES = {
     "coalesce_layer_norm_backward": (_i32, [_p, _i64, _p, _p, _p, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _p, _i64,
                                             _i64, _i32, _i32, _i32, _i32, _f64, _u64, _u64, _p, _p, _sz, _p]),
     "coalesce_dropout": (_i32, [_p, _i64, _p, _i64, _p, _i64, _i64, _i64, _i32, _i32, _f64, _u64, _u64, _p, _p]),
+    "coalesce_quantize_rows": (_i32, [_p, _i64, _p, _i64, _p, _i64, _i64, _i32, _p]),
+    "coalesce_quantize_columns": (_i32, [_p, _i64, _p, _i64, _p, _i64, _i64, _i32, _p]),
+    "coalesce_gemm_int8_workspace_size": (_sz, [_i64, _i64, _i64]),
+    "coalesce_gemm_int8": (_i32, [_p, _i64, _p, _i64, _p, _p, _p, _p, _i64, _p, _i64, _i64, _i64, _i64, _i32, _i32, _p,
+                                  _sz, _p]),
+    "coalesce_gated_gemm_int8_workspace_size": (_sz, [_i64, _i64, _i64]),
+    "coalesce_gated_gemm_int8": (_i32, [_p, _i64, _p, _p, _i64, _p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i64, _i32,
+                                        _i32, _p, _sz, _p]),
     "coalesce_autotune_clear": (_i32, []),
     "coalesce_bias_add": (_i32, [_p, _i64, _p, _p, _i64, _i64, _i64, _i32, _i32, _i32, _p]),
     "coalesce_activation": (_i32, [_p, _i64, _p, _i64, _i64, _i64, _i32, _i32, _p]),
@@ -686,3 +694,4 @@ from .ffn import (GatedFFN, GatedGrads, GemmGrads, clip_grad_norm, gated_gemm, g
                   gated_gemm_train, gemm_residual, gemm_residual_backward, gemm_residual_train, grad_norm)
 from .norm import (NormGrads, add_layer_norm, add_layer_norm_train, dropout, dropout_backward,  # noqa: E402,F401
                    layer_norm, layer_norm_backward, layer_norm_train)
+from .int8 import gated_gemm_int8, gemm_int8, quantize_columns, quantize_rows  # noqa: E402,F401

@@ -23,7 +23,9 @@ BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["mlp.hip", "mlp_alt.hip", "mlp_small.hip", "mlp_stream.hip", "mlp_bwd.hip", "mlp_bwd_stream.hip",
            "gemm16.hip", "gemm32.hip", "elementwise.hip", "matrix_rate.hip", "weightnorm.hip", "ffn.hip",
            "ffn_gated_bf16.hip", "ffn_gated_f16.hip", "ffn_resid_bf16.hip", "ffn_resid_f16.hip",
-           "ffn_bwd_bf16.hip", "ffn_bwd_f16.hip", "gradnorm.hip", "norm.hip", "norm_bwd.hip", "dropout.hip",
+           "ffn_bwd_bf16.hip", "ffn_bwd_f16.hip", "gradnorm.hip", "norm.hip", "norm_bwd.hip", "dropout.hip", "quantize.hip", "int8.hip",
+           "int8_gated_bf16.hip", "int8_gated_f16.hip", "int8_gated_f32.hip", "int8_resid_bf16.hip",
+           "int8_resid_f16.hip", "int8_resid_f32.hip",
            "abi.cpp", "abi_block.cpp"]
 ARCH = "gfx950"
 

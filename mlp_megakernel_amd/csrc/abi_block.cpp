@@ -53,9 +53,166 @@ void add_seed(Operands& ops, const Drop& d) {
   if (d.device_seed) ops.run(false, {(uintptr_t)d.device_seed, (uintptr_t)d.device_seed + 16}, "the seed");
 }
 
+// A matrix of 8-bit operands: K is limited by what its products may sum to.
+constexpr int64_t kMaxInt8K = 131071;  // 128 * 128 * 131071 < 2^31
+
+coalesce_status check_int8(int64_t M, int64_t N, int64_t K, coalesce_dtype out, coalesce_act act) {
+  if (M < 0 || N < 0 || K < 0)
+    return fail(COALESCE_ERR_INVALID_ARGUMENT, "negative extent (M=%lld N=%lld K=%lld)", (long long)M, (long long)N,
+                (long long)K);
+  if (!valid_dtype(out)) return fail(COALESCE_ERR_INVALID_ARGUMENT, "unknown dtype");
+  if (!valid_ffn_act(act)) return fail(COALESCE_ERR_INVALID_ARGUMENT, "unknown activation %d", (int)act);
+  const int64_t lim = kMaxExtent - 256;
+  if (M > lim || N > lim) return fail(COALESCE_ERR_UNSUPPORTED, "extents must be below 2^31 - 256");
+  if (K > kMaxInt8K) return fail(COALESCE_ERR_UNSUPPORTED, "K above %lld may overflow the int32 sums", (long long)kMaxInt8K);
+  if (N && M > (int64_t(1) << 41) / N) return fail(COALESCE_ERR_UNSUPPORTED, "a product of two extents above 2^41");
+  return COALESCE_OK;
+}
+
+// Both products; B[1] only for the gated one, R only for the other.
+coalesce_status int8_product(bool gated, const int8_t* A, int64_t lda, const int8_t* const (&B)[2], int64_t ldb,
+                             const float* scale_a, const float* const (&scale_b)[2], const float* const (&bias)[2],
+                             const void* R, int64_t ldr, void* Y, int64_t ldy, int64_t M, int64_t N, int64_t K,
+                             coalesce_dtype out, coalesce_act act, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  coalesce_status s = check_int8(M, N, K, out, act);
+  if (s != COALESCE_OK) return s;
+  if (M == 0 || N == 0) return ok();
+  const int64_t os = dsize(out);
+  static const char* const bn[2] = {"B (or Bg)", "Bu"};
+  static const char* const sn[2] = {"scale_b (or scale_g)", "scale_u"};
+  static const char* const vn[2] = {"bias (or bias_g)", "bias_u"};
+  Operands ops;
+  if ((s = check_mat(Y, ldy, N, os, "Y")) != COALESCE_OK) return s;
+  ops.mat(true, Y, M, N, ldy, os, "Y");
+  if (K > 0) {
+    if ((s = check_mat(A, lda, K, 1, "A")) != COALESCE_OK) return s;
+    ops.mat(false, A, M, K, lda, 1, "A");
+  }
+  if (!scale_a) return fail(COALESCE_ERR_INVALID_ARGUMENT, "scale_a is NULL");
+  if ((s = check_vec(scale_a, "scale_a")) != COALESCE_OK) return s;
+  ops.mat(false, scale_a, 1, M, M, 4, "scale_a");
+  for (int i = 0; i < (gated ? 2 : 1); ++i) {
+    if (K > 0) {
+      if ((s = check_mat(B[i], ldb, K, 1, bn[i])) != COALESCE_OK) return s;
+      ops.mat(false, B[i], N, K, ldb, 1, bn[i]);
+    }
+    if (!scale_b[i]) return fail(COALESCE_ERR_INVALID_ARGUMENT, "%s is NULL", sn[i]);
+    if ((s = check_vec(scale_b[i], sn[i])) != COALESCE_OK) return s;
+    ops.mat(false, scale_b[i], 1, N, N, 4, sn[i]);
+    if ((s = check_vec(bias[i], vn[i])) != COALESCE_OK) return s;
+    ops.mat(false, bias[i], 1, N, N, 4, vn[i]);
+  }
+  if (R) {
+    if ((s = check_mat(R, ldr, N, os, "R")) != COALESCE_OK) return s;
+    if (R == Y && ldr != ldy) return fail(COALESCE_ERR_INVALID_ARGUMENT, "in-place residual with different pitches");
+    if (R != Y) ops.mat(false, R, M, N, ldr, os, "R");
+  }
+  if ((s = ops.check()) != COALESCE_OK) return s;
+  int cus = 0;
+  if ((s = current_cus(&cus)) != COALESCE_OK) return s;
+  const size_t need = int8_workspace(M, N, K, gated, cus);
+  if ((s = check_workspace(workspace, workspace_bytes, need)) != COALESCE_OK) return s;
+  if (need) {
+    ops.run(true, {(uintptr_t)workspace, (uintptr_t)workspace + need}, "the workspace");
+    if ((s = ops.check()) != COALESCE_OK) return s;
+  }
+  Int8Params q{};
+  q.A = A;
+  q.scale_a = scale_a;
+  for (int i = 0; i < (gated ? 2 : 1); ++i) {
+    q.B[i] = B[i];
+    q.scale_b[i] = scale_b[i];
+    q.bias[i] = bias[i];
+  }
+  q.R = R;
+  q.Y = Y;
+  q.lda = lda;
+  q.ldb = ldb;
+  q.ldr = ldr;
+  q.ldy = ldy;
+  q.M = (int)M;
+  q.N = (int)N;
+  q.K = (int)K;
+  q.act = ffn_act_code(act);
+  hipError_t e = launch_int8(q, gated, dt_code(out), (hipStream_t)stream, cus, workspace);
+  if (e != hipSuccess) return device_fail(e, gated ? "gated 8-bit product launch" : "8-bit product launch");
+  return ok();
+}
+
+size_t int8_workspace_size(bool gated, int64_t M, int64_t N, int64_t K) {
+  if (check_int8(M, N, K, COALESCE_F32, COALESCE_ACT_NONE) != COALESCE_OK) return 0;
+  int cus = 0;
+  if (current_cus(&cus) != COALESCE_OK) return 0;
+  ok();
+  return M == 0 || N == 0 ? 0 : int8_workspace(M, N, K, gated, cus);
+}
+
+// Rows or columns of X to 8 bits; Q has `rows` rows of `cols`.
+coalesce_status quantize(bool columns, const void* X, int64_t ldx, int8_t* Q, int64_t ldq, float* scale, int64_t M,
+                         int64_t N, coalesce_dtype dtype, void* stream) {
+  coalesce_status s = check_rows(M, N);
+  if (s != COALESCE_OK) return s;
+  if (!valid_dtype(dtype)) return fail(COALESCE_ERR_INVALID_ARGUMENT, "unknown dtype");
+  const int64_t rows = columns ? N : M, cols = columns ? M : N;  // of Q
+  if (rows == 0) return ok();
+  if (!scale) return fail(COALESCE_ERR_INVALID_ARGUMENT, "scale is NULL");
+  if ((s = check_vec(scale, "scale")) != COALESCE_OK) return s;
+  Operands ops;
+  ops.mat(true, scale, 1, rows, rows, 4, "scale");
+  if (cols > 0) {
+    if ((s = check_mat(X, ldx, N, dsize(dtype), "X")) != COALESCE_OK) return s;
+    ops.mat(false, X, M, N, ldx, dsize(dtype), "X");
+    if ((s = check_mat(Q, ldq, cols, 1, "Q")) != COALESCE_OK) return s;
+    ops.mat(true, Q, rows, cols, ldq, 1, "Q");
+  }
+  if ((s = ops.check()) != COALESCE_OK) return s;
+  int cus = 0;
+  if ((s = current_cus(&cus)) != COALESCE_OK) return s;  // a device that answers, as in every other entry point
+  QuantParams q{X, Q, scale, ldx, ldq, (int)M, (int)N};
+  hipError_t e = columns ? launch_quantize_columns(q, dt_code(dtype), (hipStream_t)stream)
+                         : launch_quantize_rows(q, dt_code(dtype), (hipStream_t)stream);
+  if (e != hipSuccess) return device_fail(e, "quantisation launch");
+  return ok();
+}
+
 }  // namespace
 
 extern "C" {
+
+coalesce_status coalesce_quantize_rows(const void* X, int64_t ldx, int8_t* Q, int64_t ldq, float* scale, int64_t M,
+                                       int64_t N, coalesce_dtype dtype, void* stream) {
+  return quantize(false, X, ldx, Q, ldq, scale, M, N, dtype, stream);
+}
+
+coalesce_status coalesce_quantize_columns(const void* X, int64_t ldx, int8_t* Q, int64_t ldq, float* scale, int64_t M,
+                                          int64_t N, coalesce_dtype dtype, void* stream) {
+  return quantize(true, X, ldx, Q, ldq, scale, M, N, dtype, stream);
+}
+
+size_t coalesce_gemm_int8_workspace_size(int64_t M, int64_t N, int64_t K) {
+  return int8_workspace_size(false, M, N, K);
+}
+size_t coalesce_gated_gemm_int8_workspace_size(int64_t M, int64_t N, int64_t K) {
+  return int8_workspace_size(true, M, N, K);
+}
+
+coalesce_status coalesce_gemm_int8(const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb, const float* scale_a,
+                                   const float* scale_b, const float* bias, const void* R, int64_t ldr, void* Y,
+                                   int64_t ldy, int64_t M, int64_t N, int64_t K, coalesce_dtype out_dtype,
+                                   coalesce_act act, void* workspace, size_t workspace_bytes, void* stream) {
+  return int8_product(false, A, lda, {B, nullptr}, ldb, scale_a, {scale_b, nullptr}, {bias, nullptr}, R, ldr, Y, ldy,
+                      M, N, K, out_dtype, act, workspace, workspace_bytes, stream);
+}
+
+coalesce_status coalesce_gated_gemm_int8(const int8_t* A, int64_t lda, const int8_t* Bg, const int8_t* Bu, int64_t ldb,
+                                         const float* scale_a, const float* scale_g, const float* scale_u,
+                                         const float* bias_g, const float* bias_u, void* Y, int64_t ldy, int64_t M,
+                                         int64_t N, int64_t K, coalesce_dtype out_dtype, coalesce_act act,
+                                         void* workspace, size_t workspace_bytes, void* stream) {
+  return int8_product(true, A, lda, {Bg, Bu}, ldb, scale_a, {scale_g, scale_u}, {bias_g, bias_u}, nullptr, 0, Y, ldy,
+                      M, N, K, out_dtype, act, workspace, workspace_bytes, stream);
+}
 
 coalesce_status coalesce_layer_norm(const void* X, int64_t ldx, const void* R, int64_t ldr, void* S, int64_t lds,
                                     const void* weight, const void* bias, void* Y, int64_t ldy, float* mean,

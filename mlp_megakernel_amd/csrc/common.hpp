@@ -34,6 +34,12 @@ struct u16x2x4 {
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+// Two consecutive 8-bit integers of a row: what the 16-bit tile machinery moves
+// of an 8-bit operand.
+struct i8pair {
+  short v;
+};
 
 #define LDS_PTR(p) ((__attribute__((address_space(3))) void*)(p))
 
@@ -146,6 +152,16 @@ __device__ __forceinline__ f32x4 mfma16x16x32(i16x8 a, i16x8 b, f32x4 c, __bf16)
 __device__ __forceinline__ f32x4 mfma16x16x32(i16x8 a, i16x8 b, f32x4 c, _Float16) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
                                                 0);
+}
+
+// 8-bit integers, two per 16-bit place of the fragments: lane l holds A[l%16][16(l/16)+e],
+// e = 0..15 (v_mfma_i32_16x16x64_i8), so the bytes lie where those of the 16-bit
+// forms do and twice the products cost the same time.  The int32 sums travel in the
+// registers of the fp32 ones.
+__device__ __forceinline__ f32x4 mfma16x16x32(i16x8 a, i16x8 b, f32x4 c, i8pair) {
+  return __builtin_bit_cast(
+      f32x4, __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b),
+                                                   __builtin_bit_cast(i32x4, c), 0, 0, 0));
 }
 
 __device__ __forceinline__ void wait_vmcnt0() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }

@@ -3,7 +3,7 @@
 #pragma once
 #include <algorithm>
 
-#include "launch.hpp"
+#include "block.hpp"
 
 namespace coalesce {
 namespace {
@@ -117,6 +117,18 @@ ForwardPlan plan_forward(int64_t m, int64_t n, int64_t k, bool gated, int num_cu
     }
   }
   if (f.strip) f.tiles.splits = 1;
+  return f;
+}
+
+// The plan of an 8-bit product: the few-row kernel or tiles, whose K steps hold 128
+// values (the bytes and the time of a 16-bit step of 64).
+struct Int8Plan {
+  bool few;
+  TilePlan tiles;
+};
+Int8Plan plan_int8(int64_t m, int64_t n, int64_t k, bool gated, int num_cus) {
+  Int8Plan f{false, plan_tiles(m, n, gated, 1, (k + 127) / 128, true, num_cus)};
+  f.few = m <= 64;
   return f;
 }
 

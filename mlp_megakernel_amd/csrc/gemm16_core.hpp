@@ -58,7 +58,18 @@ __device__ __forceinline__ f32x4 load4(const T* src, int valid) {
 }
 
 enum Lay { LAY_K = 0, LAY_X = 1 };
-enum Epi { EPI_STORE = 0, EPI_RESID = 1, EPI_GATED = 2 };
+enum Epi { EPI_STORE = 0, EPI_RESID = 1, EPI_GATED = 2, EPI_INT8_RESID = 3, EPI_INT8_GATED = 4 };
+
+// Values of k in one element of T: 8-bit operands travel as pairs, in units of
+// which the pitches are counted too; the extent K stays that of the values.
+template <typename T>
+struct PerElement {
+  static constexpr int N = 1;
+};
+template <>
+struct PerElement<i8pair> {
+  static constexpr int N = 2;
+};
 
 // Tile geometry: BM x BN accumulators per workgroup, NW waves in a WGM x
 // NW / WGM grid, NS stages in LDS.  With two stages a copy has one K step's time
@@ -111,8 +122,8 @@ struct CopyRows {
   static constexpr int N = L == LAY_K ? 8 : 512 / BX;
 };
 
-// Masked register loads of the same 16 bytes (elements at k >= K become 0):
-// the last, partial K step.
+// Masked register loads of the same 16 bytes (elements at k >= K become 0, and the
+// upper half of a pair whose second value is): the last, partial K step.
 template <typename T, Lay L, int BX>
 __device__ __forceinline__ i16x8 tail_chunk(const Side& s, int g, int lane, int k0, int K) {
   i16x8 v = (i16x8){0, 0, 0, 0, 0, 0, 0, 0};
@@ -120,11 +131,14 @@ __device__ __forceinline__ i16x8 tail_chunk(const Side& s, int g, int lane, int 
     const int row = g * 8 + (lane >> 3);
     const int k = k0 + ((lane & 7) ^ swzA(row)) * 8;
     const int gx = min(s.x0 + row, s.X - 1);
-    if (k < K) {
+    constexpr int V = PerElement<T>::N;
+    if (k * V < K) {
       v = *(const i16x8*)((const T*)s.p + (int64_t)gx * s.ld + k);
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (k + e >= K) v[e] = 0;
+      for (int e = 0; e < 8; ++e) {
+        if ((k + e) * V >= K) v[e] = 0;
+        if (V == 2 && (k + e) * V + 1 == K) v[e] &= 0xff;
+      }
     }
   } else {
     constexpr int CPR = BX / 8, RPC = 64 / CPR;
@@ -208,6 +222,8 @@ struct TileFrags {
 template <typename T, typename TO, Lay LA, Lay LB, int SEGS, int EPI, typename G>
 struct Tile {
   static constexpr int RA = CopyRows<LA, G::BM>::N, RB = CopyRows<LB, G::SUBN>::N;
+  static constexpr int V = PerElement<T>::N;
+  static_assert(V == 1 || (LA == LAY_K && LB == LAY_K), "pairs lie along the contraction");
   static_assert(SEGS == 1 || G::NSUB == 1, "segments of a gated product are not implemented");
 
   // What the K loop needs of the tile, in scalar registers: the matrices at
@@ -367,7 +383,7 @@ struct Tile {
   static __device__ __forceinline__ void fill(Args k, const TileAt& at, int seg, const Hot& h, const Pats& pt, int s,
                                               uint32_t stage, T* a, T* b, int wu, int lane) {
     const Step st = step_at(h, s);
-    if (st.k0 + BK <= h.K) {
+    if ((st.k0 + BK) * V <= h.K) {
 #pragma unroll
       for (int j = 0; j < G::C; ++j) copy(h, pt, st, j, stage, a, b, wu);
     } else {
@@ -536,6 +552,47 @@ struct Tile {
         put<TO>(Y, p->ldy, p, wr0, wc0, inside, region, lane, none,
                 [&](int, int t, int s, int, int, int, const char*) { return acc[t + sub * G::NTO][s]; });
       }
+    } else if constexpr (EPI == EPI_INT8_RESID || EPI == EPI_INT8_GATED) {
+      // acc holds int32 sums; to fp32 (half a step of it above 2^24), times the row's
+      // scale, times the column's
+      const int act = p->act, q = lane & 15;
+      float sa[G::MT];
+#pragma unroll
+      for (int s = 0; s < G::MT; ++s) sa[s] = p->scale_m[min(wr0 + 16 * s + q, p->M - 1)];
+      struct Cols {
+        f32x4 scale, bias;
+      };
+      auto cols = [&](int i, int n, int valid) {
+        return Cols{load4<float>(p->scale_n[i] + n, valid),
+                    p->bias[i] ? load4<float>((const float*)p->bias[i] + n, valid) : (f32x4){0.f, 0.f, 0.f, 0.f}};
+      };
+      auto z = [&](const Cols& c, int t, int s) {
+        const i32x4 a = __builtin_bit_cast(i32x4, acc[t][s]);
+        f32x4 v;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf((float)a[r] * sa[s], c.scale[r], c.bias[r]);
+        return v;
+      };
+      if constexpr (EPI == EPI_INT8_GATED) {
+        struct Pair {
+          Cols g, u;
+        };
+        put<TO>((TO*)p->Y[0], p->ldy, p, wr0, wc0, inside, region, lane,
+                [&](int, int n, int valid) { return Pair{cols(0, n, valid), cols(1, n, valid)}; },
+                [&](const Pair& c, int t, int s, int, int, int, const char*) {
+                  return act_any(act, z(c.g, t, s)) * z(c.u, t + G::NTO, s);
+                });
+      } else {
+        const TO* R = (const TO*)p->R;
+        if (O16 && R && inside) stage_rows<TO>(R + (int64_t)wr0 * p->ldr + wc0, p->ldr, region, lane);
+        put<TO>((TO*)p->Y[0], p->ldy, p, wr0, wc0, inside, region, lane,
+                [&](int, int n, int valid) { return cols(0, n, valid); },
+                [&](const Cols& c, int t, int s, int m, int n, int valid, const char* cell) {
+                  const f32x4 v = act_any(act, z(c, t, s));
+                  if (!R) return v;
+                  return load4<TO>(cell ? (const TO*)cell : R + (int64_t)m * p->ldr + n, valid) + v;
+                });
+      }
     } else {
       const int act = p->act;
       auto bias_g = [&](int, int n, int valid) { return bias4(p->bias[0], n, valid); };
@@ -585,7 +642,7 @@ struct Tile {
     at.pair = tn >= p->tiles_n ? 1 : 0;
     at.m0 = tm * G::BM;
     at.n0 = (tn - at.pair * p->tiles_n) * G::ON;
-    const int64_t total = (int64_t)((p->K + BK - 1) / BK) * SEGS;
+    const int64_t total = (int64_t)((p->K + BK * V - 1) / (BK * V)) * SEGS;
     at.s0 = (int)(total * at.split / p->splits);
     at.s1 = (int)(total * (at.split + 1) / p->splits);
     return at;
@@ -593,7 +650,7 @@ struct Tile {
   // The part of the tile's K steps that lies in a segment.
   static __device__ __forceinline__ Range1 part(const TileAt& at, const Hot& h, int seg) {
     if constexpr (SEGS == 1) return Range1{at.s0, at.s1 - at.s0};
-    const int kt = (h.K + BK - 1) / BK;
+    const int kt = (h.K + BK * V - 1) / (BK * V);
     const int lo = max(at.s0 - seg * kt, 0), hi = min(at.s1 - seg * kt, kt);
     return Range1{lo, max(hi - lo, 0)};
   }
@@ -663,7 +720,7 @@ struct Tile {
               if (i + 1 < r.n) {
                 // the copies of step i + 2 may stay in flight, if that step has
                 // any
-                if (G::NS > 2 && i + 2 < r.n && (r.s + i + 2) * BK + BK <= h.K)
+                if (G::NS > 2 && i + 2 < r.n && ((r.s + i + 2) * BK + BK) * V <= h.K)
                   wait_steps<G::NS - 2>();
                 else if (EPI != EPI_STORE || G::NS > 2 || i > 0)  // both of two stages have landed before step 0
                   wait_vmcnt0();
@@ -672,7 +729,7 @@ struct Tile {
               bool cp = false;
               if (i + G::NS < r.n) {
                 st = step_at(h, r.s + i + G::NS);
-                cp = st.k0 + BK <= h.K;
+                cp = (st.k0 + BK) * V <= h.K;
                 if (!cp) tail(k, at, seg, st, sa(c), sb(c), wu, lane);
               }
               slice(f1, acc, f0, sa(nx), sb(nx), 0, wm, wn, lane, cp, h, pt, st, c, sa(c), sb(c), wu);

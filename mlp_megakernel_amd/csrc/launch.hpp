@@ -179,6 +179,8 @@ struct TileOp {
   int64_t ldy;
   int act;                        // for kernels that are not compiled per activation
   int tiles_m, tiles_n, group_m;  // set by the launcher
+  const float* scale_m;           // of 8-bit operands: a scale per row of the m side,
+  const float* scale_n[2];        // and of the n side
 };
 
 // Forward of the gated product and of the GEMM with residual (ffn_forward.hpp):

@@ -102,3 +102,62 @@ def test_dropout_accepts(kw, status):
 def test_generator_gives_the_published_vectors(counter, key, want):
     got = ref.philox([np.array([c]) for c in counter], key)
     assert [int(g[0]) for g in got] == want
+
+
+# ---------------------------------------------------------------------------
+# 8-bit operands
+# ---------------------------------------------------------------------------
+
+K = 48
+INT8 = dict(A=P, lda=K, B=2 * P, ldb=K, sa=3 * P, sb=4 * P, bias=5 * P, R=6 * P, ldr=N, Y=7 * P, ldy=N, M=M, N=N, K=K,
+            odt=mk.BF16, act=mk.ACT_GELU_ERF, ws=16 * P, n=1 << 30)
+GATED8 = dict(A=P, lda=K, Bg=2 * P, Bu=3 * P, ldb=K, sa=4 * P, sg=5 * P, su=6 * P, bg=7 * P, bu=8 * P, Y=9 * P, ldy=N,
+              M=M, N=N, K=K, odt=mk.F32, act=mk.ACT_SILU, ws=16 * P, n=1 << 30)
+QUANT = dict(X=P, ldx=N, Q=2 * P, ldq=N, scale=3 * P, M=N, N=N, dt=mk.BF16)
+BOTH = [(dict(M=-1), INV), (dict(N=-2), INV), (dict(K=-1), INV), (dict(K=131072, lda=131072, ldb=131072), UNS),
+        (dict(M=(1 << 31) - 200), UNS), (dict(M=1 << 21, N=1 << 21), UNS), (dict(odt=5), INV), (dict(act=9), INV),
+        (dict(A=None), INV), (dict(A=P + 8), UNS), (dict(lda=K - 16), INV), (dict(lda=K + 8), UNS),
+        (dict(lda=1 << 23), UNS), (dict(ldb=K - 16), INV), (dict(sa=None), INV), (dict(sa=3 * P + 4), UNS),
+        (dict(Y=None), INV), (dict(ldy=N - 8), INV), (dict(Y=P + 16), INV)]
+
+
+@pytest.mark.parametrize("kw,status", BOTH + [
+    (dict(B=None), INV), (dict(B=2 * P + 4), UNS), (dict(sb=None), INV), (dict(sb=4 * P + 8), UNS),
+    (dict(bias=5 * P + 4), UNS), (dict(R=7 * P, ldr=N + 8), INV), (dict(R=7 * P + 32), INV), (dict(R=6 * P + 2), UNS),
+    (dict(bias=7 * P), INV), (dict(sb=7 * P), INV)])
+def test_int8_refuses(kw, status):
+    assert call("coalesce_gemm_int8", INT8, kw) == status
+
+
+@pytest.mark.parametrize("kw,status", BOTH + [
+    (dict(Bg=None), INV), (dict(Bu=None), INV), (dict(Bu=3 * P + 4), UNS), (dict(sg=None), INV), (dict(su=None), INV),
+    (dict(su=6 * P + 4), UNS), (dict(bu=8 * P + 4), UNS), (dict(bu=9 * P), INV)])
+def test_gated_int8_refuses(kw, status):
+    assert call("coalesce_gated_gemm_int8", GATED8, kw) == status
+
+
+@pytest.mark.parametrize("kw", [dict(M=-1), dict(dt=4)])
+def test_quantize_refuses_invalid(kw):
+    for name in ("coalesce_quantize_rows", "coalesce_quantize_columns"):
+        assert call(name, QUANT, kw) == INV
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(X=None), INV), (dict(X=P + 2), UNS), (dict(Q=None), INV), (dict(Q=2 * P + 8), UNS), (dict(ldq=N - 16), INV),
+    (dict(ldq=N + 8), UNS), (dict(ldx=N - 8), INV), (dict(scale=None), INV), (dict(scale=3 * P + 4), UNS),
+    (dict(Q=P), INV), (dict(scale=2 * P), INV), (dict(M=(1 << 31) - 1), UNS), (dict(), DEV), (dict(M=0, N=0), 0)])
+def test_quantize_checks(kw, status):
+    for name in ("coalesce_quantize_rows", "coalesce_quantize_columns"):
+        assert call(name, QUANT, kw) == status
+
+
+def test_int8_accepts():
+    for name, defaults in (("coalesce_gemm_int8", INT8), ("coalesce_gated_gemm_int8", GATED8)):
+        assert call(name, defaults, {}) == DEV
+        assert call(name, defaults, dict(K=131071, lda=131072, ldb=131072, N=8)) == DEV
+        assert call(name, defaults, dict(K=0, A=None)) == DEV
+        assert call(name, defaults, dict(M=0, A=None, Y=None)) == 0
+    assert call("coalesce_gemm_int8", INT8, dict(R=7 * P)) == DEV
+    assert call("coalesce_quantize_rows", QUANT, dict(M=0)) == 0
+    assert call("coalesce_quantize_rows", QUANT, dict(N=0, X=None, Q=None)) == DEV
+    assert mk.load_library().coalesce_gemm_int8_workspace_size(8, 64, 131072) == 0
