@@ -690,8 +690,9 @@ class FusedMLPSoftplusWN(torch.nn.Module):
         return mlp_forward(x, weight_norm(vs, gs), hidden_act=self.hidden_act)
 
 
-from .ffn import (GatedFFN, GatedGrads, GemmGrads, clip_grad_norm, gated_gemm, gated_gemm_backward,  # noqa: E402,F401
-                  gated_gemm_train, gemm_residual, gemm_residual_backward, gemm_residual_train, grad_norm)
+from .ffn import (GatedFFN, GatedGrads, GemmGrads, QuantizedGatedFFN, clip_grad_norm, gated_gemm,  # noqa: E402,F401
+                  gated_gemm_backward, gated_gemm_train, gemm_residual, gemm_residual_backward, gemm_residual_train,
+                  grad_norm)
 from .norm import (NormGrads, add_layer_norm, add_layer_norm_train, dropout, dropout_backward,  # noqa: E402,F401
                    layer_norm, layer_norm_backward, layer_norm_train)
 from .int8 import gated_gemm_int8, gemm_int8, quantize_columns, quantize_rows  # noqa: E402,F401

@@ -417,8 +417,13 @@ def _norm_call(lists, max_norm, norm_type, norm, workspace, stream):
 
 
 # ---------------------------------------------------------------------------
-# Module
+# Modules
 # ---------------------------------------------------------------------------
+
+from .int8 import gated_gemm_int8, gemm_int8, quantize_columns, quantize_rows  # noqa: E402 (they use what is above)
+from .norm import dropout as _dropout  # noqa: E402
+from .norm import dropout_backward, layer_norm, layer_norm_backward, layer_norm_train  # noqa: E402
+
 
 def _rows16(t: torch.Tensor) -> torch.Tensor:
     """`t` with 16-byte aligned rows and unit inner stride (a copy if it has not)."""
@@ -456,49 +461,79 @@ class _EagerGraph:
                                    "drop its outputs before the capture, or warm up on the stream of the capture")
 
 
-def _refuse_recorded(tensors):
+def _refuse_recorded(tensors, what="GatedFFN", trace="GatedFFN without gradients cannot be traced: trace it with "
+                                                      "gradients enabled"):
     """The plain calls are no torch operations: what records those would miss
     them, a tangent be lost and a trace return memory that nothing wrote."""
     if torch.jit.is_tracing():
-        raise RuntimeError("GatedFFN without gradients cannot be traced: trace it with gradients enabled")
+        raise RuntimeError(trace)
     if getattr(forward_ad, "_current_level", 0) >= 0 and \
             any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
-        raise NotImplementedError("GatedFFN has no forward-mode derivative")
+        raise NotImplementedError("%s has no forward-mode derivative" % what)
+
+
+def _draw_seed(device) -> torch.Tensor:
+    """(seed, offset) of a dropout mask, from torch's generator of the device: it
+    goes by torch.manual_seed, and a captured graph draws anew at every replay."""
+    return torch.randint(-2 ** 63, 2 ** 63 - 1, (2,), device=device, dtype=torch.int64)
+
+
+def _down(H, Wd, bd, skip, p, seed):
+    """skip + dropout(H Wd + bd); without a dropout in the product's own epilogue."""
+    if seed is None:
+        return gemm_residual(H, Wd, skip, bd)
+    h = gemm_residual(H, Wd, None, bd)
+    return _dropout(h, p, seed, residual=skip, out=h)
 
 
 class _GatedFFNFunction(torch.autograd.Function):
-    """x + (act(x Wg + bg) * (x Wu + bu)) Wd + bd as one autograd node."""
+    """x + dropout((act(n Wg + bg) * (n Wu + bu)) Wd + bd) as one autograd node, n = x or its layer norm."""
 
     @staticmethod
-    def forward(ctx, graph, x, act, residual, Wg, Wu, Wd, bg, bu, bd):
-        H, (Zg, Zu) = gated_gemm_train(x, Wg, Wu, bg, bu, act=act)
-        y = gemm_residual(H, Wd, x if residual else None, bd)
-        ctx.act, ctx.residual, ctx.graph = act, residual, graph
-        ctx.save_for_backward(x, Wg, Wu, Wd, Zg, Zu, H)
+    def forward(ctx, graph, x, act, residual, norm, eps, p, seed, Wg, Wu, Wd, bg, bu, bd, nw, nb):
+        n, stats = (x, (None, None)) if not norm else layer_norm_train(x, nw, nb, eps)
+        H, (Zg, Zu) = gated_gemm_train(n, Wg, Wu, bg, bu, act=act)
+        y = _down(H, Wd, bd, x if residual else None, p, seed)
+        ctx.act, ctx.residual, ctx.norm, ctx.p, ctx.graph = act, residual, norm, p, graph
+        ctx.save_for_backward(x, n, Wg, Wu, Wd, Zg, Zu, H, nw, seed, *stats)
         return y
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
-        x, Wg, Wu, Wd, Zg, Zu, H = ctx.saved_tensors
-        need = ctx.needs_input_grad[1:]
+        x, n, Wg, Wu, Wd, Zg, Zu, H, nw, seed, *stats = ctx.saved_tensors
+        need_x = ctx.needs_input_grad[1]
+        need = dict(zip(("Wg", "Wu", "Wd", "bg", "bu", "bd", "nw", "nb"), ctx.needs_input_grad[8:]))
         dy = _rows16(dy.to(x.dtype))
+        dh = dy if seed is None else dropout_backward(dy, ctx.p, seed)
         # dH is rounded to the type as H was: it is an operand of the next products'
-        # dZ.  The skip's dy joins dx after dx's own rounding, a second half step.
-        down = gemm_residual_backward(H, Wd, dy, want_dB=need[5], want_dbias=need[8], grad_dtype=Wd.dtype)
-        up = gated_gemm_backward(x, Wg, Wu, (Zg, Zu), down.dA, act=ctx.act, want_dA=need[0],
-                                 want_dB=need[3] or need[4], want_dbias=need[6] or need[7], grad_dtype=Wg.dtype)
-        dx = up.dA
-        if need[0] and ctx.residual:
+        # dZ.  The skip's dy joins dx after dx's own rounding, a second half step (with a
+        # norm in its backward, before the one rounding).
+        down = gemm_residual_backward(H, Wd, dh, want_dB=need["Wd"], want_dbias=need["bd"], grad_dtype=Wd.dtype)
+        up = gated_gemm_backward(n, Wg, Wu, (Zg, Zu), down.dA, act=ctx.act,
+                                 want_dA=need_x or need["nw"] or need["nb"], want_dB=need["Wg"] or need["Wu"],
+                                 want_dbias=need["bg"] or need["bu"], grad_dtype=Wg.dtype)
+        dx, dnw, dnb = up.dA, None, None
+        if ctx.norm:
+            if dx is not None:
+                g = layer_norm_backward(x, nw, stats, dx, dy if ctx.residual else None, want_dx=need_x,
+                                        want_dweight=need["nw"], want_dbias=need["nb"], grad_dtype=nw.dtype)
+                dx, dnw, dnb = g.dx, g.dweight, g.dbias
+        elif need_x and ctx.residual:
             dx = dx + dy
-        return None, dx, None, None, up.dBg, up.dBu, down.dB, up.dbias_g, up.dbias_u, down.dbias
+        return (None, dx, None, None, None, None, None, None, up.dBg, up.dBu, down.dB, up.dbias_g, up.dbias_u,
+                down.dbias, dnw, dnb)
 
 
 class GatedFFN(torch.nn.Module):
-    """The gated feed-forward block ``y = x + (act(x Wg + bg) * (x Wu + bu)) Wd + bd``.
+    """The gated feed-forward block ``y = x + dropout((act(n Wg + bg) * (n Wu + bu)) Wd + bd)``.
 
     Weights in the x @ W orientation.  ``residual=False`` leaves out the
-    ``x +``, ``bias=False`` (the default) the biases.  x is ``[..., D]``.
+    ``x +``, ``bias=False`` (the default) the biases.  x is ``[..., D]``.  n is x,
+    or with ``norm=True`` its layer norm (over the last dimension, ``eps``, with
+    weight and bias).  ``dropout`` is the probability that an element is dropped
+    while the module trains; the mask is never stored, its seed comes from torch's
+    generator of the device.  :meth:`quantized` gives the block with 8-bit weights.
 
     The forward and backward can be captured in a graph after a warm-up on a
     side stream; a capture while an autograd graph that a GatedFFN made of the
@@ -511,10 +546,13 @@ class GatedFFN(torch.nn.Module):
     """
 
     def __init__(self, D: int, H: int, act="silu", bias: bool = False, residual: bool = True, device="cuda",
-                 dtype=torch.bfloat16):
+                 dtype=torch.bfloat16, norm: bool = False, dropout: float = 0.0, eps: float = 1e-5):
         super().__init__()
         _act(act)
+        if not 0.0 <= dropout <= 1.0:
+            raise ValueError("dropout must lie in [0, 1], not %r" % (dropout,))
         self.act, self.residual, self.D, self.H = act, residual, D, H
+        self.norm, self.dropout, self.eps = norm, dropout, eps
 
         def param(*shape, std=0.0):
             p = torch.nn.Parameter(torch.zeros(*shape, device=device, dtype=dtype))
@@ -525,6 +563,20 @@ class GatedFFN(torch.nn.Module):
         self.Wg, self.Wu = param(D, H, std=D ** -0.5), param(D, H, std=D ** -0.5)
         self.Wd = param(H, D, std=H ** -0.5)
         self.bg, self.bu, self.bd = (param(H), param(H), param(D)) if bias else (None, None, None)
+        self.norm_weight = self.norm_bias = None
+        if norm:
+            self.norm_weight, self.norm_bias = torch.nn.Parameter(torch.ones(D, device=device, dtype=dtype)), param(D)
+
+    def __setstate__(self, state):
+        # modules pickled before there was a norm and a dropout have neither
+        for name, value in (("norm", False), ("dropout", 0.0), ("eps", 1e-5), ("norm_weight", None), ("norm_bias", None)):
+            if name not in state and name not in state.get("_parameters", {}):
+                state[name] = value
+        super().__setstate__(state)
+
+    def quantized(self) -> "QuantizedGatedFFN":
+        """This block with its weights as they are now in 8 bits, for inference."""
+        return QuantizedGatedFFN(self)
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         shape = x.shape
@@ -533,6 +585,8 @@ class GatedFFN(torch.nn.Module):
         x2 = _rows16(x.reshape(-1, self.D))
         Wg, Wu, Wd = _rows16(self.Wg), _rows16(self.Wu), _rows16(self.Wd)
         bg, bu, bd = _vec16(self.bg), _vec16(self.bu), _vec16(self.bd)
+        nw, nb = _vec16(self.norm_weight), _vec16(self.norm_bias)
+        p = self.dropout if self.training else 0.0
         if torch.is_grad_enabled() and (x.requires_grad or any(p.requires_grad for p in self.parameters())):
             leaves = (x, *self.parameters())
             graph = None
@@ -540,9 +594,51 @@ class GatedFFN(torch.nn.Module):
                 _EagerGraph.refuse_capture(leaves)
             elif torch.cuda.current_stream(x.device) == torch.cuda.default_stream(x.device):
                 graph = _EagerGraph(leaves)
-            y = _GatedFFNFunction.apply(graph, x2, self.act, self.residual, Wg, Wu, Wd, bg, bu, bd)
+            seed = _draw_seed(x2.device) if p > 0 else None
+            y = _GatedFFNFunction.apply(graph, x2, self.act, self.residual, self.norm, self.eps, p, seed, Wg, Wu, Wd,
+                                        bg, bu, bd, nw, nb)
         else:
-            _refuse_recorded((x2, Wg, Wu, Wd, bg, bu, bd))
-            h = gated_gemm(x2, Wg, Wu, bg, bu, act=self.act)
-            y = gemm_residual(h, Wd, x2 if self.residual else None, bd)
+            _refuse_recorded((x2, Wg, Wu, Wd, bg, bu, bd, nw, nb))
+            n = layer_norm(x2, nw, nb, self.eps) if self.norm else x2
+            h = gated_gemm(n, Wg, Wu, bg, bu, act=self.act)
+            y = _down(h, Wd, bd, x2 if self.residual else None, p, _draw_seed(x2.device) if p > 0 else None)
+        return y.reshape(shape)
+
+
+class QuantizedGatedFFN(torch.nn.Module):
+    """A :class:`GatedFFN` for inference with its weights in 8 bits, one scale per
+    channel, and the tokens quantised in front of each product, one scale per token.
+
+    Made by :meth:`GatedFFN.quantized`.  x is of the block's type; nothing
+    depends on the other tokens of a call.  There is no gradient and no dropout.
+    """
+
+    def __init__(self, block: GatedFFN):
+        super().__init__()
+        self.act, self.residual, self.norm, self.eps = block.act, block.residual, block.norm, block.eps
+        self.D, self.H, self.dtype = block.D, block.H, block.Wg.dtype
+        with torch.no_grad():
+            for name in ("Wg", "Wu", "Wd"):
+                q, scale = quantize_columns(_rows16(getattr(block, name).detach()))
+                self.register_buffer(name, q)
+                self.register_buffer(name + "_scale", scale)
+            for name in ("bg", "bu", "bd", "norm_weight", "norm_bias"):
+                t = getattr(block, name)
+                self.register_buffer(name, None if t is None else t.detach().float().clone())
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        shape = x.shape
+        if not shape or shape[-1] != self.D or x.dtype is not self.dtype:
+            raise ValueError("x must be [..., %d] of %s, not %s of %s" % (self.D, self.dtype, tuple(shape), x.dtype))
+        if torch.is_grad_enabled() and x.requires_grad:
+            raise RuntimeError("QuantizedGatedFFN has no gradient")
+        x2 = _rows16(x.reshape(-1, self.D))
+        _refuse_recorded((x2,), "QuantizedGatedFFN", "QuantizedGatedFFN cannot be traced")
+        n = layer_norm(x2, self.norm_weight, self.norm_bias, self.eps) if self.norm else x2
+        q, s = quantize_rows(n)
+        h = gated_gemm_int8(q, _rows16(self.Wg), _rows16(self.Wu), s, self.Wg_scale, self.Wu_scale, self.bg, self.bu,
+                            act=self.act, out_dtype=self.dtype)
+        q, s = quantize_rows(h)
+        y = gemm_int8(q, _rows16(self.Wd), s, self.Wd_scale, self.bd, x2 if self.residual else None,
+                      out_dtype=self.dtype)
         return y.reshape(shape)
