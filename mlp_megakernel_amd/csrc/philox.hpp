@@ -31,7 +31,8 @@ struct DropKey {
   uint32_t k0, k1, o0, o1, last;
   float scale;
 };
-__device__ __forceinline__ DropKey drop_key(const Drop& d) {
+template <typename D>  // Drop, in either address space
+__device__ __forceinline__ DropKey drop_key(const D& d) {
   uint64_t seed = d.seed, offset = d.offset;
   if (d.device_seed) {
     seed = d.device_seed[0];

@@ -129,54 +129,76 @@ __global__ __launch_bounds__(1024) void quant_long_kernel(QuantParams p) {
   if (threadIdx.x == 0) p.scale[row] = s.scale;
 }
 
-// Columns: 64 of them per workgroup, which reads them twice (once for the largest
-// magnitude, once for the values) and turns 64 x 64 blocks over in LDS, so that rows of
-// Q are written in whole 64-byte pieces.  Weights go through it once.
+// Columns, in four small launches: largest magnitudes set to 0; their maximum over
+// ranges of rows, kept as integers in the place of the scales (an integer maximum is
+// the same in any order); the values, turned over 64 x 64 at a time in LDS so that rows
+// of Q are written in whole 64-byte pieces; and the scales.  Weights go through it once.
+__global__ __launch_bounds__(256) void columns_zero_kernel(QuantParams p) {
+  const int n = (int)blockIdx.x * 256 + (int)threadIdx.x;
+  if (n < p.N) ((uint32_t*)p.scale)[n] = 0u;
+}
+
+constexpr int kTopRows = 512;  // rows of a range
 template <typename T>
-__global__ __launch_bounds__(1024) void quant_columns_kernel(QuantParams p) {
-  __shared__ uint32_t tops[16][64];
-  __shared__ Scale scales[64];
-  __shared__ int8_t block[64][64 + 4];
+__global__ __launch_bounds__(256) void columns_top_kernel(QuantParams p, int col_blocks) {
+  __shared__ uint32_t tops[4][64];
   const int c = threadIdx.x & 63, r = threadIdx.x >> 6;
-  const int n0 = (int)blockIdx.x * 64, n = n0 + c;
-  const T* x = (const T*)p.X + n;
-  const bool in = n < p.N;
+  const int n = (int)(blockIdx.x % col_blocks) * 64 + c;
+  const int64_t m0 = (int64_t)(blockIdx.x / col_blocks) * kTopRows;
+  const int rows = (int)min((int64_t)kTopRows, (int64_t)p.M - m0);
   uint32_t top = 0;
-  for (int m = r; m < p.M; m += 64) {
+  if (n < p.N) {
+    const T* x = (const T*)p.X + m0 * p.ldx + n;
+    for (int m = r; m < rows; m += 32) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (in && m + 16 * u < p.M) top = max(top, magnitude((float)x[(int64_t)(m + 16 * u) * p.ldx]));
+      for (int u = 0; u < 8; ++u)
+        if (m + 4 * u < rows) top = max(top, magnitude((float)x[(int64_t)(m + 4 * u) * p.ldx]));
+    }
   }
   tops[r][c] = top;
   __syncthreads();
-  if (r == 0) {
+  if (r == 0 && n < p.N) {
 #pragma unroll
-    for (int i = 1; i < 16; ++i) top = max(top, tops[i][c]);
-    scales[c] = scale_of(top);
-    if (in) p.scale[n] = scales[c].scale;
+    for (int i = 1; i < 4; ++i) top = max(top, tops[i][c]);
+    atomicMax((uint32_t*)p.scale + n, top);
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void columns_turn_kernel(QuantParams p, int col_blocks) {
+  __shared__ int8_t block[64][64 + 4];
+  const int c = threadIdx.x & 63, r = threadIdx.x >> 6;
+  const int n0 = (int)(blockIdx.x % col_blocks) * 64, n = n0 + c;
+  const int64_t m0 = (int64_t)(blockIdx.x / col_blocks) * 64;
+  const int rows = (int)min((int64_t)64, (int64_t)p.M - m0);
+  if (n < p.N) {
+    const Scale s = scale_of(((const uint32_t*)p.scale)[n]);
+    const T* x = (const T*)p.X + m0 * p.ldx + n;
+#pragma unroll
+    for (int u = 0; u < 16; ++u) {
+      const int m = r + 4 * u;
+      if (m < rows) block[c][m] = (int8_t)quant((float)x[(int64_t)m * p.ldx], s);
+    }
   }
   __syncthreads();
-  const Scale s = scales[c];
-  for (int m0 = 0; m0 < p.M; m0 += 64) {
+  // 16 threads of 4 bytes per row of Q
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int m = m0 + r + 16 * u;
-      block[c][r + 16 * u] = in && m < p.M ? (int8_t)quant((float)x[(int64_t)m * p.ldx], s) : (int8_t)0;
+  for (int u = 0; u < 4; ++u) {
+    const int row = (threadIdx.x >> 4) + 16 * u, k = (threadIdx.x & 15) * 4;
+    if (n0 + row >= p.N) continue;
+    int8_t* q = p.Q + (int64_t)(n0 + row) * p.ldq + m0 + k;
+    const int valid = rows - k;
+    if (valid >= 4) {
+      *(uint32_t*)q = *(const uint32_t*)&block[row][k];
+    } else {
+      for (int e = 0; e < valid; ++e) q[e] = block[row][k + e];
     }
-    __syncthreads();
-    // 16 threads of 4 bytes per row of Q
-    const int row = threadIdx.x >> 4, k = (threadIdx.x & 15) * 4;
-    if (n0 + row < p.N) {
-      int8_t* q = p.Q + (int64_t)(n0 + row) * p.ldq + m0 + k;
-      const int valid = p.M - m0 - k;
-      if (valid >= 4) {
-        *(uint32_t*)q = pack4(block[row][k], block[row][k + 1], block[row][k + 2], block[row][k + 3]);
-      } else {
-        for (int e = 0; e < valid; ++e) q[e] = block[row][k + e];
-      }
-    }
-    __syncthreads();
   }
+}
+
+__global__ __launch_bounds__(256) void columns_scale_kernel(QuantParams p) {
+  const int n = (int)blockIdx.x * 256 + (int)threadIdx.x;
+  if (n < p.N) p.scale[n] = scale_of(((const uint32_t*)p.scale)[n]).scale;
 }
 
 template <typename T>
@@ -205,7 +227,16 @@ hipError_t rows_typed(const QuantParams& p, hipStream_t stream) {
 
 template <typename T>
 hipError_t columns_typed(const QuantParams& p, hipStream_t stream) {
-  hipLaunchKernelGGL((quant_columns_kernel<T>), dim3((unsigned)((p.N + 63) / 64)), dim3(1024), 0, stream, p);
+  const int64_t col_blocks = ((int64_t)p.N + 63) / 64, ranges = ((int64_t)p.M + kTopRows - 1) / kTopRows;
+  const dim3 vec((unsigned)(((int64_t)p.N + 255) / 256));
+  hipLaunchKernelGGL(columns_zero_kernel, vec, dim3(256), 0, stream, p);
+  if (p.M > 0) {
+    hipLaunchKernelGGL((columns_top_kernel<T>), dim3((unsigned)(col_blocks * ranges)), dim3(256), 0, stream, p,
+                       (int)col_blocks);
+    hipLaunchKernelGGL((columns_turn_kernel<T>), dim3((unsigned)(col_blocks * (((int64_t)p.M + 63) / 64))), dim3(256),
+                       0, stream, p, (int)col_blocks);
+  }
+  hipLaunchKernelGGL(columns_scale_kernel, vec, dim3(256), 0, stream, p);
   return hipGetLastError();
 }
 

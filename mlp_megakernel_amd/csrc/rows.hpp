@@ -83,6 +83,18 @@ struct Row {
   }
 };
 
+// A launch's arguments in the kernel-argument segment, behind an opaque copy of the
+// pointer: each place loads what it needs (a scalar load that the cache serves)
+// instead of all of it living in scalar registers, whose spills a loop would read
+// back by vector instructions.
+template <typename P>
+using ArgsOf = const __attribute__((address_space(4))) P*;
+template <typename P>
+__device__ __forceinline__ ArgsOf<P> again(ArgsOf<P> k) {
+  asm volatile("" : "+s"(k));
+  return k;
+}
+
 // A vector of N values of a type that the launch names (a uniform branch).
 template <typename T>
 __device__ __forceinline__ void read_vec(const void* v, bool f32, int n, int N, float (&w)[8]) {
