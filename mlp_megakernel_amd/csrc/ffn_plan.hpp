@@ -48,6 +48,22 @@ static const TileShape kGated[kShapes] = {
     {224, 128, 1, {1290}, 4000, 5000}, {192, 128, 1, {1180}, 4000, 5000},     {160, 128, 1, {1010}, 4000, 5000},
     {64, 64, 0, {0}, 0, 0},            {128, 64, 0, {0}, 0, 0}};
 
+// The same for 8-bit operands, whose step of 128 values has the bytes of a 16-bit step
+// of 64 but both sides along the contraction, so no transposing reads: the smaller
+// shapes' steps are shorter.  Beside twice the rate the end of a tile weighs more:
+// reading a residual and writing the results of one round of 256 x 256 tiles takes 20
+// us.  Measured at K = 4096 to 16384.
+static const TileShape kPlain8[kShapes] = {
+    {256, 256, 1, {1500}, 4000, 18000},            {128, 128, 2, {690, 900}, 4000, 9000},
+    {64, 64, 4, {425, 450, 515, 650}, 3000, 5000}, {224, 256, 1, {1280}, 4000, 14500},
+    {192, 256, 1, {1140}, 4000, 13500},            {160, 256, 1, {1030}, 4000, 11500},
+    {64, 64, 3, {290, 360, 515}, 3000, 5000},
+    {128, 128, 1, {515}, 4000, 8000}};
+static const TileShape kGated8[kShapes] = {
+    {256, 128, 1, {1450}, 4000, 9000}, {128, 64, 2, {710, 930}, 3000, 5500}, {64, 64, 3, {550, 585, 850}, 3000, 3500},
+    {224, 128, 1, {1330}, 4000, 6500}, {192, 128, 1, {1190}, 4000, 6000},    {160, 128, 1, {1005}, 4000, 6500},
+    {64, 64, 0, {0}, 0, 0},            {128, 64, 0, {0}, 0, 0}};
+
 // The plan with the smallest estimated time.  A launch is `units` workgroup
 // tiles (tiles x splits), run in rounds of what the compute units hold.  A split
 // product (128 x 128 or 64 x 64 tiles) writes and reads its fp32 partial results
@@ -55,12 +71,14 @@ static const TileShape kGated[kShapes] = {
 // operands from memory takes its time too: 4.5 TB/s with three or more tiles on
 // each compute unit, 4.0 and 3.0 with two and one, in proportion below.  `rows`:
 // the m side lies along the contraction, every shape may be used.
-TilePlan plan_tiles(int64_t m, int64_t n, bool gated, int batch, int64_t ksteps, bool rows, int num_cus) {
+TilePlan plan_tiles(int64_t m, int64_t n, bool gated, int batch, int64_t ksteps, bool rows, int num_cus,
+                    const TileShape* shapes = nullptr) {
+  if (!shapes) shapes = gated ? kGated : kPlain;
   static const int ranges[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
   const double operand_bytes = (double)ksteps * 128.0 * ((double)m + (double)n * (gated ? 2 : batch));
   TilePlan best{kShape64, 1, 1e300};
   for (int v = 1; v <= kShapes; ++v) {
-    const TileShape& s = gated ? kGated[v - 1] : kPlain[v - 1];
+    const TileShape& s = shapes[v - 1];
     if (s.slots == 0 || (!rows && (v == kShape224 || v == kShape192 || v == kShape160))) continue;
     const int64_t tiles = ((m + s.bm - 1) / s.bm) * ((n + s.bn - 1) / s.bn) * batch;
     for (int splits : ranges) {
@@ -120,15 +138,16 @@ ForwardPlan plan_forward(int64_t m, int64_t n, int64_t k, bool gated, int num_cu
   return f;
 }
 
-// The plan of an 8-bit product: the few-row kernel or tiles, whose K steps hold 128
-// values (the bytes and the time of a 16-bit step of 64).
+// The plan of an 8-bit product: the few-row kernel up to 64 rows (where tiles come
+// nearest, gated 64 x 16384 x 4096, 37.6 us against 39; plain 64 x 1024 x 2731 6.2 against
+// 10), tiles above.
 struct Int8Plan {
   bool few;
   TilePlan tiles;
 };
 Int8Plan plan_int8(int64_t m, int64_t n, int64_t k, bool gated, int num_cus) {
-  Int8Plan f{false, plan_tiles(m, n, gated, 1, (k + 127) / 128, true, num_cus)};
-  f.few = m <= 64;
+  Int8Plan f{m <= 64, {0, 1, 0.0}};
+  if (!f.few) f.tiles = plan_tiles(m, n, gated, 1, (k + 127) / 128, true, num_cus, gated ? kGated8 : kPlain8);
   return f;
 }
 

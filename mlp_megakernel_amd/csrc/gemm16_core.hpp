@@ -190,6 +190,20 @@ __device__ __forceinline__ i16x8 read_frag(const T* t, int ks, int x0, int i, in
   }
 }
 
+// tile_coords for any number of tiles: XCD x takes every eighth workgroup from x on,
+// one run of total / 8 neighbouring tiles, or one more where total mod 8 > x.
+__device__ __forceinline__ void tile_coords_any(int bid, int tiles_m, int tiles_n, int group_m, int& tm, int& tn) {
+  const int total = tiles_m * tiles_n, x = bid & 7;
+  const int t = x * (total >> 3) + min(x, total & 7) + (bid >> 3);
+  const int per_group = group_m * tiles_n;
+  const int g = t / per_group;
+  const int first_m = g * group_m;
+  const int gm = tiles_m - first_m < group_m ? tiles_m - first_m : group_m;
+  const int r = t - g * per_group;
+  tm = first_m + r % gm;
+  tn = r / gm;
+}
+
 // The launch's arguments in the kernel-argument segment.  Code outside the K
 // loop reads them through fresh(): an opaque copy of the pointer, so that each
 // place loads what it needs instead of the whole struct living in scalar
@@ -207,6 +221,7 @@ struct TileAt {
   int pair;     // product of a batch of two
   int split;
   int s0, s1;   // range of K steps over all segments
+  int turn;     // the step of the range that the tile begins with (TURN)
 };
 struct Range1 {
   int s, n;  // first K step and number of steps in one segment
@@ -224,6 +239,12 @@ struct Tile {
   static constexpr int RA = CopyRows<LA, G::BM>::N, RB = CopyRows<LB, G::SUBN>::N;
   static constexpr int V = PerElement<T>::N;
   static_assert(V == 1 || (LA == LAY_K && LB == LAY_K), "pairs lie along the contraction");
+  // The int32 sums do not mind the order of the steps: the XCDs begin at different
+  // ones, so that they ask different channels of the memory (8192 x 4096 x 16384 459 ->
+  // 454 us, at a pitch of 16400 554 -> 510, gated 777 x 16384 x 4096 117 -> 111).  The tiles of
+  // four waves are better off when they read the same lines at the same time (400 x 4096 x
+  // 16384 53 -> 59).
+  static constexpr bool TURN = V == 2 && G::NW == 8;
   static_assert(SEGS == 1 || G::NSUB == 1, "segments of a gated product are not implemented");
 
   // What the K loop needs of the tile, in scalar registers: the matrices at
@@ -638,13 +659,17 @@ struct Tile {
     const int64_t tiles = (int64_t)p->tiles_m * tn_all;
     at.split = (int)(v / tiles);
     int tm, tn;
-    tile_coords((int)(v - at.split * tiles), p->tiles_m, tn_all, p->group_m, tm, tn);
+    if constexpr (V == 2)
+      tile_coords_any((int)(v - at.split * tiles), p->tiles_m, tn_all, p->group_m, tm, tn);
+    else
+      tile_coords((int)(v - at.split * tiles), p->tiles_m, tn_all, p->group_m, tm, tn);
     at.pair = tn >= p->tiles_n ? 1 : 0;
     at.m0 = tm * G::BM;
     at.n0 = (tn - at.pair * p->tiles_n) * G::ON;
     const int64_t total = (int64_t)((p->K + BK * V - 1) / (BK * V)) * SEGS;
     at.s0 = (int)(total * at.split / p->splits);
     at.s1 = (int)(total * (at.split + 1) / p->splits);
+    at.turn = TURN ? ((int)(v & 7) * (at.s1 - at.s0)) >> 3 : 0;
     return at;
   }
   // The part of the tile's K steps that lies in a segment.
@@ -655,6 +680,15 @@ struct Tile {
     return Range1{lo, max(hi - lo, 0)};
   }
 
+  // The i-th K step of a tile.
+  static __device__ __forceinline__ int step_no(const TileAt& at, const Range1& r, int i) {
+    if constexpr (TURN) {
+      i += at.turn;
+      if (i >= r.n) i -= r.n;
+    }
+    return r.s + i;
+  }
+
   static __device__ __forceinline__ void run(Args k, T* lds) {
     const Args p = fresh(k);
     auto sa = [&](int i) { return lds + i * G::STAGE_A; };
@@ -662,7 +696,7 @@ struct Tile {
     auto fill_first = [&](const TileAt& at, int seg, const Hot& h, const Range1& r, const Pats& pt, int wu, int lane) {
 #pragma unroll
       for (int i = 0; i < G::NS; ++i)
-        if (i < r.n) fill(k, at, seg, h, pt, r.s + i, (uint32_t)i, sa(i), sb(i), wu, lane);
+        if (i < r.n) fill(k, at, seg, h, pt, step_no(at, r, i), (uint32_t)i, sa(i), sb(i), wu, lane);
     };
     const int64_t total = (int64_t)p->tiles_m * p->tiles_n * p->batch * p->splits;
     int64_t v = blockIdx.x;
@@ -720,7 +754,7 @@ struct Tile {
               if (i + 1 < r.n) {
                 // the copies of step i + 2 may stay in flight, if that step has
                 // any
-                if (G::NS > 2 && i + 2 < r.n && ((r.s + i + 2) * BK + BK) * V <= h.K)
+                if (G::NS > 2 && i + 2 < r.n && (step_no(at, r, i + 2) * BK + BK) * V <= h.K)
                   wait_steps<G::NS - 2>();
                 else if (EPI != EPI_STORE || G::NS > 2 || i > 0)  // both of two stages have landed before step 0
                   wait_vmcnt0();
@@ -728,7 +762,7 @@ struct Tile {
               }
               bool cp = false;
               if (i + G::NS < r.n) {
-                st = step_at(h, r.s + i + G::NS);
+                st = step_at(h, step_no(at, r, i + G::NS));
                 cp = (st.k0 + BK) * V <= h.K;
                 if (!cp) tail(k, at, seg, st, sa(c), sb(c), wu, lane);
               }

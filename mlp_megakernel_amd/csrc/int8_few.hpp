@@ -2,12 +2,17 @@
 // the weights once.
 //
 // The weights lie channel by channel (N x K), so a fragment of the matrix
-// instruction is 16 consecutive bytes of a row in memory: no LDS, no transposing.
-// A workgroup owns 16 NT channels (of both matrices of a gated product) and
-// deals the K steps of 64 SL bytes to its waves in turn; a wave loads a step's fragments
-// straight into registers, one step ahead of the products, and never meets a barrier
-// until the end, where the waves' int32 sums meet in LDS.  Integer sums do not depend
-// on their order, so a row's result is the one that any other kernel gives.
+// instruction is 16 consecutive bytes of a row; but its lanes go over the rows
+// first, and loads into registers in that order look up one cache line per lane: 16
+// bytes a cycle and compute unit, weights and tokens together (64 x 4096 x 16384: 40
+// us).  So both go through LDS by direct copies of whole 128-byte lines (20 us; 1 x 16384
+// x 4096 gated 27.9, 4.8 TB/s; 1 x 2731 x 1001 4.0).
+// A workgroup owns 16 NT channels (of both matrices of a gated product) and deals
+// the K steps of 128 to its waves in turn; a wave streams its steps through a private
+// ring of D stages and never meets a barrier until the end: it waits for its own
+// oldest stage by the count of copies in flight, takes the fragments and refills the
+// slot.  At the end the waves' int32 sums meet in LDS; they do not depend on their
+// order, so a row's result is the one that any other kernel gives.
 // Rows past M and channels past N read as zero by the buffers' ranges; k past K
 // inside a row of X is masked, which settles it for the weights too.
 #pragma once
@@ -16,56 +21,77 @@
 namespace coalesce {
 namespace {
 
-// NB matrices, NT blocks of 16 channels of each, MT blocks of 16 rows, SL slices
-// of 64 k per step, NW waves.
-template <int NB_, int NT_, int MT_, int SL_, int NW_>
+// NB matrices, NT blocks of 16 channels of each, MH times 8 rows (1, 2, 4 or 8), NW
+// waves, D stages.
+template <int NB_, int NT_, int MH_, int NW_, int D_>
 struct Few8Geo {
-  static constexpr int NB = NB_, NT = NT_, MT = MT_, SL = SL_, NW = NW_, KB = NB * NT, STEP = 64 * SL;
-  static_assert(NW * KB * MT <= 144, "the sums exceed the LDS");
+  static constexpr int NB = NB_, NT = NT_, MH = MH_, MT = (MH + 1) / 2, NW = NW_, D = D_, KB = NB * NT;
+  static constexpr int C = 2 * KB + MH;  // 1 KB copies per stage: 8 rows of 128 bytes each
+  static constexpr int STAGE = C * 1024, RING = D * STAGE;
+  static constexpr int SUMS = NW * KB * MT * 1024;
+  static constexpr int LDS = NW * RING > SUMS ? NW * RING : SUMS;
+  static_assert(LDS <= 160 * 1024 && (D - 1) * C < 64, "few-row plan");
 };
 
-template <typename G>
-struct Few8Step {
-  u32x4 b[G::KB][G::SL], x[G::MT][G::SL];
-};
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
 
 template <typename TO, int EPI, typename G>
 __global__ __launch_bounds__(G::NW * 64) void few8_kernel(TileOp p) {
-  constexpr int NB = G::NB, NT = G::NT, MT = G::MT, SL = G::SL, NW = G::NW, KB = G::KB;
-  __shared__ __attribute__((aligned(16))) i32x4 sums[NW][MT][KB][64];
+  constexpr int NB = G::NB, NT = G::NT, MT = G::MT, NW = G::NW, D = G::D, KB = G::KB;
+  __shared__ __attribute__((aligned(1024))) char few_lds[G::LDS];
   const int lane = threadIdx.x & 63, q = lane & 15, g = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n0 = (int)blockIdx.x * 16 * NT;
-  const int steps = (p.K + G::STEP - 1) / G::STEP;
+  const int steps = (p.K + 127) / 128;
   const uint32_t row_bytes = (uint32_t)((p.K + 15) & ~15);
   const uint32_t lda = (uint32_t)p.lda * 2u, ldb = (uint32_t)p.ldb * 2u;  // pitches count pairs
+  char* const ring = few_lds + w * G::RING;
+  const uint32_t ring_at = lds_addr(ring);
 
   // 16 rows of a matrix from row r0 on, as far as it has them.
   auto rows16 = [&](const void* base, uint32_t ld, int64_t r0, int all) {
     const int left = (int)min((int64_t)16, (int64_t)all - r0);
-    return __builtin_amdgcn_make_buffer_rsrc((void*)((const char*)base + (left > 0 ? r0 : 0) * (int64_t)ld), 0,
-                                             left > 0 ? (uint32_t)(left - 1) * ld + row_bytes : 0u, 0x00020000);
+    const uint64_t v = (uint64_t)(uintptr_t)((const char*)base + (left > 0 ? r0 : 0) * (int64_t)ld);
+    return (u32x4){(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v),
+                   (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32)) & 0xffffu,
+                   (uint32_t)__builtin_amdgcn_readfirstlane((int)(left > 0 ? (uint32_t)(left - 1) * ld + row_bytes : 0u)),
+                   0x00020000u};
   };
-  __amdgpu_buffer_rsrc_t rb[KB], rx[MT];
+  u32x4 rb[KB], rx[MT];
 #pragma unroll
   for (int i = 0; i < KB; ++i) rb[i] = rows16(p.b[i / NT], ldb, n0 + 16 * (i % NT), p.N);
 #pragma unroll
   for (int m = 0; m < MT; ++m) rx[m] = rows16(p.a[0], lda, 16 * m, p.M);
-  const int ob = (int)((uint32_t)q * ldb) + 16 * g, ox = (int)((uint32_t)q * lda) + 16 * g;
-
-  // (the whole offset per lane: a range is checked against that)
-  auto load = [&](int s, Few8Step<G>& f) {
-    const int kb = ob + s * G::STEP, kx = ox + s * G::STEP;
+  // lane offsets of the two copies of 16 rows: eight lanes per row, the 16-byte pieces
+  // in the tiles' order (swzA)
+  uint32_t ob[2], ox[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int row = 8 * h + (lane >> 3);
+    const uint32_t at = (uint32_t)((lane & 7) ^ swzA(row)) * 16u;
+    ob[h] = (uint32_t)row * ldb + at;
+    ox[h] = (uint32_t)row * lda + at;
+  }
+  // K step s into ring slot `slot`; a step past the last lies outside every range and
+  // reads nothing, which keeps the count of copies per step the same.
+  auto issue = [&](int s, int slot) {
+    const uint32_t shift = s < steps ? (uint32_t)s * 128u : 1u << 30;
+    uint32_t at = ring_at + (uint32_t)(slot * G::STAGE);
 #pragma unroll
     for (int i = 0; i < KB; ++i)
 #pragma unroll
-      for (int j = 0; j < SL; ++j)
-        f.b[i][j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rb[i], kb + 64 * j, 0, 0));
+      for (int h = 0; h < 2; ++h) {
+        dma16_buf(rb[i], ob[h], shift, at);
+        at += 1024u;
+      }
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int j = 0; j < SL; ++j)
-        f.x[m][j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx[m], kx + 64 * j, 0, 0));
+    for (int h = 0; h < G::MH; ++h) {
+      dma16_buf(rx[h / 2], ox[h % 2], shift, at);
+      at += 1024u;
+    }
   };
 
   i32x4 acc[KB][MT];
@@ -73,34 +99,49 @@ __global__ __launch_bounds__(G::NW * 64) void few8_kernel(TileOp p) {
   for (int i = 0; i < KB; ++i)
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[i][m] = (i32x4){0, 0, 0, 0};
-  Few8Step<G> f, nx;
-  if (w < steps) load(w, f);
-  for (int s = w; s < steps; s += NW) {
-    if (s + NW < steps) load(s + NW, nx);
-    if ((s + 1) * G::STEP > p.K) {
 #pragma unroll
-      for (int j = 0; j < SL; ++j) {
-        const int left = p.K - s * G::STEP - 64 * j - 16 * g;  // valid bytes of this lane's sixteen
+  for (int d = 0; d < D; ++d) issue(w + d * NW, d);
+  int slot = 0;
+  for (int s = w; s < steps; s += NW) {
+    wait_copies<(D - 1) * G::C>();
+    const char* st = ring + slot * G::STAGE;
+    const int xr = G::MH == 1 ? q & 7 : q;  // (up to 8 rows: the other 8 results are no one's)
+    i32x4 fb[KB][2], fx[MT][2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int cb = q * 128 + ((4 * j + g) ^ swzA(q)) * 16, cx = xr * 128 + ((4 * j + g) ^ swzA(xr)) * 16;
+#pragma unroll
+      for (int i = 0; i < KB; ++i) fb[i][j] = *(const i32x4*)(st + i * 2048 + cb);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) fx[m][j] = *(const i32x4*)(st + (KB + m) * 2048 + cx);
+    }
+    if ((s + 1) * 128 > p.K) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int left = p.K - s * 128 - 64 * j - 16 * g;  // valid bytes of this lane's sixteen
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
           const int n = left - 4 * d;
-          const uint32_t mask = n >= 4 ? 0xffffffffu : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
+          const int mask = n >= 4 ? -1 : n <= 0 ? 0 : (int)((1u << (8 * n)) - 1u);
 #pragma unroll
-          for (int m = 0; m < MT; ++m) f.x[m][j][d] &= mask;
+          for (int m = 0; m < MT; ++m) fx[m][j][d] &= mask;
         }
       }
     }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slot is read: refill it
+    issue(s + D * NW, slot);
+    slot = slot + 1 == D ? 0 : slot + 1;
 #pragma unroll
-    for (int j = 0; j < SL; ++j)
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int i = 0; i < KB; ++i)
 #pragma unroll
         for (int m = 0; m < MT; ++m)
-          acc[i][m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, f.b[i][j]),
-                                                            __builtin_bit_cast(i32x4, f.x[m][j]), acc[i][m], 0, 0, 0);
-    f = nx;
+          acc[i][m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[i][j], fx[m][j], acc[i][m], 0, 0, 0);
   }
-
+  wait_copies<0>();  // no copy may land after the LDS changes hands
+  __syncthreads();
+  i32x4(*const sums)[MT][KB][64] = (i32x4(*)[MT][KB][64])few_lds;
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -141,11 +182,20 @@ hipError_t few8_launch(const TileOp& o, hipStream_t stream) {
 }
 
 template <typename TO, int EPI>
-hipError_t launch_few8(const TileOp& o, hipStream_t stream) {
+hipError_t launch_few8(const TileOp& o, hipStream_t stream, int num_cus) {
   constexpr int NB = EPI == EPI_INT8_GATED ? 2 : 1;
-  if (o.M <= 16) return few8_launch<TO, EPI, Few8Geo<NB, 1, 1, 4, 8>>(o, stream);
-  if (o.M <= 32) return few8_launch<TO, EPI, Few8Geo<NB, 1, 2, 4, 8>>(o, stream);
-  return few8_launch<TO, EPI, Few8Geo<NB, 1, 4, 2, 8>>(o, stream);
+  if (o.M <= 8) {
+    // With at most one strip per compute unit eight waves draw more than four (plain,
+    // 1 x 4096 x 16384: 15.0 us, 15.6), with more the smaller workgroups overlap (gated,
+    // 1 x 16384 x 4096: 30.3, 27.9).
+    if (NB == 1 && o.N <= 16 * num_cus) return few8_launch<TO, EPI, Few8Geo<NB, 1, 1, 8, 3>>(o, stream);
+    return few8_launch<TO, EPI, Few8Geo<NB, 1, 1, 4, 3>>(o, stream);
+  }
+  if (o.M <= 16) return few8_launch<TO, EPI, Few8Geo<NB, 1, 2, 4, 2>>(o, stream);
+  if (o.M <= 32) return few8_launch<TO, EPI, Few8Geo<NB, 1, 4, 4, 2>>(o, stream);
+  // Two blocks of channels per wave halve what a gated product draws of X (64 x 16384 x
+  // 4096: 37.6 us, 43.6 with one).
+  return few8_launch<TO, EPI, Few8Geo<NB, NB, 8, 4, 2>>(o, stream);
 }
 
 }  // namespace
