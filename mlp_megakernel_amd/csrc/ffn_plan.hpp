@@ -139,7 +139,7 @@ ForwardPlan plan_forward(int64_t m, int64_t n, int64_t k, bool gated, int num_cu
 }
 
 // The plan of an 8-bit product: the few-row kernel up to 64 rows (where tiles come
-// nearest, gated 64 x 16384 x 4096, 37.6 us against 39; plain 64 x 1024 x 2731 6.2 against
+// nearest, gated 64 x 16384 x 4096, 36 us against 39; plain 64 x 1024 x 2731 6.2 against
 // 10), tiles above.
 struct Int8Plan {
   bool few;

@@ -6,7 +6,7 @@
 // first, and loads into registers in that order look up one cache line per lane: 16
 // bytes a cycle and compute unit, weights and tokens together (64 x 4096 x 16384: 40
 // us).  So both go through LDS by direct copies of whole 128-byte lines (20 us; 1 x 16384
-// x 4096 gated 27.9, 4.8 TB/s; 1 x 2731 x 1001 4.0).
+// x 4096 gated 25.1, 5.3 TB/s; 1 x 2731 x 1001 3.3).
 // A workgroup owns 16 NT channels (of both matrices of a gated product) and deals
 // the K steps of 128 to its waves in turn; a wave streams its steps through a private
 // ring of D stages and never meets a barrier until the end: it waits for its own
@@ -20,6 +20,16 @@
 
 namespace coalesce {
 namespace {
+
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+// dma16_buf for bytes that no other workgroup reads: the caches need not keep them.
+__device__ __forceinline__ void dma16_once(u32x4 rsrc, uint32_t off, uint32_t shift, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %3 offen nt lds" ::"v"(off), "s"(rsrc),
+               "s"(lds), "s"(shift)
+               : "memory", "m0");
+}
+#pragma clang diagnostic pop
 
 // NB matrices, NT blocks of 16 channels of each, MH times 8 rows (1, 2, 4 or 8), NW
 // waves, D stages.
@@ -38,7 +48,8 @@ __device__ __forceinline__ void wait_copies() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-template <typename TO, int EPI, typename G>
+// ONCE: the weights go past the caches.
+template <typename TO, int EPI, typename G, bool ONCE>
 __global__ __launch_bounds__(G::NW * 64) void few8_kernel(TileOp p) {
   constexpr int NB = G::NB, NT = G::NT, MT = G::MT, NW = G::NW, D = G::D, KB = G::KB;
   __shared__ __attribute__((aligned(1024))) char few_lds[G::LDS];
@@ -84,7 +95,10 @@ __global__ __launch_bounds__(G::NW * 64) void few8_kernel(TileOp p) {
     for (int i = 0; i < KB; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        dma16_buf(rb[i], ob[h], shift, at);
+        if constexpr (ONCE)
+          dma16_once(rb[i], ob[h], shift, at);
+        else
+          dma16_buf(rb[i], ob[h], shift, at);
         at += 1024u;
       }
 #pragma unroll
@@ -174,9 +188,9 @@ __global__ __launch_bounds__(G::NW * 64) void few8_kernel(TileOp p) {
   }
 }
 
-template <typename TO, int EPI, typename G>
+template <typename TO, int EPI, typename G, bool ONCE = false>
 hipError_t few8_launch(const TileOp& o, hipStream_t stream) {
-  hipLaunchKernelGGL((few8_kernel<TO, EPI, G>), dim3((unsigned)((o.N + 16 * G::NT - 1) / (16 * G::NT))),
+  hipLaunchKernelGGL((few8_kernel<TO, EPI, G, ONCE>), dim3((unsigned)((o.N + 16 * G::NT - 1) / (16 * G::NT))),
                      dim3(G::NW * 64), 0, stream, o);
   return hipGetLastError();
 }
@@ -184,18 +198,32 @@ hipError_t few8_launch(const TileOp& o, hipStream_t stream) {
 template <typename TO, int EPI>
 hipError_t launch_few8(const TileOp& o, hipStream_t stream, int num_cus) {
   constexpr int NB = EPI == EPI_INT8_GATED ? 2 : 1;
+  const bool one_round = o.N <= 16 * num_cus;  // of strips of 16 channels
+  // Weights that would fill a quarter of the memory's cache of 256 MB are not kept
+  // there (gated, 1 x 16384 x 4096 27.5 -> 25.1 us); smaller ones may still lie in it (1 x
+  // 5461 x 2048 7.6 us, 8.6 past it), and the X of more than 16 rows wants the caches too.
+  const bool once = (int64_t)NB * o.N * o.K >= (int64_t)64 << 20;
   if (o.M <= 8) {
-    // With at most one strip per compute unit eight waves draw more than four (plain,
-    // 1 x 4096 x 16384: 15.0 us, 15.6), with more the smaller workgroups overlap (gated,
-    // 1 x 16384 x 4096: 30.3, 27.9).
-    if (NB == 1 && o.N <= 16 * num_cus) return few8_launch<TO, EPI, Few8Geo<NB, 1, 1, 8, 3>>(o, stream);
+    // 160 KB of stages per compute unit, as one workgroup where there is one strip for
+    // each (plain, 1 x 4096 x 16384: 14.6 us, 15.1 with smaller ones), as two where
+    // strips follow each other (gated, 1 x 16384 x 4096: 25.1, 26.6 with four waves, 27.5
+    // with one workgroup); in between the smaller workgroups win (1 x 5461 x 2048 6.6,
+    // 6.9).
+    if (NB == 1 && one_round) return few8_launch<TO, EPI, Few8Geo<NB, 1, 1, 8, 3>>(o, stream);
+    if (NB == 2 && o.N > 32 * num_cus && once) return few8_launch<TO, EPI, Few8Geo<NB, 1, 1, 8, 2>, true>(o, stream);
+    if (once) return few8_launch<TO, EPI, Few8Geo<NB, 1, 1, 4, 3>, true>(o, stream);
     return few8_launch<TO, EPI, Few8Geo<NB, 1, 1, 4, 3>>(o, stream);
   }
-  if (o.M <= 16) return few8_launch<TO, EPI, Few8Geo<NB, 1, 2, 4, 2>>(o, stream);
+  if (o.M <= 16) {
+    if (once) return few8_launch<TO, EPI, Few8Geo<NB, 1, 2, 4, 2>, true>(o, stream);
+    return few8_launch<TO, EPI, Few8Geo<NB, 1, 2, 4, 2>>(o, stream);
+  }
   if (o.M <= 32) return few8_launch<TO, EPI, Few8Geo<NB, 1, 4, 4, 2>>(o, stream);
-  // Two blocks of channels per wave halve what a gated product draws of X (64 x 16384 x
-  // 4096: 37.6 us, 43.6 with one).
-  return few8_launch<TO, EPI, Few8Geo<NB, NB, 8, 4, 2>>(o, stream);
+  // Where strips follow each other two blocks of channels per wave halve what is drawn of
+  // X (64 x 16384 x 4096: gated 36 us, 43 with one, plain 20 and 24; but gated 64 x 1024 x
+  // 512 5.5 and 4.3).
+  if (one_round) return few8_launch<TO, EPI, Few8Geo<NB, 1, 8, 4, 2>>(o, stream);
+  return few8_launch<TO, EPI, Few8Geo<NB, 2, 8, 2 * NB, NB == 2 ? 2 : 3>>(o, stream);
 }
 
 }  // namespace
