@@ -64,7 +64,8 @@ coalesce_status check_int8(int64_t M, int64_t N, int64_t K, coalesce_dtype out, 
   if (!valid_ffn_act(act)) return fail(COALESCE_ERR_INVALID_ARGUMENT, "unknown activation %d", (int)act);
   const int64_t lim = kMaxExtent - 256;
   if (M > lim || N > lim) return fail(COALESCE_ERR_UNSUPPORTED, "extents must be below 2^31 - 256");
-  if (K > kMaxInt8K) return fail(COALESCE_ERR_UNSUPPORTED, "K above %lld may overflow the int32 sums", (long long)kMaxInt8K);
+  if (K > kMaxInt8K)
+    return fail(COALESCE_ERR_UNSUPPORTED, "K above %lld may overflow the int32 sums", (long long)kMaxInt8K);
   if (N && M > (int64_t(1) << 41) / N) return fail(COALESCE_ERR_UNSUPPORTED, "a product of two extents above 2^41");
   return COALESCE_OK;
 }
@@ -223,7 +224,8 @@ coalesce_status coalesce_layer_norm(const void* X, int64_t ldx, const void* R, i
   if (s != COALESCE_OK) return s;
   if ((s = check_types(dtype, stream_dtype)) != COALESCE_OK) return s;
   if ((s = check_types(dtype, weight_dtype)) != COALESCE_OK) return s;
-  if (!(eps >= 0.0) || std::isinf(eps)) return fail(COALESCE_ERR_INVALID_ARGUMENT, "eps must be a number of at least 0");
+  if (!(eps >= 0.0) || std::isinf(eps))
+    return fail(COALESCE_ERR_INVALID_ARGUMENT, "eps must be a number of at least 0");
   Drop drop{};
   if ((s = make_drop(p, seed, offset, device_seed, &drop)) != COALESCE_OK) return s;
   if (!R && (S || p != 0.0))

@@ -68,7 +68,7 @@ __global__ __launch_bounds__(G::NW * 64) void few8_kernel(TileOp p) {
     const uint64_t v = (uint64_t)(uintptr_t)((const char*)base + (left > 0 ? r0 : 0) * (int64_t)ld);
     return (u32x4){(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v),
                    (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32)) & 0xffffu,
-                   (uint32_t)__builtin_amdgcn_readfirstlane((int)(left > 0 ? (uint32_t)(left - 1) * ld + row_bytes : 0u)),
+                   left > 0 ? (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)(left - 1) * ld + row_bytes)) : 0u,
                    0x00020000u};
   };
   u32x4 rb[KB], rx[MT];

@@ -1,8 +1,12 @@
-// Lists of tensors as the C entry points take them: addresses, element counts
-// and types in host arrays, read and checked in one pass.  A Python extension
-// beside libcoalesce.so, which knows nothing of torch: in Python each of the ten
-// questions to ask of a gradient and its output takes some 80 ns, 170 us for a
-// list of 200, where the kernels take 20.
+// What the binding does for the C entry points in compiled code.  A Python extension
+// beside libcoalesce.so, which knows nothing of torch: in Python each question to ask of
+// a tensor takes some 80 ns.
+// Lists of tensors as the entry points take them: addresses, element counts and
+// types in host arrays, read and checked in one pass (170 us for a list of 200, where
+// the kernels take 20).
+// And the short way into the entry points whose kernels take 3 us: it reads the
+// operands, and where every one is as it should be makes the call.  Where one is
+// not it gives None, and the binding's own checks in Python say what is wrong.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -10,6 +14,8 @@
 #include <cstdint>
 #include <exception>
 #include <vector>
+
+#include "../../include/coalesce.h"
 
 namespace {
 
@@ -120,7 +126,183 @@ PyObject* grad_list(PyObject*, PyObject* args) {
   return Py_BuildValue("nlOOOOOOO", n, device, src.p, separate ? dst.p : src.p, numel.p, types.p, c.p, l.p, lo.p);
 }
 
+// ---- the short way ------------------------------------------------------------
+
+struct Mat {
+  void* p = nullptr;
+  int64_t ld = 0;
+};
+
+// What one call asks of its operands; `fine` falls with the first that is not so.
+struct Reader {
+  int64_t device;
+  bool fine = true;
+
+  const at::Tensor* tensor(PyObject* o) {
+    if (!THPVariable_Check(o)) return fine = false, nullptr;
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (!t.is_cuda() || t.layout() != at::kStrided || t.get_device() != device) return fine = false, nullptr;
+    return &t;
+  }
+  // A matrix of unit inner stride (a single row has the next multiple of 16 bytes for a pitch).
+  Mat mat(PyObject* o, int64_t rows, int64_t cols, at::ScalarType type, bool optional = false) {
+    if (optional && o == Py_None) return {};
+    const at::Tensor* t = tensor(o);
+    if (!t || t->dim() != 2 || t->scalar_type() != type || t->size(0) != rows || t->size(1) != cols ||
+        (cols > 1 && t->stride(1) != 1))
+      return fine = false, Mat{};
+    const int64_t per = 16 / (int64_t)t->element_size(), row = cols > per ? (cols + per - 1) / per * per : per;
+    return {t->data_ptr(), rows > 1 ? t->stride(0) : row};
+  }
+  void* vec(PyObject* o, int64_t n, at::ScalarType type, bool optional = false) {
+    if (optional && o == Py_None) return nullptr;
+    const at::Tensor* t = tensor(o);
+    if (!t || t->dim() != 1 || t->scalar_type() != type || t->size(0) != n || !t->is_contiguous())
+      return fine = false, nullptr;
+    return t->data_ptr();
+  }
+  at::ScalarType type(PyObject* o, at::ScalarType other) {
+    return o != Py_None && THPVariable_Check(o) ? THPVariable_Unpack(o).scalar_type() : other;
+  }
+};
+
+// The entry point at an address, and the call without the interpreter's lock.
+template <typename F, typename... A>
+PyObject* enter(PyObject* address, A... args) {
+  F* const f = reinterpret_cast<F*>(PyLong_AsVoidPtr(address));
+  if (!f) return nullptr;
+  coalesce_status s;
+  Py_BEGIN_ALLOW_THREADS
+  s = f(args...);
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong((long)s);
+}
+
+bool count(Py_ssize_t n, Py_ssize_t want) {
+  if (n != want) PyErr_Format(PyExc_TypeError, "%zd arguments, not %zd", n, want);
+  return n == want;
+}
+
+// The work of a short way: None where an operand is not as it should be, or where torch threw.
+template <typename W>
+PyObject* shortly(W work) {
+  try {
+    PyObject* r = work();
+    if (r || PyErr_Occurred()) return r;
+  } catch (const std::exception&) {
+  }
+  Py_RETURN_NONE;
+}
+
+// layer_norm(address, device, stream, x, residual, sum, weight, bias, out, mean, rstd, eps, p, seed, offset)
+PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 15)) return nullptr;
+  return shortly([&]() -> PyObject* {
+    Reader r{PyLong_AsLongLong(a[1])};
+    const at::Tensor *x = r.tensor(a[3]), *y = r.tensor(a[8]);
+    if (!r.fine || x->dim() != 2 || !PyLong_Check(a[13]) || !PyLong_Check(a[14])) return nullptr;
+    const bool add = a[4] != Py_None;
+    const int64_t M = x->size(0), N = x->size(1);
+    const at::ScalarType dt = y->scalar_type(), st = add ? r.type(a[4], dt) : x->scalar_type();
+    const at::ScalarType wt = r.type(a[6], r.type(a[7], dt));
+    if (code_of(dt) < 0 || (st != at::kFloat && st != dt) || (wt != at::kFloat && wt != dt)) return nullptr;
+    const Mat X = r.mat(a[3], M, N, add ? dt : st), R = r.mat(a[4], M, N, st, true), S = r.mat(a[5], M, N, st, true),
+              Y = r.mat(a[8], M, N, dt);
+    void *w = r.vec(a[6], N, wt, true), *b = r.vec(a[7], N, wt, true), *mean = r.vec(a[9], M, at::kFloat, true),
+         *rstd = r.vec(a[10], M, at::kFloat, true);
+    const double eps = PyFloat_AsDouble(a[11]), p = PyFloat_AsDouble(a[12]);
+    if (!r.fine || PyErr_Occurred()) return nullptr;
+    return enter<decltype(coalesce_layer_norm)>(
+        a[0], X.p, X.ld, R.p, R.ld, S.p, S.ld, w, b, Y.p, Y.ld, (float*)mean, (float*)rstd, M, N,
+        (coalesce_dtype)code_of(dt), (coalesce_dtype)code_of(st), (coalesce_dtype)code_of(wt), eps, p,
+        PyLong_AsUnsignedLongLongMask(a[13]), PyLong_AsUnsignedLongLongMask(a[14]), nullptr, PyLong_AsVoidPtr(a[2]));
+  });
+}
+
+// dropout(address, device, stream, x, residual, out, p, seed, offset)
+PyObject* dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 9)) return nullptr;
+  return shortly([&]() -> PyObject* {
+    Reader r{PyLong_AsLongLong(a[1])};
+    const at::Tensor *x = r.tensor(a[3]), *y = r.tensor(a[5]);
+    if (!r.fine || x->dim() != 2 || !PyLong_Check(a[7]) || !PyLong_Check(a[8])) return nullptr;
+    const int64_t M = x->size(0), N = x->size(1);
+    const at::ScalarType dt = x->scalar_type(), ot = y->scalar_type();
+    if (code_of(dt) < 0 || (ot != at::kFloat && ot != dt)) return nullptr;
+    const Mat X = r.mat(a[3], M, N, dt), R = r.mat(a[4], M, N, ot, true), Y = r.mat(a[5], M, N, ot);
+    const double p = PyFloat_AsDouble(a[6]);
+    if (!r.fine || PyErr_Occurred()) return nullptr;
+    return enter<decltype(coalesce_dropout)>(a[0], X.p, X.ld, R.p, R.ld, Y.p, Y.ld, M, N, (coalesce_dtype)code_of(dt),
+                                             (coalesce_dtype)code_of(ot), p, PyLong_AsUnsignedLongLongMask(a[7]),
+                                             PyLong_AsUnsignedLongLongMask(a[8]), nullptr, PyLong_AsVoidPtr(a[2]));
+  });
+}
+
+// quantize(address, device, stream, columns, x, out, scale)
+PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 7)) return nullptr;
+  return shortly([&]() -> PyObject* {
+    Reader r{PyLong_AsLongLong(a[1])};
+    const at::Tensor* x = r.tensor(a[4]);
+    if (!r.fine || x->dim() != 2 || code_of(x->scalar_type()) < 0) return nullptr;
+    const bool columns = a[3] == Py_True;
+    const int64_t M = x->size(0), N = x->size(1), rows = columns ? N : M, cols = columns ? M : N;
+    const Mat X = r.mat(a[4], M, N, x->scalar_type()), Q = r.mat(a[5], rows, cols, at::kChar);
+    void* scale = r.vec(a[6], rows, at::kFloat);
+    if (!r.fine) return nullptr;
+    return enter<decltype(coalesce_quantize_rows)>(a[0], X.p, X.ld, (int8_t*)Q.p, Q.ld, (float*)scale, M, N,
+                                                   (coalesce_dtype)code_of(x->scalar_type()), PyLong_AsVoidPtr(a[2]));
+  });
+}
+
+// gemm_int8(address, device, stream, A, B, a_scale, b_scale, bias, residual, out, act, workspace, its bytes)
+PyObject* gemm_int8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 13)) return nullptr;
+  return shortly([&]() -> PyObject* {
+    Reader r{PyLong_AsLongLong(a[1])};
+    const at::Tensor *A = r.tensor(a[3]), *B = r.tensor(a[4]), *y = r.tensor(a[9]);
+    if (!r.fine || A->dim() != 2 || B->dim() != 2 || code_of(y->scalar_type()) < 0) return nullptr;
+    const int64_t M = A->size(0), K = A->size(1), N = B->size(0);
+    const Mat a8 = r.mat(a[3], M, K, at::kChar), b8 = r.mat(a[4], N, K, at::kChar),
+              R = r.mat(a[8], M, N, y->scalar_type(), true), Y = r.mat(a[9], M, N, y->scalar_type());
+    void *sa = r.vec(a[5], M, at::kFloat), *sb = r.vec(a[6], N, at::kFloat), *bias = r.vec(a[7], N, at::kFloat, true);
+    if (!r.fine) return nullptr;
+    return enter<decltype(coalesce_gemm_int8)>(
+        a[0], (int8_t*)a8.p, a8.ld, (int8_t*)b8.p, b8.ld, (float*)sa, (float*)sb, (float*)bias, R.p, R.ld, Y.p, Y.ld, M,
+        N, K, (coalesce_dtype)code_of(y->scalar_type()), (coalesce_act)PyLong_AsLong(a[10]),
+        a[11] == Py_None ? nullptr : PyLong_AsVoidPtr(a[11]), PyLong_AsSize_t(a[12]), PyLong_AsVoidPtr(a[2]));
+  });
+}
+
+// gated_gemm_int8(address, device, stream, A, Bg, Bu, a_scale, bg_scale, bu_scale, bias_g, bias_u, out, act,
+//                 workspace, its bytes)
+PyObject* gated_gemm_int8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 15)) return nullptr;
+  return shortly([&]() -> PyObject* {
+    Reader r{PyLong_AsLongLong(a[1])};
+    const at::Tensor *A = r.tensor(a[3]), *B = r.tensor(a[4]), *y = r.tensor(a[11]);
+    if (!r.fine || A->dim() != 2 || B->dim() != 2 || code_of(y->scalar_type()) < 0) return nullptr;
+    const int64_t M = A->size(0), K = A->size(1), N = B->size(0);
+    const Mat a8 = r.mat(a[3], M, K, at::kChar), g8 = r.mat(a[4], N, K, at::kChar), u8 = r.mat(a[5], N, K, at::kChar),
+              Y = r.mat(a[11], M, N, y->scalar_type());
+    void *sa = r.vec(a[6], M, at::kFloat), *sg = r.vec(a[7], N, at::kFloat), *su = r.vec(a[8], N, at::kFloat),
+         *bg = r.vec(a[9], N, at::kFloat, true), *bu = r.vec(a[10], N, at::kFloat, true);
+    if (!r.fine || g8.ld != u8.ld) return nullptr;
+    return enter<decltype(coalesce_gated_gemm_int8)>(
+        a[0], (int8_t*)a8.p, a8.ld, (int8_t*)g8.p, (int8_t*)u8.p, g8.ld, (float*)sa, (float*)sg, (float*)su, (float*)bg,
+        (float*)bu, Y.p, Y.ld, M, N, K, (coalesce_dtype)code_of(y->scalar_type()), (coalesce_act)PyLong_AsLong(a[12]),
+        a[13] == Py_None ? nullptr : PyLong_AsVoidPtr(a[13]), PyLong_AsSize_t(a[14]), PyLong_AsVoidPtr(a[2]));
+  });
+}
+
+#define COALESCE_SHORT(NAME) \
+  { #NAME, (PyCFunction)(void (*)(void))NAME, METH_FASTCALL, "The short way into coalesce_" #NAME "." }
 PyMethodDef kMethods[] = {{"grad_list", grad_list, METH_VARARGS, "The host arrays of a list of gradients."},
+                          COALESCE_SHORT(layer_norm),
+                          COALESCE_SHORT(dropout),
+                          COALESCE_SHORT(quantize),
+                          COALESCE_SHORT(gemm_int8),
+                          COALESCE_SHORT(gated_gemm_int8),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 

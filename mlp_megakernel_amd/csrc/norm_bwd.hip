@@ -35,18 +35,6 @@ __global__ __launch_bounds__(TPR * ROWS) void norm_bwd_kernel(NormBwdParams) {  
   // spilled registers, 68 so; 70 with the next row's loads ahead, which spill again).
   constexpr bool IN_LDS = TPR == 1024 && CH == 2;
   __shared__ f32x4 acc[IN_LDS ? 4 * CH : 1][IN_LDS ? TPR : 1];
-  float aw[CH][8], ab[CH][8], w[CH][8];
-#pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    const auto p = again<NormBwdParams>(k);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) aw[c][e] = ab[c][e] = 0.0f, w[c][e] = 1.0f;
-    if constexpr (IN_LDS) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[4 * c + i][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    }
-    if (p->weight) read_vec<T>(p->weight, p->wt == DT_F32, (c * TPR + t) * 8, p->N, w[c]);
-  }
   const int M = k->M, N = k->N;
   const float inv_n = 1.0f / (float)N;
 
@@ -84,6 +72,19 @@ __global__ __launch_bounds__(TPR * ROWS) void norm_bwd_kernel(NormBwdParams) {  
   constexpr bool AHEAD = !IN_LDS;
   In in, nx;
   if constexpr (AHEAD) load(row0 + sub, in);
+  // (behind the first row's loads)
+  float aw[CH][8], ab[CH][8], w[CH][8];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const auto p = again<NormBwdParams>(k);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) aw[c][e] = ab[c][e] = 0.0f, w[c][e] = 1.0f;
+    if constexpr (IN_LDS) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[4 * c + i][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    }
+    if (p->weight) read_vec<T>(p->weight, p->wt == DT_F32, (c * TPR + t) * 8, p->N, w[c]);
+  }
   for (int parity = 0; row0 < M; row0 += step, parity ^= 1) {
     const int64_t row = row0 + sub;
     if constexpr (AHEAD)
@@ -334,7 +335,8 @@ __global__ __launch_bounds__(512) void norm_sums_kernel(NormBwdParams p) {
       f32x4 v[8];
 #pragma unroll
       for (int u = 0; u < 8; ++u)
-        v[u] = g + 64 * u < p.groups ? *(const f32x4*)(src + (int64_t)(g + 64 * u) * p.ldp) : (f32x4){0.f, 0.f, 0.f, 0.f};
+        v[u] = g + 64 * u < p.groups ? *(const f32x4*)(src + (int64_t)(g + 64 * u) * p.ldp)
+                                     : (f32x4){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int u = 0; u < 8; ++u) s += v[u];
     }

@@ -8,6 +8,7 @@ for the inputs is the caller's part.
 """
 from __future__ import annotations
 
+import ctypes
 import math
 import weakref
 from typing import Iterable, NamedTuple, Optional, Tuple
@@ -128,6 +129,26 @@ def _new(rows: int, cols: int, dtype, device, stream):
     ld = _row_pitch(cols, dtype)
     t = _empty((rows, ld), dtype, device, stream)
     return t if ld == cols else t[:, :cols]
+
+
+# The short ways of the compiled extension: (function, address of the entry point).
+_short_ways = {}
+
+
+def _short(name: str, entry: str, stream, *operands):
+    """The status of an entry point called by the compiled extension, which reads
+    the operands itself; None where one is not as it should be, or the extension is
+    not built: the checks in Python then say what is wrong, or make the call."""
+    way = _short_ways.get(entry)
+    if way is None:
+        try:
+            from . import _marshal
+            way = getattr(_marshal, name), ctypes.cast(getattr(load_library(), entry), ctypes.c_void_p).value
+        except (ImportError, AttributeError):
+            return None
+        _short_ways[entry] = way
+    dev = _current_device()
+    return way[0](way[1], dev, _raw_stream(stream, dev) or 0, *operands)
 
 
 def _there(dev: int, call, *args):
@@ -569,7 +590,8 @@ class GatedFFN(torch.nn.Module):
 
     def __setstate__(self, state):
         # modules pickled before there was a norm and a dropout have neither
-        for name, value in (("norm", False), ("dropout", 0.0), ("eps", 1e-5), ("norm_weight", None), ("norm_bias", None)):
+        for name, value in (("norm", False), ("dropout", 0.0), ("eps", 1e-5), ("norm_weight", None),
+                            ("norm_bias", None)):
             if name not in state and name not in state.get("_parameters", {}):
                 state[name] = value
         super().__setstate__(state)

@@ -11,7 +11,8 @@ from typing import Optional, Tuple
 import torch
 
 from . import _DTYPES, _check, _empty, _matrix, _ptr, load_library
-from .ffn import _act, _current_device, _mat, _new, _one_pitch, _raw_stream, _row_pitch, _there, _vec, _workspace
+from .ffn import (_act, _current_device, _mat, _new, _one_pitch, _raw_stream, _row_pitch, _short, _there, _vec,
+                  _workspace)
 
 
 def _int8_pitch(cols: int) -> int:
@@ -50,6 +51,13 @@ def quantize_columns(x: torch.Tensor, out: Optional[torch.Tensor] = None, scale:
 
 
 def _quantize(x, out, scale, stream, columns):
+    if out is not None and scale is not None and x.is_cuda:
+        status = _short("quantize", "coalesce_quantize_columns" if columns else "coalesce_quantize_rows", stream,
+                        columns, x, out, scale)
+        if status == 0:
+            return out, scale
+        if status is not None:
+            _check(status)
     M, N, ldx = _matrix(x, "x")
     dev = x.get_device()
     if x.dtype not in _DTYPES:
@@ -102,6 +110,15 @@ def gemm_int8(A: torch.Tensor, B: torch.Tensor, a_scale: torch.Tensor, b_scale: 
     float32, float16 or bfloat16 (``out_dtype``, else that of ``out`` or of the
     residual, else bfloat16); the residual has its type and may be ``out``.
     """
+    if out is not None and out_dtype in (None, out.dtype) and A.is_cuda and A.get_device() == _current_device():
+        # (what is no pair of matrices is left to the checks below)
+        M, K, N = A.shape + B.shape[:1] if A.dim() == 2 and B.dim() == 2 else (0, 0, 0)
+        ws, nws, _keep = _workspace("coalesce_gemm_int8_workspace_size", A.get_device(), M, N, K, workspace, stream)
+        status = _short("gemm_int8", "coalesce_gemm_int8", stream, A, B, a_scale, b_scale, bias, residual, out, _act(act), ws, nws)
+        if status == 0:
+            return out
+        if status is not None:
+            _check(status)
     M, K, lda, dev = _tokens(A)
     if _current_device() != dev:
         return _there(dev, gemm_int8, A, B, a_scale, b_scale, bias, residual, act, out_dtype, out, workspace, stream)
@@ -130,6 +147,16 @@ def gated_gemm_int8(A: torch.Tensor, Bg: torch.Tensor, Bu: torch.Tensor, a_scale
     """act(zg) * zu with z = (A @ B.t()) * a_scale[:, None] * b_scale + bias for both
     weights, in one fused kernel (coalesce_gated_gemm_int8); operands as in
     :func:`gemm_int8`, Bg and Bu of one row pitch."""
+    if out is not None and out_dtype in (None, out.dtype) and A.is_cuda and A.get_device() == _current_device():
+        # (what is no pair of matrices is left to the checks below)
+        M, K, N = A.shape + Bg.shape[:1] if A.dim() == 2 and Bg.dim() == 2 else (0, 0, 0)
+        ws, nws, _keep = _workspace("coalesce_gated_gemm_int8_workspace_size", A.get_device(), M, N, K, workspace, stream)
+        status = _short("gated_gemm_int8", "coalesce_gated_gemm_int8", stream, A, Bg, Bu, a_scale, bg_scale, bu_scale,
+                        bias_g, bias_u, out, _act(act), ws, nws)
+        if status == 0:
+            return out
+        if status is not None:
+            _check(status)
     M, K, lda, dev = _tokens(A)
     if _current_device() != dev:
         return _there(dev, gated_gemm_int8, A, Bg, Bu, a_scale, bg_scale, bu_scale, bias_g, bias_u, act, out_dtype, out,

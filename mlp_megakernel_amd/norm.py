@@ -12,7 +12,7 @@ from typing import NamedTuple, Optional, Tuple, Union
 import torch
 
 from . import _DTYPES, _check, _empty, _matrix, _ptr, load_library
-from .ffn import _current_device, _mat, _new, _raw_stream, _row_pitch, _take, _there, _vec, _ws_sizes
+from .ffn import _current_device, _mat, _new, _raw_stream, _row_pitch, _short, _take, _there, _vec, _ws_sizes
 
 Seed = Union[int, torch.Tensor]
 
@@ -129,6 +129,14 @@ def _sum_like(x, residual, stream):
 
 
 def _norm(x, residual, weight, bias, eps, p, seed, offset, out_dtype, out, sum_out, add, stats, stream):
+    if out is not None and x.is_cuda and out_dtype in (None, out.dtype) and (stats is None or len(stats) == 2):
+        mean, rstd = stats or (None, None)
+        status = _short("layer_norm", "coalesce_layer_norm", stream, x, residual, sum_out, weight, bias, out, mean,
+                        rstd, eps, p, seed, offset)
+        if status == 0:
+            return out
+        if status is not None:
+            _check(status)
     M, N, ldx, dev = _rows(x, "x")
     if _current_device() != dev:
         return _there(dev, _norm, x, residual, weight, bias, eps, p, seed, offset, out_dtype, out, sum_out, add, stats,
@@ -230,6 +238,12 @@ def dropout(x: torch.Tensor, p: float, seed: Seed, offset: int = 0, residual: Op
     their own.  The result has the residual's type, x's or float32; ``out``
     may be the residual, or x where they share a type.
     """
+    if out is not None and x.is_cuda:
+        status = _short("dropout", "coalesce_dropout", stream, x, residual, out, p, seed, offset)
+        if status == 0:
+            return out
+        if status is not None:
+            _check(status)
     M, N, ldx, dev = _rows(x, "x")
     if _current_device() != dev:
         return _there(dev, dropout, x, p, seed, offset, residual, out, stream)

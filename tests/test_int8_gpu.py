@@ -269,7 +269,8 @@ def test_refusals():
               lambda: mk.gemm_int8(A, A, s, s, s.half()), lambda: mk.gemm_int8(A, A, s, s, act="tanh"),
               lambda: mk.gemm_int8(A, A, s, s, out_dtype=torch.int32), lambda: mk.gemm_int8(A, A.cpu(), s, s),
               lambda: mk.gemm_int8(A, A, s, s, residual=x), lambda: mk.gated_gemm_int8(A, A, A[:3], s, s, s),
-              lambda: mk.gated_gemm_int8(A, A, A, s, s, s[:2]), lambda: mk.quantize_rows(A), lambda: mk.quantize_rows(x[0]),
+              lambda: mk.gated_gemm_int8(A, A, A, s, s, s[:2]), lambda: mk.quantize_rows(A),
+              lambda: mk.quantize_rows(x[0]),
               lambda: mk.quantize_rows(x, out=A[:2]), lambda: mk.quantize_columns(x, out=A),
               lambda: mk.quantize_rows(x, scale=s[:2])):
         with pytest.raises(ValueError):

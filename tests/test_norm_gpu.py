@@ -233,7 +233,8 @@ def test_binding_refuses():
     st = torch.zeros(4, device="cuda"), torch.ones(4, device="cuda")
     calls = [lambda: mk.layer_norm(x.long()), lambda: mk.layer_norm(x[0]), lambda: mk.layer_norm(x.t()),
              lambda: mk.layer_norm(x.cpu()), lambda: mk.layer_norm(x, out_dtype=torch.float32),
-             lambda: mk.layer_norm(x, v[:16]), lambda: mk.layer_norm(x, v.half()), lambda: mk.layer_norm(x, v, v.bfloat16()),
+             lambda: mk.layer_norm(x, v[:16]), lambda: mk.layer_norm(x, v.half()),
+             lambda: mk.layer_norm(x, v, v.bfloat16()),
              lambda: mk.layer_norm(x, out=x[:2].clone()), lambda: mk.add_layer_norm(x, f[:2]),
              lambda: mk.add_layer_norm(x, x.half()), lambda: mk.add_layer_norm(f, x),
              lambda: mk.add_layer_norm(x, x, seed=torch.zeros(1, device="cuda", dtype=torch.int64)),
