@@ -14,8 +14,9 @@ namespace {
 // A workgroup covers 2^lg 8-column pieces of 256 >> lg rows.
 template <typename T, typename TO>
 __global__ __launch_bounds__(256) void dropout_kernel(DropoutParams p, int lg, int col_blocks) {
-  const int64_t band = blockIdx.x / col_blocks;
-  const int part = blockIdx.x - (int)band * col_blocks;
+  const uint32_t block = (uint32_t)block_no(), band_no = block / (uint32_t)col_blocks;  // (2^41 elements: 2^31 blocks)
+  const int64_t band = band_no;
+  const int part = (int)(block - band_no * (uint32_t)col_blocks);
   const int64_t row = band * (256 >> lg) + (threadIdx.x >> lg);
   const int n = ((part << lg) + (int)(threadIdx.x & ((1 << lg) - 1))) * 8;
   if (row >= p.M || n >= p.N) return;
@@ -70,7 +71,7 @@ hipError_t dropout_typed(const DropoutParams& p, hipStream_t stream) {
   while (lg < 8 && ((int64_t)1 << lg) < pieces) ++lg;
   const int64_t col_blocks = (pieces + ((int64_t)1 << lg) - 1) >> lg, rows = 256 >> lg;
   const int64_t bands = (p.M + rows - 1) / rows;
-  hipLaunchKernelGGL((dropout_kernel<T, TO>), dim3((unsigned)(bands * col_blocks)), dim3(256), 0, stream, p, lg,
+  hipLaunchKernelGGL((dropout_kernel<T, TO>), blocks_grid(bands * col_blocks), dim3(256), 0, stream, p, lg,
                      (int)col_blocks);
   return hipGetLastError();
 }

@@ -33,7 +33,7 @@ template <typename T, typename TS, int TPR, int CH>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormParams p) {
   constexpr int THREADS = TPR < 256 ? 256 : TPR, ROWS = THREADS / TPR, WAVES = TPR / 64;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t row = (int64_t)blockIdx.x * ROWS + wave / WAVES;
+  const int64_t row = block_no() * ROWS + wave / WAVES;
   if (row >= p.M) return;  // (whole workgroups where a row has more than one wave)
   const int t = threadIdx.x % TPR;
   __shared__ float part[2][WAVES];
@@ -123,7 +123,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormParams 
 template <typename T, typename TS>
 __global__ __launch_bounds__(1024) void norm_long_kernel(NormParams p) {
   __shared__ float part[2][16];
-  const int64_t row = blockIdx.x;
+  const int64_t row = block_no();
+  if (row >= p.M) return;
   const Input<T, TS> in(p, row);
   const DropKey key = drop_key(p.drop);
   auto read = [&](int n, float (&v)[8]) {
@@ -184,9 +185,9 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormParams p) {
 
 template <typename T, typename TS>
 hipError_t norm_typed(const NormParams& p, hipStream_t stream) {
-#define COALESCE_NORM(TPR, CH)                                                                                    \
-  hipLaunchKernelGGL((norm_kernel<T, TS, TPR, CH>), dim3((unsigned)((p.M + (TPR < 256 ? 256 / TPR : 1) - 1) /     \
-                                                                    (TPR < 256 ? 256 / TPR : 1))),                \
+#define COALESCE_NORM(TPR, CH)                                                                                       \
+  hipLaunchKernelGGL((norm_kernel<T, TS, TPR, CH>),                                                                  \
+                     blocks_grid(TPR < 256 ? ((int64_t)p.M + 256 / TPR - 1) / (256 / TPR) : p.M),                     \
                      dim3(TPR < 256 ? 256 : TPR), 0, stream, p)
   if (p.N <= 512)
     COALESCE_NORM(64, 1);
@@ -201,7 +202,7 @@ hipError_t norm_typed(const NormParams& p, hipStream_t stream) {
   else if (p.N <= 16384)
     COALESCE_NORM(1024, 2);
   else
-    hipLaunchKernelGGL((norm_long_kernel<T, TS>), dim3((unsigned)p.M), dim3(1024), 0, stream, p);
+    hipLaunchKernelGGL((norm_long_kernel<T, TS>), blocks_grid(p.M), dim3(1024), 0, stream, p);
 #undef COALESCE_NORM
   return hipGetLastError();
 }

@@ -209,7 +209,8 @@ __global__ __launch_bounds__(TPR * ROWS) void norm_bwd_kernel(NormBwdParams) {  
 template <typename T, typename TS>
 __global__ __launch_bounds__(1024) void norm_bwd_long_kernel(NormBwdParams p) {
   __shared__ f32x2 part[16];
-  const int64_t row = blockIdx.x;
+  const int64_t row = block_no();
+  if (row >= p.M) return;
   const Row<T> dyr = Row<T>::in(p.dY, p.ldy, row, p.N);
   const Row<TS> sr = Row<TS>::in(p.S, p.lds, row, p.N);
   const float mean = p.mean[row], rstd = p.rstd[row];
@@ -407,7 +408,7 @@ hipError_t bwd_typed(NormBwdParams p, hipStream_t stream, int num_cus) {
       COALESCE_NORM(1024, 2, 1);
     else {
       if (p.dX || p.dB)
-        hipLaunchKernelGGL((norm_bwd_long_kernel<T, TS>), dim3((unsigned)p.M), dim3(1024), 0, stream, p);
+        hipLaunchKernelGGL((norm_bwd_long_kernel<T, TS>), blocks_grid(p.M), dim3(1024), 0, stream, p);
       if (sums)
         hipLaunchKernelGGL((norm_cols_kernel<T, TS>), dim3((unsigned)((p.ldp + 255) / 256), p.groups), dim3(256), 0,
                            stream, p);

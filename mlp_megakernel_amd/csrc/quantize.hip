@@ -68,7 +68,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void quant_rows_kernel(Quant
   constexpr int THREADS = TPR < 256 ? 256 : TPR, ROWS = THREADS / TPR, WAVES = TPR / 64;
   __shared__ uint32_t part[WAVES];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t row = (int64_t)blockIdx.x * ROWS + wave / WAVES;
+  const int64_t row = block_no() * ROWS + wave / WAVES;
   if (row >= p.M) return;
   const int t = threadIdx.x % TPR;
   const Row<T> in = Row<T>::in(p.X, p.ldx, row, p.N);
@@ -106,7 +106,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void quant_rows_kernel(Quant
 template <typename T>
 __global__ __launch_bounds__(1024) void quant_long_kernel(QuantParams p) {
   __shared__ uint32_t part[16];
-  const int64_t row = blockIdx.x;
+  const int64_t row = block_no();
+  if (row >= p.M) return;
   const Row<T> in = Row<T>::in(p.X, p.ldx, row, p.N);
   uint32_t top = 0;
   for (int n = threadIdx.x * 8; n < p.N; n += 8192) {
@@ -143,8 +144,9 @@ template <typename T>
 __global__ __launch_bounds__(256) void columns_top_kernel(QuantParams p, int col_blocks) {
   __shared__ uint32_t tops[4][64];
   const int c = threadIdx.x & 63, r = threadIdx.x >> 6;
-  const int n = (int)(blockIdx.x % col_blocks) * 64 + c;
-  const int64_t m0 = (int64_t)(blockIdx.x / col_blocks) * kTopRows;
+  const uint32_t no = (uint32_t)block_no(), band = no / (uint32_t)col_blocks;  // (2^41 elements: 2^30 blocks)
+  const int n = (int)(no - band * (uint32_t)col_blocks) * 64 + c;
+  const int64_t m0 = (int64_t)band * kTopRows;
   const int rows = (int)min((int64_t)kTopRows, (int64_t)p.M - m0);
   uint32_t top = 0;
   if (n < p.N) {
@@ -168,8 +170,9 @@ template <typename T>
 __global__ __launch_bounds__(256) void columns_turn_kernel(QuantParams p, int col_blocks) {
   __shared__ int8_t block[64][64 + 4];
   const int c = threadIdx.x & 63, r = threadIdx.x >> 6;
-  const int n0 = (int)(blockIdx.x % col_blocks) * 64, n = n0 + c;
-  const int64_t m0 = (int64_t)(blockIdx.x / col_blocks) * 64;
+  const uint32_t no = (uint32_t)block_no(), band = no / (uint32_t)col_blocks;
+  const int n0 = (int)(no - band * (uint32_t)col_blocks) * 64, n = n0 + c;
+  const int64_t m0 = (int64_t)band * 64;
   const int rows = (int)min((int64_t)64, (int64_t)p.M - m0);
   if (n < p.N) {
     const Scale s = scale_of(((const uint32_t*)p.scale)[n]);
@@ -203,9 +206,9 @@ __global__ __launch_bounds__(256) void columns_scale_kernel(QuantParams p) {
 
 template <typename T>
 hipError_t rows_typed(const QuantParams& p, hipStream_t stream) {
-#define COALESCE_ROWS(TPR, CH)                                                                                    \
-  hipLaunchKernelGGL((quant_rows_kernel<T, TPR, CH>), dim3((unsigned)((p.M + (TPR < 256 ? 256 / TPR : 1) - 1) /   \
-                                                                      (TPR < 256 ? 256 / TPR : 1))),              \
+#define COALESCE_ROWS(TPR, CH)                                                                                       \
+  hipLaunchKernelGGL((quant_rows_kernel<T, TPR, CH>),                                                                \
+                     blocks_grid(TPR < 256 ? ((int64_t)p.M + 256 / TPR - 1) / (256 / TPR) : p.M),                     \
                      dim3(TPR < 256 ? 256 : TPR), 0, stream, p)
   if (p.N <= 512)
     COALESCE_ROWS(64, 1);
@@ -220,7 +223,7 @@ hipError_t rows_typed(const QuantParams& p, hipStream_t stream) {
   else if (p.N <= 16384)
     COALESCE_ROWS(1024, 2);
   else
-    hipLaunchKernelGGL((quant_long_kernel<T>), dim3((unsigned)p.M), dim3(1024), 0, stream, p);
+    hipLaunchKernelGGL((quant_long_kernel<T>), blocks_grid(p.M), dim3(1024), 0, stream, p);
 #undef COALESCE_ROWS
   return hipGetLastError();
 }
@@ -231,10 +234,10 @@ hipError_t columns_typed(const QuantParams& p, hipStream_t stream) {
   const dim3 vec((unsigned)(((int64_t)p.N + 255) / 256));
   hipLaunchKernelGGL(columns_zero_kernel, vec, dim3(256), 0, stream, p);
   if (p.M > 0) {
-    hipLaunchKernelGGL((columns_top_kernel<T>), dim3((unsigned)(col_blocks * ranges)), dim3(256), 0, stream, p,
+    hipLaunchKernelGGL((columns_top_kernel<T>), blocks_grid(col_blocks * ranges), dim3(256), 0, stream, p,
                        (int)col_blocks);
-    hipLaunchKernelGGL((columns_turn_kernel<T>), dim3((unsigned)(col_blocks * (((int64_t)p.M + 63) / 64))), dim3(256),
-                       0, stream, p, (int)col_blocks);
+    hipLaunchKernelGGL((columns_turn_kernel<T>), blocks_grid(col_blocks * (((int64_t)p.M + 63) / 64)), dim3(256), 0,
+                       stream, p, (int)col_blocks);
   }
   hipLaunchKernelGGL(columns_scale_kernel, vec, dim3(256), 0, stream, p);
   return hipGetLastError();

@@ -104,6 +104,13 @@ __device__ __forceinline__ void read_vec(const void* v, bool f32, int n, int N, 
     Row<T>::in(v, 0, 0, N).read(n, w);
 }
 
+// Launches count the threads of a dimension in 32 bits, so many blocks go over two.
+inline dim3 blocks_grid(int64_t blocks) {
+  const int64_t x = blocks < (int64_t(1) << 21) ? blocks : int64_t(1) << 21;
+  return dim3((unsigned)x, (unsigned)((blocks + x - 1) / x));
+}
+__device__ __forceinline__ int64_t block_no() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
 // The sum over a wave, in a fixed order, by the data-parallel row shifts and
 // broadcasts (six additions, no LDS); every lane gets it.
 template <int CTRL, int ROWS>
