@@ -138,16 +138,56 @@ ForwardPlan plan_forward(int64_t m, int64_t n, int64_t k, bool gated, int num_cu
   return f;
 }
 
-// The plan of an 8-bit product: the few-row kernel up to 64 rows (where tiles come
-// nearest, gated 64 x 16384 x 4096, 36 us against 39; plain 64 x 1024 x 2731 6.2 against
-// 10), tiles above.
+// The plan of an 8-bit product: the few-row kernel (int8_few.hpp) in one of its forms,
+// or (FEW8_NONE) tiles.
+enum Few8Kind {
+  FEW8_NONE = 0,
+  FEW8_8_WIDE,    // up to 8 rows; eight waves, one workgroup per compute unit
+  FEW8_8_LONG,    // eight waves, two workgroups per compute unit, weights past the caches
+  FEW8_8_ONCE,    // four waves, weights past the caches
+  FEW8_8,         // four waves
+  FEW8_16_ONCE,   // up to 16 rows
+  FEW8_16,
+  FEW8_32,        // up to 32
+  FEW8_64,        // up to 64
+  FEW8_64_PAIRS,  // with two blocks of channels per wave
+};
+// Up to 64 rows (where tiles come nearest, gated 64 x 16384 x 4096, 36 us against 39; plain
+// 64 x 1024 x 2731 6.2 against 10), with a strip of 16 channels per workgroup of up to 512
+// threads, whose launch counts its threads in 32 bits.
+Few8Kind plan_few8(int64_t m, int64_t n, int64_t k, bool gated, int num_cus) {
+  if (m > 64 || n > (int64_t(1) << 26)) return FEW8_NONE;
+  const bool one_round = n <= 16 * (int64_t)num_cus;  // of strips
+  // Weights that would fill a quarter of the memory's cache of 256 MB are not kept
+  // there (gated, 1 x 16384 x 4096 27.5 -> 25.1 us); smaller ones may still lie in it (1 x
+  // 5461 x 2048 7.6 us, 8.6 past it), and the X of more than 16 rows wants the caches too.
+  const bool once = (gated ? 2 : 1) * n * k >= (int64_t)64 << 20;
+  if (m <= 8) {
+    // 160 KB of stages per compute unit, as one workgroup where there is one strip for
+    // each (plain, 1 x 4096 x 16384: 14.6 us, 15.1 with smaller ones), as two where
+    // strips follow each other (gated, 1 x 16384 x 4096: 25.1, 26.6 with four waves, 27.5
+    // with one workgroup); in between the smaller workgroups win (1 x 5461 x 2048 6.6,
+    // 6.9).
+    if (!gated && one_round) return FEW8_8_WIDE;
+    if (gated && n > 32 * (int64_t)num_cus && once) return FEW8_8_LONG;
+    return once ? FEW8_8_ONCE : FEW8_8;
+  }
+  if (m <= 16) return once ? FEW8_16_ONCE : FEW8_16;
+  if (m <= 32) return FEW8_32;
+  // Where strips follow each other two blocks of channels per wave halve what is drawn of
+  // X (64 x 16384 x 4096: gated 36 us, 43 with one, plain 20 and 24; but gated 64 x 1024 x
+  // 512 5.5 and 4.3).
+  return one_round ? FEW8_64 : FEW8_64_PAIRS;
+}
+
 struct Int8Plan {
-  bool few;
+  Few8Kind few;
   TilePlan tiles;
 };
 Int8Plan plan_int8(int64_t m, int64_t n, int64_t k, bool gated, int num_cus) {
-  Int8Plan f{m <= 64, {0, 1, 0.0}};
-  if (!f.few) f.tiles = plan_tiles(m, n, gated, 1, (k + 127) / 128, true, num_cus, gated ? kGated8 : kPlain8);
+  Int8Plan f{plan_few8(m, n, k, gated, num_cus), {0, 1, 0.0}};
+  if (f.few == FEW8_NONE)
+    f.tiles = plan_tiles(m, n, gated, 1, (k + 127) / 128, true, num_cus, gated ? kGated8 : kPlain8);
   return f;
 }
 

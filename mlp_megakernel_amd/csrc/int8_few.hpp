@@ -195,35 +195,27 @@ hipError_t few8_launch(const TileOp& o, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// The choice is plan_int8's.
 template <typename TO, int EPI>
-hipError_t launch_few8(const TileOp& o, hipStream_t stream, int num_cus) {
+hipError_t launch_few8(const TileOp& o, Few8Kind kind, hipStream_t stream) {
   constexpr int NB = EPI == EPI_INT8_GATED ? 2 : 1;
-  const bool one_round = o.N <= 16 * num_cus;  // of strips of 16 channels
-  // Weights that would fill a quarter of the memory's cache of 256 MB are not kept
-  // there (gated, 1 x 16384 x 4096 27.5 -> 25.1 us); smaller ones may still lie in it (1 x
-  // 5461 x 2048 7.6 us, 8.6 past it), and the X of more than 16 rows wants the caches too.
-  const bool once = (int64_t)NB * o.N * o.K >= (int64_t)64 << 20;
-  if (o.M <= 8) {
-    // 160 KB of stages per compute unit, as one workgroup where there is one strip for
-    // each (plain, 1 x 4096 x 16384: 14.6 us, 15.1 with smaller ones), as two where
-    // strips follow each other (gated, 1 x 16384 x 4096: 25.1, 26.6 with four waves, 27.5
-    // with one workgroup); in between the smaller workgroups win (1 x 5461 x 2048 6.6,
-    // 6.9).
-    if (NB == 1 && one_round) return few8_launch<TO, EPI, Few8Geo<NB, 1, 1, 8, 3>>(o, stream);
-    if (NB == 2 && o.N > 32 * num_cus && once) return few8_launch<TO, EPI, Few8Geo<NB, 1, 1, 8, 2>, true>(o, stream);
-    if (once) return few8_launch<TO, EPI, Few8Geo<NB, 1, 1, 4, 3>, true>(o, stream);
-    return few8_launch<TO, EPI, Few8Geo<NB, 1, 1, 4, 3>>(o, stream);
+  switch (kind) {
+    case FEW8_8_WIDE:
+      if constexpr (NB == 1) return few8_launch<TO, EPI, Few8Geo<NB, 1, 1, 8, 3>>(o, stream);
+      break;
+    case FEW8_8_LONG:
+      if constexpr (NB == 2) return few8_launch<TO, EPI, Few8Geo<NB, 1, 1, 8, 2>, true>(o, stream);
+      break;
+    case FEW8_8_ONCE: return few8_launch<TO, EPI, Few8Geo<NB, 1, 1, 4, 3>, true>(o, stream);
+    case FEW8_8: return few8_launch<TO, EPI, Few8Geo<NB, 1, 1, 4, 3>>(o, stream);
+    case FEW8_16_ONCE: return few8_launch<TO, EPI, Few8Geo<NB, 1, 2, 4, 2>, true>(o, stream);
+    case FEW8_16: return few8_launch<TO, EPI, Few8Geo<NB, 1, 2, 4, 2>>(o, stream);
+    case FEW8_32: return few8_launch<TO, EPI, Few8Geo<NB, 1, 4, 4, 2>>(o, stream);
+    case FEW8_64: return few8_launch<TO, EPI, Few8Geo<NB, 1, 8, 4, 2>>(o, stream);
+    case FEW8_64_PAIRS: return few8_launch<TO, EPI, Few8Geo<NB, 2, 8, 2 * NB, NB == 2 ? 2 : 3>>(o, stream);
+    default: break;
   }
-  if (o.M <= 16) {
-    if (once) return few8_launch<TO, EPI, Few8Geo<NB, 1, 2, 4, 2>, true>(o, stream);
-    return few8_launch<TO, EPI, Few8Geo<NB, 1, 2, 4, 2>>(o, stream);
-  }
-  if (o.M <= 32) return few8_launch<TO, EPI, Few8Geo<NB, 1, 4, 4, 2>>(o, stream);
-  // Where strips follow each other two blocks of channels per wave halve what is drawn of
-  // X (64 x 16384 x 4096: gated 36 us, 43 with one, plain 20 and 24; but gated 64 x 1024 x
-  // 512 5.5 and 4.3).
-  if (one_round) return few8_launch<TO, EPI, Few8Geo<NB, 1, 8, 4, 2>>(o, stream);
-  return few8_launch<TO, EPI, Few8Geo<NB, 2, 8, 2 * NB, NB == 2 ? 2 : 3>>(o, stream);
+  return hipErrorInvalidValue;
 }
 
 }  // namespace

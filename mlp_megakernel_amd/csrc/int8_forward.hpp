@@ -63,7 +63,7 @@ hipError_t int8_forward(const Int8Params& q, hipStream_t stream, int num_cus, vo
   o.ldy = q.ldy;
   o.act = q.act;
   const Int8Plan f = plan_int8(q.M, q.N, q.K, gated, num_cus);
-  if (f.few) return launch_few8<TO, EPI>(o, stream, num_cus);
+  if (f.few) return launch_few8<TO, EPI>(o, f.few, stream);
   o.splits = f.tiles.splits;
   if (o.splits == 1) return int8_tiles<TO, EPI>(o, f.tiles.variant, stream, num_cus);
   Int8Join j{};
