@@ -641,7 +641,7 @@ coalesce_status coalesce_dropout(const void* X, int64_t ldx, const void* R, int6
  * elements); a row that holds an infinity or a NaN has scale NaN and q = 0.
  *   X      device, M x N of dtype (ldx)
  *   Q      device, M x N (columns: N x M) bytes, pitch ldq (a multiple of 16)
- *   scale  device, M (columns: N) floats, 16-byte aligned
+ *   scale  device, M (columns: N) floats
  */
 coalesce_status coalesce_quantize_rows(const void* X, int64_t ldx, int8_t* Q, int64_t ldq, float* scale, int64_t M,
                                        int64_t N, coalesce_dtype dtype, void* stream);
@@ -656,7 +656,7 @@ coalesce_status coalesce_quantize_columns(const void* X, int64_t ldx, int8_t* Q,
  *   coalesce_gated_gemm_int8  Y = act(zg) zu
  *   A      device, M x K bytes (lda);  B  device, N x K bytes (ldb): one row per
  *          channel, as coalesce_quantize_columns gives; pitches are multiples of 16
- *   scale_a, scale_b  device, M and N floats, 16-byte aligned
+ *   scale_a, scale_b  device, M and N floats, scale_b 16-byte aligned
  *   bias   device, N floats, 16-byte aligned, or NULL
  *   R      device, M x N of out_dtype (ldr), or NULL; may be Y with ldr == ldy
  *   Y      device, M x N of out_dtype: F32, F16 or BF16 (ldy)

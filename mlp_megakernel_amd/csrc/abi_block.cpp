@@ -91,7 +91,7 @@ coalesce_status int8_product(bool gated, const int8_t* A, int64_t lda, const int
     ops.mat(false, A, M, K, lda, 1, "A");
   }
   if (!scale_a) return fail(COALESCE_ERR_INVALID_ARGUMENT, "scale_a is NULL");
-  if ((s = check_vec(scale_a, "scale_a")) != COALESCE_OK) return s;
+  if ((s = check_stat(scale_a, "scale_a")) != COALESCE_OK) return s;
   ops.mat(false, scale_a, 1, M, M, 4, "scale_a");
   for (int i = 0; i < (gated ? 2 : 1); ++i) {
     if (K > 0) {
@@ -158,7 +158,7 @@ coalesce_status quantize(bool columns, const void* X, int64_t ldx, int8_t* Q, in
   const int64_t rows = columns ? N : M, cols = columns ? M : N;  // of Q
   if (rows == 0) return ok();
   if (!scale) return fail(COALESCE_ERR_INVALID_ARGUMENT, "scale is NULL");
-  if ((s = check_vec(scale, "scale")) != COALESCE_OK) return s;
+  if ((s = check_stat(scale, "scale")) != COALESCE_OK) return s;
   Operands ops;
   ops.mat(true, scale, 1, rows, rows, 4, "scale");
   if (cols > 0) {

@@ -118,7 +118,7 @@ QUANT = dict(X=P, ldx=N, Q=2 * P, ldq=N, scale=3 * P, M=N, N=N, dt=mk.BF16)
 BOTH = [(dict(M=-1), INV), (dict(N=-2), INV), (dict(K=-1), INV), (dict(K=131072, lda=131072, ldb=131072), UNS),
         (dict(M=(1 << 31) - 200), UNS), (dict(M=1 << 21, N=1 << 21), UNS), (dict(odt=5), INV), (dict(act=9), INV),
         (dict(A=None), INV), (dict(A=P + 8), UNS), (dict(lda=K - 16), INV), (dict(lda=K + 8), UNS),
-        (dict(lda=1 << 23), UNS), (dict(ldb=K - 16), INV), (dict(sa=None), INV), (dict(sa=3 * P + 4), UNS),
+        (dict(lda=1 << 23), UNS), (dict(ldb=K - 16), INV), (dict(sa=None), INV), (dict(sa=3 * P + 2), UNS),
         (dict(Y=None), INV), (dict(ldy=N - 8), INV), (dict(Y=P + 16), INV)]
 
 
@@ -145,7 +145,7 @@ def test_quantize_refuses_invalid(kw):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(X=None), INV), (dict(X=P + 2), UNS), (dict(Q=None), INV), (dict(Q=2 * P + 8), UNS), (dict(ldq=N - 16), INV),
-    (dict(ldq=N + 8), UNS), (dict(ldx=N - 8), INV), (dict(scale=None), INV), (dict(scale=3 * P + 4), UNS),
+    (dict(ldq=N + 8), UNS), (dict(ldx=N - 8), INV), (dict(scale=None), INV), (dict(scale=3 * P + 2), UNS),
     (dict(Q=P), INV), (dict(scale=2 * P), INV), (dict(M=(1 << 31) - 1), UNS), (dict(), DEV), (dict(M=0, N=0), 0)])
 def test_quantize_checks(kw, status):
     for name in ("coalesce_quantize_rows", "coalesce_quantize_columns"):
@@ -158,7 +158,8 @@ def test_int8_accepts():
         assert call(name, defaults, dict(K=131071, lda=131072, ldb=131072, N=8)) == DEV
         assert call(name, defaults, dict(K=0, A=None)) == DEV
         assert call(name, defaults, dict(M=0, A=None, Y=None)) == 0
-    assert call("coalesce_gemm_int8", INT8, dict(R=7 * P)) == DEV
+    assert call("coalesce_gemm_int8", INT8, dict(R=7 * P, sa=3 * P + 4)) == DEV
+    assert call("coalesce_quantize_rows", QUANT, dict(scale=3 * P + 4)) == DEV
     assert call("coalesce_quantize_rows", QUANT, dict(M=0)) == 0
     assert call("coalesce_quantize_rows", QUANT, dict(N=0, X=None, Q=None)) == DEV
     assert mk.load_library().coalesce_gemm_int8_workspace_size(8, 64, 131072) == 0

@@ -100,8 +100,8 @@ def test_a_row_does_not_depend_on_the_others(gated):
 
         def run(a, b):
             if gated:
-                return mk.gated_gemm_int8(A[a:b], *Bs, sa[a:b].clone(), *sb, *bias, out_dtype=torch.float32)
-            return mk.gemm_int8(A[a:b], Bs[0], sa[a:b].clone(), sb[0], bias[0], act="gelu", out_dtype=torch.float32)
+                return mk.gated_gemm_int8(A[a:b], *Bs, sa[a:b], *sb, *bias, out_dtype=torch.float32)
+            return mk.gemm_int8(A[a:b], Bs[0], sa[a:b], sb[0], bias[0], act="gelu", out_dtype=torch.float32)
 
         whole = run(0, 1500)
         for a, b in ((0, 1), (5, 8), (20, 40), (100, 150), (200, 264), (300, 400), (500, 900), (1, 1200)):
@@ -225,7 +225,7 @@ def test_replays_streams_and_workspaces():
     def step():
         q, s = mk.quantize_rows(x)
         return (q, s, mk.gemm_int8(q, Bs[0], s, sb[0], bias[0], R, "gelu"),
-                mk.gated_gemm_int8(q[:9], *Bs, s[:9].clone(), *sb, *bias))
+                mk.gated_gemm_int8(q[:9], *Bs, s[:9], *sb, *bias))
 
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
