@@ -153,10 +153,9 @@ enum Few8Kind {
   FEW8_64_PAIRS,  // with two blocks of channels per wave
 };
 // Up to 64 rows (where tiles come nearest, gated 64 x 16384 x 4096, 36 us against 39; plain
-// 64 x 1024 x 2731 6.2 against 10), with a strip of 16 channels per workgroup of up to 512
-// threads, whose launch counts its threads in 32 bits.
+// 64 x 1024 x 2731 6.2 against 10).
 Few8Kind plan_few8(int64_t m, int64_t n, int64_t k, bool gated, int num_cus) {
-  if (m > 64 || n > (int64_t(1) << 26)) return FEW8_NONE;
+  if (m > 64) return FEW8_NONE;
   const bool one_round = n <= 16 * (int64_t)num_cus;  // of strips
   // Weights that would fill a quarter of the memory's cache of 256 MB are not kept
   // there (gated, 1 x 16384 x 4096 27.5 -> 25.1 us); smaller ones may still lie in it (1 x
