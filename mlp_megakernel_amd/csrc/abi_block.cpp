@@ -306,6 +306,7 @@ coalesce_status coalesce_layer_norm_backward(const void* S, int64_t lds, const v
   if ((s = make_drop(p, seed, offset, device_seed, &drop)) != COALESCE_OK) return s;
   if (M == 0) dX = dB = nullptr;
   if (N == 0 || (!dX && !dB && !dweight && !dbias)) return ok();
+  if (N >= (int64_t(1) << 23)) return fail(COALESCE_ERR_UNSUPPORTED, "rows must be shorter than 2^23");  // as pitches
   const int64_t es = dsize(dtype), ss = dsize(stream_dtype), gs = dsize(grad_dtype);
   Operands ops;
   if (M > 0) {

@@ -66,7 +66,8 @@ def test_norm_accepts(kw, status):
     (dict(S=None), INV), (dict(dY=None), INV), (dict(mean=None), INV), (dict(rstd=None), INV),
     (dict(rstd=4 * P + 1), UNS),
     (dict(dS=7 * P, ldg=N + 8), INV), (dict(dX=7 * P + 8), UNS), (dict(dX=5 * P), INV), (dict(dB=7 * P + 64), INV),
-    (dict(dweight=9 * P + 4), UNS), (dict(dbias=9 * P), INV), (dict(dweight=2 * P), INV), (dict(ldb=N - 8), INV)])
+    (dict(dweight=9 * P + 4), UNS), (dict(dbias=9 * P), INV), (dict(dweight=2 * P), INV), (dict(ldb=N - 8), INV),
+    (dict(M=0, N=1 << 28), UNS)])
 def test_norm_backward_refuses(kw, status):
     assert call("coalesce_layer_norm_backward", BACK, kw) == status
 
