@@ -58,34 +58,46 @@ __device__ __forceinline__ float softplus(float z) {
 // added to it would hide that the product was none.
 __device__ __forceinline__ float relu_nan(float z) { return z < 0.0f ? 0.0f : z; }
 
-// The activation a launch names: a uniform branch per four values, nothing
+// The activation a launch names: a uniform branch per N times four values, nothing
 // beside a tile's K loop (and a fifth of the kernels that one per activation
 // would take).
-__device__ __forceinline__ f32x4 act_any(int act, f32x4 z) {
-  f32x4 f = z;
+template <int N>
+__device__ __forceinline__ void act_all(int act, f32x4 (&z)[N]) {
   switch (act) {
     case ACT_GELU:
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        float e;
-        f[r] = z[r] * normal_cdf(z[r], e);
-      }
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float e;
+          z[i][r] *= normal_cdf(z[i][r], e);
+        }
       break;
     case ACT_SOFTPLUS:
 #pragma unroll
-      for (int r = 0; r < 4; ++r) f[r] = softplus(z[r]);
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) z[i][r] = softplus(z[i][r]);
       break;
     case ACT_RELU:
 #pragma unroll
-      for (int r = 0; r < 4; ++r) f[r] = relu_nan(z[r]);
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) z[i][r] = relu_nan(z[i][r]);
       break;
     case ACT_SILU:
 #pragma unroll
-      for (int r = 0; r < 4; ++r) f[r] = silu(z[r]);
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) z[i][r] = silu(z[i][r]);
       break;
     default: break;
   }
-  return f;
+}
+__device__ __forceinline__ f32x4 act_any(int act, f32x4 z) {
+  f32x4 f[1] = {z};
+  act_all(act, f);
+  return f[0];
 }
 
 // act(z) and act'(z).
