@@ -656,11 +656,13 @@ class QuantizedGatedFFN(torch.nn.Module):
             raise RuntimeError("QuantizedGatedFFN has no gradient")
         x2 = _rows16(x.reshape(-1, self.D))
         _refuse_recorded((x2,), "QuantizedGatedFFN", "QuantizedGatedFFN cannot be traced")
-        n = layer_norm(x2, self.norm_weight, self.norm_bias, self.eps) if self.norm else x2
+        n = x2
+        if self.norm:
+            n = layer_norm(x2, _vec16(self.norm_weight), _vec16(self.norm_bias), self.eps)
         q, s = quantize_rows(n)
-        h = gated_gemm_int8(q, _rows16(self.Wg), _rows16(self.Wu), s, self.Wg_scale, self.Wu_scale, self.bg, self.bu,
-                            act=self.act, out_dtype=self.dtype)
+        h = gated_gemm_int8(q, _rows16(self.Wg), _rows16(self.Wu), s, _vec16(self.Wg_scale), _vec16(self.Wu_scale),
+                            _vec16(self.bg), _vec16(self.bu), act=self.act, out_dtype=self.dtype)
         q, s = quantize_rows(h)
-        y = gemm_int8(q, _rows16(self.Wd), s, self.Wd_scale, self.bd, x2 if self.residual else None,
+        y = gemm_int8(q, _rows16(self.Wd), s, _vec16(self.Wd_scale), _vec16(self.bd), x2 if self.residual else None,
                       out_dtype=self.dtype)
         return y.reshape(shape)

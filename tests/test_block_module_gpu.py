@@ -294,3 +294,19 @@ def test_a_block_stored_without_norm_and_dropout():
     with torch.no_grad():
         assert torch.equal(old(x), m(x))
     assert sorted(m.state_dict()) == ["Wd", "Wg", "Wu"]
+
+
+def test_quantized_block_with_its_vectors_in_a_flat_buffer():
+    # as load_state_dict(assign=True) may leave them: at any multiple of 4 bytes
+    torch.manual_seed(4)
+    block = mk.GatedFFN(64, 160, bias=True, norm=True).quantized()
+    x = torch.randn(5, 64, device="cuda", dtype=torch.bfloat16)
+    want = block(x)
+    vectors = {n: b for n, b in block.named_buffers() if b.dim() == 1}
+    flat, at = torch.empty(sum(b.numel() for b in vectors.values()) + 1, device="cuda"), 1
+    for n, b in vectors.items():
+        part = flat[at:at + b.numel()]
+        part.copy_(b)
+        setattr(block, n, part)
+        at += b.numel()
+    assert len(vectors) == 8 and torch.equal(block(x), want)
