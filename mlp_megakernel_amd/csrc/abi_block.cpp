@@ -228,9 +228,9 @@ coalesce_status coalesce_layer_norm(const void* X, int64_t ldx, const void* R, i
     return fail(COALESCE_ERR_INVALID_ARGUMENT, "eps must be a number of at least 0");
   Drop drop{};
   if ((s = make_drop(p, seed, offset, device_seed, &drop)) != COALESCE_OK) return s;
+  if (M == 0 || N == 0) return ok();  // (R of no rows may have no address)
   if (!R && (S || p != 0.0))
     return fail(COALESCE_ERR_INVALID_ARGUMENT, "a sum or a dropout without the stream that X is added to");
-  if (M == 0 || N == 0) return ok();
   const int64_t es = dsize(dtype), ss = dsize(stream_dtype), xs = R ? es : ss, ws = dsize(weight_dtype);
   Operands ops;
   if ((s = check_mat(X, ldx, N, xs, "X")) != COALESCE_OK) return s;

@@ -55,8 +55,8 @@ def test_norm_refuses(kw, status):
 @pytest.mark.parametrize("kw,status", [
     (dict(), DEV), (dict(S=2 * P), DEV), (dict(S=None), DEV), (dict(R=None, S=None, p=0.0), DEV),
     (dict(sdt=mk.F32, wdt=mk.F32), DEV), (dict(mean=None, rstd=None, weight=None, bias=None), DEV),
-    (dict(M=0), 0), (dict(N=0), 0), (dict(M=0, X=None, Y=None), 0), (dict(p=1.0, dev=12 * P), DEV),
-    (dict(dev=6 * P, p=0.0), DEV)])
+    (dict(M=0), 0), (dict(N=0), 0), (dict(M=0, X=None, Y=None), 0), (dict(M=0, R=None), 0),
+    (dict(p=1.0, dev=12 * P), DEV), (dict(dev=6 * P, p=0.0), DEV)])
 def test_norm_accepts(kw, status):
     assert call("coalesce_layer_norm", NORM, kw) == status
 
