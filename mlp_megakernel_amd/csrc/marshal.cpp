@@ -5,12 +5,15 @@
 // types in host arrays, read and checked in one pass (170 us for a list of 200, where
 // the kernels take 20).
 // And the short way into the entry points whose kernels take 3 us: it reads the
-// operands, and where every one is as it should be makes the call.  Where one is
-// not it gives None, and the binding's own checks in Python say what is wrong.
+// operands, makes the results that a backward returns, and where every operand is as
+// it should be makes the call.  Where one is not it gives None, and the binding's own
+// checks in Python say what is wrong.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
+#include <ATen/ops/empty.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <exception>
 #include <vector>
@@ -133,6 +136,18 @@ struct Mat {
   int64_t ld = 0;
 };
 
+// The pitch of rows of so many of t's elements on 16-byte boundaries.
+int64_t row_pitch(int64_t cols, const at::Tensor& t) {
+  const int64_t per = 16 / (int64_t)t.element_size();
+  return std::max(per, (cols + per - 1) / per * per);
+}
+
+struct Mask {
+  double p;
+  uint64_t seed, offset;
+  const uint64_t* device;
+};
+
 // What one call asks of its operands; `fine` falls with the first that is not so.
 struct Reader {
   int64_t device;
@@ -151,8 +166,7 @@ struct Reader {
     if (!t || t->dim() != 2 || t->scalar_type() != type || t->size(0) != rows || t->size(1) != cols ||
         (cols > 1 && t->stride(1) != 1))
       return fine = false, Mat{};
-    const int64_t per = 16 / (int64_t)t->element_size(), row = cols > per ? (cols + per - 1) / per * per : per;
-    return {t->data_ptr(), rows > 1 ? t->stride(0) : row};
+    return {t->data_ptr(), rows > 1 ? t->stride(0) : row_pitch(cols, *t)};
   }
   void* vec(PyObject* o, int64_t n, at::ScalarType type, bool optional = false) {
     if (optional && o == Py_None) return nullptr;
@@ -160,6 +174,17 @@ struct Reader {
     if (!t || t->dim() != 1 || t->scalar_type() != type || t->size(0) != n || !t->is_contiguous())
       return fine = false, nullptr;
     return t->data_ptr();
+  }
+  // Seed and offset of a mask: two integers, or a tensor of both in device memory.
+  Mask mask(PyObject* p, PyObject* seed, PyObject* offset) {
+    Mask m{PyFloat_AsDouble(p), 0, 0, nullptr};
+    if (!PyLong_Check(offset) || (!PyLong_Check(seed) && !THPVariable_Check(seed))) return fine = false, m;
+    m.offset = PyLong_AsUnsignedLongLongMask(offset);
+    if (PyLong_Check(seed))
+      m.seed = PyLong_AsUnsignedLongLongMask(seed);
+    else if ((m.device = (const uint64_t*)vec(seed, 2, at::kLong)) && m.offset)
+      fine = false;
+    return m;
   }
   at::ScalarType type(PyObject* o, at::ScalarType other) {
     return o != Py_None && THPVariable_Check(o) ? THPVariable_Unpack(o).scalar_type() : other;
@@ -200,7 +225,7 @@ PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return shortly([&]() -> PyObject* {
     Reader r{PyLong_AsLongLong(a[1])};
     const at::Tensor *x = r.tensor(a[3]), *y = r.tensor(a[8]);
-    if (!r.fine || x->dim() != 2 || !PyLong_Check(a[13]) || !PyLong_Check(a[14])) return nullptr;
+    if (!r.fine || x->dim() != 2) return nullptr;
     const bool add = a[4] != Py_None;
     const int64_t M = x->size(0), N = x->size(1);
     const at::ScalarType dt = y->scalar_type(), st = add ? r.type(a[4], dt) : x->scalar_type();
@@ -210,12 +235,87 @@ PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
               Y = r.mat(a[8], M, N, dt);
     void *w = r.vec(a[6], N, wt, true), *b = r.vec(a[7], N, wt, true), *mean = r.vec(a[9], M, at::kFloat, true),
          *rstd = r.vec(a[10], M, at::kFloat, true);
-    const double eps = PyFloat_AsDouble(a[11]), p = PyFloat_AsDouble(a[12]);
+    const double eps = PyFloat_AsDouble(a[11]);
+    const Mask m = r.mask(a[12], a[13], a[14]);
     if (!r.fine || PyErr_Occurred()) return nullptr;
     return enter<decltype(coalesce_layer_norm)>(
         a[0], X.p, X.ld, R.p, R.ld, S.p, S.ld, w, b, Y.p, Y.ld, (float*)mean, (float*)rstd, M, N,
-        (coalesce_dtype)code_of(dt), (coalesce_dtype)code_of(st), (coalesce_dtype)code_of(wt), eps, p,
-        PyLong_AsUnsignedLongLongMask(a[13]), PyLong_AsUnsignedLongLongMask(a[14]), nullptr, PyLong_AsVoidPtr(a[2]));
+        (coalesce_dtype)code_of(dt), (coalesce_dtype)code_of(st), (coalesce_dtype)code_of(wt), eps, m.p, m.seed,
+        m.offset, m.device, PyLong_AsVoidPtr(a[2]));
+  });
+}
+
+// A rows x cols result like those of the binding: rows on 16-byte boundaries.
+at::Tensor result(const at::Tensor& like, int64_t rows, int64_t cols, at::ScalarType type) {
+  const int64_t per = 16 / (int64_t)at::elementSize(type), ld = std::max(per, (cols + per - 1) / per * per);
+  at::Tensor t = at::empty({rows, ld}, like.options().dtype(type));
+  return ld == cols ? t : t.narrow(1, 0, cols);
+}
+
+// layer_norm_backward(address, device, stream, address of the workspace's size, x, weight, mean, rstd, dout, dsum,
+//                     dx, dbranch, workspace, want_dx, want_dbranch, want_dweight, want_dbias, type of the last two,
+//                     p, seed, offset): (status, dx, dbranch, dweight, dbias)
+// The stream is the device's current one: what is None and wanted is made here.
+PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 21)) return nullptr;
+  return shortly([&]() -> PyObject* {
+    Reader r{PyLong_AsLongLong(a[1])};
+    const at::Tensor *x = r.tensor(a[4]), *dy = r.tensor(a[8]);
+    if (!r.fine || x->dim() != 2) return nullptr;
+    const int64_t M = x->size(0), N = x->size(1);
+    const at::ScalarType dt = dy->scalar_type(), st = x->scalar_type(), wt = r.type(a[5], dt);
+    const long gc = PyLong_AsLong(a[17]);
+    if (code_of(dt) < 0 || (st != at::kFloat && st != dt) || (wt != at::kFloat && wt != dt) ||
+        (gc != code_of(at::kFloat) && gc != code_of(dt)))
+      return nullptr;
+    const at::ScalarType gt = gc == code_of(at::kFloat) ? at::kFloat : dt;
+    const Mat S = r.mat(a[4], M, N, st), dY = r.mat(a[8], M, N, dt), dS = r.mat(a[9], M, N, st, true);
+    void *w = r.vec(a[5], N, wt, true), *mean = r.vec(a[6], M, at::kFloat), *rstd = r.vec(a[7], M, at::kFloat);
+    const Mask m = r.mask(a[18], a[19], a[20]);
+    // what is returned: what was given, or else made
+    bool want[4];
+    for (int i = 0; i < 4; ++i) want[i] = PyObject_IsTrue(a[13 + i]) == 1;
+    at::Tensor made[4];
+    Mat dX, dB;
+    if (want[0]) dX = r.mat(a[10], M, N, st, true);
+    if (want[1]) dB = r.mat(a[11], M, N, dt, true);
+    if (!r.fine || PyErr_Occurred()) return nullptr;
+    if (want[0] && a[10] == Py_None) {
+      made[0] = result(*x, M, N, st);
+      dX = {made[0].data_ptr(), M > 1 ? made[0].stride(0) : row_pitch(N, made[0])};
+    }
+    if (want[1] && a[11] == Py_None) {
+      made[1] = result(*x, M, N, dt);
+      dB = {made[1].data_ptr(), M > 1 ? made[1].stride(0) : row_pitch(N, made[1])};
+    }
+    for (int i = 2; i < 4; ++i)
+      if (want[i]) made[i] = at::empty({N}, x->options().dtype(gt));
+    at::Tensor ws;
+    const at::Tensor* space = nullptr;
+    if (a[12] != Py_None) {
+      space = r.tensor(a[12]);
+      if (!space || !space->is_contiguous()) return nullptr;
+    } else if (want[2] || want[3]) {
+      auto* const need = reinterpret_cast<decltype(coalesce_layer_norm_backward_workspace_size)*>(PyLong_AsVoidPtr(a[3]));
+      if (!need) return nullptr;
+      ws = at::empty({(int64_t)need(M, N)}, x->options().dtype(at::kByte));
+      space = &ws;
+    }
+    Ref status(enter<decltype(coalesce_layer_norm_backward)>(
+        a[0], S.p, S.ld, w, (const float*)mean, (const float*)rstd, dY.p, dY.ld, dS.p, dS.ld, dX.p, dX.ld, dB.p, dB.ld,
+        want[2] ? made[2].data_ptr() : nullptr, want[3] ? made[3].data_ptr() : nullptr, M, N,
+        (coalesce_dtype)code_of(dt), (coalesce_dtype)code_of(st), (coalesce_dtype)code_of(wt), (coalesce_dtype)gc, m.p,
+        m.seed, m.offset, m.device, space ? space->data_ptr() : nullptr, space ? space->nbytes() : (size_t)0,
+        PyLong_AsVoidPtr(a[2])));
+    if (!status.p) return nullptr;
+    PyObject* out[4];
+    for (int i = 0; i < 4; ++i) {
+      if (made[i].defined())
+        out[i] = THPVariable_Wrap(std::move(made[i]));
+      else
+        Py_INCREF(out[i] = want[i] ? a[10 + i] : Py_None);
+    }
+    return Py_BuildValue("ONNNN", status.p, out[0], out[1], out[2], out[3]);
   });
 }
 
@@ -225,16 +325,16 @@ PyObject* dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return shortly([&]() -> PyObject* {
     Reader r{PyLong_AsLongLong(a[1])};
     const at::Tensor *x = r.tensor(a[3]), *y = r.tensor(a[5]);
-    if (!r.fine || x->dim() != 2 || !PyLong_Check(a[7]) || !PyLong_Check(a[8])) return nullptr;
+    if (!r.fine || x->dim() != 2) return nullptr;
     const int64_t M = x->size(0), N = x->size(1);
     const at::ScalarType dt = x->scalar_type(), ot = y->scalar_type();
     if (code_of(dt) < 0 || (ot != at::kFloat && ot != dt)) return nullptr;
     const Mat X = r.mat(a[3], M, N, dt), R = r.mat(a[4], M, N, ot, true), Y = r.mat(a[5], M, N, ot);
-    const double p = PyFloat_AsDouble(a[6]);
+    const Mask m = r.mask(a[6], a[7], a[8]);
     if (!r.fine || PyErr_Occurred()) return nullptr;
     return enter<decltype(coalesce_dropout)>(a[0], X.p, X.ld, R.p, R.ld, Y.p, Y.ld, M, N, (coalesce_dtype)code_of(dt),
-                                             (coalesce_dtype)code_of(ot), p, PyLong_AsUnsignedLongLongMask(a[7]),
-                                             PyLong_AsUnsignedLongLongMask(a[8]), nullptr, PyLong_AsVoidPtr(a[2]));
+                                             (coalesce_dtype)code_of(ot), m.p, m.seed, m.offset, m.device,
+                                             PyLong_AsVoidPtr(a[2]));
   });
 }
 
@@ -299,6 +399,7 @@ PyObject* gated_gemm_int8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   { #NAME, (PyCFunction)(void (*)(void))NAME, METH_FASTCALL, "The short way into coalesce_" #NAME "." }
 PyMethodDef kMethods[] = {{"grad_list", grad_list, METH_VARARGS, "The host arrays of a list of gradients."},
                           COALESCE_SHORT(layer_norm),
+                          COALESCE_SHORT(layer_norm_backward),
                           COALESCE_SHORT(dropout),
                           COALESCE_SHORT(quantize),
                           COALESCE_SHORT(gemm_int8),

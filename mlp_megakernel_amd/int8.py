@@ -51,7 +51,12 @@ def quantize_columns(x: torch.Tensor, out: Optional[torch.Tensor] = None, scale:
 
 
 def _quantize(x, out, scale, stream, columns):
-    if out is not None and scale is not None and x.is_cuda:
+    if x.is_cuda and x.dim() == 2:
+        rows, cols = x.shape[::-1] if columns else x.shape
+        if out is None:
+            out = _new_int8(rows, cols, x.device, stream)
+        if scale is None:
+            scale = _empty(rows, torch.float32, x.device, stream)
         status = _short("quantize", "coalesce_quantize_columns" if columns else "coalesce_quantize_rows", stream,
                         columns, x, out, scale)
         if status == 0:
@@ -65,10 +70,6 @@ def _quantize(x, out, scale, stream, columns):
     if _current_device() != dev:
         return _there(dev, _quantize, x, out, scale, stream, columns)
     rows, cols = (N, M) if columns else (M, N)
-    if out is None:
-        out = _new_int8(rows, cols, x.device, stream)
-    if scale is None:
-        scale = _empty(rows, torch.float32, x.device, stream)
     ldq = _mat8(out, "out", rows, cols, dev)
     _vec(scale, "scale", rows, torch.float32, dev)
     call = load_library().coalesce_quantize_columns if columns else load_library().coalesce_quantize_rows
@@ -110,11 +111,17 @@ def gemm_int8(A: torch.Tensor, B: torch.Tensor, a_scale: torch.Tensor, b_scale: 
     float32, float16 or bfloat16 (``out_dtype``, else that of ``out`` or of the
     residual, else bfloat16); the residual has its type and may be ``out``.
     """
-    if out is not None and out_dtype in (None, out.dtype) and A.is_cuda and A.get_device() == _current_device():
-        # (what is no pair of matrices is left to the checks below)
-        M, K, N = A.shape + B.shape[:1] if A.dim() == 2 and B.dim() == 2 else (0, 0, 0)
+    # (what is no pair of matrices is left to the checks below)
+    if A.is_cuda and A.dim() == B.dim() == 2 and A.get_device() == _current_device():
+        M, K, N = A.shape + B.shape[:1]
+        odt = _out_type(out_dtype, out, residual)
+        if out is None:
+            out = _new(M, N, odt, A.device, stream)
         ws, nws, _keep = _workspace("coalesce_gemm_int8_workspace_size", A.get_device(), M, N, K, workspace, stream)
-        status = _short("gemm_int8", "coalesce_gemm_int8", stream, A, B, a_scale, b_scale, bias, residual, out, _act(act), ws, nws)
+        status = None
+        if out.dtype is odt:
+            status = _short("gemm_int8", "coalesce_gemm_int8", stream, A, B, a_scale, b_scale, bias, residual, out,
+                            _act(act), ws, nws)
         if status == 0:
             return out
         if status is not None:
@@ -147,12 +154,17 @@ def gated_gemm_int8(A: torch.Tensor, Bg: torch.Tensor, Bu: torch.Tensor, a_scale
     """act(zg) * zu with z = (A @ B.t()) * a_scale[:, None] * b_scale + bias for both
     weights, in one fused kernel (coalesce_gated_gemm_int8); operands as in
     :func:`gemm_int8`, Bg and Bu of one row pitch."""
-    if out is not None and out_dtype in (None, out.dtype) and A.is_cuda and A.get_device() == _current_device():
-        # (what is no pair of matrices is left to the checks below)
-        M, K, N = A.shape + Bg.shape[:1] if A.dim() == 2 and Bg.dim() == 2 else (0, 0, 0)
+    # (what is no pair of matrices is left to the checks below)
+    if A.is_cuda and A.dim() == Bg.dim() == 2 and A.get_device() == _current_device():
+        M, K, N = A.shape + Bg.shape[:1]
+        odt = _out_type(out_dtype, out, None)
+        if out is None:
+            out = _new(M, N, odt, A.device, stream)
         ws, nws, _keep = _workspace("coalesce_gated_gemm_int8_workspace_size", A.get_device(), M, N, K, workspace, stream)
-        status = _short("gated_gemm_int8", "coalesce_gated_gemm_int8", stream, A, Bg, Bu, a_scale, bg_scale, bu_scale,
-                        bias_g, bias_u, out, _act(act), ws, nws)
+        status = None
+        if out.dtype is odt:
+            status = _short("gated_gemm_int8", "coalesce_gated_gemm_int8", stream, A, Bg, Bu, a_scale, bg_scale,
+                            bu_scale, bias_g, bias_u, out, _act(act), ws, nws)
         if status == 0:
             return out
         if status is not None:

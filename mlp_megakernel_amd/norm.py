@@ -7,6 +7,8 @@ that device's current stream.
 """
 from __future__ import annotations
 
+import ctypes
+import functools
 from typing import NamedTuple, Optional, Tuple, Union
 
 import torch
@@ -122,6 +124,13 @@ def add_layer_norm_train(x: torch.Tensor, residual: torch.Tensor, weight: Option
     return y, sum_out, tuple(stats)
 
 
+def _like(x, dtype, stream):
+    """A result of x's shape, or None where x is no matrix on a GPU (the checks of the call say so)."""
+    if x.is_cuda and x.dim() == 2 and dtype in _DTYPES:
+        return _new(*x.shape, dtype, x.device, stream)
+    return None
+
+
 def _sum_like(x, residual, stream):
     M, N, _, dev = _rows(x, "x")
     _mat(residual, "residual", M, N, residual.dtype if residual.dtype is torch.float32 else x.dtype, dev)
@@ -129,6 +138,8 @@ def _sum_like(x, residual, stream):
 
 
 def _norm(x, residual, weight, bias, eps, p, seed, offset, out_dtype, out, sum_out, add, stats, stream):
+    if out is None:
+        out = _like(x, x.dtype if add or out_dtype is None else out_dtype, stream)
     if out is not None and x.is_cuda and out_dtype in (None, out.dtype) and (stats is None or len(stats) == 2):
         mean, rstd = stats or (None, None)
         status = _short("layer_norm", "coalesce_layer_norm", stream, x, residual, sum_out, weight, bias, out, mean,
@@ -165,6 +176,12 @@ def _norm(x, residual, weight, bias, eps, p, seed, offset, out_dtype, out, sum_o
     return out
 
 
+@functools.lru_cache(maxsize=None)
+def _short_size() -> int:
+    """The address of coalesce_layer_norm_backward_workspace_size."""
+    return ctypes.cast(load_library().coalesce_layer_norm_backward_workspace_size, ctypes.c_void_p).value
+
+
 def layer_norm_backward(x: torch.Tensor, weight: Optional[torch.Tensor], stats: Tuple[torch.Tensor, torch.Tensor],
                         dout: torch.Tensor, dsum: Optional[torch.Tensor] = None, p: float = 0.0, seed: Seed = 0,
                         offset: int = 0, want_dx: bool = True, want_dbranch: bool = False, want_dweight: bool = True,
@@ -180,6 +197,13 @@ def layer_norm_backward(x: torch.Tensor, weight: Optional[torch.Tensor], stats: 
     of ``p``, ``seed`` and ``offset`` (rounded by itself, not from dx).
     dweight and dbias are of ``grad_dtype``: float32 or dout's.
     """
+    if stream is None and x.is_cuda and len(stats) == 2:
+        got = _short("layer_norm_backward", "coalesce_layer_norm_backward", None, _short_size(), x, weight, stats[0],
+                     stats[1], dout, dsum, dx, dbranch, workspace, want_dx, want_dbranch, want_dweight, want_dbias,
+                     _DTYPES.get(grad_dtype, -1), p, seed, offset)
+        if got is not None:
+            _check(got[0])
+            return NormGrads(*got[1:])
     M, N, ldx, dev = _rows(x, "x")
     if _current_device() != dev:
         return _there(dev, layer_norm_backward, x, weight, stats, dout, dsum, p, seed, offset, want_dx, want_dbranch,
@@ -238,6 +262,8 @@ def dropout(x: torch.Tensor, p: float, seed: Seed, offset: int = 0, residual: Op
     their own.  The result has the residual's type, x's or float32; ``out``
     may be the residual, or x where they share a type.
     """
+    if out is None:
+        out = _like(x, x.dtype if residual is None else residual.dtype, stream)
     if out is not None and x.is_cuda:
         status = _short("dropout", "coalesce_dropout", stream, x, residual, out, p, seed, offset)
         if status == 0:
