@@ -44,6 +44,7 @@ struct NormBwdParams {
   int64_t lds, ldy, ldg, ldx, ldb;
   int M, N;
   int groups, ldp;  // partial sums per column and their pitch (set by the launcher)
+  bool alone;       // one workgroup, which writes dweight and dbias itself
   DType wt, gt;
   Drop drop;
 };

@@ -9,7 +9,8 @@
 // 5.2): workgroups take rows in turn, a
 // thread keeps the sums of its columns in registers from row to row while the next
 // row's loads are in flight, and writes them once as a partial sum.  A second small
-// launch adds the partials in order (no atomics: the same bits every time).
+// launch adds the partials in order (no atomics: the same bits every time); a few
+// short rows need none.
 // Sums and statistics are fp32.  Rows longer than the registers take one kernel per
 // row and one per block of columns instead.
 #include <algorithm>
@@ -19,6 +20,28 @@
 
 namespace coalesce {
 namespace {
+
+// The sums of columns n to n + 3 of a workgroup: a partial result, or, of the only
+// workgroup, the gradient of the weight (i = 0) or of the bias.
+__device__ __forceinline__ void put_sums(ArgsOf<NormBwdParams> p, int i, int n, f32x4 s) {
+  if (n >= p->ldp) return;
+  if (!p->alone) {
+    *(f32x4*)(p->partial + ((int64_t)i * gridDim.x + blockIdx.x) * p->ldp + n) = s;
+    return;
+  }
+  void* const out = i ? p->dbias : p->dweight;
+  if (!out) return;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (n + e >= p->N) continue;
+    if (p->gt == DT_F32)
+      ((float*)out)[n + e] = s[e];
+    else if (p->gt == DT_BF16)
+      ((__bf16*)out)[n + e] = (__bf16)s[e];
+    else
+      ((_Float16*)out)[n + e] = (_Float16)s[e];
+  }
+}
 
 // TPR threads per row, CH times 8 columns each; rows of one wave lie four to a
 // workgroup, whose waves' sums meet in LDS at the end.
@@ -165,11 +188,9 @@ __global__ __launch_bounds__(TPR * ROWS) void norm_bwd_kernel(NormBwdParams) {  
 
   const auto p = again<NormBwdParams>(k);
   if (!p->dweight && !p->dbias) return;
-  const int ldp = p->ldp;
   // partial[0]: dw, partial[1]: db, a row of ldp per workgroup
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    float* out = p->partial + ((int64_t)i * gridDim.x + blockIdx.x) * ldp;
     if constexpr (ROWS > 1) {
       __shared__ f32x4 meet[ROWS][2 * CH][TPR];
       __syncthreads();
@@ -186,7 +207,7 @@ __global__ __launch_bounds__(TPR * ROWS) void norm_bwd_kernel(NormBwdParams) {  
         f32x4 s = meet[0][q][l];
 #pragma unroll
         for (int r = 1; r < ROWS; ++r) s += meet[r][q][l];
-        if (n < ldp) *(f32x4*)(out + n) = s;
+        put_sums(p, i, n, s);
       }
     } else {
 #pragma unroll
@@ -195,11 +216,10 @@ __global__ __launch_bounds__(TPR * ROWS) void norm_bwd_kernel(NormBwdParams) {  
         for (int h = 0; h < 2; ++h) {
           const int n = (c * TPR + t) * 8 + 4 * h;
           const float(&a)[8] = i ? ab[c] : aw[c];
-          if (n >= ldp) continue;
           if constexpr (IN_LDS)
-            *(f32x4*)(out + n) = acc[4 * c + 2 * i + h][t];
+            put_sums(p, i, n, acc[4 * c + 2 * i + h][t]);
           else
-            *(f32x4*)(out + n) = (f32x4){a[4 * h], a[4 * h + 1], a[4 * h + 2], a[4 * h + 3]};
+            put_sums(p, i, n, (f32x4){a[4 * h], a[4 * h + 1], a[4 * h + 2], a[4 * h + 3]});
         }
     }
   }
@@ -364,9 +384,10 @@ constexpr int kLongRow = 16384;
 // of a long one.
 struct SumsPlan {
   int groups, ldp;
+  bool alone;
 };
 SumsPlan sums_plan(int64_t M, int64_t N, int num_cus) {
-  SumsPlan s;
+  SumsPlan s{};
   s.ldp = (int)((N + 7) / 8 * 8);
   if (N > kLongRow) {
     s.groups = (int)std::min<int64_t>((M + 63) / 64, 64);
@@ -378,6 +399,11 @@ SumsPlan sums_plan(int64_t M, int64_t N, int num_cus) {
   const int64_t rows = N <= 1024 ? 4 : 1;
   const int64_t per_cu = N <= 4096 ? 3 : 1;
   s.groups = (int)std::min<int64_t>((M + rows - 1) / rows, num_cus * per_cu);
+  // Few short rows are one workgroup's, which writes the gradients itself (8 x 512 bf16:
+  // 5.0 us and one launch, 5.7 and two; but 16 x 512 6.8 and 5.7, 2 x 2048 5.9 and 5.8, 1 x
+  // 4096 7.3 and 6.7).
+  s.alone = M > 0 && (N <= 1024 ? M <= 8 : N <= 2048 && M == 1);
+  if (s.alone) s.groups = 1;
   return s;
 }
 
@@ -385,6 +411,7 @@ template <typename T, typename TS>
 hipError_t bwd_typed(NormBwdParams p, hipStream_t stream, int num_cus) {
   const SumsPlan plan = sums_plan(p.M, p.N, num_cus);
   p.groups = plan.groups;
+  p.alone = plan.alone;
   // fp32 streams take more registers: two workgroups of 16 columns per thread fit a
   // compute unit, and a third would run by itself
   const bool wide = (p.N > 512 && p.N <= 1024) || (p.N > 2048 && p.N <= 4096);
@@ -417,7 +444,7 @@ hipError_t bwd_typed(NormBwdParams p, hipStream_t stream, int num_cus) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !sums) return e;
   }
-  if (!sums) return hipSuccess;
+  if (!sums || p.alone) return hipSuccess;
   const dim3 grid((unsigned)((p.N + 31) / 32), 2);
   if (p.gt == DT_F32)
     hipLaunchKernelGGL((norm_sums_kernel<float>), grid, dim3(512), 0, stream, p);

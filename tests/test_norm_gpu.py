@@ -255,3 +255,20 @@ def test_binding_refuses():
                                              workspace=torch.empty(16, device="cuda", dtype=torch.uint8))):
         with pytest.raises(mk.CoalesceError):
             c()
+
+
+@pytest.mark.parametrize("types", TYPES, ids="-".join)
+def test_norm_backward_of_few_rows(types):
+    # one workgroup writes the sums, and one row or column more takes two launches
+    dt, sdt = DT[types[0]], DT[types[1]]
+    for j, (M, N) in enumerate([(8, 1023), (8, 1024), (9, 1024), (8, 1), (1, 1025), (1, 2047), (1, 2048), (1, 2049),
+                                (2, 2048), (8, 301), (9, 301)]):
+        progress("few rows %s %s" % (types, (M, N)))
+        gen, w, _, S, _ = setup(M, N, dt, sdt, j, 3)
+        dy = ref.rows(gen, M, N, dt)
+        _, (mean, rstd) = mk.layer_norm_train(S, w, out_dtype=dt)
+        for gd in (dt, torch.float32):
+            g = mk.layer_norm_backward(S, w, (mean, rstd), dy, grad_dtype=gd)
+            r = ref.norm_backward(S, w, mean, rstd, dy, None, (0.0, 0, 0), dt, sdt, gd)
+            for name in ("dx", "dweight", "dbias"):
+                ref.check(getattr(g, name), r[name], "%s %s" % (name, (M, N)))
