@@ -5,8 +5,8 @@
 // types in host arrays, read and checked in one pass (170 us for a list of 200, where
 // the kernels take 20).
 // And the short way into the entry points whose kernels take 3 us: it reads the
-// operands, makes the results that a backward returns, and where every operand is as
-// it should be makes the call.  Where one is not it gives None, and the binding's own
+// operands, makes the results of a norm and of its backward, and where every operand is
+// as it should be makes the call.  Where one is not it gives None, and the binding's own
 // checks in Python say what is wrong.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -25,6 +25,10 @@ namespace {
 // COALESCE_F32, F16, BF16; -1 for others.
 int code_of(at::ScalarType t) {
   return t == at::kFloat ? 0 : t == at::kHalf ? 1 : t == at::kBFloat16 ? 2 : -1;
+}
+
+at::ScalarType type_of(long code) {
+  return code == 0 ? at::kFloat : code == 1 ? at::kHalf : code == 2 ? at::kBFloat16 : at::ScalarType::Undefined;
 }
 
 struct Ref {
@@ -219,37 +223,74 @@ PyObject* shortly(W work) {
   Py_RETURN_NONE;
 }
 
-// layer_norm(address, device, stream, x, residual, sum, weight, bias, out, mean, rstd, eps, p, seed, offset)
-PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!count(n, 15)) return nullptr;
-  return shortly([&]() -> PyObject* {
-    Reader r{PyLong_AsLongLong(a[1])};
-    const at::Tensor *x = r.tensor(a[3]), *y = r.tensor(a[8]);
-    if (!r.fine || x->dim() != 2) return nullptr;
-    const bool add = a[4] != Py_None;
-    const int64_t M = x->size(0), N = x->size(1);
-    const at::ScalarType dt = y->scalar_type(), st = add ? r.type(a[4], dt) : x->scalar_type();
-    const at::ScalarType wt = r.type(a[6], r.type(a[7], dt));
-    if (code_of(dt) < 0 || (st != at::kFloat && st != dt) || (wt != at::kFloat && wt != dt)) return nullptr;
-    const Mat X = r.mat(a[3], M, N, add ? dt : st), R = r.mat(a[4], M, N, st, true), S = r.mat(a[5], M, N, st, true),
-              Y = r.mat(a[8], M, N, dt);
-    void *w = r.vec(a[6], N, wt, true), *b = r.vec(a[7], N, wt, true), *mean = r.vec(a[9], M, at::kFloat, true),
-         *rstd = r.vec(a[10], M, at::kFloat, true);
-    const double eps = PyFloat_AsDouble(a[11]);
-    const Mask m = r.mask(a[12], a[13], a[14]);
-    if (!r.fine || PyErr_Occurred()) return nullptr;
-    return enter<decltype(coalesce_layer_norm)>(
-        a[0], X.p, X.ld, R.p, R.ld, S.p, S.ld, w, b, Y.p, Y.ld, (float*)mean, (float*)rstd, M, N,
-        (coalesce_dtype)code_of(dt), (coalesce_dtype)code_of(st), (coalesce_dtype)code_of(wt), eps, m.p, m.seed,
-        m.offset, m.device, PyLong_AsVoidPtr(a[2]));
-  });
-}
-
 // A rows x cols result like those of the binding: rows on 16-byte boundaries.
 at::Tensor result(const at::Tensor& like, int64_t rows, int64_t cols, at::ScalarType type) {
   const int64_t per = 16 / (int64_t)at::elementSize(type), ld = std::max(per, (cols + per - 1) / per * per);
   at::Tensor t = at::empty({rows, ld}, like.options().dtype(type));
   return ld == cols ? t : t.narrow(1, 0, cols);
+}
+
+// (status, and four results: what was made, or else what was given)
+PyObject* returned(const Ref& status, PyObject* const (&given)[4], at::Tensor (&made)[4]) {
+  PyObject* out[4];
+  for (int i = 0; i < 4; ++i) {
+    if (made[i].defined())
+      out[i] = THPVariable_Wrap(std::move(made[i]));
+    else
+      Py_INCREF(out[i] = given[i]);
+  }
+  return Py_BuildValue("ONNNN", status.p, out[0], out[1], out[2], out[3]);
+}
+
+// layer_norm(address, device, stream, x, residual, sum, weight, bias, out, mean, rstd, type of out, eps, p, seed,
+//            offset): (status, out, sum, mean, rstd)
+// Where out, sum, mean or rstd is True it is made here, for the device's current stream.
+PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 16)) return nullptr;
+  return shortly([&]() -> PyObject* {
+    Reader r{PyLong_AsLongLong(a[1])};
+    const at::Tensor* x = r.tensor(a[3]);
+    if (!r.fine || x->dim() != 2) return nullptr;
+    const bool add = a[4] != Py_None;
+    const int64_t M = x->size(0), N = x->size(1);
+    const long oc = PyLong_AsLong(a[11]);
+    const at::ScalarType xt = x->scalar_type(), dt = a[8] != Py_True ? r.type(a[8], xt) : oc < 0 ? xt : type_of(oc);
+    const at::ScalarType st = add ? r.type(a[4], dt) : xt, wt = r.type(a[6], r.type(a[7], dt));
+    if (code_of(dt) < 0 || (oc != -1 && oc != code_of(dt)) || (st != at::kFloat && st != dt) ||
+        (wt != at::kFloat && wt != dt))
+      return nullptr;
+    const Mat X = r.mat(a[3], M, N, add ? dt : st), R = r.mat(a[4], M, N, st, true);
+    void *w = r.vec(a[6], N, wt, true), *b = r.vec(a[7], N, wt, true);
+    const double eps = PyFloat_AsDouble(a[12]);
+    const Mask m = r.mask(a[13], a[14], a[15]);
+    // out, sum, mean, rstd
+    PyObject* const given[4] = {a[8], a[5], a[9], a[10]};
+    const at::ScalarType types[2] = {dt, st};
+    at::Tensor made[4];
+    Mat mats[2];
+    float* stats[2];
+    for (int i = 0; i < 2; ++i)
+      if (given[i] != Py_True) mats[i] = r.mat(given[i], M, N, types[i], i > 0);
+    for (int i = 0; i < 2; ++i)
+      if (given[2 + i] != Py_True) stats[i] = (float*)r.vec(given[2 + i], M, at::kFloat, true);
+    if (!r.fine || PyErr_Occurred()) return nullptr;
+    for (int i = 0; i < 2; ++i)
+      if (given[i] == Py_True) {
+        made[i] = result(*x, M, N, types[i]);
+        mats[i] = {made[i].data_ptr(), M > 1 ? made[i].stride(0) : row_pitch(N, made[i])};
+      }
+    for (int i = 0; i < 2; ++i)
+      if (given[2 + i] == Py_True) {
+        made[2 + i] = at::empty({M}, x->options().dtype(at::kFloat));
+        stats[i] = (float*)made[2 + i].data_ptr();
+      }
+    Ref status(enter<decltype(coalesce_layer_norm)>(
+        a[0], X.p, X.ld, R.p, R.ld, mats[1].p, mats[1].ld, w, b, mats[0].p, mats[0].ld, stats[0], stats[1], M, N,
+        (coalesce_dtype)code_of(dt), (coalesce_dtype)code_of(st), (coalesce_dtype)code_of(wt), eps, m.p, m.seed,
+        m.offset, m.device, PyLong_AsVoidPtr(a[2])));
+    if (!status.p) return nullptr;
+    return returned(status, given, made);
+  });
 }
 
 // layer_norm_backward(address, device, stream, address of the workspace's size, x, weight, mean, rstd, dout, dsum,
@@ -308,14 +349,8 @@ PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         m.seed, m.offset, m.device, space ? space->data_ptr() : nullptr, space ? space->nbytes() : (size_t)0,
         PyLong_AsVoidPtr(a[2])));
     if (!status.p) return nullptr;
-    PyObject* out[4];
-    for (int i = 0; i < 4; ++i) {
-      if (made[i].defined())
-        out[i] = THPVariable_Wrap(std::move(made[i]));
-      else
-        Py_INCREF(out[i] = want[i] ? a[10 + i] : Py_None);
-    }
-    return Py_BuildValue("ONNNN", status.p, out[0], out[1], out[2], out[3]);
+    PyObject* const given[4] = {want[0] ? a[10] : Py_None, want[1] ? a[11] : Py_None, Py_None, Py_None};
+    return returned(status, given, made);
   });
 }
 

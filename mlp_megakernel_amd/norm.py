@@ -77,7 +77,7 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     ``x`` is a residual stream: float32, or of the result's type.  ``weight``
     and ``bias`` are float32 or of the result's type, both of the same.
     """
-    return _norm(x, None, weight, bias, eps, 0.0, 0, 0, out_dtype, out, None, False, None, stream)
+    return _norm(x, None, weight, bias, eps, 0.0, 0, 0, out_dtype, out, None, False, None, stream)[0]
 
 
 def layer_norm_train(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
@@ -86,11 +86,9 @@ def layer_norm_train(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bia
                      stream=None) -> Tuple[torch.Tensor, Tuple[torch.Tensor, torch.Tensor]]:
     """(y, (mean, rstd)): layer_norm and the statistics that
     layer_norm_backward needs, float32, one per row."""
-    if stats is None:
-        _rows(x, "x")
-        stats = _new_stats(x, stream)
-    y = _norm(x, None, weight, bias, eps, 0.0, 0, 0, out_dtype, out, None, False, stats, stream)
-    return y, tuple(stats)
+    y, _, stats = _norm(x, None, weight, bias, eps, 0.0, 0, 0, out_dtype, out, None, False,
+                        True if stats is None else stats, stream)
+    return y, stats
 
 
 def add_layer_norm(x: torch.Tensor, residual: torch.Tensor, weight: Optional[torch.Tensor] = None,
@@ -104,10 +102,7 @@ def add_layer_norm(x: torch.Tensor, residual: torch.Tensor, weight: Optional[tor
     sum before its rounding.  The mask is that of :func:`dropout` with the same
     ``p``, ``seed`` and ``offset``.
     """
-    if sum_out is None:
-        sum_out = _sum_like(x, residual, stream)
-    y = _norm(x, residual, weight, bias, eps, p, seed, offset, None, out, sum_out, True, None, stream)
-    return y, sum_out
+    return _norm(x, residual, weight, bias, eps, p, seed, offset, None, out, sum_out, True, None, stream)[:2]
 
 
 def add_layer_norm_train(x: torch.Tensor, residual: torch.Tensor, weight: Optional[torch.Tensor] = None,
@@ -116,12 +111,8 @@ def add_layer_norm_train(x: torch.Tensor, residual: torch.Tensor, weight: Option
                          stats: Optional[Tuple[torch.Tensor, torch.Tensor]] = None, stream=None):
     """(y, s, (mean, rstd)): add_layer_norm and the statistics that
     layer_norm_backward (of s) needs."""
-    if sum_out is None:
-        sum_out = _sum_like(x, residual, stream)
-    if stats is None:
-        stats = _new_stats(x, stream)
-    y = _norm(x, residual, weight, bias, eps, p, seed, offset, None, out, sum_out, True, stats, stream)
-    return y, sum_out, tuple(stats)
+    return _norm(x, residual, weight, bias, eps, p, seed, offset, None, out, sum_out, True,
+                 True if stats is None else stats, stream)
 
 
 def _like(x, dtype, stream):
@@ -138,16 +129,23 @@ def _sum_like(x, residual, stream):
 
 
 def _norm(x, residual, weight, bias, eps, p, seed, offset, out_dtype, out, sum_out, add, stats, stream):
-    if out is None:
+    """(y, sum, (mean, rstd)); stats: None for none, True for new ones."""
+    if stream is not None and out is None:
         out = _like(x, x.dtype if add or out_dtype is None else out_dtype, stream)
-    if out is not None and x.is_cuda and out_dtype in (None, out.dtype) and (stats is None or len(stats) == 2):
-        mean, rstd = stats or (None, None)
-        status = _short("layer_norm", "coalesce_layer_norm", stream, x, residual, sum_out, weight, bias, out, mean,
-                        rstd, eps, p, seed, offset)
-        if status == 0:
-            return out
-        if status is not None:
-            _check(status)
+    if stream is not None and add and sum_out is None:
+        sum_out = _sum_like(x, residual, stream)
+    if stream is not None and stats is True:
+        _rows(x, "x")
+        stats = _new_stats(x, stream)
+    made = stats is None or stats is True
+    if x.is_cuda and (not add or residual is not None) and (made or len(stats) == 2):
+        mean, rstd = (stats, stats) if made else stats
+        got = _short("layer_norm", "coalesce_layer_norm", stream, x, residual, True if add and sum_out is None else sum_out,
+                     weight, bias, True if out is None else out, mean, rstd,
+                     -1 if out_dtype is None else _DTYPES.get(out_dtype, -2), eps, p, seed, offset)
+        if got is not None:
+            _check(got[0])
+            return got[1], got[2], got[3:]
     M, N, ldx, dev = _rows(x, "x")
     if _current_device() != dev:
         return _there(dev, _norm, x, residual, weight, bias, eps, p, seed, offset, out_dtype, out, sum_out, add, stats,
@@ -163,8 +161,12 @@ def _norm(x, residual, weight, bias, eps, p, seed, offset, out_dtype, out, sum_o
     mask = _mask(p, seed, offset, dev)
     ldr = lds = 0
     if add:
+        if sum_out is None:
+            sum_out = _sum_like(x, residual, stream)
         ldr = _mat(residual, "residual", M, N, sdt, dev)
         lds = _mat(sum_out, "sum_out", M, N, sdt, dev)
+    if stats is True:
+        stats = _new_stats(x, stream)
     mean, rstd = (None, None) if stats is None else _stats(stats, M, dev)
     if out is None:
         out = _new(M, N, dt, x.device, stream)
@@ -173,7 +175,7 @@ def _norm(x, residual, weight, bias, eps, p, seed, offset, out_dtype, out, sum_o
         x.data_ptr(), ldx, _ptr(residual), ldr, _ptr(sum_out), lds, _ptr(weight), _ptr(bias), out.data_ptr(), ldy,
         _ptr(mean), _ptr(rstd), M, N, _DTYPES[dt], _DTYPES[sdt], _DTYPES[wt], float(eps), *mask,
         _raw_stream(stream, dev)))
-    return out
+    return out, sum_out, (mean, rstd)
 
 
 @functools.lru_cache(maxsize=None)
