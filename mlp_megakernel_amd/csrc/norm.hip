@@ -3,9 +3,13 @@
 //   s = R + keep(X) / (1 - p)   (or s = X)
 //   y = (s - mean) rstd w + b,  mean = sum s / N,  rstd = 1 / sqrt(sum (s - mean)^2 / N + eps)
 // Memory is what bounds it, so each row is read once: its values stay in
-// registers, the mean is exact before the squares of the deviations are summed
-// (a sum of squares less a squared mean would cancel where the mean is large),
-// and all of it is fp32 until the one rounding of each result.  y comes from the
+// registers, and all of it is fp32 until the one rounding of each result.  The mean
+// comes first, then the squares of the deviations from it (a sum of squares less a
+// squared mean would cancel where the mean is large).  The sum's roundings leave the
+// mean off by some steps of the values' size, which is nothing beside the deviations
+// unless the mean is larger than those (a constant row of 1e5 would give 0.9 for 0):
+// there the mean of the deviations is found too and taken from them.  (For every row
+// that took 8 % at 2048 x 16384 and 20000 x 777.)  y comes from the
 // sum before its rounding.  Rows of up to 16384 live in the registers of one
 // wave or one workgroup, the choice by N; longer ones are read once per pass, which
 // the caches serve.
@@ -27,6 +31,10 @@ struct Input {
         sum(p.R != nullptr) {}
 };
 
+// Whether a mean is so large beside the deviations (ve: their variance and eps) that its
+// own rounding counts.
+__device__ __forceinline__ bool far(float mean, float ve) { return !(mean * mean <= ve); }
+
 // One row per TPR threads, CH times 8 of its columns per thread; THREADS / TPR
 // rows per workgroup.  A row of one wave needs no barrier.
 template <typename T, typename TS, int TPR, int CH>
@@ -36,7 +44,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormParams 
   const int64_t row = block_no() * ROWS + wave / WAVES;
   if (row >= p.M) return;  // (whole workgroups where a row has more than one wave)
   const int t = threadIdx.x % TPR;
-  __shared__ float part[2][WAVES];
+  __shared__ float part[4][WAVES];
   const Input<T, TS> in(p, row);
   float v[CH][8];
   {
@@ -85,7 +93,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormParams 
   for (int c = 0; c < CH; ++c)
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum += v[c][e];
-  const float mean = total(sum, 0) / count;
+  float mean = total(sum, 0) / count;
   float sq = 0.0f;
   const bool whole = p.N == TPR * CH * 8;
 #pragma unroll
@@ -97,7 +105,25 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormParams 
       v[c][e] = d;
       sq = __builtin_fmaf(d, d, sq);
     }
-  const float rstd = 1.0f / __builtin_sqrtf(total(sq, 1) / count + p.eps);
+  float var = total(sq, 1) / count;
+  if (far(mean, var + p.eps)) {
+    sum = sq = 0.0f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum += v[c][e];
+    const float off = total(sum, 2) / count;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[c][e] = (c * TPR + t) * 8 + e < p.N ? v[c][e] - off : 0.0f;
+        sq = __builtin_fmaf(v[c][e], v[c][e], sq);
+      }
+    var = total(sq, 3) / count;
+    mean += off;
+  }
+  const float rstd = 1.0f / __builtin_sqrtf(var + p.eps);
   const Row<T> out = Row<T>::out(p.Y, p.ldy, row, p.N);
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
@@ -117,12 +143,13 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormParams 
   }
 }
 
-// Rows longer than the registers: one workgroup per row, three passes.  Each
+// Rows longer than the registers: one workgroup per row, three passes
+// (five of a row far from zero).  Each
 // thread meets the same columns in every pass and writes them in the last, so the
 // sum may be formed in place.
 template <typename T, typename TS>
 __global__ __launch_bounds__(1024) void norm_long_kernel(NormParams p) {
-  __shared__ float part[2][16];
+  __shared__ float part[4][16];
   const int64_t row = block_no();
   if (row >= p.M) return;
   const Input<T, TS> in(p, row);
@@ -154,6 +181,7 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormParams p) {
     for (int e = 0; e < 8; ++e) sum += v[e];
   }
   const float mean = total(sum, 0) / count;
+  float off = 0.0f;  // what is taken from the deviations
   for (int n = threadIdx.x * 8; n < p.N; n += 8192) {
     float v[8];
     read(n, v);
@@ -163,7 +191,28 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormParams p) {
       sq = __builtin_fmaf(d, d, sq);
     }
   }
-  const float rstd = 1.0f / __builtin_sqrtf(total(sq, 1) / count + p.eps);
+  float var = total(sq, 1) / count;
+  if (far(mean, var + p.eps)) {
+    sum = sq = 0.0f;
+    for (int n = threadIdx.x * 8; n < p.N; n += 8192) {
+      float v[8];
+      read(n, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum += n + e < p.N ? v[e] - mean : 0.0f;
+    }
+    off = total(sum, 2) / count;
+    for (int n = threadIdx.x * 8; n < p.N; n += 8192) {
+      float v[8];
+      read(n, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float d = n + e < p.N ? (v[e] - mean) - off : 0.0f;
+        sq = __builtin_fmaf(d, d, sq);
+      }
+    }
+    var = total(sq, 3) / count;
+  }
+  const float rstd = 1.0f / __builtin_sqrtf(var + p.eps);
   const Row<T> out = Row<T>::out(p.Y, p.ldy, row, p.N);
   for (int n = threadIdx.x * 8; n < p.N; n += 8192) {
     float v[8], w[8], b[8];
@@ -174,11 +223,11 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormParams p) {
     if (p.weight) read_vec<T>(p.weight, p.wt == DT_F32, n, p.N, w);
     if (p.bias) read_vec<T>(p.bias, p.wt == DT_F32, n, p.N, b);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf((v[e] - mean) * rstd, w[e], b[e]);
+    for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(((v[e] - mean) - off) * rstd, w[e], b[e]);
     out.store(n, v, (T*)p.Y + row * p.ldy);
   }
   if (threadIdx.x == 0) {
-    if (p.mean) p.mean[row] = mean;
+    if (p.mean) p.mean[row] = mean + off;
     if (p.rstd) p.rstd[row] = rstd;
   }
 }

@@ -1,10 +1,12 @@
 """Layer norm and its gradients at the edges of their range: rows whose values, mean or
 deviations are far from 1, against 64-bit references."""
+import numpy as np
 import pytest
 import torch
 
 import block_reference as ref
 import mlp_megakernel_amd as mk
+from ffn_reference import U32 as U
 from helpers import progress
 
 pytestmark = pytest.mark.gpu
@@ -50,3 +52,70 @@ def test_backward_of_a_constant_row(dt):
     y, stats = mk.layer_norm_train(S)
     assert bool((y == 0).all())
     check_backward(S, None, stats, ref.rows(gen, 1, 100, DT[dt]), None, (0.0, 0, 0), DT[dt], "a constant row")
+
+
+# ---------------------------------------------------------------------------
+# Forward
+# ---------------------------------------------------------------------------
+
+def norm64(s, w, b, eps, dt):
+    """dict of (value, bound) of y, mean and rstd of a stream s, whose mean is corrected where it is large.
+
+    The mean found first is off by at most DEPTH + 1 roundings of the values' mean size; the deviations d from it
+    are off by one rounding each.  Where its square is above the variance and eps (half as much again, so that
+    this and the kernel's own values agree), the mean of d is found by so many roundings of the size of d and
+    taken from them, which leaves a second-order term of the first error.
+    """
+    s = ref.f64(s)
+    eps = float(np.float32(eps))
+    k = min(s.shape[1], ref.DEPTH) + 2
+    mean = s.mean(1, keepdim=True)
+    dev = s - mean
+    var = dev.square().mean(1, keepdim=True)
+    e0 = k * U * s.abs().mean(1, keepdim=True)
+    size = dev.abs() + e0                                 # of d
+    em = torch.where(mean.square() > 1.5 * (var + eps), k * U * size.mean(1, keepdim=True), e0)
+    ed = em + 3 * U * size                                # d's rounding, that of its mean and of their difference
+    ev = (2 * dev.abs() * ed + ed * ed).mean(1, keepdim=True)
+    ev = ev + (k + 3) * U * (var + ev)
+    rstd = 1 / torch.sqrt(var + eps)
+    hi, lo = 1 / torch.sqrt(torch.clamp(var - ev, min=0) + eps), 1 / torch.sqrt(var + ev + eps)
+    er = torch.maximum(hi - rstd, rstd - lo) + 3 * U * hi
+    t = dev * rstd
+    et = ed * rstd + dev.abs() * er + ed * er + U * (t.abs() + ed * hi)
+    y = t * ref.f64(w) + ref.f64(b)
+    ey = et * ref.f64(w).abs() + U * (y.abs() + et * ref.f64(w).abs())
+    return {"y": (y, ref.rounded(y, ey, dt)), "mean": (mean[:, 0], (em + U * (mean.abs() + em))[:, 0]),
+            "rstd": (rstd[:, 0], er[:, 0])}
+
+
+def check_forward(S, w, b, eps, dt, what):
+    y, (mean, rstd) = mk.layer_norm_train(S, w, b, eps=eps, out_dtype=dt)
+    r = norm64(S, w, b, eps, dt)
+    for got, name in ((y, "y"), (mean, "mean"), (rstd, "rstd")):
+        ref.check(got, r[name], "%s of %s" % (name, what))
+    return y, mean, rstd
+
+
+def affine(N, seed):
+    gen = torch.Generator().manual_seed(seed)
+    return gen, (1 + 0.3 * torch.randn(N, generator=gen)).cuda(), (0.3 * torch.randn(N, generator=gen)).cuda()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+def test_rows_far_from_zero(dt):
+    # constant rows whose sums are not exact: y is the bias; and rows of unit deviation, or of some steps of
+    # their own type, around a far mean
+    for N in WIDTHS + [96, 768, 1000, 4096, 16384, 40001]:
+        progress("far from zero %s %d" % (dt, N))
+        gen, w, b = affine(N, N)
+        S = ref.rows(gen, 9, N, torch.float32)
+        S[0], S[1], S[2], S[3] = 1000.1, 12345.678, 100000.3, -3.1e7
+        S[4:] += torch.tensor([1000.1, 12345.678, -100000.3, 4096.0, 1e6], device="cuda")[:, None]
+        check_forward(S, w, b, 1e-5, DT[dt], N)
+        # the same as the sum of a stream and a branch (exact: the halves of each value)
+        half = ref.rows(gen, 9, N, torch.float32)
+        half.copy_(S * 0.5)
+        if dt == "f32":
+            y, s, _ = mk.add_layer_norm_train(half, half, w, b)
+            assert torch.equal(s, S) and torch.equal(y, mk.layer_norm(S, w, b))
