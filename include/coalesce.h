@@ -582,7 +582,8 @@ coalesce_status coalesce_clip_grad_norm_rows(const void* const* grads, void* con
  *   Y      device, M x N of dtype (ldy)
  *   mean, rstd  device, M floats each, written for the backward, or NULL
  * stream_dtype and weight_dtype are dtype or F32.  All of it is fp32, the mean
- * before the squares of the deviations; Y comes from the sum before its rounding.
+ * before the squares of the deviations, which may lie outside the range of fp32 (a row
+ * whose sum does is NaN); Y comes from the sum before its rounding.
  * p, seed, offset, device_seed: the mask (without R p must be 0).  M == 0 or N == 0
  * is a no-op.  eps must be a number of at least 0.
  */

@@ -32,8 +32,16 @@ struct Input {
 };
 
 // Whether a mean is so large beside the deviations (ve: their variance and eps) that its
-// own rounding counts.
-__device__ __forceinline__ bool far(float mean, float ve) { return !(mean * mean <= ve); }
+// own rounding counts, or ve so large or small that their squares left fp32.
+__device__ __forceinline__ bool far(float mean, float ve) {
+  return !(mean * mean <= ve && ve >= 0x1p-80f && ve < __builtin_inff());
+}
+// What such a row's deviations are multiplied by before they are squared.  Those of a small
+// ve are at most the root of N 2^-80, those of a large one at most 2^128: lifted, the sum
+// of N < 2^23 squares is below 2^103 and 2^119.
+__device__ __forceinline__ float lift_of(float ve) {
+  return ve < 0x1p-80f ? 0x1p80f : ve < __builtin_inff() ? 1.0f : 0x1p-80f;
+}
 
 // One row per TPR threads, CH times 8 of its columns per thread; THREADS / TPR
 // rows per workgroup.  A row of one wave needs no barrier.
@@ -105,13 +113,17 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormParams 
       v[c][e] = d;
       sq = __builtin_fmaf(d, d, sq);
     }
-  float var = total(sq, 1) / count;
-  if (far(mean, var + p.eps)) {
+  float ve = total(sq, 1) / count + p.eps, lift = 1.0f;
+  if (far(mean, ve)) {
+    lift = lift_of(ve);
     sum = sq = 0.0f;
 #pragma unroll
     for (int c = 0; c < CH; ++c)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum += v[c][e];
+      for (int e = 0; e < 8; ++e) {
+        v[c][e] *= lift;
+        sum += v[c][e];
+      }
     const float off = total(sum, 2) / count;
 #pragma unroll
     for (int c = 0; c < CH; ++c)
@@ -120,10 +132,10 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormParams 
         v[c][e] = (c * TPR + t) * 8 + e < p.N ? v[c][e] - off : 0.0f;
         sq = __builtin_fmaf(v[c][e], v[c][e], sq);
       }
-    var = total(sq, 3) / count;
-    mean += off;
+    ve = total(sq, 3) / count + p.eps * lift * lift;
+    mean += off / lift;
   }
-  const float rstd = 1.0f / __builtin_sqrtf(var + p.eps);
+  const float rstd = 1.0f / __builtin_sqrtf(ve);  // of v
   const Row<T> out = Row<T>::out(p.Y, p.ldy, row, p.N);
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
@@ -139,7 +151,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormParams 
   }
   if (t == 0) {
     if (p.mean) p.mean[row] = mean;
-    if (p.rstd) p.rstd[row] = rstd;
+    if (p.rstd) p.rstd[row] = rstd * lift;
   }
 }
 
@@ -181,7 +193,7 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormParams p) {
     for (int e = 0; e < 8; ++e) sum += v[e];
   }
   const float mean = total(sum, 0) / count;
-  float off = 0.0f;  // what is taken from the deviations
+  float off = 0.0f, lift = 1.0f;  // what is taken from the lifted deviations
   for (int n = threadIdx.x * 8; n < p.N; n += 8192) {
     float v[8];
     read(n, v);
@@ -191,14 +203,15 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormParams p) {
       sq = __builtin_fmaf(d, d, sq);
     }
   }
-  float var = total(sq, 1) / count;
-  if (far(mean, var + p.eps)) {
+  float ve = total(sq, 1) / count + p.eps;
+  if (far(mean, ve)) {
+    lift = lift_of(ve);
     sum = sq = 0.0f;
     for (int n = threadIdx.x * 8; n < p.N; n += 8192) {
       float v[8];
       read(n, v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum += n + e < p.N ? v[e] - mean : 0.0f;
+      for (int e = 0; e < 8; ++e) sum += n + e < p.N ? (v[e] - mean) * lift : 0.0f;
     }
     off = total(sum, 2) / count;
     for (int n = threadIdx.x * 8; n < p.N; n += 8192) {
@@ -206,13 +219,13 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormParams p) {
       read(n, v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float d = n + e < p.N ? (v[e] - mean) - off : 0.0f;
+        const float d = n + e < p.N ? (v[e] - mean) * lift - off : 0.0f;
         sq = __builtin_fmaf(d, d, sq);
       }
     }
-    var = total(sq, 3) / count;
+    ve = total(sq, 3) / count + p.eps * lift * lift;
   }
-  const float rstd = 1.0f / __builtin_sqrtf(var + p.eps);
+  const float rstd = 1.0f / __builtin_sqrtf(ve);
   const Row<T> out = Row<T>::out(p.Y, p.ldy, row, p.N);
   for (int n = threadIdx.x * 8; n < p.N; n += 8192) {
     float v[8], w[8], b[8];
@@ -223,12 +236,12 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormParams p) {
     if (p.weight) read_vec<T>(p.weight, p.wt == DT_F32, n, p.N, w);
     if (p.bias) read_vec<T>(p.bias, p.wt == DT_F32, n, p.N, b);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(((v[e] - mean) - off) * rstd, w[e], b[e]);
+    for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(((v[e] - mean) * lift - off) * rstd, w[e], b[e]);
     out.store(n, v, (T*)p.Y + row * p.ldy);
   }
   if (threadIdx.x == 0) {
-    if (p.mean) p.mean[row] = mean + off;
-    if (p.rstd) p.rstd[row] = rstd;
+    if (p.mean) p.mean[row] = mean + off / lift;
+    if (p.rstd) p.rstd[row] = rstd * lift;
   }
 }
 

@@ -17,10 +17,10 @@ TYPES = [("bf16", "bf16"), ("bf16", "f32"), ("f16", "f32"), ("f32", "f32")]
 WIDTHS = [100, 701, 1500, 2048, 3001, 5000, 9003, 16400]
 
 
-def check_backward(S, w, stats, dy, dsum, mask, dt, what):
-    g = mk.layer_norm_backward(S, w, stats, dy, dsum, *mask, want_dbranch=True)
+def check_backward(S, w, stats, dy, dsum, mask, dt, what, branch=True):
+    g = mk.layer_norm_backward(S, w, stats, dy, dsum, *mask, want_dbranch=branch)
     r = ref.norm_backward(S, w, *stats, dy, dsum, mask, dt, S.dtype, torch.float32)
-    for name in ("dx", "dbranch", "dweight", "dbias"):
+    for name in ("dx", "dbranch", "dweight", "dbias") if branch else ("dx", "dweight", "dbias"):
         ref.check(getattr(g, name), r[name], "%s of %s" % (name, what))
 
 
@@ -119,3 +119,20 @@ def test_rows_far_from_zero(dt):
         if dt == "f32":
             y, s, _ = mk.add_layer_norm_train(half, half, w, b)
             assert torch.equal(s, S) and torch.equal(y, mk.layer_norm(S, w, b))
+
+
+@pytest.mark.parametrize("types", TYPES, ids="-".join)
+def test_deviations_whose_squares_leave_fp32(types):
+    # 2^70 and 2^100 overflow when squared, 2^-70 and 2^-100 vanish, and without an eps they count
+    dt, sdt = DT[types[0]], DT[types[1]]
+    for N in WIDTHS + [4096]:
+        progress("range %s %d" % (types, N))
+        gen, w, b = affine(N, N)
+        S = ref.rows(gen, 7, N, sdt, mean=0.25)
+        S *= torch.tensor([2.0 ** k for k in (70, 100, -70, -100, 0, -45, 60)], device="cuda", dtype=sdt)[:, None]
+        y, mean, rstd = check_forward(S, w, b, 0.0, dt, N)
+        dy = ref.rows(gen, 7, N, dt)
+        check_backward(S, w, (mean, rstd), dy, None, (0.0, 0, 0), dt, N, branch=dt is not torch.float16)
+        # beside an eps the small ones are nothing, and the large ones as before
+        again, _, _ = check_forward(S, w, b, 1e-5, dt, N)
+        assert torch.equal(again[[0, 1, 6]], y[[0, 1, 6]])
