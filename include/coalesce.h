@@ -585,7 +585,7 @@ coalesce_status coalesce_clip_grad_norm_rows(const void* const* grads, void* con
  * before the squares of the deviations, which may lie outside the range of fp32 (a row
  * whose sum does is NaN); Y comes from the sum before its rounding.
  * p, seed, offset, device_seed: the mask (without R p must be 0).  M == 0 or N == 0
- * is a no-op.  eps must be a number of at least 0.
+ * is a no-op.  eps must be a number of at least 0 and finite in fp32.
  */
 coalesce_status coalesce_layer_norm(const void* X, int64_t ldx, const void* R, int64_t ldr, void* S, int64_t lds,
                                     const void* weight, const void* bias, void* Y, int64_t ldy, float* mean,

@@ -224,8 +224,8 @@ coalesce_status coalesce_layer_norm(const void* X, int64_t ldx, const void* R, i
   if (s != COALESCE_OK) return s;
   if ((s = check_types(dtype, stream_dtype)) != COALESCE_OK) return s;
   if ((s = check_types(dtype, weight_dtype)) != COALESCE_OK) return s;
-  if (!(eps >= 0.0) || std::isinf(eps))
-    return fail(COALESCE_ERR_INVALID_ARGUMENT, "eps must be a number of at least 0");
+  if (!(eps >= 0.0) || std::isinf((float)eps))
+    return fail(COALESCE_ERR_INVALID_ARGUMENT, "eps must be a number of at least 0 and finite in fp32");
   Drop drop{};
   if ((s = make_drop(p, seed, offset, device_seed, &drop)) != COALESCE_OK) return s;
   if (M == 0 || N == 0) return ok();  // (R of no rows may have no address)
