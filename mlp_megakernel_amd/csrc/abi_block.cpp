@@ -128,8 +128,8 @@ coalesce_status int8_product(bool gated, const int8_t* A, int64_t lda, const int
   }
   q.R = R;
   q.Y = Y;
-  q.lda = lda;
-  q.ldb = ldb;
+  q.lda = K > 0 ? lda : 0;  // (unchecked where the operands have no elements)
+  q.ldb = K > 0 ? ldb : 0;
   q.ldr = ldr;
   q.ldy = ldy;
   q.M = (int)M;
