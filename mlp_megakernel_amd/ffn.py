@@ -633,6 +633,8 @@ class QuantizedGatedFFN(torch.nn.Module):
 
     Made by :meth:`GatedFFN.quantized`.  x is of the block's type; nothing
     depends on the other tokens of a call.  There is no gradient and no dropout.
+    ``half()``, ``bfloat16()``, ``float()`` and ``to(dtype)`` change the type of x
+    and of the result alone: weights stay 8-bit, scales and biases float32.
     """
 
     def __init__(self, block: GatedFFN):
@@ -647,6 +649,24 @@ class QuantizedGatedFFN(torch.nn.Module):
             for name in ("bg", "bu", "bd", "norm_weight", "norm_bias"):
                 t = getattr(block, name)
                 self.register_buffer(name, None if t is None else t.detach().float().clone())
+
+    def _apply(self, fn, recurse=True):
+        dtype = fn(self.Wg_scale.new_empty(0, dtype=self.dtype)).dtype
+        if dtype not in _DTYPES:
+            raise TypeError("QuantizedGatedFFN takes float32, float16 or bfloat16, not %s" % dtype)
+
+        def moved(t):  # fn without its change of type, which leaves integers as they are
+            s = fn(t)
+            if s.dtype is t.dtype:
+                return s
+            s = fn(t.view(torch.uint8))
+            if s.dtype is not torch.uint8:
+                raise TypeError("the weights of a QuantizedGatedFFN stay 8-bit")
+            return s.view(t.dtype)
+
+        super()._apply(moved, recurse)
+        self.dtype = dtype
+        return self
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         shape = x.shape
