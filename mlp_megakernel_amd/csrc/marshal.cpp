@@ -253,6 +253,7 @@ PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!r.fine || x->dim() != 2) return nullptr;
     const bool add = a[4] != Py_None;
     const int64_t M = x->size(0), N = x->size(1);
+    if (N == 0) return nullptr;  // the binding writes the statistics of nothing
     const long oc = PyLong_AsLong(a[11]);
     const at::ScalarType xt = x->scalar_type(), dt = a[8] != Py_True ? r.type(a[8], xt) : oc < 0 ? xt : type_of(oc);
     const at::ScalarType st = add ? r.type(a[4], dt) : xt, wt = r.type(a[6], r.type(a[7], dt));

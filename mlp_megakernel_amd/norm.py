@@ -13,7 +13,7 @@ from typing import NamedTuple, Optional, Tuple, Union
 
 import torch
 
-from . import _DTYPES, _check, _empty, _matrix, _ptr, load_library
+from . import _DTYPES, _check, _empty, _matrix, _ptr, _stream_object, load_library
 from .ffn import _current_device, _mat, _new, _raw_stream, _row_pitch, _short, _take, _there, _vec, _ws_sizes
 
 Seed = Union[int, torch.Tensor]
@@ -85,7 +85,7 @@ def layer_norm_train(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bia
                      stats: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
                      stream=None) -> Tuple[torch.Tensor, Tuple[torch.Tensor, torch.Tensor]]:
     """(y, (mean, rstd)): layer_norm and the statistics that
-    layer_norm_backward needs, float32, one per row."""
+    layer_norm_backward needs, float32, one per row (NaN without columns)."""
     y, _, stats = _norm(x, None, weight, bias, eps, 0.0, 0, 0, out_dtype, out, None, False,
                         True if stats is None else stats, stream)
     return y, stats
@@ -175,6 +175,10 @@ def _norm(x, residual, weight, bias, eps, p, seed, offset, out_dtype, out, sum_o
         x.data_ptr(), ldx, _ptr(residual), ldr, _ptr(sum_out), lds, _ptr(weight), _ptr(bias), out.data_ptr(), ldy,
         _ptr(mean), _ptr(rstd), M, N, _DTYPES[dt], _DTYPES[sdt], _DTYPES[wt], float(eps), *mask,
         _raw_stream(stream, dev)))
+    if N == 0 and mean is not None:  # the call did nothing
+        with torch.cuda.stream(None if stream is None else _stream_object(stream, x.device)):
+            mean.fill_(float("nan"))
+            rstd.fill_(float("nan"))
     return out, sum_out, (mean, rstd)
 
 

@@ -136,3 +136,21 @@ def test_deviations_whose_squares_leave_fp32(types):
         # beside an eps the small ones are nothing, and the large ones as before
         again, _, _ = check_forward(S, w, b, 1e-5, dt, N)
         assert torch.equal(again[[0, 1, 6]], y[[0, 1, 6]])
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_statistics_of_rows_without_columns(given):
+    # 0 / 0, whatever the memory held
+    x = torch.empty(5, 0, device="cuda", dtype=torch.bfloat16)
+    for stream in (None, torch.cuda.Stream()):
+        for call in (lambda **kw: mk.layer_norm_train(x, stream=stream, **kw),
+                     lambda **kw: mk.add_layer_norm_train(x, x, stream=stream, **kw)):
+            torch.full((1 << 12,), 3.0, device="cuda")  # (freed: what comes next may hold it)
+            stats = tuple(torch.full((5,), 7.0, device="cuda") for _ in range(2)) if given else None
+            torch.cuda.synchronize()
+            got = call(stats=stats)
+            torch.cuda.synchronize()
+            assert got[0].shape == (5, 0)
+            for i in range(2):
+                assert got[-1][i].shape == (5,) and bool(got[-1][i].isnan().all())
+                assert not given or got[-1][i] is stats[i]
