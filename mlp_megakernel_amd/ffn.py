@@ -651,7 +651,7 @@ class QuantizedGatedFFN(torch.nn.Module):
                 self.register_buffer(name, None if t is None else t.detach().float().clone())
 
     def _apply(self, fn, recurse=True):
-        dtype = fn(self.Wg_scale.new_empty(0, dtype=self.dtype)).dtype
+        dtype = fn(self.Wg_scale.new_empty(1, dtype=self.dtype)).dtype
         if dtype not in _DTYPES:
             raise TypeError("QuantizedGatedFFN takes float32, float16 or bfloat16, not %s" % dtype)
 

@@ -54,3 +54,14 @@ def test_other_types_are_refused_and_change_nothing(change):
     with pytest.raises(TypeError):
         change(q)
     assert torch.equal(q(x), want)
+
+
+def test_storage_shared_between_processes_and_left_empty():
+    q = block()
+    cpu = copy.deepcopy(q).cpu().share_memory()
+    assert cpu.Wg.is_shared() and cpu.dtype is q.dtype
+    x = torch.randn(5, 72, device="cuda").bfloat16()
+    assert torch.equal(cpu.cuda()(x), q(x))
+    empty = copy.deepcopy(q).to_empty(device="cuda")
+    empty.load_state_dict(q.state_dict())
+    assert torch.equal(empty(x), q(x))
