@@ -257,7 +257,7 @@ coalesce_status coalesce_layer_norm(const void* X, int64_t ldx, const void* R, i
   add_seed(ops, drop);
   if ((s = ops.check()) != COALESCE_OK) return s;
   int cus = 0;
-  if ((s = current_cus(&cus)) != COALESCE_OK) return s;
+  if ((s = current_cus(&cus)) != COALESCE_OK) return s;  // a device that answers, as in every other entry point
   NormParams q{};
   q.X = X;
   q.R = R;
@@ -276,7 +276,7 @@ coalesce_status coalesce_layer_norm(const void* X, int64_t ldx, const void* R, i
   q.eps = (float)eps;
   q.wt = dt_code(weight_dtype);
   q.drop = drop;
-  hipError_t e = launch_norm(q, dt_code(dtype), dt_code(stream_dtype), (hipStream_t)stream, cus);
+  hipError_t e = launch_norm(q, dt_code(dtype), dt_code(stream_dtype), (hipStream_t)stream);
   if (e != hipSuccess) return device_fail(e, "layer norm launch");
   return ok();
 }

@@ -29,7 +29,7 @@ struct NormParams {
   DType wt;  // type of weight and bias
   Drop drop;
 };
-hipError_t launch_norm(const NormParams& p, DType operand, DType stream_type, hipStream_t stream, int num_cus);
+hipError_t launch_norm(const NormParams& p, DType operand, DType stream_type, hipStream_t stream);
 
 struct NormBwdParams {
   const void* S;   // the stream (TS)

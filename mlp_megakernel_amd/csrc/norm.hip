@@ -271,7 +271,7 @@ hipError_t norm_typed(const NormParams& p, hipStream_t stream) {
 
 }  // namespace
 
-hipError_t launch_norm(const NormParams& p, DType operand, DType stream_type, hipStream_t stream, int) {
+hipError_t launch_norm(const NormParams& p, DType operand, DType stream_type, hipStream_t stream) {
   if (operand == DT_F32) return norm_typed<float, float>(p, stream);
   if (operand == DT_BF16)
     return stream_type == DT_F32 ? norm_typed<__bf16, float>(p, stream) : norm_typed<__bf16, __bf16>(p, stream);

@@ -31,7 +31,7 @@ extern "C" hipError_t hipGetDevice(int* d) { return *d = 0, hipSuccess; }
 extern "C" hipError_t hipDeviceGetAttribute(int* v, hipDeviceAttribute_t, int) { return *v = 256, hipSuccess; }
 extern "C" const char* hipGetErrorString(hipError_t) { return ""; }
 namespace coalesce {
-hipError_t launch_norm(const NormParams&, DType, DType, hipStream_t, int) { return hipSuccess; }
+hipError_t launch_norm(const NormParams&, DType, DType, hipStream_t) { return hipSuccess; }
 size_t norm_backward_workspace(int64_t, int64_t, int) { return 0; }
 hipError_t launch_norm_backward(NormBwdParams, DType, DType, hipStream_t, int) { return hipSuccess; }
 hipError_t launch_dropout(const DropoutParams&, DType, DType, hipStream_t) { return hipSuccess; }
