@@ -152,21 +152,23 @@ enum Few8Kind {
   FEW8_64,        // up to 64
   FEW8_64_PAIRS,  // with two blocks of channels per wave
 };
-// Up to 64 rows (where tiles come nearest, gated 64 x 16384 x 4096, 36 us against 39; plain
-// 64 x 1024 x 2731 6.2 against 10).
+// Up to 64 rows (where tiles come nearest, 64 x 4096 x 16384, 20.8 us against 20.9; gated 64 x
+// 16384 x 4096 35.5 against 39.0, 64 x 1024 x 2731 6.0 against 11.0).  All figures here with
+// weights that change from call to call, as a model's layers do.
 Few8Kind plan_few8(int64_t m, int64_t n, int64_t k, bool gated, int num_cus) {
   if (m > 64) return FEW8_NONE;
   const bool one_round = n <= 16 * (int64_t)num_cus;  // of strips
   // Weights that would fill a quarter of the memory's cache of 256 MB are not kept
-  // there (gated, 1 x 16384 x 4096 27.5 -> 25.1 us); smaller ones may still lie in it (1 x
-  // 5461 x 2048 7.6 us, 8.6 past it), and the X of more than 16 rows wants the caches too.
+  // there (gated, 1 x 16384 x 4096 27.9 -> 27.2 us); smaller ones may still lie in it (1 x
+  // 5461 x 2048 6.1 us then, 6.5 past it; 6.9 and 7.1 where they do not), and the X of more
+  // than 16 rows wants the caches too (plain, 64 x 4096 x 16384 20.8, 24.3 past them).
   const bool once = (gated ? 2 : 1) * n * k >= (int64_t)64 << 20;
   if (m <= 8) {
     // 160 KB of stages per compute unit, as one workgroup where there is one strip for
-    // each (plain, 1 x 4096 x 16384: 14.6 us, 15.1 with smaller ones), as two where
-    // strips follow each other (gated, 1 x 16384 x 4096: 25.1, 26.6 with four waves, 27.5
-    // with one workgroup); in between the smaller workgroups win (1 x 5461 x 2048 6.6,
-    // 6.9).
+    // each (plain, 1 x 4096 x 16384: 15.5 us, 16.6 with smaller ones), as two where
+    // strips follow each other (gated, 1 x 16384 x 4096: 27.2, 28.8 with four waves, 29.3
+    // with one workgroup); in between the smaller workgroups win (1 x 5461 x 2048 6.9,
+    // 7.5).
     if (!gated && one_round) return FEW8_8_WIDE;
     if (gated && n > 32 * (int64_t)num_cus && once) return FEW8_8_LONG;
     return once ? FEW8_8_ONCE : FEW8_8;
@@ -174,8 +176,8 @@ Few8Kind plan_few8(int64_t m, int64_t n, int64_t k, bool gated, int num_cus) {
   if (m <= 16) return once ? FEW8_16_ONCE : FEW8_16;
   if (m <= 32) return FEW8_32;
   // Where strips follow each other two blocks of channels per wave halve what is drawn of
-  // X (64 x 16384 x 4096: gated 36 us, 43 with one, plain 20 and 24; but gated 64 x 1024 x
-  // 512 5.5 and 4.3).
+  // X (64 x 16384 x 4096: gated 35.5 us, 46.1 with one, plain 16.2 and 24.0; but 64 x 4096 x
+  // 16384, a strip for each compute unit, 25.5 and 20.8, and 64 x 1024 x 2731 8.5 and 6.0).
   return one_round ? FEW8_64 : FEW8_64_PAIRS;
 }
 

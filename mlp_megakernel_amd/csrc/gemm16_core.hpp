@@ -240,10 +240,11 @@ struct Tile {
   static constexpr int V = PerElement<T>::N;
   static_assert(V == 1 || (LA == LAY_K && LB == LAY_K), "pairs lie along the contraction");
   // The int32 sums do not mind the order of the steps: the XCDs begin at different
-  // ones, so that they ask different channels of the memory (8192 x 4096 x 16384 459 ->
-  // 454 us, at a pitch of 16400 554 -> 510, gated 777 x 16384 x 4096 117 -> 111).  The tiles of
-  // four waves are better off when they read the same lines at the same time (400 x 4096 x
-  // 16384 53 -> 59).
+  // ones, so that they ask different channels of the memory (operands that change from call
+  // to call, 8192 x 4096 x 16384 430 -> 418 us, at a pitch of 16400 536 -> 488; one round of
+  // tiles has little of it, gated 777 x 16384 x 4096 107.9 -> 107.2, 777 x 5461 x 2048 22.0 ->
+  // 22.9).  The tiles of four waves are better off when they read the same lines at the same
+  // time (400 x 4096 x 16384 48 -> 53).
   static constexpr bool TURN = V == 2 && G::NW == 8;
   static_assert(SEGS == 1 || G::NSUB == 1, "segments of a gated product are not implemented");
 

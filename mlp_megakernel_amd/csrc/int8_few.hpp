@@ -4,9 +4,10 @@
 // The weights lie channel by channel (N x K), so a fragment of the matrix
 // instruction is 16 consecutive bytes of a row; but its lanes go over the rows
 // first, and loads into registers in that order look up one cache line per lane: 16
-// bytes a cycle and compute unit, weights and tokens together (64 x 4096 x 16384: 40
-// us).  So both go through LDS by direct copies of whole 128-byte lines (20 us; 1 x 16384
-// x 4096 gated 25.1, 5.3 TB/s; 1 x 2731 x 1001 3.3).
+// bytes a cycle and compute unit, weights and tokens together (64 x 4096 x 16384, weights
+// that the caches may hold: 40 us).  So both go through LDS by direct copies of whole
+// 128-byte lines (20 us; weights that change from call to call 21 to 23, 1 x 16384 x 4096
+// gated 27, 5.0 TB/s, and 1 x 2731 x 1001 3.8).
 // A workgroup owns 16 NT channels (of both matrices of a gated product) and deals
 // the K steps of 128 to its waves in turn; a wave streams its steps through a private
 // ring of D stages and never meets a barrier until the end: it waits for its own

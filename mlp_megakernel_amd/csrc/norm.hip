@@ -8,11 +8,11 @@
 // squared mean would cancel where the mean is large).  The sum's roundings leave the
 // mean off by some steps of the values' size, which is nothing beside the deviations
 // unless the mean is larger than those (a constant row of 1e5 would give 0.9 for 0):
-// there the mean of the deviations is found too and taken from them.  (For every row
-// that took 8 % at 2048 x 16384 and 20000 x 777.)  y comes from the
-// sum before its rounding.  Rows of up to 16384 live in the registers of one
-// wave or one workgroup, the choice by N; longer ones are read once per pass, which
-// the caches serve.
+// there the mean of the deviations is found too and taken from them (8192 x 4096 bf16 22.9
+// us, 25.1 where all rows are so; done for every row, it took 8 % at 2048 x 16384 and
+// 20000 x 777).  y comes from the sum before its rounding.  Rows of up to 16384 live in
+// the registers of one wave or one workgroup, the choice by N; longer ones are read once
+// per pass (4096 x 28672 bf16: 141 us, 470 MB in 91 at the rate of a copy).
 #include "philox.hpp"
 #include "rows.hpp"
 

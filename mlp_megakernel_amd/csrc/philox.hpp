@@ -13,8 +13,8 @@ namespace coalesce {
 namespace {
 
 // Ten rounds; a round's two 32 x 32 -> 64-bit products are one instruction each.
-// 8192 x 4096 bf16 with a residual: 29.4 us with a constant in the words' place,
-// 29.5 with 7 rounds, 29.9 with 10; without one 20.1, 22.2 and 28.5.
+// 8192 x 4096 bf16, operands that change from call to call: with a residual 36.5 us without
+// rounds, 37.0 with 7 and 37.2 with 10; without one 24.4, 25.0 and 28.0.
 __device__ __forceinline__ u32x4 philox(u32x4 c, uint32_t k0, uint32_t k1) {
 #pragma unroll
   for (int r = 0; r < 10; ++r) {

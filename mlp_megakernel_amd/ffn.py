@@ -500,7 +500,12 @@ def _draw_seed(device) -> torch.Tensor:
 
 
 def _down(H, Wd, bd, skip, p, seed):
-    """skip + dropout(H Wd + bd); without a dropout in the product's own epilogue."""
+    """skip + dropout(H Wd + bd); without a dropout in the product's own epilogue.
+
+    With one H Wd + bd is rounded to the type in between, half a step of its own more
+    than in the epilogue: the dropout reads what a product of that type gives, and an
+    fp32 one would cost it 4 more bytes an element written and read.
+    """
     if seed is None:
         return gemm_residual(H, Wd, skip, bd)
     h = gemm_residual(H, Wd, None, bd)

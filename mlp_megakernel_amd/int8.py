@@ -2,7 +2,7 @@
 
 As the rest of the binding: argument checks and marshalling only, all
 arithmetic in ``libcoalesce.so``.  Tensors must live on one device; the calls
-run there, on ``stream`` or that device's current stream.
+run there, on ``stream`` or that device's current stream.  They have no gradients.
 """
 from __future__ import annotations
 

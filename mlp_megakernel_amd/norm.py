@@ -3,7 +3,8 @@
 As the rest of the binding: argument checks and marshalling only, all
 arithmetic in ``libcoalesce.so``.  Tensors are 2-D with 16-byte aligned rows (any
 number of columns) and live on one device; the calls run there, on ``stream`` or
-that device's current stream.
+that device's current stream.  They are not seen by autograd: results have no
+gradient, whatever the operands require (:class:`GatedFFN` does).
 """
 from __future__ import annotations
 
