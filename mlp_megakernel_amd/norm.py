@@ -176,10 +176,11 @@ def _norm(x, residual, weight, bias, eps, p, seed, offset, out_dtype, out, sum_o
         x.data_ptr(), ldx, _ptr(residual), ldr, _ptr(sum_out), lds, _ptr(weight), _ptr(bias), out.data_ptr(), ldy,
         _ptr(mean), _ptr(rstd), M, N, _DTYPES[dt], _DTYPES[sdt], _DTYPES[wt], float(eps), *mask,
         _raw_stream(stream, dev)))
-    if N == 0 and mean is not None:  # the call did nothing
+    if N == 0:  # the call did nothing
         with torch.cuda.stream(None if stream is None else _stream_object(stream, x.device)):
-            mean.fill_(float("nan"))
-            rstd.fill_(float("nan"))
+            for t in (mean, rstd):
+                if t is not None:
+                    t.fill_(float("nan"))
     return out, sum_out, (mean, rstd)
 
 

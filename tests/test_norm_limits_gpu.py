@@ -154,3 +154,5 @@ def test_statistics_of_rows_without_columns(given):
             for i in range(2):
                 assert got[-1][i].shape == (5,) and bool(got[-1][i].isnan().all())
                 assert not given or got[-1][i] is stats[i]
+            _, (mean, rstd) = mk.layer_norm_train(x, stats=(got[-1][0].zero_(), None))  # one of them
+            assert bool(mean.isnan().all()) and rstd is None
