@@ -12,9 +12,9 @@ from helpers import progress
 pytestmark = pytest.mark.gpu
 
 DT = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
-# a wave per row, four at a time (3072 rows in one turn of 768 workgroups), a workgroup per row (768; 512 of an fp32
-# stream with 16 columns per thread; 256 beyond 4096 columns), each for at least two turns and a part of a third;
-# and rows longer than the registers, whose columns are summed over several ranges of 64 rows or more
+# a wave per row, four to a workgroup, then a workgroup per row (768 of them at once; 512 of an fp32 stream with 16
+# columns per thread; 256 beyond 4096 columns), each for at least two turns and a part of a third; and rows longer
+# than the registers, whose columns are summed over several ranges of rows
 SHAPES = [(6500, 40), (6301, 701), (1700, 1500), (1701, 2731), (1537, 4096), (801, 4100), (600, 8200), (515, 16384),
           (200, 16392), (70, 20001)]
 
